@@ -11,6 +11,9 @@ rnn_workspace_bytes, rnn_forward_raw (= C rnn_forward), rnn_read_status,
 rnn_device_check, rnn_plan_info, rnn_exchange_roundtrip_ns. High level: rnn_forward (LSTM / GRU / LSTMP, padded or
 packed, multi-layer, bidirectional), rssm_prior_unroll and rssm_actor_unroll; training:
 rnn_forward_train and rnn_backward (fp32 LSTM / LSTMP / GRU).
+
+Operators of a decoder block: layer_norm (with the residual add) and gated_scan (a gated linear recurrence), each with a
+_train form that also returns a context and a _backward that takes it.
 """
 
 from .binding import (  # noqa: F401
@@ -18,4 +21,8 @@ from .binding import (  # noqa: F401
     rnn_abi_version, rnn_strerror, rnn_workspace_bytes, rnn_forward_raw, rnn_read_status,
     rnn_device_check, rnn_exchange_roundtrip_ns, rnn_forward, rssm_prior_unroll, rssm_actor_unroll, rnn_plan_info,
     MODES, PIPE_MODES, STATUS, CLIP_CELL, CLIP_PROJ, RnnGrads, rnn_forward_train, rnn_backward, TrainContext,
+)
+from .block_ops import (  # noqa: F401
+    RnnNormDesc, RnnGatedScanDesc, RnnGatedScanIO, RnnGatedScanGrads, BlockContext,
+    layer_norm, layer_norm_train, layer_norm_backward, gated_scan, gated_scan_train, gated_scan_backward,
 )

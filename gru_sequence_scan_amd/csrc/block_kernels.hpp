@@ -1,0 +1,62 @@
+// Interfaces between the host code of the decoder block's operators
+// (block_api.cpp) and their kernels. Sizes and strides are in elements.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernels.hpp"
+
+namespace rnnk {
+
+// Compute units and XCDs of the current device; RNN_E_DEVICE when it is not
+// a gfx950.
+int current_device_facts(int* cus, int* xcds);
+
+// Gated linear recurrence (gated_scan.hip).
+constexpr int kGatedScanChunk = 128;  // steps between two boundary states
+struct GatedScanArgs {
+  int T, B, H, reverse;
+  const void* x; int64_t x_t, x_b;
+  const void* f; int64_t f_t, f_b;
+  const void* i; int64_t i_t, i_b;  // null: coupled gates
+  const int* lengths;               // device [B] or null
+  const float* h0;                  // [B, H] or null
+  void* y;                          // [T, B, H]
+  float* h_n;                       // [B, H] or null
+  int keep_state;                   // training: `state` is filled whatever the chunk count
+  // backward
+  const void* dy; const float* dh_n;
+  void* dx; void* df; void* di; float* dh0;
+  // chunking
+  int width;                        // channels per access: 4, or 1 where rows are not aligned to it
+  int chunks;
+  float* map_p; float* map_s;       // [chunks, B, H] composed maps (workspace; chunks > 1)
+  float* state;                     // [chunks, B, H] state entering a chunk
+  float* back_state;                // [chunks, B, H] its gradient's counterpart
+  int tiles;                        // set by launch_gated_scan
+};
+hipError_t launch_gated_scan(GatedScanArgs a, bool bf16_storage, bool backward, hipStream_t stream);
+
+// Layer norm (layer_norm.hip).
+struct NormArgs {
+  int64_t rows; int N; float eps;
+  const void* x; int64_t ldx;
+  const void* r; int64_t ldr;       // residual or null
+  const void* w; const void* b;     // [N] or null
+  void* y; void* sum;               // [rows, N]; sum only with r
+  float* stats;                     // [rows, 2] mean, 1 / sqrt(var + eps); forward: may be null
+  // backward (x = the tensor that was normalised)
+  const void* dy; const void* ds;   // [rows, N]; ds may be null
+  void* dx; float* dw; float* db;   // dw, db may be null
+  float* part;                      // [blocks, 2, N]
+  int blocks;
+  int vec;                          // rows take 8-element accesses
+};
+constexpr int kNormMaxN = 16384;
+// Workgroups of the backward pass, each with one row of partial sums.
+int norm_backward_blocks(int64_t rows, int N, int cus);
+hipError_t launch_layer_norm(const NormArgs& a, bool bf16_storage, hipStream_t stream);
+hipError_t launch_layer_norm_backward(const NormArgs& a, bool bf16_storage, hipStream_t stream);
+
+}  // namespace rnnk

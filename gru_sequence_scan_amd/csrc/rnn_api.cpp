@@ -16,7 +16,7 @@
 #include <vector>
 
 #include "../../include/rnn.h"
-#include "kernels.hpp"
+#include "block_kernels.hpp"
 
 using namespace rnnk;
 
@@ -72,6 +72,18 @@ int current_device_info(DeviceInfo* out) {
   *out = g_dev[dev];
   return out->ok ? RNN_OK : RNN_E_DEVICE;
 }
+
+}  // namespace
+
+int rnnk::current_device_facts(int* cus, int* xcds) {
+  DeviceInfo info;
+  const int rc = current_device_info(&info);
+  *cus = info.cus;
+  *xcds = info.xcds;
+  return rc;
+}
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Validation

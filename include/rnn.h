@@ -426,6 +426,111 @@ int rnn_device_check(void);
  * (the two workgroups were not resident together). */
 int rnn_exchange_roundtrip_ns(void* buffer, size_t bytes, int iters, void* stream, double* ns_per_round_trip);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a decoder block beside the recurrences: layer norm with the
+ * residual add, and a gated linear recurrence. Conventions as above (caller-owned buffers, validation
+ * before anything is enqueued, no synchronisation, deterministic results),
+ * with these differences:
+ *   - Inputs carry strides (in elements); their last dimension is
+ *     contiguous. Outputs, gradients and the incoming gradients are dense.
+ *     Rows whose addresses and strides are multiples of 16 bytes (gated
+ *     scan: four elements) take wide accesses, others element accesses.
+ *   - Lengths are a DEVICE int32 array, so that a call can be captured and
+ *     never reads host memory. A value is clamped to [0, T]: 0 is a row with
+ *     no steps (its outputs are zero, its state passes through).
+ *   - What lies past a row's length is never read, so it may hold anything
+ *     (NaN included); outputs and gradients there are written as zero.
+ *   - None of the kernels waits for another workgroup, so there is no device
+ *     status and they may share the device with other work.
+ *   - A workspace or reserve may be NULL when its size is 0.
+ * Statistics, states and sums are fp32; dtype is the storage type of the
+ * tensors whose type is not given.
+ * ------------------------------------------------------------------------- */
+
+#define RNN_NORM_MAX_N 16384
+
+/* Layer norm over the last dimension of [rows, N]:
+ *   s = x + residual (rounded to the storage type; s = x without one)
+ *   y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias                   */
+typedef struct RnnNormDesc {
+  int32_t dtype;         /* RnnDtype                                           */
+  int32_t N;             /* row length, 1 .. RNN_NORM_MAX_N                    */
+  int64_t rows;          /* >= 1                                               */
+  int64_t x_ld;          /* elements between rows of x (>= N)                  */
+  int64_t residual_ld;   /* ... of residual (ignored without one)              */
+  float eps;             /* >= 0, finite                                       */
+  int32_t reserved;      /* must be zero                                       */
+} RnnNormDesc;
+
+/* y [rows, N]. residual: NULL, or [rows, N] added in front, the sum written
+ * to `sum` [rows, N] (required then). weight, bias [N]: NULL = ones, zeros.
+ * stats: NULL, or fp32 [rows, 2] (mean, 1 / sqrt(var + eps)) for the
+ * backward pass. */
+int rnn_layer_norm(const RnnNormDesc* desc, const void* x, const void* residual, const void* weight,
+                   const void* bias, void* y, void* sum, float* stats, void* stream);
+
+int rnn_layer_norm_backward_workspace_bytes(const RnnNormDesc* desc, size_t* bytes);
+
+/* Gradients for the row tensor that was normalised (`s`: x, or `sum` with
+ * x_ld = N when there was a residual) and the parameters. dy [rows, N];
+ * dsum: NULL, or the gradient that reaches the sum by another way (the
+ * residual stream), added to dx. dx [rows, N] is the gradient of s, hence of
+ * x and of residual alike. dweight, dbias: fp32 [N], both or neither (NULL =
+ * skip; no workspace is needed then); written, not accumulated. */
+int rnn_layer_norm_backward(const RnnNormDesc* desc, const void* s, const void* weight, const float* stats,
+                            const void* dy, const void* dsum, void* dx, float* dweight, float* dbias,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* Gated linear recurrence per channel of [T, B, H], for t < L_b:
+ *   a_t = sigma(f_t)
+ *   h_t = a_t h_{t-1} + (1 - a_t) x_t            without an input gate
+ *   h_t = a_t h_{t-1} + sigma(i_t) x_t           with one
+ *   y_t = h_t
+ * The reverse direction starts at t = L_b - 1 from h0 and ends at t = 0. */
+typedef struct RnnGatedScanDesc {
+  int32_t dtype;         /* RnnDtype of x, f, i, y and their gradients         */
+  int32_t T, B, H;       /* >= 1                                               */
+  int32_t reverse;       /* 0 or 1                                             */
+  int32_t input_gate;    /* 0 or 1: whether i is given                         */
+  int64_t x_t, x_b;      /* elements between time steps and batch rows of x    */
+  int64_t f_t, f_b;
+  int64_t i_t, i_b;
+} RnnGatedScanDesc;
+
+typedef struct RnnGatedScanIO {
+  const void* x;           /* [T, B, H]                                        */
+  const void* f;           /* [T, B, H]                                        */
+  const void* i;           /* [T, B, H] with input_gate                        */
+  const int32_t* lengths;  /* device [B], NULL = every row has T steps         */
+  const float* h0;         /* fp32 [B, H], NULL = zeros                        */
+  void* y;                 /* [T, B, H]                                        */
+  float* h_n;              /* fp32 [B, H] state after each row's last step;
+                              NULL = skip                                      */
+} RnnGatedScanIO;
+
+typedef struct RnnGatedScanGrads {
+  const void* dy;          /* [T, B, H]                                        */
+  const float* dh_n;       /* fp32 [B, H], NULL = zeros                        */
+  void* dx;                /* [T, B, H]                                        */
+  void* df;                /* [T, B, H]                                        */
+  void* di;                /* [T, B, H] with input_gate                        */
+  float* dh0;              /* fp32 [B, H], NULL = skip                         */
+} RnnGatedScanGrads;
+
+/* Workspace of the forward and of the backward pass (the same size), and the
+ * reserve between the two (the fp32 state at every 128th step). */
+int rnn_gated_scan_workspace_bytes(const RnnGatedScanDesc* desc, size_t* bytes);
+int rnn_gated_scan_reserve_bytes(const RnnGatedScanDesc* desc, size_t* bytes);
+int rnn_gated_scan(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io, void* workspace, size_t ws_bytes,
+                   void* stream);
+int rnn_gated_scan_train(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io, void* reserve,
+                         size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream);
+/* io as for rnn_gated_scan_train (x, f, i and lengths are read; y, h0 and
+ * h_n are not). */
+int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io,
+                            const RnnGatedScanGrads* grads, const void* reserve, size_t reserve_bytes,
+                            void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

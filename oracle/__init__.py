@@ -44,4 +44,7 @@ from .rnn import (  # noqa: F401
     run_direction_backward,
     pack_sequence, unpack_sequence, packed_offsets, round_to_bf16,
 )
+from .block import (  # noqa: F401
+    layer_norm, layer_norm_backward, gated_scan, gated_scan_backward,
+)
 from .rssm import rssm_prior_step, rssm_prior_unroll, actor_mlp, rssm_actor_unroll  # noqa: F401
