@@ -12,8 +12,8 @@ rnn_device_check, rnn_plan_info, rnn_exchange_roundtrip_ns. High level: rnn_forw
 packed, multi-layer, bidirectional), rssm_prior_unroll and rssm_actor_unroll; training:
 rnn_forward_train and rnn_backward (fp32 LSTM / LSTMP / GRU).
 
-Operators of a decoder block: layer_norm (with the residual add) and gated_scan (a gated linear recurrence), each with a
-_train form that also returns a context and a _backward that takes it.
+Operators of a decoder block: layer_norm (with the residual add), gated_scan (a gated linear recurrence) and
+cross_attention (over an encoder's states), each with a _train form that also returns a context and a _backward that takes it.
 """
 
 from .binding import (  # noqa: F401
@@ -25,4 +25,5 @@ from .binding import (  # noqa: F401
 from .block_ops import (  # noqa: F401
     RnnNormDesc, RnnGatedScanDesc, RnnGatedScanIO, RnnGatedScanGrads, BlockContext,
     layer_norm, layer_norm_train, layer_norm_backward, gated_scan, gated_scan_train, gated_scan_backward,
+    RnnAttentionDesc, RnnAttentionIO, RnnAttentionGrads, cross_attention, cross_attention_train, cross_attention_backward,
 )

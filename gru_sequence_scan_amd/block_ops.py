@@ -1,5 +1,5 @@
 """ctypes binding of the decoder block's operators in include/rnn.h: layer
-norm and the gated linear scan.
+norm, the gated linear scan and cross attention.
 
 As in binding.py, only argument marshalling happens here: checks, strides,
 outputs and workspace from torch, and the call on torch's current HIP stream
@@ -35,6 +35,20 @@ class RnnGatedScanGrads(ctypes.Structure):
     _fields_ = [("dy", _P), ("dh_n", _P), ("dx", _P), ("df", _P), ("di", _P), ("dh0", _P)]
 
 
+class RnnAttentionDesc(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("B", _I32), ("Tq", _I32), ("Tk", _I32), ("heads", _I32), ("kv_heads", _I32),
+                ("D", _I32), ("scale", ctypes.c_float), ("q_t", _I64), ("q_b", _I64), ("q_h", _I64), ("k_t", _I64),
+                ("k_b", _I64), ("k_h", _I64), ("v_t", _I64), ("v_b", _I64), ("v_h", _I64)]
+
+
+class RnnAttentionIO(ctypes.Structure):
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("lengths", _P), ("o", _P)]
+
+
+class RnnAttentionGrads(ctypes.Structure):
+    _fields_ = [("d_o", _P), ("dq", _P), ("dk", _P), ("dv", _P)]
+
+
 _REF = ctypes.POINTER
 _SIGNATURES = {
     "rnn_layer_norm": [_REF(RnnNormDesc)] + [_P] * 8,
@@ -46,6 +60,13 @@ _SIGNATURES = {
     "rnn_gated_scan_train": [_REF(RnnGatedScanDesc), _REF(RnnGatedScanIO), _P, _SZ, _P, _SZ, _P],
     "rnn_gated_scan_backward": [_REF(RnnGatedScanDesc), _REF(RnnGatedScanIO), _REF(RnnGatedScanGrads), _P, _SZ, _P, _SZ,
                                 _P],
+    "rnn_cross_attention_workspace_bytes": [_REF(RnnAttentionDesc), _REF(_SZ)],
+    "rnn_cross_attention_reserve_bytes": [_REF(RnnAttentionDesc), _REF(_SZ)],
+    "rnn_cross_attention_backward_workspace_bytes": [_REF(RnnAttentionDesc), _REF(_SZ)],
+    "rnn_cross_attention": [_REF(RnnAttentionDesc), _REF(RnnAttentionIO), _P, _SZ, _P],
+    "rnn_cross_attention_train": [_REF(RnnAttentionDesc), _REF(RnnAttentionIO), _P, _SZ, _P, _SZ, _P],
+    "rnn_cross_attention_backward": [_REF(RnnAttentionDesc), _REF(RnnAttentionIO), _REF(RnnAttentionGrads), _P, _SZ, _P,
+                                     _SZ, _P],
 }
 
 _ready = None
@@ -332,3 +353,77 @@ def gated_scan_backward(ctx, dy, dh_n=None):
         _ok(_lib().rnn_gated_scan_backward(ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ctx.reserve),
                                            ctx.reserve.numel(), _ptr(ws), size, st), "rnn_gated_scan_backward")
     return dx, df, di, dh0
+
+
+# ---------------------------------------------------------------------------
+# Cross attention
+# ---------------------------------------------------------------------------
+
+def _cross_attention(q, k, v, lengths, scale, train):
+    _tensor(q, "q", 4)
+    _tensor(k, "k", 4)
+    Tq, B, heads, D = q.shape
+    Tk, _, kv_heads, _ = k.shape
+    device, dtype = q.device, q.dtype
+    q = _strided(q, "q", (Tq, B, heads, D), q)
+    k = _strided(k, "k", (Tk, B, kv_heads, D), q)
+    v = _strided(v, "v", (Tk, B, kv_heads, D), q)
+    lengths = _lengths(lengths, B, Tk, device)
+    o = torch.empty((Tq, B, heads, D), dtype=dtype, device=device)
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    desc = RnnAttentionDesc(DTYPES[dtype], B, Tq, Tk, heads, kv_heads, D, scale, *q.stride()[:3], *k.stride()[:3],
+                            *v.stride()[:3])
+    io = RnnAttentionIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(lengths), o.data_ptr())
+    size = _bytes("rnn_cross_attention_workspace_bytes", desc)
+    ws = _buffer(size, device)
+    with _on(device) as st:
+        if not train:
+            _ok(_lib().rnn_cross_attention(ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size, st), "rnn_cross_attention")
+            return o
+        rsize = _bytes("rnn_cross_attention_reserve_bytes", desc)
+        reserve = _buffer(rsize, device)
+        _ok(_lib().rnn_cross_attention_train(ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws), size, st),
+            "rnn_cross_attention_train")
+    return o, BlockContext(device, st, desc=desc, io=io, q=q, k=k, v=v, lengths=lengths, o=o, reserve=reserve)
+
+
+def cross_attention(q, k, v, *, lengths=None, scale=None):
+    """Attention of queries q [Tq, B, heads, D] over an encoder's states k, v
+    [Tk, B, kv_heads, D] (float32 or bfloat16): softmax(scale q k^T) v over
+    the first lengths[b] states of each batch row, zero where there are none.
+
+    heads is a multiple of kv_heads, whose query heads share a key head; D is
+    at most 128. Every tensor may be a strided view (time-major, batch-major,
+    slices of one projection) whose last dimension is contiguous. lengths: B
+    values in [0, Tk], a device int32 tensor or host values (which are
+    copied); states past them are not read. scale: default D ** -0.5.
+    Returns o [Tq, B, heads, D]. A serving step is Tq = 1."""
+    return _cross_attention(q, k, v, lengths, scale, False)
+
+
+def cross_attention_train(q, k, v, *, lengths=None, scale=None):
+    """cross_attention that also keeps the fp32 log-sum-exp of every query's
+    scores. Returns (o, ctx); pass ctx to cross_attention_backward. ctx holds
+    q, k, v and o: do not change them in place before the backward pass."""
+    return _cross_attention(q, k, v, lengths, scale, True)
+
+
+def cross_attention_backward(ctx, do):
+    """Gradients of cross_attention_train, given do (shape and dtype of o).
+    Returns dense (dq, dk, dv); dk and dv are summed over the query heads of
+    a key head and zero past a row's length."""
+    o, device = ctx.o, ctx.device
+    do = _check(do, "do", tuple(o.shape), o.dtype, device)
+    dq = torch.empty(o.shape, dtype=o.dtype, device=device)
+    dk = torch.empty(ctx.k.shape, dtype=o.dtype, device=device)
+    dv = torch.empty(ctx.k.shape, dtype=o.dtype, device=device)
+    grads = RnnAttentionGrads(do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
+    size = _bytes("rnn_cross_attention_backward_workspace_bytes", ctx.desc)
+    ws = _buffer(size, device)
+    with _on(device) as st:
+        ctx._use(st, ctx.q, ctx.k, ctx.v, ctx.lengths, o, ctx.reserve)
+        _ok(_lib().rnn_cross_attention_backward(ctypes.byref(ctx.desc), ctypes.byref(ctx.io), ctypes.byref(grads),
+                                                ctx.reserve.data_ptr(), ctx.reserve.numel(), _ptr(ws), size, st),
+            "rnn_cross_attention_backward")
+    return dq, dk, dv

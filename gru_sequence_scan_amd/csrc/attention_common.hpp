@@ -1,0 +1,239 @@
+// Building blocks of the cross-attention kernels.
+//
+// Products run on the 16x16 matrix instructions. An operand fragment is eight
+// elements per lane: lane l holds row (or column) l % 16 and the eight
+// elements of the summed dimension that belong to its group g = l / 16. Which
+// eight they are does not matter as long as both operands agree; a fp32
+// fragment is fed to eight 16x16x4 instructions, a bf16 one to a single
+// 16x16x32. A 16x16 result has column l % 16 and rows 4 g .. 4 g + 3 in a
+// lane. So two results stacked along their rows are, lane by lane, an operand
+// fragment whose summed dimension is those 32 rows, in the order
+// 4 g + j (j < 4) and 16 + 4 g + j - 4 (j >= 4): probabilities go from one
+// product into the next without leaving their registers.
+#pragma once
+
+#include "block_kernels.hpp"
+#include "device_common.hpp"
+
+namespace rnnk {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kAttnThreads = 256;
+
+// Launches beyond 64 KiB of LDS have to be asked for.
+template <typename F>
+inline hipError_t allow_lds(F kernel, int bytes) {
+  if (bytes <= 64 * 1024) return hipSuccess;
+  return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename DT>
+struct Frag;
+template <>
+struct Frag<bf16> {
+  bf16x8 v;
+  __device__ __forceinline__ void set(int j, float x) { v[j] = (bf16)x; }
+  __device__ __forceinline__ float get(int j) const { return (float)v[j]; }
+};
+template <>
+struct Frag<float> {
+  float v[8];
+  __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
+  __device__ __forceinline__ float get(int j) const { return v[j]; }
+};
+
+__device__ __forceinline__ f32x4 mma(const Frag<bf16>& a, const Frag<bf16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Frag<float>& a, const Frag<float>& b, f32x4 c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+  return c;
+}
+
+// Rows of a tile in LDS lie DP elements plus a pad apart. With 16 bytes of
+// pad a wave's fragment reads (16 rows, 16 bytes each) fall on different
+// banks, with 32 bytes the transposed reads of bf16 tiles (8 rows, 32 bytes
+// each) do; a bf16 tile read both ways takes the pad of its more frequent
+// use.
+template <typename DT, int DP, bool TR>
+struct TileShape {
+  static constexpr int kPad = (TR && sizeof(DT) == 2 ? 32 : 16) / sizeof(DT);
+  static constexpr int kLd = DP + kPad;
+};
+
+// Eight neighbouring elements of row `row`, from column col0 + 8 g.
+template <typename DT>
+__device__ __forceinline__ Frag<DT> read_rows(const DT* lds, int ld, int row, int col);
+template <>
+__device__ __forceinline__ Frag<bf16> read_rows<bf16>(const bf16* lds, int ld, int row, int col) {
+  Frag<bf16> f;
+  f.v = *reinterpret_cast<const bf16x8*>(lds + row * ld + col);
+  return f;
+}
+template <>
+__device__ __forceinline__ Frag<float> read_rows<float>(const float* lds, int ld, int row, int col) {
+  Frag<float> f;
+  const f32x4 a = *reinterpret_cast<const f32x4*>(lds + row * ld + col);
+  const f32x4 b = *reinterpret_cast<const f32x4*>(lds + row * ld + col + 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = b[j];
+  return f;
+}
+
+// The transposed fragment: column col0 + l % 16 of the 32 rows from row0 on,
+// in the order of stacked results (see above).
+template <typename DT>
+__device__ __forceinline__ Frag<DT> read_cols(const DT* lds, int ld, int row0, int col0, int lane);
+template <>
+__device__ __forceinline__ Frag<bf16> read_cols<bf16>(const bf16* lds, int ld, int row0, int col0, int lane) {
+  // The transposing read hands 16 lanes the columns of the 4 x 16 block that
+  // their 8-byte reads make up, four lanes a row.
+  typedef __attribute__((address_space(3))) s16x4* LdsPtr;
+  const int g = lane >> 4, i = lane & 15;
+  const bf16* p = lds + (row0 + 4 * g + (i >> 2)) * ld + col0 + 4 * (i & 3);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 16 * ld));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  Frag<bf16> f;
+  f.v = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  return f;
+}
+template <>
+__device__ __forceinline__ Frag<float> read_cols<float>(const float* lds, int ld, int row0, int col0, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const float* p = lds + (row0 + 4 * g) * ld + col0 + i;
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f.v[j] = p[j * ld], f.v[4 + j] = p[(16 + j) * ld];
+  return f;
+}
+
+// Two stacked results as the fragment they are.
+template <typename DT>
+__device__ __forceinline__ Frag<DT> stack(const f32x4& a, const f32x4& b) {
+  Frag<DT> f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f.set(j, a[j]);
+    f.set(4 + j, b[j]);
+  }
+  return f;
+}
+
+// Max and sum over the four lanes that hold a column.
+__device__ __forceinline__ float col_max(float v) {
+  v = __builtin_fmaxf(v, __shfl_xor(v, 16, 64));
+  return __builtin_fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// Eight elements of a row in global memory from column col on; columns past D
+// are zero. `vec`: rows take 16-byte accesses and D is a multiple of them.
+template <typename DT>
+__device__ __forceinline__ Frag<DT> load8(const DT* row, int col, int D, bool vec) {
+  Frag<DT> f;
+  if (vec) {
+    if constexpr (sizeof(DT) == 2) {
+      const u32x4 z = {0, 0, 0, 0};
+      f.v = __builtin_bit_cast(bf16x8, col < D ? *reinterpret_cast<const u32x4*>(row + col) : z);
+    } else {
+      const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+      const f32x4 a = col < D ? *reinterpret_cast<const f32x4*>(row + col) : z;
+      const f32x4 b = col + 4 < D ? *reinterpret_cast<const f32x4*>(row + col + 4) : z;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = b[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.set(j, col + j < D ? to_f32<DT>(row[col + j]) : 0.f);
+  }
+  return f;
+}
+
+template <typename DT>
+__device__ __forceinline__ Frag<DT> zero_frag() {
+  Frag<DT> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.set(j, 0.f);
+  return f;
+}
+
+template <typename DT>
+__device__ __forceinline__ void put8(DT* lds, const Frag<DT>& f) {
+  if constexpr (sizeof(DT) == 2) {
+    *reinterpret_cast<bf16x8*>(lds) = f.v;
+  } else {
+    *reinterpret_cast<f32x4*>(lds) = f32x4{f.v[0], f.v[1], f.v[2], f.v[3]};
+    *reinterpret_cast<f32x4*>(lds + 4) = f32x4{f.v[4], f.v[5], f.v[6], f.v[7]};
+  }
+}
+
+// Four results of a lane (neighbouring columns of one row) to global memory.
+template <typename DT>
+__device__ __forceinline__ void store4(DT* row, int col, int D, bool vec, const f32x4& v) {
+  if (vec) {
+    if (col < D) {
+      if constexpr (sizeof(DT) == 2) {
+        bf16x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = (bf16)v[j];
+        *reinterpret_cast<bf16x4*>(row + col) = o;
+      } else {
+        *reinterpret_cast<f32x4*>(row + col) = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < D) row[col + j] = from_f32<DT>(v[j]);
+  }
+}
+
+// A tile of ROWS rows from global memory into LDS; row(r) gives a row's
+// address or null, whose row is zero.
+template <typename DT, int DP, int ROWS, int LD, typename RowFn>
+__device__ __forceinline__ void stage(DT* lds, int D, bool vec, RowFn row) {
+  constexpr int kCols = DP / 8, kTotal = ROWS * kCols, kIters = (kTotal + kAttnThreads - 1) / kAttnThreads;
+  Frag<DT> f[kIters];
+#pragma unroll
+  for (int n = 0; n < kIters; ++n) {
+    const int k = n * kAttnThreads + threadIdx.x;
+    const int r = k / kCols, c = (k % kCols) * 8;
+    const DT* p = k < kTotal ? row(r) : nullptr;
+    f[n] = p ? load8<DT>(p, c, D, vec) : zero_frag<DT>();
+  }
+#pragma unroll
+  for (int n = 0; n < kIters; ++n) {
+    const int k = n * kAttnThreads + threadIdx.x;
+    const int r = k / kCols, c = (k % kCols) * 8;
+    if (k < kTotal) put8<DT>(lds + r * LD + c, f[n]);
+  }
+}
+
+// Query rows of one key head: row m is step m / G of query head hk G + m % G.
+struct QRows {
+  int M, G;
+  template <typename DT>
+  __device__ __forceinline__ const DT* in(const void* p, int64_t st, int64_t sh, int m) const {
+    const int t = m / G;
+    return (const DT*)p + t * st + (m - t * G) * sh;
+  }
+  // offset of row m in a dense [Tq, B, heads, D]
+  __device__ __forceinline__ int64_t dense(const AttentionArgs& a, int b, int hk, int m) const {
+    const int t = m / G;
+    return (((int64_t)t * a.B + b) * a.heads + hk * G + (m - t * G)) * a.D;
+  }
+};
+
+__device__ __forceinline__ int key_count(const AttentionArgs& a, int b) {
+  const int n = a.lengths ? a.lengths[b] : a.Tk;
+  return n < 0 ? 0 : (n > a.Tk ? a.Tk : n);
+}
+
+}  // namespace rnnk

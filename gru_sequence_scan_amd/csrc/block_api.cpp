@@ -148,6 +148,82 @@ int scan_forward(const RnnGatedScanDesc* d, const RnnGatedScanIO* io, void* rese
   return hip_status(launch_gated_scan(a, d->dtype == RNN_DTYPE_BF16, false, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------------------
+// Cross attention
+// ---------------------------------------------------------------------------
+int64_t query_rows(const RnnAttentionDesc* d) { return (int64_t)d->Tq * (d->heads / d->kv_heads); }
+
+AttentionPlan plan_of(const RnnAttentionDesc* d) {
+  return attention_plan(d->B, d->Tq, d->Tk, d->heads, d->kv_heads, d->dtype == RNN_DTYPE_BF16, kPlanCus);
+}
+
+int validate(const RnnAttentionDesc* d) {
+  if (!d) return RNN_E_NULL;
+  if (!dtype_ok(d->dtype)) return RNN_E_UNSUPPORTED;
+  if (d->B < 1 || d->Tq < 1 || d->Tk < 1 || d->heads < 1 || d->kv_heads < 1 || d->D < 1) return RNN_E_SHAPE;
+  if (d->heads % d->kv_heads != 0 || !std::isfinite(d->scale)) return RNN_E_SHAPE;
+  if (d->D > RNN_ATTENTION_MAX_D) return RNN_E_UNSUPPORTED;
+  for (int64_t s : {d->q_t, d->q_b, d->q_h, d->k_t, d->k_b, d->k_h, d->v_t, d->v_b, d->v_h})
+    if (s < 0) return RNN_E_SHAPE;
+  // row numbers, and the workgroups of the widest launch (16 rows each and
+  // at most 64 splits of the keys), stay 32-bit
+  const double groups = (double)d->B * d->kv_heads;
+  if (d->Tk > kMaxGrid - 1024 || query_rows(d) > kMaxGrid - 1024) return RNN_E_SHAPE;
+  if (groups * ((double)query_rows(d) / 16 + 64) > (double)kMaxGrid || groups * ((double)d->Tk / 16 + 1) > (double)kMaxGrid)
+    return RNN_E_SHAPE;
+  return RNN_OK;
+}
+
+size_t attention_stat_bytes(const RnnAttentionDesc* d) {
+  return (size_t)d->B * d->kv_heads * (size_t)query_rows(d) * sizeof(float);
+}
+
+size_t attention_workspace(const RnnAttentionDesc* d) {
+  const size_t n = (size_t)plan_of(d).splits;
+  return n > 1 ? n * (attention_stat_bytes(d) * ((size_t)d->D + 2) + 16) : 0;
+}
+
+int attention_args(const RnnAttentionDesc* d, const RnnAttentionIO* io, AttentionArgs* a) {
+  if (!io) return RNN_E_NULL;
+  const size_t e = (size_t)esize_of(d->dtype);
+  RETURN_IF_BAD(need(io->q, e));
+  RETURN_IF_BAD(need(io->k, e));
+  RETURN_IF_BAD(need(io->v, e));
+  RETURN_IF_BAD(need(io->o, e));
+  RETURN_IF_BAD(optional(io->lengths, 4));
+  *a = AttentionArgs{};
+  a->B = d->B; a->Tq = d->Tq; a->Tk = d->Tk; a->heads = d->heads; a->kv_heads = d->kv_heads; a->D = d->D;
+  a->scale = d->scale;
+  a->q = io->q; a->q_t = d->q_t; a->q_b = d->q_b; a->q_h = d->q_h;
+  a->k = io->k; a->k_t = d->k_t; a->k_b = d->k_b; a->k_h = d->k_h;
+  a->v = io->v; a->v_t = d->v_t; a->v_b = d->v_b; a->v_h = d->v_h;
+  a->lengths = io->lengths;
+  a->o = io->o;
+  a->splits = 1;
+  const int64_t m = 16 / (int64_t)e;
+  bool vec = d->D % m == 0 && aligned(a->q, 16) && aligned(a->k, 16) && aligned(a->v, 16) && aligned(a->o, 16);
+  for (int64_t s : {d->q_t, d->q_b, d->q_h, d->k_t, d->k_b, d->k_h, d->v_t, d->v_b, d->v_h}) vec = vec && s % m == 0;
+  a->vec = vec;
+  return RNN_OK;
+}
+
+int attention_forward(const RnnAttentionDesc* d, const RnnAttentionIO* io, void* reserve, void* ws, size_t ws_bytes,
+                      void* stream) {
+  AttentionArgs a;
+  RETURN_IF_BAD(attention_args(d, io, &a));
+  RETURN_IF_BAD(need_memory(ws, ws_bytes, attention_workspace(d)));
+  int cus;
+  RETURN_IF_BAD(on_device(&cus));
+  const AttentionPlan p = plan_of(d);
+  a.splits = p.splits;
+  if (p.splits > 1) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = a.part_o + (size_t)p.splits * (attention_stat_bytes(d) / sizeof(float)) * d->D;
+  }
+  a.lse = static_cast<float*>(reserve);
+  return hip_status(launch_attention(a, p, d->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -265,6 +341,62 @@ int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* 
   a.dh0 = grads->dh0;
   if (!aligned(a.dy, 4 * e) || !aligned(a.dx, 4 * e) || !aligned(a.df, 4 * e) || !aligned(a.di, 4 * e)) a.width = 1;
   return hip_status(launch_gated_scan(a, desc->dtype == RNN_DTYPE_BF16, true, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int rnn_cross_attention_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes) {
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = attention_workspace(desc);
+  return RNN_OK;
+}
+
+int rnn_cross_attention_reserve_bytes(const RnnAttentionDesc* desc, size_t* bytes) {
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = attention_stat_bytes(desc);
+  return RNN_OK;
+}
+
+int rnn_cross_attention_backward_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes) {
+  return rnn_cross_attention_reserve_bytes(desc, bytes);  // delta, one value per query row
+}
+
+int rnn_cross_attention(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  Range range("rnn_cross_attention");
+  RETURN_IF_BAD(validate(desc));
+  return attention_forward(desc, io, nullptr, workspace, ws_bytes, stream);
+}
+
+int rnn_cross_attention_train(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* reserve, size_t reserve_bytes,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  Range range("rnn_cross_attention_train");
+  RETURN_IF_BAD(validate(desc));
+  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_stat_bytes(desc)));
+  return attention_forward(desc, io, reserve, workspace, ws_bytes, stream);
+}
+
+int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentionIO* io, const RnnAttentionGrads* grads,
+                                 const void* reserve, size_t reserve_bytes, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  Range range("rnn_cross_attention_backward");
+  RETURN_IF_BAD(validate(desc));
+  if (!grads) return RNN_E_NULL;
+  AttentionArgs a;
+  RETURN_IF_BAD(attention_args(desc, io, &a));
+  const size_t e = (size_t)esize_of(desc->dtype);
+  for (const void* p : {grads->d_o, (const void*)grads->dq, (const void*)grads->dk, (const void*)grads->dv}) {
+    RETURN_IF_BAD(need(p, e));
+    if (!aligned(p, 16)) a.vec = 0;
+  }
+  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_stat_bytes(desc)));
+  RETURN_IF_BAD(need_memory(workspace, ws_bytes, attention_stat_bytes(desc)));
+  int cus;
+  RETURN_IF_BAD(on_device(&cus));
+  a.lse = const_cast<float*>(static_cast<const float*>(reserve));
+  a.delta = static_cast<float*>(workspace);
+  a.d_o = grads->d_o; a.dq = grads->dq; a.dk = grads->dk; a.dv = grads->dv;
+  return hip_status(launch_attention_backward(a, desc->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

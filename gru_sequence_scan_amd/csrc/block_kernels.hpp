@@ -59,4 +59,35 @@ int norm_backward_blocks(int64_t rows, int N, int cus);
 hipError_t launch_layer_norm(const NormArgs& a, bool bf16_storage, hipStream_t stream);
 hipError_t launch_layer_norm_backward(const NormArgs& a, bool bf16_storage, hipStream_t stream);
 
+// Cross attention (attention.hip, attention_bwd.hip).
+struct AttentionArgs {
+  int B, Tq, Tk, heads, kv_heads, D;
+  float scale;
+  const void* q; int64_t q_t, q_b, q_h;
+  const void* k; int64_t k_t, k_b, k_h;
+  const void* v; int64_t v_t, v_b, v_h;
+  const int* lengths;               // device [B] or null
+  void* o;                          // [Tq, B, heads, D]
+  float* lse;                       // [B, kv_heads, Tq * G] base-2 log-sum-exp, or null
+  int vec;                          // rows take 16-byte accesses
+  // split of the keys over workgroups (forward)
+  int splits;
+  float* part_o;                    // [splits, B, kv_heads, Tq * G, D]
+  float* part_ml;                   // [splits, B, kv_heads, Tq * G, 2]
+  // backward
+  const void* d_o;
+  void* dq; void* dk; void* dv;
+  float* delta;                     // [B, kv_heads, Tq * G]
+};
+// How the forward pass is tiled: query rows per workgroup, keys per tile and
+// how many workgroups share the keys of a row.
+struct AttentionPlan {
+  int rows;      // query rows (of one key head) per workgroup
+  int narrow;    // the workgroup's waves share its rows and divide the keys
+  int splits;
+};
+AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, bool bf16_storage, int cus);
+hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& p, bool bf16_storage, hipStream_t stream);
+hipError_t launch_attention_backward(const AttentionArgs& a, bool bf16_storage, hipStream_t stream);
+
 }  // namespace rnnk

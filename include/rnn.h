@@ -428,13 +428,15 @@ int rnn_exchange_roundtrip_ns(void* buffer, size_t bytes, int iters, void* strea
 
 /* ---------------------------------------------------------------------------
  * Operators of a decoder block beside the recurrences: layer norm with the
- * residual add, and a gated linear recurrence. Conventions as above (caller-owned buffers, validation
+ * residual add, a gated linear recurrence, and cross attention to an
+ * encoder's states. Conventions as above (caller-owned buffers, validation
  * before anything is enqueued, no synchronisation, deterministic results),
  * with these differences:
  *   - Inputs carry strides (in elements); their last dimension is
  *     contiguous. Outputs, gradients and the incoming gradients are dense.
  *     Rows whose addresses and strides are multiples of 16 bytes (gated
- *     scan: four elements) take wide accesses, others element accesses.
+ *     scan: four elements) take wide accesses, others element accesses; the
+ *     choice is made for all tensors of a call together.
  *   - Lengths are a DEVICE int32 array, so that a call can be captured and
  *     never reads host memory. A value is clamped to [0, T]: 0 is a row with
  *     no steps (its outputs are zero, its state passes through).
@@ -448,6 +450,7 @@ int rnn_exchange_roundtrip_ns(void* buffer, size_t bytes, int iters, void* strea
  * ------------------------------------------------------------------------- */
 
 #define RNN_NORM_MAX_N 16384
+#define RNN_ATTENTION_MAX_D 128
 
 /* Layer norm over the last dimension of [rows, N]:
  *   s = x + residual (rounded to the storage type; s = x without one)
@@ -530,6 +533,52 @@ int rnn_gated_scan_train(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io,
 int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io,
                             const RnnGatedScanGrads* grads, const void* reserve, size_t reserve_bytes,
                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Cross attention: every query of [Tq, B, heads, D] attends the first L_b
+ * states of its batch row in [Tk, B, kv_heads, D]; query head h reads key
+ * head h / (heads / kv_heads):
+ *   o = softmax(scale q k^T) v, zero when L_b = 0                             */
+typedef struct RnnAttentionDesc {
+  int32_t dtype;         /* RnnDtype                                           */
+  int32_t B, Tq, Tk;     /* >= 1                                               */
+  int32_t heads;         /* a multiple of kv_heads                             */
+  int32_t kv_heads;      /* >= 1                                               */
+  int32_t D;             /* 1 .. RNN_ATTENTION_MAX_D                           */
+  float scale;           /* finite                                             */
+  int64_t q_t, q_b, q_h; /* elements between steps, batch rows and heads of q  */
+  int64_t k_t, k_b, k_h;
+  int64_t v_t, v_b, v_h;
+} RnnAttentionDesc;
+
+typedef struct RnnAttentionIO {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* lengths;  /* device [B], NULL = every row has Tk states       */
+  void* o;                 /* [Tq, B, heads, D]                                */
+} RnnAttentionIO;
+
+typedef struct RnnAttentionGrads {
+  const void* d_o;         /* [Tq, B, heads, D]                                */
+  void* dq;                /* [Tq, B, heads, D]                                */
+  void* dk;                /* [Tk, B, kv_heads, D], summed over a key head's
+                              query heads                                      */
+  void* dv;                /* [Tk, B, kv_heads, D]                             */
+} RnnAttentionGrads;
+
+int rnn_cross_attention_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes);
+/* The reserve between the passes: the fp32 log-sum-exp of every query's
+ * scores. */
+int rnn_cross_attention_reserve_bytes(const RnnAttentionDesc* desc, size_t* bytes);
+int rnn_cross_attention_backward_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes);
+int rnn_cross_attention(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* workspace, size_t ws_bytes,
+                        void* stream);
+int rnn_cross_attention_train(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* reserve,
+                              size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream);
+/* io as for rnn_cross_attention_train, with the o it wrote. */
+int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentionIO* io,
+                                 const RnnAttentionGrads* grads, const void* reserve, size_t reserve_bytes,
+                                 void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

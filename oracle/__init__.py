@@ -46,5 +46,6 @@ from .rnn import (  # noqa: F401
 )
 from .block import (  # noqa: F401
     layer_norm, layer_norm_backward, gated_scan, gated_scan_backward,
+    cross_attention, cross_attention_backward, attention_bounds,
 )
 from .rssm import rssm_prior_step, rssm_prior_unroll, actor_mlp, rssm_actor_unroll  # noqa: F401

@@ -81,3 +81,70 @@ def gated_scan_backward(x, f, i, dy, dh_n=None, h0=None, lengths=None, reverse=F
             c = a * g
         dh0[b] = c
     return dx, df, di, dh0
+
+
+def _pairs(q, k, lengths):
+    """(batch row, query head, key head, keys) of every attention problem."""
+    group = q.shape[2] // k.shape[2]
+    for b in range(q.shape[1]):
+        n = k.shape[0] if lengths is None else int(lengths[b])
+        for h in range(q.shape[2]):
+            yield b, h, h // group, n
+
+
+def _softmax(s):
+    e = np.exp(s - s.max(-1, keepdims=True))
+    return e / e.sum(-1, keepdims=True)
+
+
+def cross_attention(q, k, v, lengths=None, scale=None):
+    """o [Tq, B, heads, D] for q [Tq, B, heads, D] and k, v [Tk, B, kv, D]."""
+    q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    o = np.zeros_like(q)
+    for b, h, hk, n in _pairs(q, k, lengths):
+        if n:
+            o[:, b, h] = _softmax(scale * q[:, b, h] @ k[:n, b, hk].T) @ v[:n, b, hk]
+    return o
+
+
+def cross_attention_backward(q, k, v, do, lengths=None, scale=None):
+    """(dq, dk, dv)."""
+    q, k, v, do = (np.asarray(t, dtype=np.float64) for t in (q, k, v, do))
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    for b, h, hk, n in _pairs(q, k, lengths):
+        if not n:
+            continue
+        p = _softmax(scale * q[:, b, h] @ k[:n, b, hk].T)
+        dp = do[:, b, h] @ v[:n, b, hk].T
+        ds = p * (dp - (p * dp).sum(-1, keepdims=True)) * scale
+        dq[:, b, h] = ds @ k[:n, b, hk]
+        dk[:n, b, hk] += ds.T @ q[:, b, h]
+        dv[:n, b, hk] += p.T @ do[:, b, h]
+    return dq, dk, dv
+
+
+def attention_bounds(q, k, v, do, lengths=None, scale=None, unit=0.0):
+    """First-order bounds of (o, dq, dk, dv) against one rounding of relative
+    size `unit` of each probability p and score gradient ds inside the sums,
+    and of o inside delta = sum_d do o:
+      |d o| <= u p |v|,  |d dv| <= u p^T |do|,
+      |d ds| <= u |ds| + p |d delta|,  |d delta| <= 2 u sum_d |do| p |v|
+    (o carries its own rounding and p's), carried through ds k and ds^T q."""
+    q, k, v, do = (np.asarray(t, dtype=np.float64) for t in (q, k, v, do))
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    bo, bq, bk, bv = np.zeros_like(q), np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    for b, h, hk, n in _pairs(q, k, lengths):
+        if not n:
+            continue
+        p = _softmax(scale * q[:, b, h] @ k[:n, b, hk].T)
+        dp = do[:, b, h] @ v[:n, b, hk].T
+        ds = np.abs(p * (dp - (p * dp).sum(-1, keepdims=True)))
+        bo[:, b, h] = p @ np.abs(v[:n, b, hk])
+        delta = 2.0 * (np.abs(do[:, b, h]) * bo[:, b, h]).sum(-1, keepdims=True)
+        ds = (ds + p * delta) * abs(scale)
+        bq[:, b, h] = ds @ np.abs(k[:n, b, hk])
+        bk[:n, b, hk] += ds.T @ np.abs(q[:, b, h])
+        bv[:n, b, hk] += p.T @ np.abs(do[:, b, h])
+    return unit * bo, unit * bq, unit * bk, unit * bv

@@ -68,12 +68,36 @@ def test_gated_scan_definition(gate, reverse):
     assert np.array_equal(dh0[1], dhn[1])
 
 
+def test_cross_attention_definition():
+    rng = np.random.default_rng(3)
+    Tq, Tk, B, heads, kv, D = 3, 5, 3, 4, 2, 3
+    q, do = rng.standard_normal((2, Tq, B, heads, D))
+    k, v = rng.standard_normal((2, Tk, B, kv, D))
+    lens = [5, 0, 2]
+    o = oracle.cross_attention(q, k, v, lens)
+    t = [torch.tensor(x) for x in (q, k, v)]
+    for b, n in ((0, 5), (2, 2)):
+        ref = torch.nn.functional.scaled_dot_product_attention(
+            t[0][:, b].transpose(0, 1), t[1][:n, b].transpose(0, 1).repeat_interleave(2, 0),
+            t[2][:n, b].transpose(0, 1).repeat_interleave(2, 0))
+        assert np.allclose(o[:, b], ref.transpose(0, 1).numpy(), atol=1e-12)
+    assert (o[:, 1] == 0).all()
+    loss = lambda: float((oracle.cross_attention(q, k, v, lens, 0.7) * do).sum())  # noqa: E731
+    for got, x in zip(oracle.cross_attention_backward(q, k, v, do, lens, 0.7), (q, k, v)):
+        assert np.allclose(got, _differences(loss, x), atol=1e-8)
+    # the bounds scale with the unit and cover a rounded probability's effect
+    small, large = (oracle.attention_bounds(q, k, v, do, lens, 0.7, u) for u in (1e-3, 2e-3))
+    for a, b in zip(small, large):
+        assert np.allclose(2 * a, b) and (a >= 0).all()
+
+
 # -- layouts of the ctypes mirrors --
 
 def test_ctypes_layout_matches_c(tmp_path):
     import os
     import subprocess
-    names = ["RnnNormDesc", "RnnGatedScanDesc", "RnnGatedScanIO", "RnnGatedScanGrads"]
+    names = ["RnnNormDesc", "RnnGatedScanDesc", "RnnGatedScanIO", "RnnGatedScanGrads",
+             "RnnAttentionDesc", "RnnAttentionIO", "RnnAttentionGrads"]
     lines = [f'  printf("%zu", sizeof({n}));' + "".join(f' printf(" %zu", offsetof({n}, {f[0]}));'
                                                        for f in getattr(gss, n)._fields_) + ' printf("\\n");' for n in names]
     src = tmp_path / "layout.c"
@@ -198,11 +222,85 @@ def test_scan_pointers():
         assert fwd() == E_DEVICE and bwd() == E_DEVICE
 
 
+def _attend(**kw):
+    v = dict(dtype=0, B=2, Tq=5, Tk=70, heads=4, kv_heads=2, D=8, scale=0.5, q_t=64, q_b=32, q_h=8, k_t=32, k_b=16, k_h=8,
+             v_t=32, v_b=16, v_h=8)
+    v.update(kw)
+    return gss.RnnAttentionDesc(*v.values())
+
+
+@pytest.mark.parametrize("kw,expect", [
+    ({}, OK), ({"dtype": 1}, OK), ({"D": 128}, OK), ({"D": 1}, OK), ({"heads": 2}, OK), ({"k_b": 0}, OK),
+    ({"dtype": 7}, E_UNSUPPORTED), ({"D": 129}, E_UNSUPPORTED),
+    ({"B": 0}, E_SHAPE), ({"Tq": 0}, E_SHAPE), ({"Tk": -3}, E_SHAPE), ({"heads": 3}, E_SHAPE), ({"heads": 0}, E_SHAPE),
+    ({"kv_heads": 0}, E_SHAPE), ({"heads": 1}, E_SHAPE), ({"D": 0}, E_SHAPE), ({"scale": float("nan")}, E_SHAPE),
+    ({"scale": float("inf")}, E_SHAPE), ({"q_t": -1}, E_SHAPE), ({"k_h": -8}, E_SHAPE), ({"v_b": -1}, E_SHAPE),
+    ({"Tk": 2147483647}, E_SHAPE), ({"Tq": 2000000000}, E_SHAPE), ({"B": 2000000000, "kv_heads": 4}, E_SHAPE),
+])
+def test_attention_desc(kw, expect):
+    n = ctypes.c_size_t(0)
+    for fn in ("rnn_cross_attention_workspace_bytes", "rnn_cross_attention_reserve_bytes",
+               "rnn_cross_attention_backward_workspace_bytes"):
+        assert getattr(ops._lib(), fn)(ctypes.byref(_attend(**kw)), ctypes.byref(n)) == expect
+    if expect == OK:   # one fp32 value per query row
+        d = _attend(**kw)
+        assert n.value == d.B * d.heads * d.Tq * 4
+
+
+def test_attention_split_workspace():
+    """A call with few query rows splits the keys over workgroups, and its
+    workspace holds a partial row per split; one that fills the device does
+    not."""
+    n = ctypes.c_size_t(0)
+    fn = ops._lib().rnn_cross_attention_workspace_bytes
+    assert fn(ctypes.byref(_attend(B=1, Tq=1, Tk=32768)), ctypes.byref(n)) == OK
+    assert n.value >= 8 * 4 * (8 + 2) * 4
+    assert fn(ctypes.byref(_attend(B=64, Tq=1000, Tk=1000, heads=8, kv_heads=8)), ctypes.byref(n)) == OK and n.value == 0
+
+
+def test_attention_pointers():
+    L = ops._lib()
+    d = _attend(B=1, Tq=1, Tk=32768)
+    n, r = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert L.rnn_cross_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == OK
+    assert L.rnn_cross_attention_reserve_bytes(ctypes.byref(d), ctypes.byref(r)) == OK
+
+    def io(**kw):
+        v = dict(q=ADDR, k=ADDR, v=ADDR, lengths=None, o=ADDR)
+        v.update(kw)
+        return gss.RnnAttentionIO(*v.values())
+
+    def fwd(ws=ADDR, size=n.value, **kw):
+        return L.rnn_cross_attention(ctypes.byref(d), ctypes.byref(io(**kw)), ws, size, None)
+
+    assert L.rnn_cross_attention(None, ctypes.byref(io()), ADDR, n.value, None) == E_NULL
+    assert L.rnn_cross_attention(ctypes.byref(d), None, ADDR, n.value, None) == E_NULL
+    for k in ("q", "k", "v", "o"):
+        assert fwd(**{k: None}) == E_NULL and fwd(**{k: ADDR + 2}) == E_ALIGN, k
+    assert fwd(lengths=ADDR + 2) == E_ALIGN
+    assert fwd(ws=None) == E_WORKSPACE and fwd(size=n.value - 1) == E_WORKSPACE and fwd(ws=ADDR + 8) == E_ALIGN
+    assert L.rnn_cross_attention_train(ctypes.byref(d), ctypes.byref(io()), ADDR, r.value - 1, ADDR, n.value,
+                                       None) == E_WORKSPACE
+
+    def bwd(reserve=ADDR, ws=ADDR, size=r.value, **kw):
+        v = dict(d_o=ADDR, dq=ADDR, dk=ADDR, dv=ADDR)
+        v.update(kw)
+        return L.rnn_cross_attention_backward(ctypes.byref(d), ctypes.byref(io()), ctypes.byref(gss.RnnAttentionGrads(*v.values())),
+                                              reserve, r.value, ws, size, None)
+
+    for k in ("d_o", "dq", "dk", "dv"):
+        assert bwd(**{k: None}) == E_NULL and bwd(**{k: ADDR + 1}) == E_ALIGN, k
+    assert bwd(reserve=None) == E_WORKSPACE and bwd(ws=None) == E_WORKSPACE and bwd(ws=ADDR + 4) == E_ALIGN
+    if not torch.cuda.is_available():
+        assert fwd() == E_DEVICE and bwd() == E_DEVICE
+
+
 # -- refusals of the Python calls --
 
 def test_python_refusals():
     x = torch.zeros(4, 3, 8)
-    for call in (lambda: gss.layer_norm(x), lambda: gss.gated_scan(x, x), lambda: gss.gated_scan([1.0], x)):
+    for call in (lambda: gss.layer_norm(x), lambda: gss.gated_scan(x, x), lambda: gss.gated_scan([1.0], x),
+                 lambda: gss.cross_attention(x[None], x[None], x[None])):
         with pytest.raises(ValueError):
             call()
     with pytest.raises(ValueError, match="float32, bfloat16"):
