@@ -17,6 +17,10 @@
 namespace rnnk {
 namespace {
 
+// The running maximum of no scores: finite, so that subtracting it from the
+// -inf of a masked score never makes inf - inf.
+constexpr float kLowest = -3.402823466e38f;
+
 // WQ x WK waves: WQ sets of QT x 16 query rows, WK parts of the tile's keys,
 // KT x 16 keys each.
 template <typename DT, int DP, int WQ, int WK, int QT, int KT>
@@ -25,14 +29,16 @@ struct Shape {
   static constexpr int kKeys = WK * KT * 16;
   static constexpr int kLdK = TileShape<DT, DP, false>::kLd;
   static constexpr int kLdV = TileShape<DT, DP, true>::kLd;
-  static constexpr int kTileBytes = kKeys * (kLdK + kLdV) * (int)sizeof(DT);
+  static constexpr int kTile = kKeys * (kLdK + kLdV);  // a tile of keys and its values, kept twice
+  static constexpr int kTileBytes = 2 * kTile * (int)sizeof(DT);
   // the join of WK parts: per wave O^T [QT 16][DP + 1 pad] fp32 and m, l
   static constexpr int kJoinBytes = WK > 1 ? WK * WQ * QT * 16 * (DP + 4 + 2) * 4 : 0;
   static constexpr int kBytes = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
+  static_assert(kBytes <= 160 * 1024, "LDS of a compute unit");
 };
 
 template <typename DT, int DP, int WQ, int WK, int QT, int KT>
-__global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArgs a) {
   using S = Shape<DT, DP, WQ, WK, QT, KT>;
   static_assert(WQ * WK * 64 == kAttnThreads, "four waves");
   static_assert(KT % 2 == 0, "pairs of key tiles make a fragment");
@@ -73,20 +79,42 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttentionArgs a
   float mx[QT], sum[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    // the lowest finite value: subtracting it never makes inf - inf
-    mx[t] = -3.402823466e38f;
+    mx[t] = kLowest;
     sum[t] = 0.f;
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  const float sl = a.scale * kLog2e;
+  // A negative scale is taken into q (exactly), a zero one replaced by the
+  // smallest positive (2^(s sl) rounds to 1 alike): scores are compared before
+  // they are scaled, and the scale rides in the exponent's multiply-add.
+  const float sl = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1.17549435e-38f);
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[t][c].set(j, -q[t][c].get(j));
+  }
 
+  TileLoad<DT, DP, S::kKeys, S::kLdK> nk;
+  TileLoad<DT, DP, S::kKeys, S::kLdV> nv;
+  if (first < last) {
+    nk.load(kb, a.k_t, first * S::kKeys, L, a.D, vec);
+    nv.load(vb, a.v_t, first * S::kKeys, L, a.D, vec);
+    nk.put(lk);
+    nv.put(lv);
+  }
+  __syncthreads();
   for (int tile = first; tile < last; ++tile) {
     const int k0 = tile * S::kKeys;
-    __syncthreads();
-    stage<DT, DP, S::kKeys, S::kLdK>(lk, a.D, vec, [&](int r) { return k0 + r < L ? kb + (k0 + r) * a.k_t : nullptr; });
-    stage<DT, DP, S::kKeys, S::kLdV>(lv, a.D, vec, [&](int r) { return k0 + r < L ? vb + (k0 + r) * a.v_t : nullptr; });
-    __syncthreads();
+    const DT* ck = lk + (tile - first & 1) * S::kTile;
+    const DT* cv = ck + S::kKeys * S::kLdK;
+    if (tile + 1 < last) {
+      nk.load(kb, a.k_t, k0 + S::kKeys, L, a.D, vec);
+      nv.load(vb, a.v_t, k0 + S::kKeys, L, a.D, vec);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     f32x4 s[QT][KT];
 #pragma unroll
     for (int n = 0; n < KT; ++n) {
@@ -94,40 +122,67 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttentionArgs a
       for (int t = 0; t < QT; ++t) s[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
-        const Frag<DT> kf = read_rows<DT>(lk, S::kLdK, (wk * KT + n) * 16 + i16, 32 * c + 8 * g);
+        const Frag<DT> kf = read_rows<DT>(ck, S::kLdK, (wk * KT + n) * 16 + i16, 32 * c + 8 * g);
 #pragma unroll
         for (int t = 0; t < QT; ++t) s[t][n] = mma(kf, q[t][c], s[t][n]);
       }
     }
-    const bool edge = k0 + S::kKeys > L;
+    if (k0 + S::kKeys > L) {
+#pragma unroll
+      for (int n = 0; n < KT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k0 + (wk * KT + n) * 16 + 4 * g + j >= L) {
+#pragma unroll
+            for (int t = 0; t < QT; ++t) s[t][n][j] = -__builtin_inff();
+          }
+    }
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      float top = mx[t];
+      float top = s[t][0][0];
 #pragma unroll
       for (int n = 0; n < KT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[t][n][j] *= sl;
-          if (edge && k0 + (wk * KT + n) * 16 + 4 * g + j >= L) s[t][n][j] = -__builtin_inff();
-          top = __builtin_fmaxf(top, s[t][n][j]);
-        }
-      top = col_max(top);
-      const float keep = __builtin_amdgcn_exp2f(mx[t] - top);
-      mx[t] = top;
+        for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[t][n][j]);
+      // The maximum that is subtracted only has to keep 2^(s - m) in range:
+      // it moves when a score passes it by more than 2^kSlack, so most tiles
+      // skip the exchange between lanes and the rescaling of o.
+      constexpr float kSlack = 8.0f;
+      if (__any((top - mx[t]) * sl > kSlack)) {
+        top = __builtin_fmaxf(mx[t], col_max(top));
+        const float keep = __builtin_amdgcn_exp2f((mx[t] - top) * sl);
+        mx[t] = top;
+        sum[t] *= keep;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) o[t][d] *= keep;
+      }
+      // s sl - m sl in one multiply-add: the rounding of m sl is the same
+      // factor in every p and in their sum. Past 2^20 that rounding is no
+      // longer small against 1, and the difference is taken first.
+      const float shift = __builtin_fmaxf(mx[t] * sl, kLowest);
       float part = 0.f;
+      if (__any(__builtin_fabsf(shift) > 1048576.0f)) {
+#pragma unroll
+        for (int n = 0; n < KT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[t][n][j] = (s[t][n][j] - mx[t]) * sl;
+      } else {
+#pragma unroll
+        for (int n = 0; n < KT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[t][n][j] = __builtin_fmaf(s[t][n][j], sl, -shift);
+      }
 #pragma unroll
       for (int n = 0; n < KT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[t][n][j] = __builtin_amdgcn_exp2f(s[t][n][j] - top);
+          s[t][n][j] = __builtin_amdgcn_exp2f(s[t][n][j]);
           part += s[t][n][j];
         }
-      sum[t] = sum[t] * keep + part;  // this lane's keys; the four lanes of a row are joined at the end
-#pragma unroll
-      for (int d = 0; d < kDT; ++d) o[t][d] *= keep;
+      sum[t] += part;  // this lane's keys; the four lanes of a row are joined at the end
     }
-    // p is rounded to the storage type here (one rounding of a value in
-    // [0, 1], no worse than the rounding of o); its sum keeps 32 bits
+    // p is rounded to the storage type here (one rounding of each value, of
+    // the relative size of o's own); its sum keeps 32 bits
 #pragma unroll
     for (int n = 0; n < KT; n += 2) {
       Frag<DT> p[QT];
@@ -135,21 +190,29 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttentionArgs a
       for (int t = 0; t < QT; ++t) p[t] = stack<DT>(s[t][n], s[t][n + 1]);
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
-        const Frag<DT> vf = read_cols<DT>(lv, S::kLdV, (wk * KT + n) * 16, 16 * d, lane);
+        const Frag<DT> vf = read_cols<DT>(cv, S::kLdV, (wk * KT + n) * 16, 16 * d, lane);
 #pragma unroll
         for (int t = 0; t < QT; ++t) o[t][d] = mma(vf, p[t], o[t][d]);
       }
     }
+    if (tile + 1 < last) {
+      DT* dst = lk + (tile + 1 - first & 1) * S::kTile;
+      nk.put(dst);
+      nv.put(dst + S::kKeys * S::kLdK);
+    }
+    __syncthreads();
   }
 #pragma unroll
-  for (int t = 0; t < QT; ++t) sum[t] = col_sum(sum[t]);
+  for (int t = 0; t < QT; ++t) {
+    sum[t] = col_sum(sum[t]);
+    mx[t] = __builtin_fmaxf(mx[t] * sl, kLowest);  // base-2 units from here on, as it was subtracted
+  }
 
   if constexpr (WK > 1) {
     // join the waves' parts of the keys, in order of their number
     constexpr int kLdO = DP + 4;
     float* jo = reinterpret_cast<float*>(smem);
     float* jm = jo + WK * S::kRows * kLdO;
-    __syncthreads();
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       const int r = wk * S::kRows + (wq * QT + t) * 16 + i16;
@@ -204,32 +267,48 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttentionArgs a
   }
 }
 
-// Joins the splits' partial results, in order: one wave per query row.
+// Joins the splits' partial results of one query row: 32 threads across the
+// row (four elements each), 8 along the splits, whose sums meet in LDS.
 template <typename DT>
 __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttentionArgs a) {
+  __shared__ f32x4 lds[kAttnThreads];
+  __shared__ float lsum[8];
   const QRows rows{a.Tq * (a.heads / a.kv_heads), a.heads / a.kv_heads};
-  const int groups = a.B * a.kv_heads, lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)groups * rows.M;
-  const int64_t r = blockIdx.x * (int64_t)(kAttnThreads / 64) + (threadIdx.x >> 6);
-  if (r >= n) return;
+  const int64_t n = (int64_t)a.B * a.kv_heads * rows.M, r = blockIdx.x;
   const int bh = (int)(r / rows.M), m = (int)(r % rows.M);
-  const int L = key_count(a, bh / a.kv_heads);
-  float top = -3.402823466e38f, sum = 0.f;
-  for (int s = 0; s < a.splits; ++s) top = __builtin_fmaxf(top, a.part_ml[2 * (s * n + r)]);
-  float acc[2] = {0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
+  const int c = (threadIdx.x & 31) * 4, part = threadIdx.x >> 5;
+  // at most 64 splits: a lane each
+  const int lane = threadIdx.x & 63;
+  float top = lane < a.splits ? a.part_ml[2 * (lane * n + r)] : kLowest;
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, k, 64));
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int s = part; s < a.splits; s += 8) {
     const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * n + r)] - top);
     sum += f * a.part_ml[2 * (s * n + r) + 1];
+    const float* src = a.part_o + (s * n + r) * a.D;
+    if (a.D % 4 == 0) {
+      if (c < a.D) acc += f * *reinterpret_cast<const f32x4*>(src + c);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (lane + 64 * k < a.D) acc[k] += f * a.part_o[(s * n + r) * a.D + lane + 64 * k];
+      for (int j = 0; j < 4; ++j)
+        if (c + j < a.D) acc[j] += f * src[c + j];
+    }
   }
-  const float inv = sum > 0.f ? 1.0f / sum : (L > 0 ? __builtin_nanf("") : 0.f);
-  DT* dst = (DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m);
+  lds[threadIdx.x] = acc;
+  if ((threadIdx.x & 31) == 0) lsum[part] = sum;
+  __syncthreads();
+  if (part != 0) return;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (lane + 64 * k < a.D) dst[lane + 64 * k] = from_f32<DT>(acc[k] * inv);
-  if (a.lse && lane == 0) a.lse[r] = top + __builtin_amdgcn_logf(sum);
+  for (int k = 1; k < 8; ++k) {
+    acc += lds[k * 32 + threadIdx.x];
+    sum += lsum[k];
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : (key_count(a, bh / a.kv_heads) > 0 ? __builtin_nanf("") : 0.f);
+  store4<DT>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), c, a.D, a.vec != 0, acc * inv);
+  if (a.lse && threadIdx.x == 0) a.lse[r] = top + __builtin_amdgcn_logf(sum);
 }
 
 template <typename DT, int DP, int WQ, int WK, int QT, int KT>
@@ -242,14 +321,20 @@ hipError_t run(const AttentionArgs& a, hipStream_t st) {
   launch_kernel(attention_kernel<DT, DP, WQ, WK, QT, KT>, dim3((unsigned)grid), dim3(kAttnThreads), S::kBytes, st, a);
   if (a.splits > 1) {
     const int64_t r = M * a.B * a.kv_heads;
-    launch_kernel(attention_join_kernel<DT>, dim3((unsigned)((r + 3) / 4)), dim3(kAttnThreads), 0, st, a);
+    launch_kernel(attention_join_kernel<DT>, dim3((unsigned)r), dim3(kAttnThreads), 0, st, a);
   }
   return hipGetLastError();
 }
 
 template <typename DT, int DP>
 hipError_t run_d(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
-  if (p.narrow) return run<DT, DP, 1, 4, 1, 2>(a, st);
+  if (p.narrow) {
+    // two fp32 tiles of 128 wide keys would not fit in LDS
+    if constexpr (sizeof(DT) == 4 && DP > 64)
+      return run<DT, DP, 2, 2, 1, 2>(a, st);
+    else
+      return run<DT, DP, 1, 4, 1, 2>(a, st);
+  }
   if constexpr (sizeof(DT) == 2)
     return run<DT, DP, 4, 1, 2, 4>(a, st);
   else
@@ -272,11 +357,11 @@ AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, boo
   p.narrow = M <= 16;
   p.rows = p.narrow ? 16 : bf ? 128 : 64;
   const int keys = p.narrow ? 128 : bf ? 64 : 32;
-  // Split the keys while the launch has fewer workgroups than two a compute
-  // unit and a split keeps two tiles or more.
+  // Split the keys while the launch has fewer workgroups than compute units
+  // and a split keeps two tiles or more.
   const int64_t groups = (M + p.rows - 1) / p.rows * B * kv_heads;
   const int64_t tiles = ((int64_t)Tk + keys - 1) / keys;
-  int64_t want = (2ll * cus + groups - 1) / groups;
+  int64_t want = cus / groups;
   if (want > tiles / 2) want = tiles / 2;
   if (want > 64) want = 64;
   p.splits = want < 1 ? 1 : (int)want;

@@ -123,14 +123,34 @@ __device__ __forceinline__ Frag<DT> stack(const f32x4& a, const f32x4& b) {
   return f;
 }
 
-// Max and sum over the four lanes that hold a column.
+// Max and sum over the four lanes that hold a column (l % 16 alike): the
+// swaps hand every lane its own value and the one 16 or 32 lanes away.
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void swap16(float v, float* a, float* b) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned r0 = r[0], r1 = r[1];  // a bit cast of a vector's element reads its first
+  *a = __builtin_bit_cast(float, r0);
+  *b = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ void swap32(float v, float* a, float* b) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned r0 = r[0], r1 = r[1];
+  *a = __builtin_bit_cast(float, r0);
+  *b = __builtin_bit_cast(float, r1);
+}
 __device__ __forceinline__ float col_max(float v) {
-  v = __builtin_fmaxf(v, __shfl_xor(v, 16, 64));
-  return __builtin_fmaxf(v, __shfl_xor(v, 32, 64));
+  float a, b;
+  swap16(v, &a, &b);
+  swap32(__builtin_fmaxf(a, b), &a, &b);
+  return __builtin_fmaxf(a, b);
 }
 __device__ __forceinline__ float col_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  float a, b;
+  swap16(v, &a, &b);
+  swap32(a + b, &a, &b);
+  return a + b;
 }
 
 // Eight elements of a row in global memory from column col on; columns past D
@@ -215,6 +235,32 @@ __device__ __forceinline__ void stage(DT* lds, int D, bool vec, RowFn row) {
     if (k < kTotal) put8<DT>(lds + r * LD + c, f[n]);
   }
 }
+
+// The same in two halves, so that a tile's loads are in flight while the one
+// before it is worked on: rows row0 .. row0 + ROWS - 1 of an array whose rows
+// lie `stride` apart, zero from row `limit` on.
+template <typename DT, int DP, int ROWS, int LD>
+struct TileLoad {
+  static constexpr int kCols = DP / 8, kTotal = ROWS * kCols, kIters = (kTotal + kAttnThreads - 1) / kAttnThreads;
+  Frag<DT> f[kIters];
+  __device__ __forceinline__ void load(const DT* base, int64_t stride, int row0, int limit, int D, bool vec) {
+#pragma unroll
+    for (int n = 0; n < kIters; ++n) {
+      const int k = n * kAttnThreads + threadIdx.x;
+      const int r = k / kCols, c = (k % kCols) * 8;
+      const bool on = (kTotal % kAttnThreads == 0 || k < kTotal) && row0 + r < limit;
+      f[n] = on ? load8<DT>(base + (int64_t)row0 * stride + r * stride, c, D, vec) : zero_frag<DT>();
+    }
+  }
+  __device__ __forceinline__ void put(DT* lds) const {
+#pragma unroll
+    for (int n = 0; n < kIters; ++n) {
+      const int k = n * kAttnThreads + threadIdx.x;
+      const int r = k / kCols, c = (k % kCols) * 8;
+      if (kTotal % kAttnThreads == 0 || k < kTotal) put8<DT>(lds + r * LD + c, f[n]);
+    }
+  }
+};
 
 // Query rows of one key head: row m is step m / G of query head hk G + m % G.
 struct QRows {
