@@ -37,7 +37,7 @@ struct Shape {
   static_assert(kBytes <= 160 * 1024, "LDS of a compute unit");
 };
 
-template <typename DT, int DP, int WQ, int WK, int QT, int KT>
+template <typename DT, int DP, int WQ, int WK, int QT, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArgs a) {
   using S = Shape<DT, DP, WQ, WK, QT, KT>;
   static_assert(WQ * WK * 64 == kAttnThreads, "four waves");
@@ -47,13 +47,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
   DT* lk = reinterpret_cast<DT*>(smem);
   DT* lv = lk + S::kKeys * S::kLdK;
 
-  const int groups = a.B * a.kv_heads;
-  int id = blockIdx.x;
-  const int bh = id % groups;  // neighbours in launch order (one XCD in turn) keep one (row, head)'s keys in their L2
-  id /= groups;
-  const int split = id % a.splits, m0 = id / a.splits * S::kRows;
-  const int b = bh / a.kv_heads, hk = bh % a.kv_heads;
   const QRows rows{a.Tq * (a.heads / a.kv_heads), a.heads / a.kv_heads};
+  const int tiles_all = (rows.M + S::kRows - 1) / S::kRows * a.splits;
+  const Work w = work_of(a, tiles_all);
+  if (w.tile >= tiles_all) return;
+  const int groups = a.B * a.kv_heads, bh = w.bh;
+  const int split = w.tile % a.splits, m0 = w.tile / a.splits * S::kRows;
+  const int b = bh / a.kv_heads, hk = bh % a.kv_heads;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wq = wave % WQ, wk = wave / WQ, g = lane >> 4, i16 = lane & 15;
   const bool vec = a.vec != 0;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
     const int m = m0 + (wq * QT + t) * 16 + i16;
 #pragma unroll
     for (int c = 0; c < kC; ++c)
-      q[t][c] = m < rows.M ? load8<DT>(rows.in<DT>(qb, a.q_t, a.q_h, m), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+      q[t][c] = m < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
   }
   f32x4 o[QT][kDT];
   float mx[QT], sum[QT];
@@ -97,8 +97,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
         for (int j = 0; j < 8; ++j) q[t][c].set(j, -q[t][c].get(j));
   }
 
-  TileLoad<DT, DP, S::kKeys, S::kLdK> nk;
-  TileLoad<DT, DP, S::kKeys, S::kLdV> nv;
+  TileLoad<DT, DP, S::kKeys, S::kLdK, FAST> nk;
+  TileLoad<DT, DP, S::kKeys, S::kLdV, FAST> nv;
   if (first < last) {
     nk.load(kb, a.k_t, first * S::kKeys, L, a.D, vec);
     nv.load(vb, a.v_t, first * S::kKeys, L, a.D, vec);
@@ -255,13 +255,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
     if (a.splits > 1) {
       const int64_t r = ((int64_t)split * groups + bh) * rows.M + m;
 #pragma unroll
-      for (int d = 0; d < kDT; ++d) store4<float>(a.part_o + r * a.D, 16 * d + 4 * g, a.D, a.D % 4 == 0, o[t][d]);
+      for (int d = 0; d < kDT; ++d) store4<float, FAST>(a.part_o + r * a.D, 16 * d + 4 * g, a.D, a.D % 4 == 0, o[t][d]);
       if (g == 0) a.part_ml[2 * r] = mx[t], a.part_ml[2 * r + 1] = sum[t];
     } else {
       const float inv = sum[t] > 0.f ? 1.0f / sum[t] : (L > 0 ? __builtin_nanf("") : 0.f);
       DT* dst = (DT*)a.o + rows.dense(a, b, hk, m);
 #pragma unroll
-      for (int d = 0; d < kDT; ++d) store4<DT>(dst, 16 * d + 4 * g, a.D, vec, o[t][d] * inv);
+      for (int d = 0; d < kDT; ++d) store4<DT, FAST>(dst, 16 * d + 4 * g, a.D, vec, o[t][d] * inv);
       if (a.lse && g == 0) a.lse[(int64_t)bh * rows.M + m] = mx[t] + __builtin_amdgcn_logf(sum[t]);
     }
   }
@@ -307,22 +307,22 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttentionA
     sum += lsum[k];
   }
   const float inv = sum > 0.f ? 1.0f / sum : (key_count(a, bh / a.kv_heads) > 0 ? __builtin_nanf("") : 0.f);
-  store4<DT>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), c, a.D, a.vec != 0, acc * inv);
+  store4<DT, false>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), c, a.D, a.vec != 0, acc * inv);
   if (a.lse && threadIdx.x == 0) a.lse[r] = top + __builtin_amdgcn_logf(sum);
 }
 
 template <typename DT, int DP, int WQ, int WK, int QT, int KT>
 hipError_t run(const AttentionArgs& a, hipStream_t st) {
   using S = Shape<DT, DP, WQ, WK, QT, KT>;
+  const auto kernel = a.vec && a.near && a.D == DP ? attention_kernel<DT, DP, WQ, WK, QT, KT, true>
+                                         : attention_kernel<DT, DP, WQ, WK, QT, KT, false>;
   const int64_t M = (int64_t)a.Tq * (a.heads / a.kv_heads);
-  const int64_t grid = (M + S::kRows - 1) / S::kRows * a.splits * a.B * a.kv_heads;
-  const hipError_t e = allow_lds(attention_kernel<DT, DP, WQ, WK, QT, KT>, S::kBytes);
+  const int64_t grid = work_grid(a, (M + S::kRows - 1) / S::kRows * a.splits);
+  const hipError_t e = allow_lds(kernel, S::kBytes);
   if (e != hipSuccess) return e;
-  launch_kernel(attention_kernel<DT, DP, WQ, WK, QT, KT>, dim3((unsigned)grid), dim3(kAttnThreads), S::kBytes, st, a);
-  if (a.splits > 1) {
-    const int64_t r = M * a.B * a.kv_heads;
-    launch_kernel(attention_join_kernel<DT>, dim3((unsigned)r), dim3(kAttnThreads), 0, st, a);
-  }
+  launch_kernel(kernel, dim3((unsigned)grid), dim3(kAttnThreads), S::kBytes, st, a);
+  if (a.splits > 1)
+    launch_kernel(attention_join_kernel<DT>, dim3((unsigned)(M * a.B * a.kv_heads)), dim3(kAttnThreads), 0, st, a);
   return hipGetLastError();
 }
 

@@ -155,9 +155,21 @@ __device__ __forceinline__ float col_sum(float v) {
 
 // Eight elements of a row in global memory from column col on; columns past D
 // are zero. `vec`: rows take 16-byte accesses and D is a multiple of them.
-template <typename DT>
+// FAST kernels are for rows that do and fill their tiles (D = DP): no access
+// has a condition on its column then.
+template <typename DT, bool FAST>
 __device__ __forceinline__ Frag<DT> load8(const DT* row, int col, int D, bool vec) {
   Frag<DT> f;
+  if constexpr (FAST) {
+    if constexpr (sizeof(DT) == 2) {
+      f.v = *reinterpret_cast<const bf16x8*>(row + col);
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(row + col), b = *reinterpret_cast<const f32x4*>(row + col + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = b[j];
+    }
+    return f;
+  }
   if (vec) {
     if constexpr (sizeof(DT) == 2) {
       const u32x4 z = {0, 0, 0, 0};
@@ -195,10 +207,10 @@ __device__ __forceinline__ void put8(DT* lds, const Frag<DT>& f) {
 }
 
 // Four results of a lane (neighbouring columns of one row) to global memory.
-template <typename DT>
+template <typename DT, bool FAST>
 __device__ __forceinline__ void store4(DT* row, int col, int D, bool vec, const f32x4& v) {
-  if (vec) {
-    if (col < D) {
+  if (FAST || vec) {
+    if (FAST || col < D) {
       if constexpr (sizeof(DT) == 2) {
         bf16x4 o;
 #pragma unroll
@@ -215,49 +227,52 @@ __device__ __forceinline__ void store4(DT* row, int col, int D, bool vec, const 
   }
 }
 
-// A tile of ROWS rows from global memory into LDS; row(r) gives a row's
-// address or null, whose row is zero.
-template <typename DT, int DP, int ROWS, int LD, typename RowFn>
-__device__ __forceinline__ void stage(DT* lds, int D, bool vec, RowFn row) {
-  constexpr int kCols = DP / 8, kTotal = ROWS * kCols, kIters = (kTotal + kAttnThreads - 1) / kAttnThreads;
-  Frag<DT> f[kIters];
-#pragma unroll
-  for (int n = 0; n < kIters; ++n) {
-    const int k = n * kAttnThreads + threadIdx.x;
-    const int r = k / kCols, c = (k % kCols) * 8;
-    const DT* p = k < kTotal ? row(r) : nullptr;
-    f[n] = p ? load8<DT>(p, c, D, vec) : zero_frag<DT>();
-  }
-#pragma unroll
-  for (int n = 0; n < kIters; ++n) {
-    const int k = n * kAttnThreads + threadIdx.x;
-    const int r = k / kCols, c = (k % kCols) * 8;
-    if (k < kTotal) put8<DT>(lds + r * LD + c, f[n]);
-  }
-}
+// A row's offset: FAST kernels are launched only where every offset inside a
+// (batch row, key head) of q, do and of a tile of k and v fits 31 bits of
+// bytes, so that a load takes a scalar base and a 32-bit offset.
+template <bool FAST>
+struct Offset {
+  typedef int64_t type;
+};
+template <>
+struct Offset<true> {
+  typedef uint32_t type;
+};
 
-// The same in two halves, so that a tile's loads are in flight while the one
-// before it is worked on: rows row0 .. row0 + ROWS - 1 of an array whose rows
-// lie `stride` apart, zero from row `limit` on.
-template <typename DT, int DP, int ROWS, int LD>
+// A tile of rows row0 .. row0 + ROWS - 1 of an array whose rows lie `stride`
+// apart, zero from row `limit` on, from global memory into LDS: in two
+// halves, so that a tile's loads are in flight while the one before it is
+// worked on.
+template <typename DT, int DP, int ROWS, int LD, bool FAST>
 struct TileLoad {
+  typedef typename Offset<FAST>::type Off;
   static constexpr int kCols = DP / 8, kTotal = ROWS * kCols, kIters = (kTotal + kAttnThreads - 1) / kAttnThreads;
   Frag<DT> f[kIters];
+  __device__ __forceinline__ static Off at(int n, Off stride) {
+    const int k = n * kAttnThreads + threadIdx.x;
+    return (Off)(k / kCols) * stride + (Off)((k % kCols) * 8);
+  }
   __device__ __forceinline__ void load(const DT* base, int64_t stride, int row0, int limit, int D, bool vec) {
+    base += row0 * stride;
+    if (FAST && row0 + ROWS <= limit) {  // the same for the whole workgroup: no condition per row
+#pragma unroll
+      for (int n = 0; n < kIters; ++n)
+        if (kTotal % kAttnThreads == 0 || n * kAttnThreads + (int)threadIdx.x < kTotal)
+          f[n] = load8<DT, FAST>(base + at(n, (Off)stride), 0, D, vec);
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < kIters; ++n) {
-      const int k = n * kAttnThreads + threadIdx.x;
-      const int r = k / kCols, c = (k % kCols) * 8;
-      const bool on = (kTotal % kAttnThreads == 0 || k < kTotal) && row0 + r < limit;
-      f[n] = on ? load8<DT>(base + (int64_t)row0 * stride + r * stride, c, D, vec) : zero_frag<DT>();
+      const int k = n * kAttnThreads + threadIdx.x, c = k % kCols * 8;
+      const bool on = (kTotal % kAttnThreads == 0 || k < kTotal) && row0 + k / kCols < limit;
+      f[n] = on ? load8<DT, FAST>(base + at(n, (Off)stride) - c, c, D, vec) : zero_frag<DT>();
     }
   }
   __device__ __forceinline__ void put(DT* lds) const {
 #pragma unroll
     for (int n = 0; n < kIters; ++n) {
       const int k = n * kAttnThreads + threadIdx.x;
-      const int r = k / kCols, c = (k % kCols) * 8;
-      if (kTotal % kAttnThreads == 0 || k < kTotal) put8<DT>(lds + r * LD + c, f[n]);
+      if (kTotal % kAttnThreads == 0 || k < kTotal) put8<DT>(lds + k / kCols * LD + (k % kCols) * 8, f[n]);
     }
   }
 };
@@ -276,6 +291,98 @@ struct QRows {
     return (((int64_t)t * a.B + b) * a.heads + hk * G + (m - t * G)) * a.D;
   }
 };
+
+// The same for consecutive tiles of query rows: a thread carries each of its
+// rows along as (head in the group, offset), so that no tile divides, and
+// where G divides ROWS only the scalar base moves.
+template <typename DT, int DP, int ROWS, int LD, bool FAST, int NT = kAttnThreads>
+struct QueryLoad {
+  typedef typename Offset<FAST>::type Off;
+  static constexpr int kCols = DP / 8, kTotal = ROWS * kCols, kIters = (kTotal + NT - 1) / NT;
+  Frag<DT> f[kIters];
+  int h[kIters];
+  Off off[kIters];
+  const DT* base;
+  int64_t step;  // of the base, per tile
+  Off shift, wrap;
+  int dh;
+  __device__ __forceinline__ void start(const DT* p, int64_t st, int64_t sh, int G) {
+    base = p;
+    const int dt = ROWS / G;
+    dh = ROWS - dt * G;
+    step = dt * st;
+    shift = (Off)dh * (Off)sh;
+    wrap = (Off)st - (Off)G * (Off)sh;
+#pragma unroll
+    for (int n = 0; n < kIters; ++n) {
+      const int m = (n * NT + (int)threadIdx.x) / kCols, t = m / G;
+      h[n] = m - t * G;
+      off[n] = (Off)t * (Off)st + (Off)h[n] * (Off)sh;
+    }
+  }
+  __device__ __forceinline__ void next(int G) {
+    base += step;
+    if (dh != 0) {
+#pragma unroll
+      for (int n = 0; n < kIters; ++n) {
+        h[n] += dh;
+        const bool over = h[n] >= G;
+        off[n] += over ? shift + wrap : shift;
+        if (over) h[n] -= G;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(int m0, int M, int D, bool vec) {
+    if (FAST && m0 + ROWS <= M) {
+#pragma unroll
+      for (int n = 0; n < kIters; ++n) {
+        const int k = n * NT + threadIdx.x;
+        if (kTotal % NT == 0 || k < kTotal)
+          f[n] = load8<DT, FAST>(base + (Off)(off[n] + (Off)(k % kCols * 8)), 0, D, vec);
+      }
+      return;
+    }
+#pragma unroll
+    for (int n = 0; n < kIters; ++n) {
+      const int k = n * NT + threadIdx.x;
+      const bool on = (kTotal % NT == 0 || k < kTotal) && m0 + k / kCols < M;
+      f[n] = on ? load8<DT, FAST>(base + off[n], k % kCols * 8, D, vec) : zero_frag<DT>();
+    }
+  }
+  __device__ __forceinline__ void put(DT* lds) const {
+#pragma unroll
+    for (int n = 0; n < kIters; ++n) {
+      const int k = n * NT + threadIdx.x;
+      if (kTotal % NT == 0 || k < kTotal) put8<DT>(lds + k / kCols * LD + (k % kCols) * 8, f[n]);
+    }
+  }
+};
+
+// Which tile a workgroup owns. Workgroup ids are dealt to the XCDs in turn.
+// The tiles of one (batch row, key head) are cut into up to kParts parts
+// (every kParts-th tile); a part's tiles run on one XCD one after the other,
+// so that they share its L2, and the parts of a row fall on different XCDs,
+// so that rows of different lengths load the XCDs evenly.
+struct Work {
+  int bh, tile;  // tile < tiles, or the workgroup has none
+};
+constexpr int kParts = 4;
+inline __host__ __device__ int part_count(int tiles) { return tiles < kParts ? tiles : kParts; }
+__device__ __forceinline__ Work work_of(const AttentionArgs& a, int tiles) {
+  const int parts = part_count(tiles), each = (tiles + parts - 1) / parts;
+  const int xcd = blockIdx.x % a.xcds, slot = blockIdx.x / a.xcds;
+  const int unit = slot / each * a.xcds + xcd, within = slot % each;
+  Work w;
+  w.bh = unit / parts;
+  w.tile = within * parts + unit % parts;
+  if (w.bh >= a.B * a.kv_heads) w.tile = tiles;
+  return w;
+}
+inline int64_t work_grid(const AttentionArgs& a, int64_t tiles) {
+  const int parts = part_count((int)tiles);
+  const int64_t each = (tiles + parts - 1) / parts, units = (int64_t)a.B * a.kv_heads * parts;
+  return (units + a.xcds - 1) / a.xcds * a.xcds * each;
+}
 
 __device__ __forceinline__ int key_count(const AttentionArgs& a, int b) {
   const int n = a.lengths ? a.lengths[b] : a.Tk;

@@ -47,9 +47,9 @@ int need_memory(const void* p, size_t have, size_t want) {
   return aligned(p, 16) ? RNN_OK : RNN_E_ALIGN;
 }
 
-int on_device(int* cus) {
-  int xcds = 0;
-  return current_device_facts(cus, &xcds);
+int on_device(int* xcds) {
+  int cus = 0;
+  return current_device_facts(&cus, xcds);
 }
 
 // ---------------------------------------------------------------------------
@@ -136,8 +136,8 @@ int scan_forward(const RnnGatedScanDesc* d, const RnnGatedScanIO* io, void* rese
   const size_t e = (size_t)esize_of(d->dtype);
   RETURN_IF_BAD(need(io->y, e));
   RETURN_IF_BAD(optional(io->h_n, 4));
-  int cus;
-  RETURN_IF_BAD(on_device(&cus));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
   a.y = io->y;
   a.h_n = io->h_n;
   if (!aligned(a.y, 4 * e)) a.width = 1;
@@ -204,6 +204,10 @@ int attention_args(const RnnAttentionDesc* d, const RnnAttentionIO* io, Attentio
   bool vec = d->D % m == 0 && aligned(a->q, 16) && aligned(a->k, 16) && aligned(a->v, 16) && aligned(a->o, 16);
   for (int64_t s : {d->q_t, d->q_b, d->q_h, d->k_t, d->k_b, d->k_h, d->v_t, d->v_b, d->v_h}) vec = vec && s % m == 0;
   a->vec = vec;
+  const double span_q = (double)(d->Tq - 1) * d->q_t + (double)(d->heads - 1) * d->q_h;
+  const double span_o = (double)d->Tq * d->B * d->heads * d->D;
+  const double span_kv = 256.0 * (double)(d->k_t > d->v_t ? d->k_t : d->v_t);
+  a->near = (std::fmax(span_q, std::fmax(span_o, span_kv)) + 128.0) * (double)e < 2147483648.0;
   return RNN_OK;
 }
 
@@ -212,10 +216,11 @@ int attention_forward(const RnnAttentionDesc* d, const RnnAttentionIO* io, void*
   AttentionArgs a;
   RETURN_IF_BAD(attention_args(d, io, &a));
   RETURN_IF_BAD(need_memory(ws, ws_bytes, attention_workspace(d)));
-  int cus;
-  RETURN_IF_BAD(on_device(&cus));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
   const AttentionPlan p = plan_of(d);
   a.splits = p.splits;
+  a.xcds = xcds;
   if (p.splits > 1) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = a.part_o + (size_t)p.splits * (attention_stat_bytes(d) / sizeof(float)) * d->D;
@@ -241,8 +246,8 @@ int rnn_layer_norm(const RnnNormDesc* desc, const void* x, const void* residual,
   RETURN_IF_BAD(optional(bias, e));
   if (residual) RETURN_IF_BAD(need(sum, e));
   RETURN_IF_BAD(optional(stats, 4));
-  int cus;
-  RETURN_IF_BAD(on_device(&cus));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
   NormArgs a{};
   a.rows = desc->rows; a.N = desc->N; a.eps = desc->eps;
   a.x = x; a.ldx = desc->x_ld;
@@ -277,8 +282,8 @@ int rnn_layer_norm_backward(const RnnNormDesc* desc, const void* s, const void* 
   RETURN_IF_BAD(optional(dweight, 4));
   RETURN_IF_BAD(optional(dbias, 4));
   if (dweight) RETURN_IF_BAD(need_memory(workspace, ws_bytes, norm_workspace(desc)));
-  int cus;
-  RETURN_IF_BAD(on_device(&cus));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
   NormArgs a{};
   a.rows = desc->rows; a.N = desc->N; a.eps = desc->eps;
   a.x = s; a.ldx = desc->x_ld; a.w = weight; a.stats = const_cast<float*>(stats);
@@ -333,8 +338,8 @@ int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* 
   RETURN_IF_BAD(need(grads->df, e));
   if (desc->input_gate) RETURN_IF_BAD(need(grads->di, e));
   RETURN_IF_BAD(optional(grads->dh0, 4));
-  int cus;
-  RETURN_IF_BAD(on_device(&cus));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
   a.state = const_cast<float*>(static_cast<const float*>(reserve));
   a.dy = grads->dy; a.dh_n = grads->dh_n;
   a.dx = grads->dx; a.df = grads->df; a.di = desc->input_gate ? grads->di : nullptr;
@@ -391,10 +396,11 @@ int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentio
   }
   RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_stat_bytes(desc)));
   RETURN_IF_BAD(need_memory(workspace, ws_bytes, attention_stat_bytes(desc)));
-  int cus;
-  RETURN_IF_BAD(on_device(&cus));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
   a.lse = const_cast<float*>(static_cast<const float*>(reserve));
   a.delta = static_cast<float*>(workspace);
+  a.xcds = xcds;
   a.d_o = grads->d_o; a.dq = grads->dq; a.dk = grads->dk; a.dv = grads->dv;
   return hip_status(launch_attention_backward(a, desc->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }

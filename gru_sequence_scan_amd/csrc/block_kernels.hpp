@@ -70,6 +70,8 @@ struct AttentionArgs {
   void* o;                          // [Tq, B, heads, D]
   float* lse;                       // [B, kv_heads, Tq * G] base-2 log-sum-exp, or null
   int vec;                          // rows take 16-byte accesses
+  int near;                         // offsets inside a (batch row, key head) of q, do and of 256 keys fit 31 bits
+  int xcds;                         // XCDs of the device
   // split of the keys over workgroups (forward)
   int splits;
   float* part_o;                    // [splits, B, kv_heads, Tq * G, D]
