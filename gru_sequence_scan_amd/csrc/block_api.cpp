@@ -86,15 +86,22 @@ int validate(const RnnGatedScanDesc* d) {
   if ((d->reverse | 1) != 1 || (d->input_gate | 1) != 1) return RNN_E_SHAPE;
   if (d->x_t < 0 || d->x_b < 0 || d->f_t < 0 || d->f_b < 0) return RNN_E_SHAPE;
   if (d->input_gate && (d->i_t < 0 || d->i_b < 0)) return RNN_E_SHAPE;
-  // one workgroup per 64 channels at most, batch row and chunk
-  const double groups = (double)d->B * (((double)d->H + 63) / 64) * scan_chunks(d);
+  // at most one workgroup per 32 channels, batch row (rounded up to XCDs) and chunk
+  const double groups = ((double)d->B * scan_chunks(d) + 64) * (((double)d->H + 31) / 32);
   if (groups > (double)kMaxGrid || (double)d->B * d->H > (double)kMaxGrid * 64) return RNN_E_SHAPE;
   return RNN_OK;
 }
 
 size_t scan_state_bytes(const RnnGatedScanDesc* d) { return (size_t)scan_chunks(d) * d->B * d->H * sizeof(float); }
 
-size_t scan_workspace(const RnnGatedScanDesc* d) { return scan_chunks(d) > 1 ? 3 * ((scan_state_bytes(d) + 15) / 16 * 16) : 0; }
+// One map (two numbers a channel) per segment of the time axis.
+size_t scan_map_bytes(const RnnGatedScanDesc* d) {
+  int each = 0;
+  const size_t segs = (size_t)gated_scan_segments(d->T, d->B, d->H, d->dtype == RNN_DTYPE_BF16, kPlanCus, &each);
+  return segs > 1 ? (segs * d->B * d->H * sizeof(float) + 15) / 16 * 16 : 0;
+}
+
+size_t scan_workspace(const RnnGatedScanDesc* d) { return 2 * scan_map_bytes(d); }
 
 int scan_args(const RnnGatedScanDesc* d, const RnnGatedScanIO* io, void* ws, size_t ws_bytes, GatedScanArgs* a) {
   if (!io) return RNN_E_NULL;
@@ -115,12 +122,10 @@ int scan_args(const RnnGatedScanDesc* d, const RnnGatedScanIO* io, void* ws, siz
   a->lengths = io->lengths;
   a->h0 = io->h0;
   a->chunks = scan_chunks(d);
-  const size_t part = (scan_state_bytes(d) + 15) / 16 * 16;
-  if (a->chunks > 1) {
-    char* w = static_cast<char*>(ws);
-    a->map_p = reinterpret_cast<float*>(w);
-    a->map_s = reinterpret_cast<float*>(w + part);
-    a->state = a->back_state = reinterpret_cast<float*>(w + 2 * part);
+  a->segs = gated_scan_segments(d->T, d->B, d->H, d->dtype == RNN_DTYPE_BF16, kPlanCus, &a->seg_chunks);
+  if (a->segs > 1) {
+    a->map_p = static_cast<float*>(ws);
+    a->map_s = reinterpret_cast<float*>(static_cast<char*>(ws) + scan_map_bytes(d));
   }
   // four channels an access when every row of every tensor allows it
   auto fits = [&](const void* p, int64_t t, int64_t b) { return aligned(p, 4 * e) && t % 4 == 0 && b % 4 == 0; };
@@ -138,13 +143,11 @@ int scan_forward(const RnnGatedScanDesc* d, const RnnGatedScanIO* io, void* rese
   RETURN_IF_BAD(optional(io->h_n, 4));
   int xcds;
   RETURN_IF_BAD(on_device(&xcds));
+  a.xcds = xcds;
   a.y = io->y;
   a.h_n = io->h_n;
   if (!aligned(a.y, 4 * e)) a.width = 1;
-  if (reserve) {
-    a.keep_state = 1;
-    a.state = static_cast<float*>(reserve);
-  }
+  a.state = static_cast<float*>(reserve);
   return hip_status(launch_gated_scan(a, d->dtype == RNN_DTYPE_BF16, false, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -341,6 +344,7 @@ int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* 
   int xcds;
   RETURN_IF_BAD(on_device(&xcds));
   a.state = const_cast<float*>(static_cast<const float*>(reserve));
+  a.xcds = xcds;
   a.dy = grads->dy; a.dh_n = grads->dh_n;
   a.dx = grads->dx; a.df = grads->df; a.di = desc->input_gate ? grads->di : nullptr;
   a.dh0 = grads->dh0;

@@ -24,18 +24,18 @@ struct GatedScanArgs {
   const float* h0;                  // [B, H] or null
   void* y;                          // [T, B, H]
   float* h_n;                       // [B, H] or null
-  int keep_state;                   // training: `state` is filled whatever the chunk count
   // backward
   const void* dy; const float* dh_n;
   void* dx; void* df; void* di; float* dh0;
   // chunking
   int width;                        // channels per access: 4, or 1 where rows are not aligned to it
-  int chunks;
-  float* map_p; float* map_s;       // [chunks, B, H] composed maps (workspace; chunks > 1)
-  float* state;                     // [chunks, B, H] state entering a chunk
-  float* back_state;                // [chunks, B, H] its gradient's counterpart
+  int chunks, segs, seg_chunks;     // of the time axis; seg_chunks chunks a segment
+  float* map_p; float* map_s;       // [segs, B, H] composed maps (workspace; segs > 1)
+  float* state;                     // training: [chunks, B, H] state entering a chunk; else null
+  int xcds;                         // XCDs of the device
   int tiles;                        // set by launch_gated_scan
 };
+int gated_scan_segments(int T, int B, int H, bool bf16_storage, int cus, int* seg_chunks);
 hipError_t launch_gated_scan(GatedScanArgs a, bool bf16_storage, bool backward, hipStream_t stream);
 
 // Layer norm (layer_norm.hip).

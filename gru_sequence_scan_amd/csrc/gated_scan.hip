@@ -6,39 +6,50 @@
 //   h_t = a_t h_{t-1} + u_t
 //
 // per channel of [T, B, H]. A step is the affine map h -> a h + u, and maps
-// compose: (A, U) after (A', U') is (A A', A U' + U). So time is cut into
-// chunks that are composed independently (kernel 1), the states at the chunk
-// boundaries follow from the few composed maps (kernel 2), and every chunk
-// is then run from its own boundary state (kernel 3).
+// compose: (A, U) after (A', U') is (A A', A U' + U).
+//
+// A workgroup owns 128 bytes of channels of one batch row and walks their
+// time in chunks of 128 steps. A thread holds 4 channels x 4 steps of a chunk
+// (one channel x 16 steps where rows are not aligned) in registers: it
+// composes its own steps, a thread per channel runs the entering state
+// through the threads' maps in LDS, and every thread then runs its steps from the state that enters
+// them. So each tensor is read once, while the next chunk's loads are in
+// flight. Where that gives too few workgroups (few channels, long time) the
+// time axis is cut into segments as well: a first launch composes each
+// segment's map, a second runs the state through the segments, and the walk
+// starts from there; the inputs are read twice then.
 //
 // Backward, with g_t the gradient of h_t and c the part of it that comes
 // from later steps:
 //   g_t = dy_t + c_{t+1},  c_t = a_t g_t,  c_{L+1} = dh_n,  dh_0 = c_1
 //   coupled: df = g (h_{t-1} - x) a (1 - a), dx = g (1 - a)
 //   gate:    df = g h_{t-1} a (1 - a), di = g x s (1 - s), dx = g s
-// c runs the same chunked way from the far end. h_{t-1} is computed again in
-// fp32 from the boundary states that the training forward kept, so y (rounded
-// to the storage type) is not read.
+// c runs the same way from the far end. h_{t-1} is computed again in fp32
+// from the state at every chunk's beginning, which the training forward kept
+// (1 / 64 of a bf16 tensor), so y (rounded to the storage type) is not read.
 //
 // All states, products and sums are fp32; only x, f, i, dy and the outputs
-// y, dx, df, di have the storage type.
+// y, dx, df, di have the storage type. Bound by memory.
 #include "block_kernels.hpp"
 #include "device_common.hpp"
 
 namespace rnnk {
 namespace {
 
-constexpr int kLanes = 64;    // channels of a workgroup's tile
-constexpr int kThreads = 256;
-
-// A thread takes E neighbouring channels (one access) of kSteps consecutive
-// steps; the chunk is kChunk steps for every E, so that the boundary states
-// do not depend on how the rows happen to be aligned.
-template <int E>
+// A workgroup's tile is 128 bytes of channels wide. A thread takes E
+// neighbouring channels (one access) of kSteps consecutive steps; the chunk is
+// the same for every E, so that the kept states do not depend on how the rows
+// happen to be aligned.
+template <typename DT>
+constexpr int kScanLanes = 128 / (int)sizeof(DT);
+template <typename DT>
+constexpr int kScanThreads = kScanLanes<DT> * 8;
+template <typename DT, int E>
 struct Tile {
+  static constexpr int kLanes = kScanLanes<DT>, kThreads = kScanThreads<DT>;
   static constexpr int kGroups = kLanes / E;          // threads across the channels
   static constexpr int kSlots = kThreads / kGroups;   // threads along time
-  static constexpr int kSteps = 32 / E;
+  static constexpr int kSteps = 16 / E;
   static_assert(kSlots * kSteps == kGatedScanChunk, "chunk length");
 };
 
@@ -51,350 +62,449 @@ __device__ __forceinline__ void gates_of(float f, float* a, float* keep) {
   *a = f >= 0.f ? r : er;
   *keep = f >= 0.f ? er : r;
 }
+__device__ __forceinline__ float sigma(float f) {
+  float a, keep;
+  gates_of(f, &a, &keep);
+  return a;
+}
 
 template <typename DT, int E>
-__device__ __forceinline__ void load_vec(const DT* p, float* out) {
-  struct alignas(sizeof(DT) * E) Raw { DT v[E]; };
-  const Raw r = *reinterpret_cast<const Raw*>(p);
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = to_f32<DT>(r.v[e]);
-}
+struct alignas(sizeof(DT) * E) Raw {
+  DT v[E];
+};
 
 template <typename DT, int E>
 __device__ __forceinline__ void store_vec(DT* p, const float* in) {
-  struct alignas(sizeof(DT) * E) Raw { DT v[E]; };
-  Raw r;
+  Raw<DT, E> r;
 #pragma unroll
   for (int e = 0; e < E; ++e) r.v[e] = from_f32<DT>(in[e]);
-  *reinterpret_cast<Raw*>(p) = r;
+  *reinterpret_cast<Raw<DT, E>*>(p) = r;
 }
 
-// Where a workgroup works: channel tile, batch row, chunk of steps.
+// Where a thread works: batch row, segment of chunks, channels, place in time.
+template <typename DT, int E>
 struct Place {
-  int b, c, L;       // batch row, chunk, the row's length
-  int h;             // this thread's first channel
-  int slot, s0;      // this thread's place along time and its first step
+  int b, L;          // batch row and its length
+  int c0, c1;        // the segment's chunks
+  int seg, ct;       // segment, channel tile
+  int h, ch;         // first channel, in the tensor and in the tile
+  int slot;
   bool live;         // the thread has channels
+  __device__ __forceinline__ explicit Place(const GatedScanArgs& a) {
+    // Workgroup ids are dealt to the XCDs in turn. The tiles of one (row,
+    // segment) go to one XCD one after the other, where they share its L2:
+    // rows of H channels that are not a multiple of 128 bytes have cache lines
+    // that belong to two tiles.
+    const unsigned slot = blockIdx.x / a.xcds, unit = slot / a.tiles * a.xcds + blockIdx.x % a.xcds;
+    ct = slot % a.tiles;
+    b = unit % a.B;
+    seg = unit / a.B;
+    c0 = seg * a.seg_chunks;
+    c1 = c0 + a.seg_chunks < a.chunks ? c0 + a.seg_chunks : a.chunks;
+    const int n = a.lengths ? a.lengths[b] : a.T;
+    L = n < 0 ? 0 : (n > a.T ? a.T : n);
+    ch = threadIdx.x % Tile<DT, E>::kGroups * E;
+    this->slot = threadIdx.x / Tile<DT, E>::kGroups;
+    h = ct * Tile<DT, E>::kLanes + ch;
+    live = h < a.H;
+  }
+  __device__ __forceinline__ int step0(int chunk) const { return chunk * kGatedScanChunk + slot * Tile<DT, E>::kSteps; }
+  // the time of step s < L
+  __device__ __forceinline__ int time(const GatedScanArgs& a, int s) const { return a.reverse ? L - 1 - s : s; }
 };
 
-template <int E>
-__device__ __forceinline__ Place place_of(const GatedScanArgs& a) {
-  Place p;
-  unsigned id = blockIdx.x;
-  const int ct = id % a.tiles;
-  id /= a.tiles;
-  p.b = id % a.B;
-  p.c = id / a.B;
-  const int L = a.lengths ? a.lengths[p.b] : a.T;
-  p.L = L < 0 ? 0 : (L > a.T ? a.T : L);
-  const int grp = threadIdx.x % Tile<E>::kGroups;
-  p.slot = threadIdx.x / Tile<E>::kGroups;
-  p.h = ct * kLanes + grp * E;
-  p.live = p.h < a.H;
-  p.s0 = p.c * kGatedScanChunk + p.slot * Tile<E>::kSteps;
-  return p;
-}
-
-__device__ __forceinline__ int time_of(const GatedScanArgs& a, const Place& p, int s) {
-  return a.reverse && s < p.L ? p.L - 1 - s : s;
-}
-
-// The gate values a, 1 - a (or sigma(i)) and the input x of this thread's
-// steps; a step past the row's end is the identity map (a = 1, u = 0).
-template <typename DT, int E, bool GATE>
-__device__ __forceinline__ void load_step(const GatedScanArgs& g, const Place& p, int s, float* a, float* keep, float* w,
-                                          float* x) {
-  if (p.live && s < p.L) {
-    const int t = time_of(g, p, s);
-    float f[E];
-    load_vec<DT, E>((const DT*)g.f + t * g.f_t + p.b * g.f_b + p.h, f);
-    load_vec<DT, E>((const DT*)g.x + t * g.x_t + p.b * g.x_b + p.h, x);
-    if (GATE) {
-      float i[E];
-      load_vec<DT, E>((const DT*)g.i + t * g.i_t + p.b * g.i_b + p.h, i);
+// A thread's steps of one chunk as they lie in memory. Loads are never
+// conditional (a condition per step would make each wait for the one before
+// it): a step past the row's end reads the last one again, and a thread past
+// the last channel the first ones; neither is used.
+template <typename DT, int E, bool GATE, bool DY>
+struct Steps {
+  static constexpr int K = Tile<DT, E>::kSteps;
+  Raw<DT, E> f[K], x[K], i[GATE ? K : 1], dy[DY ? K : 1];
+  __device__ __forceinline__ void load(const GatedScanArgs& g, const Place<DT, E>& p, int chunk) {
+    const int s0 = p.step0(chunk), h = p.live ? p.h : 0;
+    const DT* pf = (const DT*)g.f + p.b * g.f_b + h;
+    const DT* px = (const DT*)g.x + p.b * g.x_b + h;
+    const DT* pi = GATE ? (const DT*)g.i + p.b * g.i_b + h : nullptr;
+    const DT* pd = DY ? (const DT*)g.dy + (int64_t)p.b * g.H + h : nullptr;
+    const int64_t d_t = (int64_t)g.B * g.H;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float no;
-        gates_of(i[e], &w[e], &no);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      gates_of(f[e], &a[e], &keep[e]);
-      if (!GATE) w[e] = keep[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      a[e] = 1.f;
-      keep[e] = 0.f;
-      w[e] = 0.f;
-      x[e] = 0.f;
+    for (int k = 0; k < K; ++k) {
+      const int s = s0 + k < p.L ? s0 + k : p.L - 1;
+      const int64_t t = p.time(g, s);
+      f[k] = *reinterpret_cast<const Raw<DT, E>*>(pf + t * g.f_t);
+      x[k] = *reinterpret_cast<const Raw<DT, E>*>(px + t * g.x_t);
+      if (GATE) i[k] = *reinterpret_cast<const Raw<DT, E>*>(pi + t * g.i_t);
+      if (DY) dy[k] = *reinterpret_cast<const Raw<DT, E>*>(pd + t * d_t);
     }
   }
+};
+
+// Runs a state through the threads' maps, in the order of their steps (or
+// against it): in P, S of every slot, out the state that enters it (in S's
+// place). One thread per channel carries the state: of the first wave, or of
+// the second for the other direction.
+template <typename DT, int E, bool AGAINST>
+__device__ __forceinline__ float run_slots(const float* P, float* S, float state, int c) {
+  constexpr int kSlots = Tile<DT, E>::kSlots, kLanes = Tile<DT, E>::kLanes;
+#pragma unroll 8
+  for (int n = 0; n < kSlots; ++n) {
+    const int k = (AGAINST ? kSlots - 1 - n : n) * kLanes + c;
+    const float p = P[k], s = S[k];
+    S[k] = state;
+    state = __builtin_fmaf(p, state, s);
+  }
+  return state;
 }
 
-// Exclusive composition of the threads' maps along time. In: each thread's
-// own map (P, S). Out: lds_p / lds_s [slot][channel] hold the composition of
-// the slots before (forward) or after (REV) it; tot the whole chunk's map.
-template <int E, bool REV>
-__device__ __forceinline__ void compose_slots(float* lds_p, float* lds_s, const float* P, const float* S, int slot, int ch,
-                                              float* tot_p, float* tot_s) {
-  constexpr int kSlots = Tile<E>::kSlots;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    lds_p[slot * kLanes + ch + e] = P[e];
-    lds_s[slot * kLanes + ch + e] = S[e];
-  }
-  __syncthreads();
-  if (threadIdx.x < kLanes) {
-    float cp = 1.f, cs = 0.f;
-#pragma unroll 4
-    for (int n = 0; n < kSlots; ++n) {
-      const int k = (REV ? kSlots - 1 - n : n) * kLanes + threadIdx.x;
-      const float p = lds_p[k], s = lds_s[k];
-      lds_p[k] = cp;
-      lds_s[k] = cs;
-      cs = p * cs + s;
-      cp = p * cp;
-    }
-    *tot_p = cp;
-    *tot_s = cs;
-  }
-  __syncthreads();
-}
-
-// Kernel 1: the composed map of every chunk. Forward: h -> P h + S.
-// Backward (BACK): c -> P c + S from the chunk's end to its beginning.
+// The composed map of a segment: h -> P h + S, or (BACK) c -> P c + S from
+// the segment's end to its beginning, walked like the main pass.
 template <typename DT, int E, bool GATE, bool BACK>
-__global__ __launch_bounds__(kThreads) void scan_compose_kernel(GatedScanArgs g) {
-  constexpr int kSteps = Tile<E>::kSteps;
-  __shared__ float lds_p[Tile<E>::kSlots * kLanes], lds_s[Tile<E>::kSlots * kLanes];
-  const Place p = place_of<E>(g);
-  float P[E], S[E];
+__global__ __launch_bounds__(kScanThreads<DT>) void scan_compose_kernel(GatedScanArgs g) {
+  constexpr int K = Tile<DT, E>::kSteps, kSlots = Tile<DT, E>::kSlots, kLanes = Tile<DT, E>::kLanes;
+  __shared__ float lds_p[2][kSlots * kLanes], lds_s[2][kSlots * kLanes];
+  const Place<DT, E> p(g);
+  if (p.seg >= g.segs) return;
+  const int at = p.slot * kLanes + p.ch;
+  if (BACK) {  // the map c -> a (c + dy) has dy in x's place
+    g.x = g.dy;
+    g.x_t = (int64_t)g.B * g.H;
+    g.x_b = g.H;
+  }
+  const int c1 = p.c1 * kGatedScanChunk < p.L ? p.c1 : (p.L + kGatedScanChunk - 1) / kGatedScanChunk;  // chunks with steps
+  const int n = c1 - p.c0;
+  float tp = 1.f, ts = 0.f;
+  Steps<DT, E, GATE && !BACK, false> in;
+  if (n > 0) in.load(g, p, BACK ? c1 - 1 : p.c0);
+  for (int q = 0; q < n; ++q) {
+    const int chunk = BACK ? c1 - 1 - q : p.c0 + q, s0 = p.step0(chunk);
+    float P[E], S[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f;
+    for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f;
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    const int s = p.s0 + (BACK ? kSteps - 1 - k : k);
-    float a[E], keep[E], w[E], x[E];
-    if (BACK) {
-      if (p.live && s < p.L) {
-        const int t = time_of(g, p, s);
-        float f[E], dy[E];
-        load_vec<DT, E>((const DT*)g.f + t * g.f_t + p.b * g.f_b + p.h, f);
-        load_vec<DT, E>((const DT*)g.dy + ((int64_t)t * g.B + p.b) * g.H + p.h, dy);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          gates_of(f[e], &a[e], &keep[e]);
-          S[e] = a[e] * (S[e] + dy[e]);
-          P[e] *= a[e];
-        }
-      }
-    } else {
-      load_step<DT, E, GATE>(g, p, s, a, keep, w, x);
+    for (int kk = 0; kk < K; ++kk) {
+      const int k = BACK ? K - 1 - kk : kk;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        S[e] = a[e] * S[e] + w[e] * x[e];
-        P[e] *= a[e];
+        float a, keep;
+        gates_of(to_f32<DT>(in.f[k].v[e]), &a, &keep);
+        const float x = to_f32<DT>(in.x[k].v[e]);
+        float s;
+        if (BACK)
+          s = a * (S[e] + x);
+        else
+          s = __builtin_fmaf(a, S[e], (GATE && !BACK ? sigma(to_f32<DT>(in.i[GATE && !BACK ? k : 0].v[e])) : keep) * x);
+        const bool on = s0 + k < p.L;
+        S[e] = on ? s : S[e];
+        P[e] = on ? P[e] * a : P[e];
+      }
+    }
+    if (q + 1 < n) in.load(g, p, BACK ? chunk - 1 : chunk + 1);
+    float *lp = lds_p[q & 1], *ls = lds_s[q & 1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) lp[at + e] = P[e], ls[at + e] = S[e];
+    lds_barrier();
+    if (threadIdx.x < kLanes) {
+#pragma unroll 8
+      for (int m = 0; m < kSlots; ++m) {
+        const int k = (BACK ? kSlots - 1 - m : m) * kLanes + threadIdx.x;
+        ts = __builtin_fmaf(lp[k], ts, ls[k]);
+        tp *= lp[k];
       }
     }
   }
-  float tp, ts;
-  compose_slots<E, BACK>(lds_p, lds_s, P, S, p.slot, (threadIdx.x % Tile<E>::kGroups) * E, &tp, &ts);
-  const int h = (blockIdx.x % g.tiles) * kLanes + threadIdx.x;
-  if (threadIdx.x < kLanes && h < g.H) {
-    const int64_t o = ((int64_t)p.c * g.B + p.b) * g.H + h;
+  const int hc = p.ct * kLanes + (int)threadIdx.x;
+  if (threadIdx.x < kLanes && hc < g.H) {
+    const int64_t o = ((int64_t)p.seg * g.B + p.b) * g.H + hc;
     g.map_p[o] = tp;
     g.map_s[o] = ts;
   }
 }
 
-// Kernel 2: the states at the chunk boundaries, one thread per channel.
-// Forward: state[c] enters chunk c, h_n leaves the last one. Backward:
-// state[c] enters chunk c from its end; dh_0 leaves the first one.
-__global__ __launch_bounds__(kThreads) void scan_carry_kernel(const float* __restrict__ map_p, const float* __restrict__ map_s,
-                                                              const float* __restrict__ first, float* __restrict__ state,
-                                                              float* __restrict__ last, int chunks, int64_t n, int back) {
-  const int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+// The states that enter the segments, one thread per channel: in the place
+// of their maps' S. Forward from h_0, backward from dh_n and the last
+// segment.
+__global__ __launch_bounds__(256) void scan_carry_kernel(const float* __restrict__ map_p, float* __restrict__ map_s,
+                                                         const float* __restrict__ first, int segs, int64_t n, int back) {
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
   if (i >= n) return;
   float h = first ? first[i] : 0.f;
-#pragma unroll 8
-  for (int k = 0; k < chunks; ++k) {
-    const int64_t o = (back ? chunks - 1 - k : k) * n + i;
-    const float p = map_p[o], s = map_s[o];
-    state[o] = h;
-    h = p * h + s;
+  constexpr int kBatch = 16;
+  for (int k0 = 0; k0 < segs; k0 += kBatch) {
+    float p[kBatch], s[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int c = k0 + k < segs ? k0 + k : segs - 1;
+      const int64_t o = (back ? segs - 1 - c : c) * n + i;
+      p[k] = map_p[o];
+      s[k] = map_s[o];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k < segs) {
+        map_s[(back ? segs - 1 - (k0 + k) : k0 + k) * n + i] = h;
+        h = __builtin_fmaf(p[k], h, s[k]);
+      }
   }
-  if (last) last[i] = h;
 }
 
-// Kernel 3, forward: runs every chunk from the state that enters it.
 template <typename DT, int E, bool GATE>
-__global__ __launch_bounds__(kThreads) void scan_forward_kernel(GatedScanArgs g) {
-  constexpr int kSteps = Tile<E>::kSteps;
-  __shared__ float lds_p[Tile<E>::kSlots * kLanes], lds_s[Tile<E>::kSlots * kLanes];
-  const Place p = place_of<E>(g);
-  const int ch = (threadIdx.x % Tile<E>::kGroups) * E;
-  float a[kSteps][E], u[kSteps][E], P[E], S[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f;
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    float keep[E], w[E], x[E];
-    load_step<DT, E, GATE>(g, p, p.s0 + k, a[k], keep, w, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      u[k][e] = w[e] * x[e];
-      S[e] = a[k][e] * S[e] + u[k][e];
-      P[e] *= a[k][e];
-    }
+__global__ __launch_bounds__(kScanThreads<DT>) void scan_forward_kernel(GatedScanArgs g) {
+  constexpr int K = Tile<DT, E>::kSteps, kSlots = Tile<DT, E>::kSlots, kLanes = Tile<DT, E>::kLanes;
+  // two sets, taken in turn: a chunk's states are read while the next one's
+  // maps are written, with one barrier between each pair of phases
+  __shared__ float lds_p[2][kSlots * kLanes], lds_s[2][kSlots * kLanes];
+  const Place<DT, E> p(g);
+  if (p.seg >= g.segs) return;
+  const int at = p.slot * kLanes + p.ch;
+  const int c = threadIdx.x & (kLanes - 1);
+  const int64_t cell = (int64_t)p.b * g.H + (p.h - p.ch) + c;  // of the channel whose state this thread carries
+  const bool carries = threadIdx.x < kLanes && p.h - p.ch + c < g.H;
+  float state = 0.f;
+  if (carries) {
+    if (g.segs > 1)
+      state = g.map_s[(int64_t)p.seg * g.B * g.H + cell];
+    else if (g.h0)
+      state = g.h0[cell];
   }
-  float tp, ts;
-  compose_slots<E, false>(lds_p, lds_s, P, S, p.slot, ch, &tp, &ts);
-  float h[E];
+  Steps<DT, E, GATE, false> in;
+  if (p.c0 * kGatedScanChunk < p.L) in.load(g, p, p.c0);
+  for (int chunk = p.c0; chunk < p.c1; ++chunk) {
+    const int s0 = p.step0(chunk);
+    if (carries && g.state) g.state[(int64_t)chunk * g.B * g.H + cell] = state;
+    if (chunk * kGatedScanChunk >= p.L) {  // nothing but zeros from here on
+      if (p.live) {
+        const float z[E] = {};
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    h[e] = 0.f;
+        for (int k = 0; k < K; ++k)
+          if (s0 + k < g.T) store_vec<DT, E>((DT*)g.y + ((int64_t)(s0 + k) * g.B + p.b) * g.H + p.h, z);
+      }
+      continue;
+    }
+    float a[K][E], u[K][E], P[E], S[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float av, keep;
+        gates_of(to_f32<DT>(in.f[k].v[e]), &av, &keep);
+        const float uv = (GATE ? sigma(to_f32<DT>(in.i[GATE ? k : 0].v[e])) : keep) * to_f32<DT>(in.x[k].v[e]);
+        const bool on = s0 + k < p.L;
+        a[k][e] = on ? av : 1.f;
+        u[k][e] = on ? uv : 0.f;
+        S[e] = __builtin_fmaf(a[k][e], S[e], u[k][e]);
+        P[e] *= a[k][e];
+      }
+    if (chunk + 1 < p.c1 && (chunk + 1) * kGatedScanChunk < p.L) in.load(g, p, chunk + 1);
+    float* lp = lds_p[chunk & 1];
+    float* ls = lds_s[chunk & 1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) lp[at + e] = P[e], ls[at + e] = S[e];
+    lds_barrier();
+    if (threadIdx.x < kLanes) state = run_slots<DT, E, false>(lp, ls, state, c);
+    lds_barrier();
     if (p.live) {
-      const int64_t o = (int64_t)p.b * g.H + p.h + e;
-      if (g.chunks > 1)
-        h[e] = g.state[(int64_t)p.c * g.B * g.H + o];
-      else if (g.h0)
-        h[e] = g.h0[o];
-      if (g.chunks == 1 && g.keep_state && p.slot == 0) g.state[o] = h[e];
+      float h[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = ls[at + e];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int s = s0 + k;
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          h[e] = __builtin_fmaf(a[k][e], h[e], u[k][e]);
+          y[e] = s < p.L ? h[e] : 0.f;
+        }
+        if (s < g.T)
+          store_vec<DT, E>((DT*)g.y + ((int64_t)(s < p.L ? p.time(g, s) : s) * g.B + p.b) * g.H + p.h, y);
+      }
     }
-    h[e] = lds_p[p.slot * kLanes + ch + e] * h[e] + lds_s[p.slot * kLanes + ch + e];
   }
-  if (!p.live) return;
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    const int s = p.s0 + k;
-    float y[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      h[e] = a[k][e] * h[e] + u[k][e];
-      y[e] = s < p.L ? h[e] : 0.f;
-    }
-    if (s < g.T) store_vec<DT, E>((DT*)g.y + ((int64_t)time_of(g, p, s) * g.B + p.b) * g.H + p.h, y);
-  }
-  // with more than one chunk kernel 2 has written h_n
-  if (g.chunks == 1 && g.h_n && p.slot == Tile<E>::kSlots - 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) g.h_n[(int64_t)p.b * g.H + p.h + e] = h[e];
-  }
+  if (carries && g.h_n && p.seg == g.segs - 1) g.h_n[cell] = state;
 }
 
-// Kernel 3, backward.
 template <typename DT, int E, bool GATE>
-__global__ __launch_bounds__(kThreads) void scan_backward_kernel(GatedScanArgs g) {
-  constexpr int kSteps = Tile<E>::kSteps;
-  __shared__ float lds_p[Tile<E>::kSlots * kLanes], lds_s[Tile<E>::kSlots * kLanes];
-  const Place p = place_of<E>(g);
-  const int ch = (threadIdx.x % Tile<E>::kGroups) * E;
-  const int at = p.slot * kLanes + ch;
-  float a[kSteps][E], keep[kSteps][E], w[kSteps][E], x[kSteps][E], hp[kSteps][E];
-  float P[E], S[E];
-  float tp, ts;
-  // h_{t-1} of every step
+__global__ __launch_bounds__(kScanThreads<DT>) void scan_backward_kernel(GatedScanArgs g) {
+  constexpr int K = Tile<DT, E>::kSteps, kSlots = Tile<DT, E>::kSlots, kLanes = Tile<DT, E>::kLanes;
+  __shared__ float lds_p[2][kSlots * kLanes], lds_s[2][kSlots * kLanes], lds_c[2][kSlots * kLanes];
+  const Place<DT, E> p(g);
+  if (p.seg >= g.segs) return;
+  const int at = p.slot * kLanes + p.ch;
+  const int c = threadIdx.x & (kLanes - 1), wave = (threadIdx.x & 63) < kLanes ? threadIdx.x >> 6 : -1;
+  const int64_t cell = (int64_t)p.b * g.H + (p.h - p.ch) + c;
+  const bool channel = p.h - p.ch + c < g.H;
+  // the first wave runs h forward through a chunk, the second c backward
+  float carry = 0.f;
+  if (wave == 1 && channel) {
+    if (g.segs > 1)
+      carry = g.map_s[(int64_t)p.seg * g.B * g.H + cell];
+    else if (g.dh_n)
+      carry = g.dh_n[cell];
+  }
+  const int64_t d_t = (int64_t)g.B * g.H;
+  Steps<DT, E, GATE, true> in;
+  int chunk = p.c1 - 1;
+  // chunks past the row's end
+  for (; chunk >= p.c0 && chunk * kGatedScanChunk >= p.L; --chunk) {
+    if (p.live) {
+      const float z[E] = {};
+      const int s0 = p.step0(chunk);
 #pragma unroll
-  for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f;
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    load_step<DT, E, GATE>(g, p, p.s0 + k, a[k], keep[k], w[k], x[k]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      S[e] = a[k][e] * S[e] + w[k][e] * x[k][e];
-      P[e] *= a[k][e];
+      for (int k = 0; k < K; ++k)
+        if (s0 + k < g.T) {
+          const int64_t o = (s0 + k) * d_t + (int64_t)p.b * g.H + p.h;
+          store_vec<DT, E>((DT*)g.dx + o, z);
+          store_vec<DT, E>((DT*)g.df + o, z);
+          if (GATE) store_vec<DT, E>((DT*)g.di + o, z);
+        }
     }
   }
-  compose_slots<E, false>(lds_p, lds_s, P, S, p.slot, ch, &tp, &ts);
+  float entering = 0.f;
+  if (chunk >= p.c0) {
+    in.load(g, p, chunk);
+    if (wave == 0 && channel) entering = g.state[chunk * d_t + cell];
+  }
+  for (; chunk >= p.c0; --chunk) {
+    const int s0 = p.step0(chunk);
+    float a[K][E], keep[K][E], w[GATE ? K : 1][E], x[K][E], dy[K][E], P[E], S[E], C[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    float h = p.live ? g.state[((int64_t)p.c * g.B + p.b) * g.H + p.h + e] : 0.f;
-    h = lds_p[at + e] * h + lds_s[at + e];
+    for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f, C[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      hp[k][e] = h;
-      h = a[k][e] * h + w[k][e] * x[k][e];
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float av, kv;
+        gates_of(to_f32<DT>(in.f[k].v[e]), &av, &kv);
+        const bool on = s0 + k < p.L;
+        a[k][e] = on ? av : 1.f;
+        keep[k][e] = on ? kv : 0.f;
+        if (GATE) w[k][e] = on ? sigma(to_f32<DT>(in.i[GATE ? k : 0].v[e])) : 0.f;
+        x[k][e] = on ? to_f32<DT>(in.x[k].v[e]) : 0.f;
+        dy[k][e] = on ? to_f32<DT>(in.dy[k].v[e]) : 0.f;
+        S[e] = __builtin_fmaf(a[k][e], S[e], (GATE ? w[GATE ? k : 0][e] : keep[k][e]) * x[k][e]);
+        P[e] *= a[k][e];
+      }
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) C[e] = a[k][e] * (C[e] + dy[k][e]);
+    float next = 0.f;
+    if (chunk > p.c0) {
+      in.load(g, p, chunk - 1);
+      if (wave == 0 && channel) next = g.state[(chunk - 1) * d_t + cell];
+    }
+    float *lp = lds_p[chunk & 1], *ls = lds_s[chunk & 1], *lc = lds_c[chunk & 1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) lp[at + e] = P[e], ls[at + e] = S[e], lc[at + e] = C[e];
+    lds_barrier();
+    if (wave == 0) run_slots<DT, E, false>(lp, ls, entering, c);
+    if (wave == 1) carry = run_slots<DT, E, true>(lp, lc, carry, c);
+    entering = next;
+    lds_barrier();
+    if (p.live) {
+      float hp[K][E], h[E], cc[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = ls[at + e], cc[e] = lc[at + e];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          hp[k][e] = h[e];
+          h[e] = __builtin_fmaf(a[k][e], h[e], (GATE ? w[GATE ? k : 0][e] : keep[k][e]) * x[k][e]);
+        }
+#pragma unroll
+      for (int k = K - 1; k >= 0; --k) {
+        const int s = s0 + k;
+        float dx[E], df[E], di[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float gt = dy[k][e] + cc[e];
+          cc[e] = a[k][e] * gt;
+          // past the row's end a = 1 carries c on, and keep = 0 (w = 0) ends the rest
+          const float ga = gt * a[k][e] * keep[k][e];
+          const float wv = GATE ? w[GATE ? k : 0][e] : keep[k][e];
+          dx[e] = gt * wv;
+          df[e] = ga * (GATE ? hp[k][e] : hp[k][e] - x[k][e]);
+          di[e] = GATE ? gt * x[k][e] * wv * (1.0f - wv) : 0.f;
+          if (s >= p.L) dx[e] = df[e] = di[e] = 0.f;
+        }
+        if (s < g.T) {
+          const int64_t o = (s < p.L ? p.time(g, s) : s) * d_t + (int64_t)p.b * g.H + p.h;
+          store_vec<DT, E>((DT*)g.dx + o, dx);
+          store_vec<DT, E>((DT*)g.df + o, df);
+          if (GATE) store_vec<DT, E>((DT*)g.di + o, di);
+        }
+      }
     }
   }
-  __syncthreads();
-  // c of every step, from the chunk's end
-  float dy[kSteps][E];
+  if (wave == 1 && channel && g.dh0 && p.seg == 0) g.dh0[cell] = carry;
+}
+
+// A few steps (one, where a model answers token by token): a thread runs E
+// channels through all of them, nothing is shared.
+constexpr int kShort = 8;
+template <typename DT, int E, bool GATE>
+__global__ __launch_bounds__(256) void scan_short_kernel(GatedScanArgs g) {
+  const int64_t per = (g.H + E - 1) / E, id = blockIdx.x * (int64_t)256 + threadIdx.x;
+  const int b = (int)(id / per), h = (int)(id % per) * E;
+  if (b >= g.B) return;
+  const int n = g.lengths ? g.lengths[b] : g.T, L = n < 0 ? 0 : (n > g.T ? g.T : n);
+  const int64_t cell = (int64_t)b * g.H + h, y_t = (int64_t)g.B * g.H;
+  float state[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) S[e] = 0.f;
+  for (int e = 0; e < E; ++e) state[e] = g.h0 ? g.h0[cell + e] : 0.f;
+  if (g.state) {
 #pragma unroll
-  for (int k = kSteps - 1; k >= 0; --k) {
-    const int s = p.s0 + k;
-    if (p.live && s < p.L) {
-      load_vec<DT, E>((const DT*)g.dy + ((int64_t)time_of(g, p, s) * g.B + p.b) * g.H + p.h, dy[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) dy[k][e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) S[e] = a[k][e] * (S[e] + dy[k][e]);
+    for (int e = 0; e < E; ++e) g.state[cell + e] = state[e];
   }
-  compose_slots<E, true>(lds_p, lds_s, P, S, p.slot, ch, &tp, &ts);
-  if (!p.live) return;
-  float c[E];
+  for (int s = 0; s < g.T; ++s) {
+    const int64_t t = g.reverse && s < L ? L - 1 - s : s;
+    float y[E] = {};
+    if (s < L) {
+      const Raw<DT, E> f = *reinterpret_cast<const Raw<DT, E>*>((const DT*)g.f + t * g.f_t + b * g.f_b + h);
+      const Raw<DT, E> x = *reinterpret_cast<const Raw<DT, E>*>((const DT*)g.x + t * g.x_t + b * g.x_b + h);
+      Raw<DT, E> i;
+      if (GATE) i = *reinterpret_cast<const Raw<DT, E>*>((const DT*)g.i + t * g.i_t + b * g.i_b + h);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int64_t o = (int64_t)p.b * g.H + p.h + e;
-    if (g.chunks > 1)
-      c[e] = g.back_state[(int64_t)p.c * g.B * g.H + o];
-    else
-      c[e] = g.dh_n ? g.dh_n[o] : 0.f;
-    c[e] = lds_p[at + e] * c[e] + lds_s[at + e];
-  }
-#pragma unroll
-  for (int k = kSteps - 1; k >= 0; --k) {
-    const int s = p.s0 + k;
-    float dx[E], df[E], di[E];
-    const bool on = s < p.L;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float gt = dy[k][e] + c[e];
-      c[e] = on ? a[k][e] * gt : c[e];
-      const float ga = gt * a[k][e] * keep[k][e];
-      dx[e] = on ? gt * w[k][e] : 0.f;
-      df[e] = on ? ga * (GATE ? hp[k][e] : hp[k][e] - x[k][e]) : 0.f;
-      di[e] = GATE && on ? gt * x[k][e] * w[k][e] * (1.0f - w[k][e]) : 0.f;
+      for (int e = 0; e < E; ++e) {
+        float a, keep;
+        gates_of(to_f32<DT>(f.v[e]), &a, &keep);
+        state[e] = y[e] = __builtin_fmaf(a, state[e], (GATE ? sigma(to_f32<DT>(i.v[e])) : keep) * to_f32<DT>(x.v[e]));
+      }
     }
-    if (s < g.T) {
-      const int64_t o = ((int64_t)time_of(g, p, s) * g.B + p.b) * g.H + p.h;
-      store_vec<DT, E>((DT*)g.dx + o, dx);
-      store_vec<DT, E>((DT*)g.df + o, df);
-      if (GATE) store_vec<DT, E>((DT*)g.di + o, di);
-    }
+    store_vec<DT, E>((DT*)g.y + t * y_t + cell, y);
   }
-  if (g.chunks == 1 && g.dh0 && p.slot == 0) {
+  if (g.h_n) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) g.dh0[(int64_t)p.b * g.H + p.h + e] = c[e];
+    for (int e = 0; e < E; ++e) g.h_n[cell + e] = state[e];
   }
 }
 
 template <typename DT, int E, bool GATE>
 hipError_t run(const GatedScanArgs& a, bool back, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.tiles * a.B * a.chunks)), block(kThreads);
-  const int64_t n = (int64_t)a.B * a.H;
-  const dim3 cgrid((unsigned)((n + kThreads - 1) / kThreads));
-  if (back) {
-    if (a.chunks > 1) {
-      launch_kernel(scan_compose_kernel<DT, E, GATE, true>, grid, block, 0, st, a);
-      launch_kernel(scan_carry_kernel, cgrid, block, 0, st, (const float*)a.map_p, (const float*)a.map_s, a.dh_n,
-                    a.back_state, a.dh0, a.chunks, n, 1);
-    }
-    launch_kernel(scan_backward_kernel<DT, E, GATE>, grid, block, 0, st, a);
-  } else {
-    if (a.chunks > 1) {
-      launch_kernel(scan_compose_kernel<DT, E, GATE, false>, grid, block, 0, st, a);
-      launch_kernel(scan_carry_kernel, cgrid, block, 0, st, (const float*)a.map_p, (const float*)a.map_s, a.h0, a.state,
-                    a.h_n, a.chunks, n, 0);
-    }
-    launch_kernel(scan_forward_kernel<DT, E, GATE>, grid, block, 0, st, a);
+  if (!back && a.T <= kShort) {
+    const int64_t n = (int64_t)a.B * ((a.H + E - 1) / E);
+    launch_kernel(scan_short_kernel<DT, E, GATE>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+    return hipGetLastError();
   }
+  const int64_t units = (int64_t)a.B * a.segs;
+  const dim3 grid((unsigned)((units + a.xcds - 1) / a.xcds * a.xcds * a.tiles)), block(Tile<DT, E>::kThreads);
+  if (a.segs > 1) {
+    if (back)
+      launch_kernel(scan_compose_kernel<DT, E, GATE, true>, grid, block, 0, st, a);
+    else
+      launch_kernel(scan_compose_kernel<DT, E, GATE, false>, grid, block, 0, st, a);
+    const int64_t n = (int64_t)a.B * a.H;
+    launch_kernel(scan_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (const float*)a.map_p, a.map_s,
+                  back ? a.dh_n : a.h0, a.segs, n, (int)back);
+  }
+  if (back)
+    launch_kernel(scan_backward_kernel<DT, E, GATE>, grid, block, 0, st, a);
+  else
+    launch_kernel(scan_forward_kernel<DT, E, GATE>, grid, block, 0, st, a);
   return hipGetLastError();
 }
 
@@ -405,8 +515,23 @@ hipError_t run_gate(const GatedScanArgs& a, bool back, hipStream_t st) {
 
 }  // namespace
 
+// Segments so that the walks fill the compute units' threads about once,
+// each over two chunks at least.
+int gated_scan_segments(int T, int B, int H, bool bf, int cus, int* seg_chunks) {
+  const int lanes = bf ? kScanLanes<bf16> : kScanLanes<float>, threads = bf ? kScanThreads<bf16> : kScanThreads<float>;
+  const int64_t tiles = (int64_t)B * ((H + lanes - 1) / lanes);
+  const int chunks = (T + kGatedScanChunk - 1) / kGatedScanChunk;
+  int64_t want = (1024 / threads) * (int64_t)cus / tiles;
+  if (want > chunks / 2) want = chunks / 2;
+  if (want < 1) want = 1;
+  *seg_chunks = (int)((chunks + want - 1) / want);
+  return (chunks + *seg_chunks - 1) / *seg_chunks;
+}
+
 hipError_t launch_gated_scan(GatedScanArgs a, bool bf, bool back, hipStream_t st) {
-  a.tiles = (a.H + kLanes - 1) / kLanes;
+  const int lanes = bf ? kScanLanes<bf16> : kScanLanes<float>;
+  a.tiles = (a.H + lanes - 1) / lanes;
+  if ((int64_t)a.B * a.segs < a.xcds) a.xcds = 1;  // fewer (row, segment)s than XCDs: spread their tiles instead
   if (a.width == 1) return bf ? run_gate<bf16, 1>(a, back, st) : run_gate<float, 1>(a, back, st);
   return bf ? run_gate<bf16, 4>(a, back, st) : run_gate<float, 4>(a, back, st);
 }
