@@ -84,22 +84,26 @@ def _lib():
     return _ready
 
 
-class _on:
-    """Makes `device` the current one for a call and gives the handle of its
-    current stream."""
+_device = torch.cuda.current_device
+# the handle alone, without a Stream object around it (1 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device):
-        self.index = device.index
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _call(name, device, *args):
+    """Calls the C function on the device's current stream, with that device
+    current, and returns the stream's handle."""
+    index = device.index
+    if _device() == index:
+        stream = _raw_stream(index)
+        status = getattr(_lib(), name)(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            stream = _raw_stream(index)
+            status = getattr(_lib(), name)(*args, stream)
+    if status != 0:
+        raise RnnError(status, name)
+    return stream
 
 
 def _ok(status, where):
@@ -134,13 +138,25 @@ def _tensor(t, name, dims):
 
 def _strided(t, name, shape, like):
     """t itself where its last dimension is contiguous, else a dense copy."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if t.dtype != like.dtype:
         raise ValueError(f"{name}: dtype {t.dtype} != {like.dtype}")
     if t.device != like.device:
         raise ValueError(f"{name}: device {t.device} != {like.device}")
     return t if t.shape[-1] == 1 or t.stride(-1) == 1 else _dense(t)
+
+
+def _plain(t, name, shape, dtype, device):
+    """_check with a short way for a tensor that is as it should be."""
+    if t is None or (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        return t
+    return _check(t, name, shape, dtype, device)
+
+
+def _dense_like(t):
+    """A new dense tensor of t's shape."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _lengths(lengths, B, T, device):
@@ -172,10 +188,10 @@ class BlockContext:
         self.device, self.stream = device, stream
         self.__dict__.update(kw)
 
-    def _use(self, stream, *tensors):
+    def _use(self, *tensors):
         # memory that the caller cannot see must outlive work on another
         # stream than the one it was allocated on
-        if stream != self.stream:
+        if _raw_stream(self.device.index) != self.stream:
             for t in tensors:
                 if t is not None:
                     t.record_stream(torch.cuda.current_stream(self.device))
@@ -215,24 +231,23 @@ def _layer_norm(x, weight, bias, residual, eps, train):
     _tensor(x, "x", x.dim())
     n, device = x.shape[-1], x.device
     rows = x.numel() // n if n else 0
-    weight = _check(weight, "weight", (n,), x.dtype, device)
-    bias = _check(bias, "bias", (n,), x.dtype, device)
+    weight = _plain(weight, "weight", (n,), x.dtype, device)
+    bias = _plain(bias, "bias", (n,), x.dtype, device)
     xr, ld = _rows(x)
-    ldr = 0
+    ldr, total = 0, None
     if residual is not None:
         residual, ldr = _rows(_strided(residual, "residual", x.shape, x))
-    y = torch.empty(x.shape, dtype=x.dtype, device=device)
-    total = torch.empty(x.shape, dtype=x.dtype, device=device) if residual is not None else None
+        total = _dense_like(x)
+    y = _dense_like(x)
     stats = torch.empty((rows, 2), dtype=torch.float32, device=device) if train else None
     desc = RnnNormDesc(DTYPES[x.dtype], n, rows, ld, ldr, eps, 0)
-    with _on(device) as st:
-        _ok(_lib().rnn_layer_norm(ctypes.byref(desc), xr.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias), y.data_ptr(),
-                                  _ptr(total), _ptr(stats), st), "rnn_layer_norm")
+    stream = _call("rnn_layer_norm", device, ctypes.byref(desc), xr.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias),
+                   y.data_ptr(), _ptr(total), _ptr(stats))
     if not train:
         return y if total is None else (y, total)
     if total is not None:
         xr, desc = total, RnnNormDesc(desc.dtype, n, rows, n, 0, eps, 0)
-    return (y, total), BlockContext(device, st, desc=desc, x=xr, weight=weight, stats=stats, shape=tuple(x.shape),
+    return (y, total), BlockContext(device, stream, desc=desc, x=xr, weight=weight, stats=stats, shape=x.shape,
                                     has_params=weight is not None or bias is not None)
 
 
@@ -260,21 +275,19 @@ def layer_norm_backward(ctx, dy, dsum=None):
     dbias): dx in x's dtype is the gradient of x and of the residual alike;
     dweight and dbias are fp32 (None when the forward had neither)."""
     x, device = ctx.x, ctx.device
-    dy = _check(dy, "dy", ctx.shape, x.dtype, device)
-    dsum = _check(dsum, "dsum", ctx.shape, x.dtype, device)
+    dy = _plain(dy, "dy", ctx.shape, x.dtype, device)
+    dsum = _plain(dsum, "dsum", ctx.shape, x.dtype, device)
     n = ctx.shape[-1]
-    dx = torch.empty(ctx.shape, dtype=x.dtype, device=device)
+    dx = _dense_like(dy)
     dw = db = ws = None
     size = 0
     if ctx.has_params:
         dw, db = torch.empty((2, n), dtype=torch.float32, device=device).unbind(0)
         size = _bytes("rnn_layer_norm_backward_workspace_bytes", ctx.desc)
         ws = _buffer(size, device)
-    with _on(device) as st:
-        ctx._use(st, x, ctx.weight, ctx.stats)
-        _ok(_lib().rnn_layer_norm_backward(ctypes.byref(ctx.desc), x.data_ptr(), _ptr(ctx.weight), ctx.stats.data_ptr(),
-                                           dy.data_ptr(), _ptr(dsum), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), size,
-                                           st), "rnn_layer_norm_backward")
+    ctx._use(x, ctx.weight, ctx.stats)
+    _call("rnn_layer_norm_backward", device, ctypes.byref(ctx.desc), x.data_ptr(), _ptr(ctx.weight), ctx.stats.data_ptr(),
+          dy.data_ptr(), _ptr(dsum), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), size)
     return dx, dw, db
 
 
@@ -286,28 +299,27 @@ def _gated_scan(x, f, i, h0, lengths, reverse, train):
     _tensor(x, "x", 3)
     T, B, H = x.shape
     device, dtype = x.device, x.dtype
-    x = _strided(x, "x", (T, B, H), x)
-    f = _strided(f, "f", (T, B, H), x)
-    i = None if i is None else _strided(i, "i", (T, B, H), x)
-    h0 = _check(h0, "h0", (B, H), torch.float32, device)
+    shape = x.shape
+    x = _strided(x, "x", shape, x)
+    f = _strided(f, "f", shape, x)
+    i = None if i is None else _strided(i, "i", shape, x)
+    h0 = _plain(h0, "h0", (B, H), torch.float32, device)
     lengths = _lengths(lengths, B, T, device)
-    y = torch.empty((T, B, H), dtype=dtype, device=device)
-    h_n = torch.empty((B, H), dtype=torch.float32, device=device)
+    y = _dense_like(x)
+    h_n = torch.empty((B, H), dtype=torch.float32, device=device) if h0 is None else torch.empty_like(h0)
     (xt, xb, _), (ft, fb, _) = x.stride(), f.stride()
     it, ib, _ = (0, 0, 0) if i is None else i.stride()
-    desc = RnnGatedScanDesc(DTYPES[dtype], T, B, H, int(bool(reverse)), int(i is not None), xt, xb, ft, fb, it, ib)
+    desc = RnnGatedScanDesc(DTYPES[dtype], T, B, H, 1 if reverse else 0, 0 if i is None else 1, xt, xb, ft, fb, it, ib)
     io = RnnGatedScanIO(x.data_ptr(), f.data_ptr(), _ptr(i), _ptr(lengths), _ptr(h0), y.data_ptr(), h_n.data_ptr())
     size = _bytes("rnn_gated_scan_workspace_bytes", desc)
     ws = _buffer(size, device)
-    with _on(device) as st:
-        if not train:
-            _ok(_lib().rnn_gated_scan(ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size, st), "rnn_gated_scan")
-            return y, h_n
-        rsize = _bytes("rnn_gated_scan_reserve_bytes", desc)
-        reserve = _buffer(rsize, device)
-        _ok(_lib().rnn_gated_scan_train(ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws), size, st),
-            "rnn_gated_scan_train")
-    return (y, h_n), BlockContext(device, st, desc=desc, x=x, f=f, i=i, lengths=lengths, reserve=reserve)
+    if not train:
+        _call("rnn_gated_scan", device, ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size)
+        return y, h_n
+    rsize = _bytes("rnn_gated_scan_reserve_bytes", desc)
+    reserve = _buffer(rsize, device)
+    stream = _call("rnn_gated_scan_train", device, ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws), size)
+    return (y, h_n), BlockContext(device, stream, desc=desc, x=x, f=f, i=i, lengths=lengths, reserve=reserve)
 
 
 def gated_scan(x, f, i=None, *, h0=None, lengths=None, reverse=False):
@@ -338,20 +350,18 @@ def gated_scan_backward(ctx, dy, dh_n=None):
     an input gate, dh0 fp32."""
     d, device, dtype = ctx.desc, ctx.device, ctx.x.dtype
     shape = (d.T, d.B, d.H)
-    dy = _check(dy, "dy", shape, dtype, device)
-    dh_n = _check(dh_n, "dh_n", (d.B, d.H), torch.float32, device)
-    dx = torch.empty(shape, dtype=dtype, device=device)
-    df = torch.empty(shape, dtype=dtype, device=device)
-    di = torch.empty(shape, dtype=dtype, device=device) if ctx.i is not None else None
+    dy = _plain(dy, "dy", shape, dtype, device)
+    dh_n = _plain(dh_n, "dh_n", (d.B, d.H), torch.float32, device)
+    dx, df = _dense_like(dy), _dense_like(dy)
+    di = _dense_like(dy) if ctx.i is not None else None
     dh0 = torch.empty((d.B, d.H), dtype=torch.float32, device=device)
     io = RnnGatedScanIO(ctx.x.data_ptr(), ctx.f.data_ptr(), _ptr(ctx.i), _ptr(ctx.lengths), None, None, None)
     grads = RnnGatedScanGrads(dy.data_ptr(), _ptr(dh_n), dx.data_ptr(), df.data_ptr(), _ptr(di), dh0.data_ptr())
     size = _bytes("rnn_gated_scan_workspace_bytes", d)
     ws = _buffer(size, device)
-    with _on(device) as st:
-        ctx._use(st, ctx.x, ctx.f, ctx.i, ctx.lengths, ctx.reserve)
-        _ok(_lib().rnn_gated_scan_backward(ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ctx.reserve),
-                                           ctx.reserve.numel(), _ptr(ws), size, st), "rnn_gated_scan_backward")
+    ctx._use(ctx.x, ctx.f, ctx.i, ctx.lengths, ctx.reserve)
+    _call("rnn_gated_scan_backward", device, ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ctx.reserve),
+          ctx.reserve.numel(), _ptr(ws), size)
     return dx, df, di, dh0
 
 
@@ -365,11 +375,12 @@ def _cross_attention(q, k, v, lengths, scale, train):
     Tq, B, heads, D = q.shape
     Tk, _, kv_heads, _ = k.shape
     device, dtype = q.device, q.dtype
-    q = _strided(q, "q", (Tq, B, heads, D), q)
-    k = _strided(k, "k", (Tk, B, kv_heads, D), q)
-    v = _strided(v, "v", (Tk, B, kv_heads, D), q)
+    q = _strided(q, "q", q.shape, q)
+    shape = (Tk, B, kv_heads, D)
+    k = _strided(k, "k", shape, q)
+    v = _strided(v, "v", shape, q)
     lengths = _lengths(lengths, B, Tk, device)
-    o = torch.empty((Tq, B, heads, D), dtype=dtype, device=device)
+    o = _dense_like(q)
     if scale is None:
         scale = D ** -0.5 if D else 1.0
     desc = RnnAttentionDesc(DTYPES[dtype], B, Tq, Tk, heads, kv_heads, D, scale, *q.stride()[:3], *k.stride()[:3],
@@ -377,15 +388,14 @@ def _cross_attention(q, k, v, lengths, scale, train):
     io = RnnAttentionIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(lengths), o.data_ptr())
     size = _bytes("rnn_cross_attention_workspace_bytes", desc)
     ws = _buffer(size, device)
-    with _on(device) as st:
-        if not train:
-            _ok(_lib().rnn_cross_attention(ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size, st), "rnn_cross_attention")
-            return o
-        rsize = _bytes("rnn_cross_attention_reserve_bytes", desc)
-        reserve = _buffer(rsize, device)
-        _ok(_lib().rnn_cross_attention_train(ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws), size, st),
-            "rnn_cross_attention_train")
-    return o, BlockContext(device, st, desc=desc, io=io, q=q, k=k, v=v, lengths=lengths, o=o, reserve=reserve)
+    if not train:
+        _call("rnn_cross_attention", device, ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size)
+        return o
+    rsize = _bytes("rnn_cross_attention_reserve_bytes", desc)
+    reserve = _buffer(rsize, device)
+    stream = _call("rnn_cross_attention_train", device, ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws),
+                   size)
+    return o, BlockContext(device, stream, desc=desc, io=io, q=q, k=k, v=v, lengths=lengths, o=o, reserve=reserve)
 
 
 def cross_attention(q, k, v, *, lengths=None, scale=None):
@@ -414,16 +424,13 @@ def cross_attention_backward(ctx, do):
     Returns dense (dq, dk, dv); dk and dv are summed over the query heads of
     a key head and zero past a row's length."""
     o, device = ctx.o, ctx.device
-    do = _check(do, "do", tuple(o.shape), o.dtype, device)
-    dq = torch.empty(o.shape, dtype=o.dtype, device=device)
-    dk = torch.empty(ctx.k.shape, dtype=o.dtype, device=device)
-    dv = torch.empty(ctx.k.shape, dtype=o.dtype, device=device)
+    do = _plain(do, "do", o.shape, o.dtype, device)
+    dq = torch.empty_like(o)
+    dk, dv = o.new_empty(ctx.k.shape), o.new_empty(ctx.k.shape)
     grads = RnnAttentionGrads(do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
     size = _bytes("rnn_cross_attention_backward_workspace_bytes", ctx.desc)
     ws = _buffer(size, device)
-    with _on(device) as st:
-        ctx._use(st, ctx.q, ctx.k, ctx.v, ctx.lengths, o, ctx.reserve)
-        _ok(_lib().rnn_cross_attention_backward(ctypes.byref(ctx.desc), ctypes.byref(ctx.io), ctypes.byref(grads),
-                                                ctx.reserve.data_ptr(), ctx.reserve.numel(), _ptr(ws), size, st),
-            "rnn_cross_attention_backward")
+    ctx._use(ctx.q, ctx.k, ctx.v, ctx.lengths, o, ctx.reserve)
+    _call("rnn_cross_attention_backward", device, ctypes.byref(ctx.desc), ctypes.byref(ctx.io), ctypes.byref(grads),
+          ctx.reserve.data_ptr(), ctx.reserve.numel(), _ptr(ws), size)
     return dq, dk, dv

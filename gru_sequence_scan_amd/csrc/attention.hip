@@ -17,30 +17,105 @@
 namespace rnnk {
 namespace {
 
+constexpr int kMaxSplits = 256;
+
 // The running maximum of no scores: finite, so that subtracting it from the
 // -inf of a masked score never makes inf - inf.
 constexpr float kLowest = -3.402823466e38f;
 
-// WQ x WK waves: WQ sets of QT x 16 query rows, WK parts of the tile's keys,
-// KT x 16 keys each.
-template <typename DT, int DP, int WQ, int WK, int QT, int KT>
+// Four waves of QT x 16 query rows share tiles of KT x 16 keys.
+template <typename DT, int DP, int QT, int KT>
 struct Shape {
-  static constexpr int kRows = WQ * QT * 16;
-  static constexpr int kKeys = WK * KT * 16;
+  static constexpr int kRows = 4 * QT * 16;
+  static constexpr int kKeys = KT * 16;
   static constexpr int kLdK = TileShape<DT, DP, false>::kLd;
   static constexpr int kLdV = TileShape<DT, DP, true>::kLd;
   static constexpr int kTile = kKeys * (kLdK + kLdV);  // a tile of keys and its values, kept twice
-  static constexpr int kTileBytes = 2 * kTile * (int)sizeof(DT);
-  // the join of WK parts: per wave O^T [QT 16][DP + 1 pad] fp32 and m, l
-  static constexpr int kJoinBytes = WK > 1 ? WK * WQ * QT * 16 * (DP + 4 + 2) * 4 : 0;
-  static constexpr int kBytes = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
+  static constexpr int kBytes = 2 * kTile * (int)sizeof(DT);
   static_assert(kBytes <= 160 * 1024, "LDS of a compute unit");
 };
 
-template <typename DT, int DP, int WQ, int WK, int QT, int KT, bool FAST>
+// A negative scale is taken into q (exactly), a zero one replaced by the
+// smallest positive (2^(s sl) rounds to 1 alike): scores are compared before
+// they are scaled, and the scale rides in the exponent's multiply-add.
+template <typename DT, int N>
+__device__ __forceinline__ float base2_scale(float scale, Frag<DT> (&q)[N]) {
+  if (scale < 0.f) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[c].set(j, -q[c].get(j));
+  }
+  return __builtin_fmaxf(__builtin_fabsf(scale) * kLog2e, 1.17549435e-38f);
+}
+
+// Scores of KT tiles of keys (raw, -inf where masked) to probabilities:
+// updates the running maximum and sum of this lane's query row and rescales
+// its part of o.
+template <int KT, int NO>
+__device__ __forceinline__ void softmax_step(f32x4 (&s)[KT], float sl, float* mx, float* sum, f32x4 (&o)[NO]) {
+  float top = s[0][0];
+#pragma unroll
+  for (int n = 0; n < KT; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[n][j]);
+  // The maximum that is subtracted only has to keep 2^(s - m) in range: it
+  // moves when a score passes it by more than 2^kSlack, so most tiles skip
+  // the exchange between lanes and the rescaling of o.
+  constexpr float kSlack = 8.0f;
+  if (__any((top - *mx) * sl > kSlack)) {
+    top = __builtin_fmaxf(*mx, col_max(top));
+    const float keep = __builtin_amdgcn_exp2f((*mx - top) * sl);
+    *mx = top;
+    *sum *= keep;
+#pragma unroll
+    for (int d = 0; d < NO; ++d) o[d] *= keep;
+  }
+  // s sl - m sl in one multiply-add: the rounding of m sl is the same factor
+  // in every p and in their sum. Past 2^20 that rounding is no longer small
+  // against 1, and the difference is taken first.
+  const float shift = __builtin_fmaxf(*mx * sl, kLowest);
+  if (__any(__builtin_fabsf(shift) > 1048576.0f)) {
+#pragma unroll
+    for (int n = 0; n < KT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[n][j] = (s[n][j] - *mx) * sl;
+  } else {
+#pragma unroll
+    for (int n = 0; n < KT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[n][j] = __builtin_fmaf(s[n][j], sl, -shift);
+  }
+  float part = 0.f;
+#pragma unroll
+  for (int n = 0; n < KT; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[n][j] = __builtin_amdgcn_exp2f(s[n][j]);
+      part += s[n][j];
+    }
+  *sum += part;  // this lane's keys; the four lanes of a row are joined at the end
+}
+
+// Four elements of a query row's result (mx in base-2 units, sum over all
+// lanes), or of its part where the keys are split.
+template <typename DT, bool FAST>
+__device__ __forceinline__ void write_part(const AttentionArgs& a, const QRows& rows, int bh, int split, int m, int L, int col,
+                                           float mx, float sum, const f32x4& o) {
+  if (a.splits > 1) {
+    const int64_t r = ((int64_t)split * a.B * a.kv_heads + bh) * rows.M + m;
+    store4<float, FAST>(a.part_o + r * a.D, col, a.D, a.D % 4 == 0, o);
+    if (col == 0) a.part_ml[2 * r] = mx, a.part_ml[2 * r + 1] = sum;
+    return;
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : (L > 0 ? __builtin_nanf("") : 0.f);
+  store4<DT, FAST>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), col, a.D, a.vec != 0, o * inv);
+  if (a.lse && col == 0) a.lse[(int64_t)bh * rows.M + m] = mx + __builtin_amdgcn_logf(sum);
+}
+
+template <typename DT, int DP, int QT, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArgs a) {
-  using S = Shape<DT, DP, WQ, WK, QT, KT>;
-  static_assert(WQ * WK * 64 == kAttnThreads, "four waves");
+  using S = Shape<DT, DP, QT, KT>;
   static_assert(KT % 2 == 0, "pairs of key tiles make a fragment");
   constexpr int kC = DP / 32, kDT = DP / 16;
   extern __shared__ __align__(16) char smem[];
@@ -51,11 +126,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
   const int tiles_all = (rows.M + S::kRows - 1) / S::kRows * a.splits;
   const Work w = work_of(a, tiles_all);
   if (w.tile >= tiles_all) return;
-  const int groups = a.B * a.kv_heads, bh = w.bh;
-  const int split = w.tile % a.splits, m0 = w.tile / a.splits * S::kRows;
+  const int bh = w.bh, split = w.tile % a.splits, m0 = w.tile / a.splits * S::kRows;
   const int b = bh / a.kv_heads, hk = bh % a.kv_heads;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wq = wave % WQ, wk = wave / WQ, g = lane >> 4, i16 = lane & 15;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
   const bool vec = a.vec != 0;
 
   const int L = key_count(a, b);
@@ -68,33 +141,19 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
   const DT* vb = (const DT*)a.v + b * a.v_b + hk * a.v_h;
 
   Frag<DT> q[QT][kC];
+  f32x4 o[QT][kDT];
+  float mx[QT], sum[QT], sl = 0.f;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const int m = m0 + (wq * QT + t) * 16 + i16;
+    const int m = m0 + (wave * QT + t) * 16 + i16;
 #pragma unroll
     for (int c = 0; c < kC; ++c)
       q[t][c] = m < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
-  }
-  f32x4 o[QT][kDT];
-  float mx[QT], sum[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
+    sl = base2_scale<DT, kC>(a.scale, q[t]);
     mx[t] = kLowest;
     sum[t] = 0.f;
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  // A negative scale is taken into q (exactly), a zero one replaced by the
-  // smallest positive (2^(s sl) rounds to 1 alike): scores are compared before
-  // they are scaled, and the scale rides in the exponent's multiply-add.
-  const float sl = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1.17549435e-38f);
-  if (a.scale < 0.f) {
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[t][c].set(j, -q[t][c].get(j));
   }
 
   TileLoad<DT, DP, S::kKeys, S::kLdK, FAST> nk;
@@ -122,7 +181,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
       for (int t = 0; t < QT; ++t) s[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
-        const Frag<DT> kf = read_rows<DT>(ck, S::kLdK, (wk * KT + n) * 16 + i16, 32 * c + 8 * g);
+        const Frag<DT> kf = read_rows<DT>(ck, S::kLdK, n * 16 + i16, 32 * c + 8 * g);
 #pragma unroll
         for (int t = 0; t < QT; ++t) s[t][n] = mma(kf, q[t][c], s[t][n]);
       }
@@ -132,55 +191,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
       for (int n = 0; n < KT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (k0 + (wk * KT + n) * 16 + 4 * g + j >= L) {
+          if (k0 + n * 16 + 4 * g + j >= L) {
 #pragma unroll
             for (int t = 0; t < QT; ++t) s[t][n][j] = -__builtin_inff();
           }
     }
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      float top = s[t][0][0];
-#pragma unroll
-      for (int n = 0; n < KT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[t][n][j]);
-      // The maximum that is subtracted only has to keep 2^(s - m) in range:
-      // it moves when a score passes it by more than 2^kSlack, so most tiles
-      // skip the exchange between lanes and the rescaling of o.
-      constexpr float kSlack = 8.0f;
-      if (__any((top - mx[t]) * sl > kSlack)) {
-        top = __builtin_fmaxf(mx[t], col_max(top));
-        const float keep = __builtin_amdgcn_exp2f((mx[t] - top) * sl);
-        mx[t] = top;
-        sum[t] *= keep;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) o[t][d] *= keep;
-      }
-      // s sl - m sl in one multiply-add: the rounding of m sl is the same
-      // factor in every p and in their sum. Past 2^20 that rounding is no
-      // longer small against 1, and the difference is taken first.
-      const float shift = __builtin_fmaxf(mx[t] * sl, kLowest);
-      float part = 0.f;
-      if (__any(__builtin_fabsf(shift) > 1048576.0f)) {
-#pragma unroll
-        for (int n = 0; n < KT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[t][n][j] = (s[t][n][j] - mx[t]) * sl;
-      } else {
-#pragma unroll
-        for (int n = 0; n < KT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[t][n][j] = __builtin_fmaf(s[t][n][j], sl, -shift);
-      }
-#pragma unroll
-      for (int n = 0; n < KT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[t][n][j] = __builtin_amdgcn_exp2f(s[t][n][j]);
-          part += s[t][n][j];
-        }
-      sum[t] += part;  // this lane's keys; the four lanes of a row are joined at the end
-    }
+    for (int t = 0; t < QT; ++t) softmax_step<KT, kDT>(s[t], sl, &mx[t], &sum[t], o[t]);
     // p is rounded to the storage type here (one rounding of each value, of
     // the relative size of o's own); its sum keeps 32 bits
 #pragma unroll
@@ -190,7 +207,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
       for (int t = 0; t < QT; ++t) p[t] = stack<DT>(s[t][n], s[t][n + 1]);
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
-        const Frag<DT> vf = read_cols<DT>(cv, S::kLdV, (wk * KT + n) * 16, 16 * d, lane);
+        const Frag<DT> vf = read_cols<DT>(cv, S::kLdV, n * 16, 16 * d, lane);
 #pragma unroll
         for (int t = 0; t < QT; ++t) o[t][d] = mma(vf, p[t], o[t][d]);
       }
@@ -204,149 +221,225 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
   }
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    sum[t] = col_sum(sum[t]);
-    mx[t] = __builtin_fmaxf(mx[t] * sl, kLowest);  // base-2 units from here on, as it was subtracted
-  }
-
-  if constexpr (WK > 1) {
-    // join the waves' parts of the keys, in order of their number
-    constexpr int kLdO = DP + 4;
-    float* jo = reinterpret_cast<float*>(smem);
-    float* jm = jo + WK * S::kRows * kLdO;
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      const int r = wk * S::kRows + (wq * QT + t) * 16 + i16;
-#pragma unroll
-      for (int d = 0; d < kDT; ++d) *reinterpret_cast<f32x4*>(jo + r * kLdO + 16 * d + 4 * g) = o[t][d];
-      if (g == 0) jm[2 * r] = mx[t], jm[2 * r + 1] = sum[t];
-    }
-    __syncthreads();
-    if (wk != 0) return;
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      const int r = (wq * QT + t) * 16 + i16;
-      float top = mx[t];
-#pragma unroll
-      for (int w = 1; w < WK; ++w) top = __builtin_fmaxf(top, jm[2 * (w * S::kRows + r)]);
-      const float keep = __builtin_amdgcn_exp2f(mx[t] - top);
-      sum[t] *= keep;
-#pragma unroll
-      for (int d = 0; d < kDT; ++d) o[t][d] *= keep;
-#pragma unroll
-      for (int w = 1; w < WK; ++w) {
-        const int rr = w * S::kRows + r;
-        const float f = __builtin_amdgcn_exp2f(jm[2 * rr] - top);
-        sum[t] += f * jm[2 * rr + 1];
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(jo + rr * kLdO + 16 * d + 4 * g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[t][d][j] += f * v[j];
-        }
-      }
-      mx[t] = top;
-    }
-  }
-
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int m = m0 + (wq * QT + t) * 16 + i16;
+    const int m = m0 + (wave * QT + t) * 16 + i16;
+    const float total = col_sum(sum[t]), top = __builtin_fmaxf(mx[t] * sl, kLowest);
     if (m >= rows.M) continue;
-    if (a.splits > 1) {
-      const int64_t r = ((int64_t)split * groups + bh) * rows.M + m;
 #pragma unroll
-      for (int d = 0; d < kDT; ++d) store4<float, FAST>(a.part_o + r * a.D, 16 * d + 4 * g, a.D, a.D % 4 == 0, o[t][d]);
-      if (g == 0) a.part_ml[2 * r] = mx[t], a.part_ml[2 * r + 1] = sum[t];
-    } else {
-      const float inv = sum[t] > 0.f ? 1.0f / sum[t] : (L > 0 ? __builtin_nanf("") : 0.f);
-      DT* dst = (DT*)a.o + rows.dense(a, b, hk, m);
-#pragma unroll
-      for (int d = 0; d < kDT; ++d) store4<DT, FAST>(dst, 16 * d + 4 * g, a.D, vec, o[t][d] * inv);
-      if (a.lse && g == 0) a.lse[(int64_t)bh * rows.M + m] = mx[t] + __builtin_amdgcn_logf(sum[t]);
-    }
+    for (int d = 0; d < kDT; ++d) write_part<DT, FAST>(a, rows, bh, split, m, L, 16 * d + 4 * g, top, total, o[t][d]);
   }
 }
 
-// Joins the splits' partial results of one query row: 32 threads across the
-// row (four elements each), 8 along the splits, whose sums meet in LDS.
+// At most 16 query rows (one token, with the heads that share a key head):
+// bound by the reading of K and V, each of which is used once. The waves
+// divide the keys, 32 at a time, and never wait for each other before the
+// end: keys go from memory straight into fragments, values through a wave's
+// own piece of LDS, which turns them. A step's keys are loaded as soon as the
+// ones before have been used, and its values likewise.
+constexpr int kStepKeys = 32, kStepThreads = 512;
+template <typename DT, int DP>
+struct StepShape {
+  static constexpr int kWaves = kStepThreads / 64;
+  static constexpr int kLdV = TileShape<DT, DP, true>::kLd, kLdO = DP + 4;
+  static constexpr int kBytesV = kWaves * kStepKeys * kLdV * (int)sizeof(DT), kBytesO = kWaves * 16 * (kLdO + 2) * 4;
+  static constexpr int kBytes = kBytesV > kBytesO ? kBytesV : kBytesO;
+};
+template <typename DT, int DP, bool FAST>
+__global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(AttentionArgs a) {
+  using S = StepShape<DT, DP>;
+  constexpr int kC = DP / 32, kDT = DP / 16, kWaves = S::kWaves, kLdV = S::kLdV, kLdO = S::kLdO;
+  constexpr int kCols = DP / 8, kV = kStepKeys * kCols / 64;  // a lane's pieces of a step's values
+  extern __shared__ __align__(16) char smem[];
+
+  const QRows rows{a.Tq * (a.heads / a.kv_heads), a.heads / a.kv_heads};
+  const Work w = work_of(a, a.splits);
+  if (w.tile >= a.splits) return;
+  const int bh = w.bh, split = w.tile;
+  const int b = bh / a.kv_heads, hk = bh % a.kv_heads;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
+  const bool vec = a.vec != 0;
+  const DT* kb = (const DT*)a.k + b * a.k_b + hk * a.k_h;
+  const DT* vb = (const DT*)a.v + b * a.v_b + hk * a.v_h;
+  DT* lv = reinterpret_cast<DT*>(smem) + wave * kStepKeys * kLdV;
+
+  const int L = key_count(a, b);
+  const int per = ((L + a.splits - 1) / a.splits + kStepKeys - 1) / kStepKeys * kStepKeys;
+  const int first = split * per, last = first + per < L ? first + per : L;
+
+  Frag<DT> k[2][kC], v[kV];
+  auto load_k = [&](int k0) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int key = k0 + 16 * n + i16;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        k[n][c] = key < last ? load8<DT, FAST>(kb + key * a.k_t, 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+    }
+  };
+  auto load_v = [&](int k0) {
+#pragma unroll
+    for (int n = 0; n < kV; ++n) {
+      const int p = n * 64 + lane, key = k0 + p / kCols;
+      v[n] = key < last ? load8<DT, FAST>(vb + key * a.v_t, p % kCols * 8, a.D, vec) : zero_frag<DT>();
+    }
+  };
+  int k0 = first + wave * kStepKeys;
+  load_k(k0);
+  load_v(k0);
+  Frag<DT> q[kC];
+  {
+    const DT* qb = (const DT*)a.q + b * a.q_b + (int64_t)hk * rows.G * a.q_h;
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      q[c] = i16 < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, i16), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+  }
+  const float sl = base2_scale<DT, kC>(a.scale, q);
+  f32x4 o[kDT];
+#pragma unroll
+  for (int d = 0; d < kDT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float mx = kLowest, sum = 0.f;
+  for (; k0 < last; k0 += kWaves * kStepKeys) {
+    f32x4 s[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      s[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kC; ++c) s[n] = mma(k[n][c], q[c], s[n]);
+    }
+    load_k(k0 + kWaves * kStepKeys);
+    if (k0 + kStepKeys > last) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k0 + n * 16 + 4 * g + j >= last) s[n][j] = -__builtin_inff();
+    }
+    softmax_step<2, kDT>(s, sl, &mx, &sum, o);
+    // the wave's own reads of the step before are done: they fed products
+    // that were issued before these writes
+#pragma unroll
+    for (int n = 0; n < kV; ++n) {
+      const int p = n * 64 + lane;
+      put8<DT>(lv + p / kCols * kLdV + p % kCols * 8, v[n]);
+    }
+    load_v(k0 + kWaves * kStepKeys);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const Frag<DT> p = stack<DT>(s[0], s[1]);
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[d] = mma(read_cols<DT>(lv, kLdV, 0, 16 * d, lane), p, o[d]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  sum = col_sum(sum);
+  mx = __builtin_fmaxf(mx * sl, kLowest);  // base-2 units, as it was subtracted
+
+  // join the waves' parts, in order of their number: four elements of a row
+  // per thread
+  float* jo = reinterpret_cast<float*>(smem);
+  float* jm = jo + kWaves * 16 * kLdO;
+  __syncthreads();
+  const int r = wave * 16 + i16;
+#pragma unroll
+  for (int d = 0; d < kDT; ++d) *reinterpret_cast<f32x4*>(jo + r * kLdO + 16 * d + 4 * g) = o[d];
+  if (g == 0) jm[2 * r] = mx, jm[2 * r + 1] = sum;
+  __syncthreads();
+  const int m = threadIdx.x / (DP / 4), col = threadIdx.x % (DP / 4) * 4;
+  if (m >= 16 || m >= rows.M) return;
+  float top = kLowest;
+#pragma unroll
+  for (int x = 0; x < kWaves; ++x) top = __builtin_fmaxf(top, jm[2 * (x * 16 + m)]);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  float total = 0.f;
+#pragma unroll
+  for (int x = 0; x < kWaves; ++x) {
+    const int rr = x * 16 + m;
+    const float f = __builtin_amdgcn_exp2f(jm[2 * rr] - top);
+    total += f * jm[2 * rr + 1];
+    acc += f * *reinterpret_cast<const f32x4*>(jo + rr * kLdO + col);
+  }
+  write_part<DT, FAST>(a, rows, bh, split, m, L, col, top, total, acc);
+}
+
+// Joins the splits' partial results of one query row: a thread per split for
+// the weights, then 32 threads across the row (four elements each) by 8 along
+// the splits, whose sums meet in LDS.
 template <typename DT>
 __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttentionArgs a) {
+  static_assert(kMaxSplits <= kAttnThreads, "a thread per split");
   __shared__ f32x4 lds[kAttnThreads];
-  __shared__ float lsum[8];
+  __shared__ float weight[kAttnThreads], wtop[4], wsum[4];
   const QRows rows{a.Tq * (a.heads / a.kv_heads), a.heads / a.kv_heads};
   const int64_t n = (int64_t)a.B * a.kv_heads * rows.M, r = blockIdx.x;
   const int bh = (int)(r / rows.M), m = (int)(r % rows.M);
-  const int c = (threadIdx.x & 31) * 4, part = threadIdx.x >> 5;
-  // at most 64 splits: a lane each
-  const int lane = threadIdx.x & 63;
-  float top = lane < a.splits ? a.part_ml[2 * (lane * n + r)] : kLowest;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const bool on = (int)threadIdx.x < a.splits;
+  const float mine = on ? a.part_ml[2 * (threadIdx.x * n + r)] : kLowest;
+  const float part = on ? a.part_ml[2 * (threadIdx.x * n + r) + 1] : 0.f;
+  float top = mine;
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, k, 64));
+  if (lane == 0) wtop[wave] = top;
+  __syncthreads();
+  top = __builtin_fmaxf(__builtin_fmaxf(wtop[0], wtop[1]), __builtin_fmaxf(wtop[2], wtop[3]));
+  const float f = __builtin_amdgcn_exp2f(mine - top);
+  weight[threadIdx.x] = f;
+  float sum = f * part;
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k, 64);
+  if (lane == 0) wsum[wave] = sum;
+  __syncthreads();
+  const int c = (threadIdx.x & 31) * 4;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-#pragma unroll 4
-  for (int s = part; s < a.splits; s += 8) {
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * n + r)] - top);
-    sum += f * a.part_ml[2 * (s * n + r) + 1];
-    const float* src = a.part_o + (s * n + r) * a.D;
-    if (a.D % 4 == 0) {
-      if (c < a.D) acc += f * *reinterpret_cast<const f32x4*>(src + c);
-    } else {
+  if (a.D % 4 == 0) {
+    if (c < a.D) {
+#pragma unroll 8
+      for (int s = threadIdx.x >> 5; s < a.splits; s += 8)
+        acc += weight[s] * *reinterpret_cast<const f32x4*>(a.part_o + (s * n + r) * a.D + c);
+    }
+  } else {
+    for (int s = threadIdx.x >> 5; s < a.splits; s += 8)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (c + j < a.D) acc[j] += f * src[c + j];
-    }
+        if (c + j < a.D) acc[j] += weight[s] * a.part_o[(s * n + r) * a.D + c + j];
   }
   lds[threadIdx.x] = acc;
-  if ((threadIdx.x & 31) == 0) lsum[part] = sum;
   __syncthreads();
-  if (part != 0) return;
+  if (threadIdx.x >= 32) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) {
-    acc += lds[k * 32 + threadIdx.x];
-    sum += lsum[k];
-  }
+  for (int k = 1; k < 8; ++k) acc += lds[k * 32 + threadIdx.x];
+  sum = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
   const float inv = sum > 0.f ? 1.0f / sum : (key_count(a, bh / a.kv_heads) > 0 ? __builtin_nanf("") : 0.f);
   store4<DT, false>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), c, a.D, a.vec != 0, acc * inv);
   if (a.lse && threadIdx.x == 0) a.lse[r] = top + __builtin_amdgcn_logf(sum);
 }
 
-template <typename DT, int DP, int WQ, int WK, int QT, int KT>
-hipError_t run(const AttentionArgs& a, hipStream_t st) {
-  using S = Shape<DT, DP, WQ, WK, QT, KT>;
-  const auto kernel = a.vec && a.near && a.D == DP ? attention_kernel<DT, DP, WQ, WK, QT, KT, true>
-                                         : attention_kernel<DT, DP, WQ, WK, QT, KT, false>;
+template <typename DT, int DP>
+hipError_t run(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
+  constexpr int QT = sizeof(DT) == 2 ? 2 : 1, KT = sizeof(DT) == 2 ? 4 : 2;
+  using S = Shape<DT, DP, QT, KT>;
+  const bool fast = a.vec && a.near && a.D == DP;
   const int64_t M = (int64_t)a.Tq * (a.heads / a.kv_heads);
-  const int64_t grid = work_grid(a, (M + S::kRows - 1) / S::kRows * a.splits);
-  const hipError_t e = allow_lds(kernel, S::kBytes);
-  if (e != hipSuccess) return e;
-  launch_kernel(kernel, dim3((unsigned)grid), dim3(kAttnThreads), S::kBytes, st, a);
+  if (p.narrow) {
+    const auto kernel = fast ? attention_step_kernel<DT, DP, true> : attention_step_kernel<DT, DP, false>;
+    const hipError_t e = allow_lds(kernel, StepShape<DT, DP>::kBytes);
+    if (e != hipSuccess) return e;
+    launch_kernel(kernel, dim3((unsigned)work_grid(a, a.splits)), dim3(kStepThreads), StepShape<DT, DP>::kBytes, st, a);
+  } else {
+    const auto kernel = fast ? attention_kernel<DT, DP, QT, KT, true> : attention_kernel<DT, DP, QT, KT, false>;
+    const hipError_t e = allow_lds(kernel, S::kBytes);
+    if (e != hipSuccess) return e;
+    launch_kernel(kernel, dim3((unsigned)work_grid(a, (M + S::kRows - 1) / S::kRows * a.splits)), dim3(kAttnThreads),
+                  S::kBytes, st, a);
+  }
   if (a.splits > 1)
     launch_kernel(attention_join_kernel<DT>, dim3((unsigned)(M * a.B * a.kv_heads)), dim3(kAttnThreads), 0, st, a);
   return hipGetLastError();
 }
 
-template <typename DT, int DP>
-hipError_t run_d(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
-  if (p.narrow) {
-    // two fp32 tiles of 128 wide keys would not fit in LDS
-    if constexpr (sizeof(DT) == 4 && DP > 64)
-      return run<DT, DP, 2, 2, 1, 2>(a, st);
-    else
-      return run<DT, DP, 1, 4, 1, 2>(a, st);
-  }
-  if constexpr (sizeof(DT) == 2)
-    return run<DT, DP, 4, 1, 2, 4>(a, st);
-  else
-    return run<DT, DP, 4, 1, 1, 2>(a, st);
-}
-
 template <typename DT>
 hipError_t run_t(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
-  if (a.D <= 32) return run_d<DT, 32>(a, p, st);
-  if (a.D <= 64) return run_d<DT, 64>(a, p, st);
-  if (a.D <= 96) return run_d<DT, 96>(a, p, st);
-  return run_d<DT, 128>(a, p, st);
+  if (a.D <= 32) return run<DT, 32>(a, p, st);
+  if (a.D <= 64) return run<DT, 64>(a, p, st);
+  if (a.D <= 96) return run<DT, 96>(a, p, st);
+  return run<DT, 128>(a, p, st);
 }
 
 }  // namespace
@@ -355,15 +448,14 @@ AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, boo
   const int64_t M = (int64_t)Tq * (heads / kv_heads);
   AttentionPlan p{};
   p.narrow = M <= 16;
-  p.rows = p.narrow ? 16 : bf ? 128 : 64;
-  const int keys = p.narrow ? 128 : bf ? 64 : 32;
-  // Split the keys while the launch has fewer workgroups than compute units
-  // and a split keeps two tiles or more.
-  const int64_t groups = (M + p.rows - 1) / p.rows * B * kv_heads;
-  const int64_t tiles = ((int64_t)Tk + keys - 1) / keys;
+  const int rows = p.narrow ? 16 : bf ? 128 : 64;
+  // A split of the keys keeps two tiles (narrow: a step of every wave) or more.
+  const int keys = p.narrow ? kStepKeys * kStepThreads / 64 : bf ? 128 : 64;
+  const int64_t groups = (M + rows - 1) / rows * B * kv_heads;
+  // Split while there are fewer workgroups than compute units.
   int64_t want = cus / groups;
-  if (want > tiles / 2) want = tiles / 2;
-  if (want > 64) want = 64;
+  if (want > Tk / keys) want = Tk / keys;
+  if (want > kMaxSplits) want = kMaxSplits;
   p.splits = want < 1 ? 1 : (int)want;
   return p;
 }

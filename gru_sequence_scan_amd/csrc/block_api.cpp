@@ -169,10 +169,10 @@ int validate(const RnnAttentionDesc* d) {
   for (int64_t s : {d->q_t, d->q_b, d->q_h, d->k_t, d->k_b, d->k_h, d->v_t, d->v_b, d->v_h})
     if (s < 0) return RNN_E_SHAPE;
   // row numbers, and the workgroups of the widest launch (16 rows each and
-  // at most 64 splits of the keys), stay 32-bit
+  // at most 256 splits of the keys), stay 32-bit
   const double groups = (double)d->B * d->kv_heads;
   if (d->Tk > kMaxGrid - 1024 || query_rows(d) > kMaxGrid - 1024) return RNN_E_SHAPE;
-  if (groups * ((double)query_rows(d) / 16 + 64) > (double)kMaxGrid || groups * ((double)d->Tk / 16 + 1) > (double)kMaxGrid)
+  if (groups * ((double)query_rows(d) / 16 + 256) > (double)kMaxGrid || groups * ((double)d->Tk / 16 + 1) > (double)kMaxGrid)
     return RNN_E_SHAPE;
   return RNN_OK;
 }

@@ -81,11 +81,11 @@ struct AttentionArgs {
   void* dq; void* dk; void* dv;
   float* delta;                     // [B, kv_heads, Tq * G]
 };
-// How the forward pass is tiled: query rows per workgroup, keys per tile and
-// how many workgroups share the keys of a row.
+// How the forward pass runs: narrow (at most 16 query rows per key head, the
+// waves of a workgroup divide the keys) or in tiles of query rows, and how
+// many workgroups share the keys of a row.
 struct AttentionPlan {
-  int rows;      // query rows (of one key head) per workgroup
-  int narrow;    // the workgroup's waves share its rows and divide the keys
+  int narrow;
   int splits;
 };
 AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, bool bf16_storage, int cus);
