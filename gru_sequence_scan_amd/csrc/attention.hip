@@ -229,8 +229,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
   }
 }
 
-// At most 16 query rows (one token, with the heads that share a key head):
-// bound by the reading of K and V, each of which is used once. The waves
+// 16 query rows a workgroup (one token, with the heads that share a key head;
+// or a few tiles of them where wider ones would leave compute units idle):
+// for one tile bound by the reading of K and V, each used once. The waves
 // divide the keys, 32 at a time, and never wait for each other before the
 // end: keys go from memory straight into fragments, values through a wave's
 // own piece of LDS, which turns them. A step's keys are loaded as soon as the
@@ -251,9 +252,10 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
   extern __shared__ __align__(16) char smem[];
 
   const QRows rows{a.Tq * (a.heads / a.kv_heads), a.heads / a.kv_heads};
-  const Work w = work_of(a, a.splits);
-  if (w.tile >= a.splits) return;
-  const int bh = w.bh, split = w.tile;
+  const int tiles_all = (rows.M + 15) / 16 * a.splits;
+  const Work w = work_of(a, tiles_all);
+  if (w.tile >= tiles_all) return;
+  const int bh = w.bh, split = w.tile % a.splits, m0 = w.tile / a.splits * 16;
   const int b = bh / a.kv_heads, hk = bh % a.kv_heads;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
   const bool vec = a.vec != 0;
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
     const DT* qb = (const DT*)a.q + b * a.q_b + (int64_t)hk * rows.G * a.q_h;
 #pragma unroll
     for (int c = 0; c < kC; ++c)
-      q[c] = i16 < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, i16), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+      q[c] = m0 + i16 < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m0 + i16), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
   }
   const float sl = base2_scale<DT, kC>(a.scale, q);
   f32x4 o[kDT];
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
   if (g == 0) jm[2 * r] = mx, jm[2 * r + 1] = sum;
   __syncthreads();
   const int m = threadIdx.x / (DP / 4), col = threadIdx.x % (DP / 4) * 4;
-  if (m >= 16 || m >= rows.M) return;
+  if (m >= 16 || m0 + m >= rows.M) return;
   float top = kLowest;
 #pragma unroll
   for (int x = 0; x < kWaves; ++x) top = __builtin_fmaxf(top, jm[2 * (x * 16 + m)]);
@@ -355,7 +357,7 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
     total += f * jm[2 * rr + 1];
     acc += f * *reinterpret_cast<const f32x4*>(jo + rr * kLdO + col);
   }
-  write_part<DT, FAST>(a, rows, bh, split, m, L, col, top, total, acc);
+  write_part<DT, FAST>(a, rows, bh, split, m0 + m, L, col, top, total, acc);
 }
 
 // Joins the splits' partial results of one query row: a thread per split for
@@ -421,7 +423,7 @@ hipError_t run(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
     const auto kernel = fast ? attention_step_kernel<DT, DP, true> : attention_step_kernel<DT, DP, false>;
     const hipError_t e = allow_lds(kernel, StepShape<DT, DP>::kBytes);
     if (e != hipSuccess) return e;
-    launch_kernel(kernel, dim3((unsigned)work_grid(a, a.splits)), dim3(kStepThreads), StepShape<DT, DP>::kBytes, st, a);
+    launch_kernel(kernel, dim3((unsigned)work_grid(a, (M + 15) / 16 * a.splits)), dim3(kStepThreads), StepShape<DT, DP>::kBytes, st, a);
   } else {
     const auto kernel = fast ? attention_kernel<DT, DP, QT, KT, true> : attention_kernel<DT, DP, QT, KT, false>;
     const hipError_t e = allow_lds(kernel, S::kBytes);
@@ -447,11 +449,18 @@ hipError_t run_t(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st)
 AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, bool bf, int cus) {
   const int64_t M = (int64_t)Tq * (heads / kv_heads);
   AttentionPlan p{};
-  p.narrow = M <= 16;
-  const int rows = p.narrow ? 16 : bf ? 128 : 64;
+  const int wide = bf ? 128 : 64;
+  const int64_t heads_all = (int64_t)B * kv_heads;
+  // Narrow also while its workgroups are at most two a compute unit and walk
+  // few steps (us, narrow / wide tiles: 500 queries, 500 keys, 16 heads of 64,
+  // bf16, 512 narrow workgroups: 9.9 / 21.8, fp32 23.7 / 29.3; 80 queries, 128
+  // heads, 640 workgroups, fp32: 44.5 / 33.8; 300 queries, 4000 keys, 8 heads
+  // of 128, bf16: 42.6 / 28.8).
+  p.narrow = M <= 16 || ((M + 15) / 16 * heads_all <= 2ll * cus && Tk <= 4 * kStepKeys * kStepThreads / 64);
+  const int rows = p.narrow ? 16 : wide;
   // A split of the keys keeps two tiles (narrow: a step of every wave) or more.
   const int keys = p.narrow ? kStepKeys * kStepThreads / 64 : bf ? 128 : 64;
-  const int64_t groups = (M + rows - 1) / rows * B * kv_heads;
+  const int64_t groups = (M + rows - 1) / rows * heads_all;
   // Split while there are fewer workgroups than compute units.
   int64_t want = cus / groups;
   if (want > Tk / keys) want = Tk / keys;

@@ -70,7 +70,7 @@ int validate(const RnnNormDesc* d) {
 }
 
 size_t norm_workspace(const RnnNormDesc* d) {
-  return (size_t)norm_backward_blocks(d->rows, d->N, kPlanCus) * 2 * (size_t)d->N * sizeof(float);
+  return (size_t)norm_backward_blocks(d->rows, d->N, kPlanCus) * 2 * (size_t)((d->N + 3) / 4 * 4) * sizeof(float);
 }
 
 // ---------------------------------------------------------------------------
@@ -292,6 +292,7 @@ int rnn_layer_norm_backward(const RnnNormDesc* desc, const void* s, const void* 
   a.x = s; a.ldx = desc->x_ld; a.w = weight; a.stats = const_cast<float*>(stats);
   a.dy = dy; a.ds = dsum; a.dx = dx; a.dw = dweight; a.db = dbias;
   a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.ld_part = (desc->N + 3) / 4 * 4;
   a.blocks = norm_backward_blocks(desc->rows, desc->N, kPlanCus);
   a.vec = a.N % 8 == 0 && a.ldx % (16 / (int64_t)e) == 0 && aligned(s, 16) && aligned(weight, 16) && aligned(dy, 16) &&
           aligned(dsum, 16) && aligned(dx, 16);

@@ -49,7 +49,7 @@ struct NormArgs {
   // backward (x = the tensor that was normalised)
   const void* dy; const void* ds;   // [rows, N]; ds may be null
   void* dx; float* dw; float* db;   // dw, db may be null
-  float* part;                      // [blocks, 2, N]
+  float* part; int64_t ld_part;     // [blocks, 2, ld_part], ld_part = N rounded up to 4
   int blocks;
   int vec;                          // rows take 8-element accesses
 };

@@ -18,8 +18,8 @@
 namespace rnnk {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kE = 8;  // elements per thread and chunk
+constexpr int threads_of(int team) { return team < 256 ? 256 : team; }
 
 // A row is spread over TEAM threads (a part of a wave, a wave, or the whole
 // workgroup) in V chunks of kE elements a thread. With 16-byte accesses a
@@ -97,8 +97,9 @@ __device__ __forceinline__ float team_sum(float v, float* lds) {
 }
 
 template <typename DT, int TEAM, int V, bool VEC, bool RES>
-__global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
-  __shared__ float lds[4];
+__global__ __launch_bounds__(threads_of(TEAM)) void norm_forward_kernel(NormArgs a) {
+  constexpr int kThreads = threads_of(TEAM);
+  __shared__ float lds[kThreads / 64];
   const int lane = threadIdx.x % TEAM;
   const int64_t row = blockIdx.x * (int64_t)(kThreads / TEAM) + threadIdx.x / TEAM;
   if (row >= a.rows) return;  // whole teams
@@ -157,13 +158,40 @@ __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
   store_row<DT, TEAM, V, VEC>((DT*)a.y + row * a.N, a.N, lane, s);
 }
 
+// A row as it lies in memory, so that the next row's loads can be in flight
+// while one is worked on. Columns past the row repeat its last ones (no load
+// is conditional) and count as zero when they are taken out.
+template <typename DT, int TEAM, int V, bool VEC>
+struct RawRow {
+  struct alignas(VEC ? 16 : sizeof(DT)) Piece { DT v[kE]; };
+  Piece p[V];
+  __device__ __forceinline__ void load(const DT* row, int N, int lane) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (VEC) {
+        const int c = col_of<TEAM, true>(v, 0, lane);
+        p[v] = *reinterpret_cast<const Piece*>(row + (c < N ? c : N - kE));
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const int c = col_of<TEAM, false>(v, e, lane);
+          p[v].v[e] = row[c < N ? c : N - 1];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int v, int e, int N, int lane) const {
+    return col_of<TEAM, VEC>(v, VEC ? 0 : e, lane) < N ? to_f32<DT>(p[v].v[e]) : 0.f;
+  }
+};
+
 // Rows are dealt to the teams in turn; a thread sums dw and db of its own
 // columns in registers over its rows, and the workgroup's teams join them in
-// LDS into one row of partial sums.
-template <typename DT, int TEAM, int V, bool VEC>
-__global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
-  constexpr int kTeams = kThreads / TEAM;
-  __shared__ float lds[4];
+// LDS into one row of partial sums. DS: a gradient of the sum is added.
+template <typename DT, int TEAM, int V, bool VEC, bool DS>
+__global__ __launch_bounds__(threads_of(TEAM)) void norm_backward_kernel(NormArgs a) {
+  constexpr int kThreads = threads_of(TEAM), kTeams = kThreads / TEAM;
+  __shared__ float lds[kThreads / 64];
   __shared__ float join[kTeams > 1 ? kThreads * kE : 1];
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
   float w[V][kE], dw[V][kE], db[V][kE];
@@ -173,37 +201,50 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
     for (int e = 0; e < kE; ++e) w[v][e] = 1.f, dw[v][e] = 0.f, db[v][e] = 0.f;
   if (a.w) load_row<DT, TEAM, V, VEC>((const DT*)a.w, a.N, lane, w);
   const float inv = 1.0f / (float)a.N;
-  for (int64_t row = blockIdx.x * (int64_t)kTeams + team; row < a.rows; row += (int64_t)gridDim.x * kTeams) {
-    float n[V][kE], g[V][kE];
-    load_row<DT, TEAM, V, VEC>((const DT*)a.x + row * a.ldx, a.N, lane, n);
-    load_row<DT, TEAM, V, VEC>((const DT*)a.dy + row * a.N, a.N, lane, g);
-    const float mu = a.stats[2 * row], rstd = a.stats[2 * row + 1];
+  // the next row's loads in flight, where there are registers for them
+  constexpr bool kAhead = V <= 2;
+  RawRow<DT, TEAM, V, VEC> rx, rdy, rds;
+  float mu = 0.f, rstd = 0.f;
+  auto load = [&](int64_t row) {
+    rx.load((const DT*)a.x + row * a.ldx, a.N, lane);
+    rdy.load((const DT*)a.dy + row * a.N, a.N, lane);
+    if (DS && kAhead) rds.load((const DT*)a.ds + row * a.N, a.N, lane);
+    mu = a.stats[2 * row];
+    rstd = a.stats[2 * row + 1];
+  };
+  const int64_t hop = (int64_t)gridDim.x * kTeams;
+  int64_t row = blockIdx.x * (int64_t)kTeams + team;
+  if (kAhead && row < a.rows) load(row);
+  for (; row < a.rows; row += hop) {
+    if (!kAhead) load(row);
+    float n[V][kE], g[V][kE], s[DS && kAhead ? V : 1][kE];
     float s1 = 0.f, s2 = 0.f;
+    const float scale = rstd;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
         // past the row g is zero, and n times it
-        n[v][e] = (n[v][e] - mu) * rstd;
+        n[v][e] = (rx.get(v, e, a.N, lane) - mu) * rstd;
+        g[v][e] = rdy.get(v, e, a.N, lane);
+        if (DS && kAhead) s[DS && kAhead ? v : 0][e] = to_f32<DT>(rds.p[v].v[e]);
         db[v][e] += g[v][e];
         dw[v][e] = __builtin_fmaf(g[v][e], n[v][e], dw[v][e]);
         g[v][e] *= w[v][e];
         s1 += g[v][e];
         s2 = __builtin_fmaf(g[v][e], n[v][e], s2);
       }
+    if (kAhead && row + hop < a.rows) load(row + hop);
+    if (DS && !kAhead) rds.load((const DT*)a.ds + row * a.N, a.N, lane);
     s1 = team_sum<TEAM>(s1, lds) * inv;
     s2 = team_sum<TEAM>(s2, lds) * inv;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int e = 0; e < kE; ++e) g[v][e] = rstd * (g[v][e] - s1 - n[v][e] * s2);
-    if (a.ds) {
-      load_row<DT, TEAM, V, VEC>((const DT*)a.ds + row * a.N, a.N, lane, n);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) g[v][e] += n[v][e];
-    }
+      for (int e = 0; e < kE; ++e) {
+        g[v][e] = scale * (g[v][e] - s1 - n[v][e] * s2);
+        if (DS) g[v][e] += kAhead ? s[DS && kAhead ? v : 0][e] : to_f32<DT>(rds.p[v].v[e]);
+      }
     store_row<DT, TEAM, V, VEC>((DT*)a.dx + row * a.N, a.N, lane, g);
   }
   if (!a.part) return;
@@ -211,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
   for (int v = 0; v < V; ++v) {
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      float* dst = a.part + ((int64_t)blockIdx.x * 2 + which) * a.N;
+      float* dst = a.part + ((int64_t)blockIdx.x * 2 + which) * a.ld_part;
       if (kTeams > 1) {
         __syncthreads();
 #pragma unroll
@@ -236,26 +277,38 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
   }
 }
 
-// dw and db from the workgroups' partial sums: 64 columns of one of the two
-// per workgroup, its four waves taking every fourth partial row.
-__global__ __launch_bounds__(kThreads) void norm_reduce_kernel(const float* __restrict__ part, int blocks, int N,
-                                                               float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float lds[kThreads];
-  const int which = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6;
-  float t = 0.f;
+// dw and db from the workgroups' partial sums: a workgroup takes 64 columns
+// of one of the two, 16 threads across (four columns each) by 64 along the
+// partial rows, whose sums then meet in LDS.
+constexpr int kReduceThreads = 1024;
+__global__ __launch_bounds__(kReduceThreads) void norm_reduce_kernel(const float* __restrict__ part, int blocks, int N,
+                                                                     int64_t ld, float* __restrict__ dw,
+                                                                     float* __restrict__ db) {
+  __shared__ f32x4 lds[kReduceThreads];
+  const int which = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 15) * 4, along = threadIdx.x >> 4;
+  f32x4 t = {0.f, 0.f, 0.f, 0.f};
   if (c < N) {
-#pragma unroll 8
-    for (int k = wave; k < blocks; k += 4) t += part[((int64_t)k * 2 + which) * N + c];
+#pragma unroll 16
+    for (int k = along; k < blocks; k += 64) t += *reinterpret_cast<const f32x4*>(part + ((int64_t)k * 2 + which) * ld + c);
   }
   lds[threadIdx.x] = t;
   __syncthreads();
+#pragma unroll
+  for (int half = 32; half > 0; half >>= 1) {
+    if (along < half) lds[threadIdx.x] = t = t + lds[threadIdx.x + half * 16];
+    __syncthreads();
+  }
   float* out = which ? db : dw;
-  if (wave == 0 && c < N && out) out[c] = (lds[threadIdx.x] + lds[threadIdx.x + 64]) + (lds[threadIdx.x + 128] + lds[threadIdx.x + 192]);
+  if (along == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < N) out[c + j] = t[j];
+  }
 }
 
 template <typename DT, int TEAM, int V, bool VEC>
 void run_forward(const NormArgs& a, hipStream_t st) {
-  constexpr int kTeams = kThreads / TEAM;
+  constexpr int kThreads = threads_of(TEAM), kTeams = kThreads / TEAM;
   const dim3 grid((unsigned)((a.rows + kTeams - 1) / kTeams)), block(kThreads);
   if (a.r)
     launch_kernel(norm_forward_kernel<DT, TEAM, V, VEC, true>, grid, block, 0, st, a);
@@ -265,11 +318,14 @@ void run_forward(const NormArgs& a, hipStream_t st) {
 
 template <typename DT, int TEAM, int V, bool VEC>
 void run_backward(const NormArgs& a, hipStream_t st) {
-  launch_kernel(norm_backward_kernel<DT, TEAM, V, VEC>, dim3((unsigned)a.blocks), dim3(kThreads), 0, st, a);
+  launch_kernel(a.ds ? norm_backward_kernel<DT, TEAM, V, VEC, true> : norm_backward_kernel<DT, TEAM, V, VEC, false>,
+                dim3((unsigned)a.blocks), dim3(threads_of(TEAM)), 0, st, a);
 }
 
-// The team of a row: 16 threads up to 128 elements, a wave up to 2048, the
-// whole workgroup beyond.
+// The team of a row: as few threads as hold it in 8 or 16 elements each (the
+// backward pass keeps about ten registers an element: with 32 it would spill).
+// 16 threads up to 128 elements, a wave up to 1024, then a workgroup of 256
+// or 512.
 template <typename DT, bool VEC, bool BACK>
 void pick(const NormArgs& a, hipStream_t st) {
 #define NORM_RUN(TEAM, V) return BACK ? run_backward<DT, TEAM, V, VEC>(a, st) : run_forward<DT, TEAM, V, VEC>(a, st)
@@ -277,19 +333,19 @@ void pick(const NormArgs& a, hipStream_t st) {
   if (N <= 128) NORM_RUN(16, 1);
   if (N <= 512) NORM_RUN(64, 1);
   if (N <= 1024) NORM_RUN(64, 2);
-  if (N <= 2048) NORM_RUN(64, 4);
+  if (N <= 2048) NORM_RUN(256, 1);
   if (N <= 4096) NORM_RUN(256, 2);
-  if (N <= 8192) NORM_RUN(256, 4);
-  NORM_RUN(256, 8);
+  if (N <= 8192) NORM_RUN(512, 2);
+  NORM_RUN(512, 4);
 #undef NORM_RUN
 }
 
 }  // namespace
 
 int norm_backward_blocks(int64_t rows, int N, int cus) {
-  const int teams = N <= 128 ? kThreads / 16 : N <= 2048 ? kThreads / 64 : 1;
-  const int64_t need = (rows + teams - 1) / teams;
-  const int64_t most = 4ll * cus;
+  // about 1024 threads a compute unit
+  const int teams = N <= 128 ? 16 : N <= 1024 ? 4 : 1, each = N <= 4096 ? 4 : N <= 8192 ? 2 : 1;
+  const int64_t need = (rows + teams - 1) / teams, most = (int64_t)each * cus;
   return (int)(need < most ? need : most);
 }
 
@@ -307,8 +363,8 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, bool bf, hipStream_t st
   else
     a.vec ? pick<float, true, true>(a, st) : pick<float, false, true>(a, st);
   if (a.part)
-    launch_kernel(norm_reduce_kernel, dim3((a.N + 63) / 64, 2), dim3(kThreads), 0, st, (const float*)a.part, a.blocks, a.N,
-                  a.dw, a.db);
+    launch_kernel(norm_reduce_kernel, dim3((a.N + 63) / 64, 2), dim3(kReduceThreads), 0, st, (const float*)a.part, a.blocks,
+                  a.N, a.ld_part, a.dw, a.db);
   return hipGetLastError();
 }
 
