@@ -97,6 +97,22 @@ __device__ __forceinline__ void softmax_step(f32x4 (&s)[KT], float sl, float* mx
   *sum += part;  // this lane's keys; the four lanes of a row are joined at the end
 }
 
+// Four elements of o and, in training, what their rounding leaves: delta in
+// the backward pass is a sum over o that is taken from values of its own
+// size, where the error of a rounded o would show.
+template <typename DT, bool FAST>
+__device__ __forceinline__ void write_o(const AttentionArgs& a, int64_t at, int col, const f32x4& o) {
+  store4<DT, FAST>((DT*)a.o + at, col, a.D, a.vec != 0, o);
+  if constexpr (sizeof(DT) == 2) {
+    if (a.o_rest) {
+      f32x4 rest;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rest[j] = o[j] - (float)(bf16)o[j];
+      store4<DT, FAST>((DT*)a.o_rest + at, col, a.D, a.vec != 0, rest);
+    }
+  }
+}
+
 // Four elements of a query row's result (mx in base-2 units, sum over all
 // lanes), or of its part where the keys are split.
 template <typename DT, bool FAST>
@@ -109,11 +125,13 @@ __device__ __forceinline__ void write_part(const AttentionArgs& a, const QRows& 
     return;
   }
   const float inv = sum > 0.f ? 1.0f / sum : (L > 0 ? __builtin_nanf("") : 0.f);
-  store4<DT, FAST>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), col, a.D, a.vec != 0, o * inv);
+  write_o<DT, FAST>(a, rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), col, o * inv);
   if (a.lse && col == 0) a.lse[(int64_t)bh * rows.M + m] = mx + __builtin_amdgcn_logf(sum);
 }
 
-template <typename DT, int DP, int QT, int KT, bool FAST>
+// TRAIN: p enters the product as its rounded value and the rest, so that o is
+// exact beyond its rounding.
+template <typename DT, int DP, int QT, int KT, bool FAST, bool TRAIN>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArgs a) {
   using S = Shape<DT, DP, QT, KT>;
   static_assert(KT % 2 == 0, "pairs of key tiles make a fragment");
@@ -175,6 +193,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
     }
     __builtin_amdgcn_sched_barrier(0);
     f32x4 s[QT][KT];
+    // the wave whose products are ready goes first: the other's exponentials
+    // fill in (2 to 4% at 1000 to 2048 keys)
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int n = 0; n < KT; ++n) {
 #pragma unroll
@@ -186,6 +207,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
         for (int t = 0; t < QT; ++t) s[t][n] = mma(kf, q[t][c], s[t][n]);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if (k0 + S::kKeys > L) {
 #pragma unroll
       for (int n = 0; n < KT; ++n)
@@ -202,14 +224,21 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
     // the relative size of o's own); its sum keeps 32 bits
 #pragma unroll
     for (int n = 0; n < KT; n += 2) {
-      Frag<DT> p[QT];
+      constexpr bool kRest = TRAIN && sizeof(DT) == 2;
+      Frag<DT> p[QT], rest[QT];
 #pragma unroll
-      for (int t = 0; t < QT; ++t) p[t] = stack<DT>(s[t][n], s[t][n + 1]);
+      for (int t = 0; t < QT; ++t) {
+        p[t] = stack<DT>(s[t][n], s[t][n + 1]);
+        if constexpr (kRest) rest[t] = stack_rest(s[t][n], s[t][n + 1], p[t]);
+      }
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         const Frag<DT> vf = read_cols<DT>(cv, S::kLdV, n * 16, 16 * d, lane);
 #pragma unroll
-        for (int t = 0; t < QT; ++t) o[t][d] = mma(vf, p[t], o[t][d]);
+        for (int t = 0; t < QT; ++t) {
+          o[t][d] = mma(vf, p[t], o[t][d]);
+          if constexpr (kRest) o[t][d] = mma(vf, rest[t], o[t][d]);
+        }
       }
     }
     if (tile + 1 < last) {
@@ -326,8 +355,14 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
     load_v(k0 + kWaves * kStepKeys);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const Frag<DT> p = stack<DT>(s[0], s[1]);
+    Frag<DT> rest;
+    if constexpr (sizeof(DT) == 2) rest = stack_rest(s[0], s[1], p);  // p is not rounded here: the products are not what takes time
 #pragma unroll
-    for (int d = 0; d < kDT; ++d) o[d] = mma(read_cols<DT>(lv, kLdV, 0, 16 * d, lane), p, o[d]);
+    for (int d = 0; d < kDT; ++d) {
+      const Frag<DT> vf = read_cols<DT>(lv, kLdV, 0, 16 * d, lane);
+      o[d] = mma(vf, p, o[d]);
+      if constexpr (sizeof(DT) == 2) o[d] = mma(vf, rest, o[d]);
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   sum = col_sum(sum);
@@ -409,7 +444,7 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttentionA
   for (int k = 1; k < 8; ++k) acc += lds[k * 32 + threadIdx.x];
   sum = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
   const float inv = sum > 0.f ? 1.0f / sum : (key_count(a, bh / a.kv_heads) > 0 ? __builtin_nanf("") : 0.f);
-  store4<DT, false>((DT*)a.o + rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), c, a.D, a.vec != 0, acc * inv);
+  write_o<DT, false>(a, rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), c, acc * inv);
   if (a.lse && threadIdx.x == 0) a.lse[r] = top + __builtin_amdgcn_logf(sum);
 }
 
@@ -425,7 +460,9 @@ hipError_t run(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
     if (e != hipSuccess) return e;
     launch_kernel(kernel, dim3((unsigned)work_grid(a, (M + 15) / 16 * a.splits)), dim3(kStepThreads), StepShape<DT, DP>::kBytes, st, a);
   } else {
-    const auto kernel = fast ? attention_kernel<DT, DP, QT, KT, true> : attention_kernel<DT, DP, QT, KT, false>;
+    constexpr bool kBf = sizeof(DT) == 2;
+    const auto kernel = a.lse && kBf ? (fast ? attention_kernel<DT, DP, QT, KT, true, kBf> : attention_kernel<DT, DP, QT, KT, false, kBf>)
+                                     : (fast ? attention_kernel<DT, DP, QT, KT, true, false> : attention_kernel<DT, DP, QT, KT, false, false>);
     const hipError_t e = allow_lds(kernel, S::kBytes);
     if (e != hipSuccess) return e;
     launch_kernel(kernel, dim3((unsigned)work_grid(a, (M + S::kRows - 1) / S::kRows * a.splits)), dim3(kAttnThreads),

@@ -51,6 +51,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
         const Frag<DT> o = load8<DT, FAST>((const DT*)a.o + at, col, a.D, vec);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(o.get(j), dO[t][c].get(j), dot);
+        if (sizeof(DT) == 2) {
+          const Frag<DT> rest = load8<DT, FAST>((const DT*)a.o_rest + at, col, a.D, vec);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(rest.get(j), dO[t][c].get(j), dot);
+        }
       }
     }
     delta[t] = col_sum(dot);
@@ -111,17 +116,24 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
             for (int t = 0; t < QT; ++t) s[t][n][j] = 0.f;
           }
     }
-    // ds is rounded to the storage type for the product (see the forward's p)
+    // ds enters the product as its rounded value and the rest: the rounding
+    // errors of a long row's ds would add up against a sum that cancels
 #pragma unroll
     for (int n = 0; n < KT; n += 2) {
-      Frag<DT> ds[QT];
+      Frag<DT> ds[QT], rest[QT];
 #pragma unroll
-      for (int t = 0; t < QT; ++t) ds[t] = stack<DT>(s[t][n], s[t][n + 1]);
+      for (int t = 0; t < QT; ++t) {
+        ds[t] = stack<DT>(s[t][n], s[t][n + 1]);
+        if constexpr (sizeof(DT) == 2) rest[t] = stack_rest(s[t][n], s[t][n + 1], ds[t]);
+      }
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         const Frag<DT> kf = read_cols<DT>(lk, kLdK, n * 16, 16 * d, lane);
 #pragma unroll
-        for (int t = 0; t < QT; ++t) dq[t][d] = mma(kf, ds[t], dq[t][d]);
+        for (int t = 0; t < QT; ++t) {
+          dq[t][d] = mma(kf, ds[t], dq[t][d]);
+          if constexpr (sizeof(DT) == 2) dq[t][d] = mma(kf, rest[t], dq[t][d]);
+        }
       }
     }
     if (more) {

@@ -123,6 +123,17 @@ __device__ __forceinline__ Frag<DT> stack(const f32x4& a, const f32x4& b) {
   return f;
 }
 
+// What the rounding of stack() leaves.
+__device__ __forceinline__ Frag<bf16> stack_rest(const f32x4& a, const f32x4& b, const Frag<bf16>& f) {
+  Frag<bf16> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r.set(j, a[j] - f.get(j));
+    r.set(4 + j, b[j] - f.get(4 + j));
+  }
+  return r;
+}
+
 // Max and sum over the four lanes that hold a column (l % 16 alike): the
 // swaps hand every lane its own value and the one 16 or 32 lanes away.
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
@@ -367,9 +378,14 @@ struct Work {
   int bh, tile;  // tile < tiles, or the workgroup has none
 };
 constexpr int kParts = 4;
-inline __host__ __device__ int part_count(int tiles) { return tiles < kParts ? tiles : kParts; }
+// With 16 (row, key head)s an XCD the rows' lengths even out by themselves,
+// and a row's tiles stay together.
+inline __host__ __device__ int part_count(const AttentionArgs& a, int tiles) {
+  if (a.B * a.kv_heads >= 16 * a.xcds) return 1;
+  return tiles < kParts ? tiles : kParts;
+}
 __device__ __forceinline__ Work work_of(const AttentionArgs& a, int tiles) {
-  const int parts = part_count(tiles), each = (tiles + parts - 1) / parts;
+  const int parts = part_count(a, tiles), each = (tiles + parts - 1) / parts;
   const int xcd = blockIdx.x % a.xcds, slot = blockIdx.x / a.xcds;
   const int unit = slot / each * a.xcds + xcd, within = slot % each;
   Work w;
@@ -379,7 +395,7 @@ __device__ __forceinline__ Work work_of(const AttentionArgs& a, int tiles) {
   return w;
 }
 inline int64_t work_grid(const AttentionArgs& a, int64_t tiles) {
-  const int parts = part_count((int)tiles);
+  const int parts = part_count(a, (int)tiles);
   const int64_t each = (tiles + parts - 1) / parts, units = (int64_t)a.B * a.kv_heads * parts;
   return (units + a.xcds - 1) / a.xcds * a.xcds * each;
 }

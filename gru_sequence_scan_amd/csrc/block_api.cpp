@@ -181,6 +181,17 @@ size_t attention_stat_bytes(const RnnAttentionDesc* d) {
   return (size_t)d->B * d->kv_heads * (size_t)query_rows(d) * sizeof(float);
 }
 
+// The reserve: the log-sum-exp and, in bf16, what the rounding of o left.
+size_t attention_reserve(const RnnAttentionDesc* d) {
+  const size_t stat = (attention_stat_bytes(d) + 15) / 16 * 16;
+  return d->dtype == RNN_DTYPE_BF16 ? stat + (size_t)d->Tq * d->B * d->heads * d->D * 2 : stat;
+}
+
+void* attention_rest(const RnnAttentionDesc* d, void* reserve) {
+  if (!reserve || d->dtype != RNN_DTYPE_BF16) return nullptr;
+  return static_cast<char*>(reserve) + (attention_stat_bytes(d) + 15) / 16 * 16;
+}
+
 size_t attention_workspace(const RnnAttentionDesc* d) {
   const size_t n = (size_t)plan_of(d).splits;
   return n > 1 ? n * (attention_stat_bytes(d) * ((size_t)d->D + 2) + 16) : 0;
@@ -229,6 +240,7 @@ int attention_forward(const RnnAttentionDesc* d, const RnnAttentionIO* io, void*
     a.part_ml = a.part_o + (size_t)p.splits * (attention_stat_bytes(d) / sizeof(float)) * d->D;
   }
   a.lse = static_cast<float*>(reserve);
+  a.o_rest = attention_rest(d, reserve);
   return hip_status(launch_attention(a, p, d->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -363,12 +375,15 @@ int rnn_cross_attention_workspace_bytes(const RnnAttentionDesc* desc, size_t* by
 int rnn_cross_attention_reserve_bytes(const RnnAttentionDesc* desc, size_t* bytes) {
   RETURN_IF_BAD(validate(desc));
   if (!bytes) return RNN_E_NULL;
-  *bytes = attention_stat_bytes(desc);
+  *bytes = attention_reserve(desc);
   return RNN_OK;
 }
 
 int rnn_cross_attention_backward_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes) {
-  return rnn_cross_attention_reserve_bytes(desc, bytes);  // delta, one value per query row
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = attention_stat_bytes(desc);  // delta, one value per query row
+  return RNN_OK;
 }
 
 int rnn_cross_attention(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* workspace, size_t ws_bytes,
@@ -382,7 +397,7 @@ int rnn_cross_attention_train(const RnnAttentionDesc* desc, const RnnAttentionIO
                               void* workspace, size_t ws_bytes, void* stream) {
   Range range("rnn_cross_attention_train");
   RETURN_IF_BAD(validate(desc));
-  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_stat_bytes(desc)));
+  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_reserve(desc)));
   return attention_forward(desc, io, reserve, workspace, ws_bytes, stream);
 }
 
@@ -399,11 +414,12 @@ int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentio
     RETURN_IF_BAD(need(p, e));
     if (!aligned(p, 16)) a.vec = 0;
   }
-  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_stat_bytes(desc)));
+  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, attention_reserve(desc)));
   RETURN_IF_BAD(need_memory(workspace, ws_bytes, attention_stat_bytes(desc)));
   int xcds;
   RETURN_IF_BAD(on_device(&xcds));
   a.lse = const_cast<float*>(static_cast<const float*>(reserve));
+  a.o_rest = attention_rest(desc, const_cast<void*>(reserve));
   a.delta = static_cast<float*>(workspace);
   a.xcds = xcds;
   a.d_o = grads->d_o; a.dq = grads->dq; a.dk = grads->dk; a.dv = grads->dv;

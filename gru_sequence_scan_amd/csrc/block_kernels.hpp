@@ -68,7 +68,8 @@ struct AttentionArgs {
   const void* v; int64_t v_t, v_b, v_h;
   const int* lengths;               // device [B] or null
   void* o;                          // [Tq, B, heads, D]
-  float* lse;                       // [B, kv_heads, Tq * G] base-2 log-sum-exp, or null
+  float* lse;                       // training: [B, kv_heads, Tq * G] base-2 log-sum-exp; else null
+  void* o_rest;                     // training in bf16: like o, what its rounding left; else null
   int vec;                          // rows take 16-byte accesses
   int near;                         // offsets inside a (batch row, key head) of q, do and of 256 keys fit 31 bits
   int xcds;                         // XCDs of the device

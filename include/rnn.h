@@ -568,7 +568,8 @@ typedef struct RnnAttentionGrads {
 
 int rnn_cross_attention_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes);
 /* The reserve between the passes: the fp32 log-sum-exp of every query's
- * scores. */
+ * scores and, in bf16, what the rounding of o left (its gradient needs o more
+ * exactly than it is stored). */
 int rnn_cross_attention_reserve_bytes(const RnnAttentionDesc* desc, size_t* bytes);
 int rnn_cross_attention_backward_workspace_bytes(const RnnAttentionDesc* desc, size_t* bytes);
 int rnn_cross_attention(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* workspace, size_t ws_bytes,

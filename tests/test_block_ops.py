@@ -244,9 +244,12 @@ def test_attention_desc(kw, expect):
     for fn in ("rnn_cross_attention_workspace_bytes", "rnn_cross_attention_reserve_bytes",
                "rnn_cross_attention_backward_workspace_bytes"):
         assert getattr(ops._lib(), fn)(ctypes.byref(_attend(**kw)), ctypes.byref(n)) == expect
-    if expect == OK:   # one fp32 value per query row
+    if expect == OK:   # one fp32 value per query row; the reserve has o's rest too in bf16
         d = _attend(**kw)
-        assert n.value == d.B * d.heads * d.Tq * 4
+        rows = d.B * d.heads * d.Tq
+        assert n.value == rows * 4
+        assert ops._lib().rnn_cross_attention_reserve_bytes(ctypes.byref(d), ctypes.byref(n)) == OK
+        assert n.value == rows * 4 + (rows * d.D * 2 if d.dtype == 1 else 0)
 
 
 def test_attention_split_workspace():
