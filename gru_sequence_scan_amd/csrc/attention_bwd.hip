@@ -166,7 +166,7 @@ struct KvShape {
   static constexpr int kBytes = 2 * kTile * (int)sizeof(DT) > kJoin ? 2 * kTile * (int)sizeof(DT) : kJoin;
 };
 
-template <typename DT, int DP, int KT, int WM, int MT, bool FAST>
+template <typename DT, int DP, int KT, int WM, int MT, bool FAST, bool REST>
 __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
   using S = KvShape<DT, DP, KT, WM, MT>;
   constexpr int kC = DP / 32, kDT = DP / 16, kKeys = S::kKeys, kRows = S::kRows, kLd = S::kLd;
@@ -265,11 +265,15 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : 1) void attenti
               dp[h][n][j] = p * (dp[h][n][j] - de[j]);
             }
         }
-        Frag<DT> p[KT], ds[KT];
+        Frag<DT> p[KT], ds[KT], p_rest[KT], ds_rest[KT];
 #pragma unroll
         for (int n = 0; n < KT; ++n) {
           p[n] = stack<DT>(s[0][n], s[1][n]);
           ds[n] = stack<DT>(dp[0][n], dp[1][n]);
+          if constexpr (REST) {
+            p_rest[n] = stack_rest(s[0][n], s[1][n], p[n]);
+            ds_rest[n] = stack_rest(dp[0][n], dp[1][n], ds[n]);
+          }
         }
 #pragma unroll
         for (int d = 0; d < kDT; ++d) {
@@ -279,6 +283,10 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : 1) void attenti
           for (int n = 0; n < KT; ++n) {
             dv[n][d] = mma(of, p[n], dv[n][d]);
             dk[n][d] = mma(qf, ds[n], dk[n][d]);
+            if constexpr (REST) {
+              dv[n][d] = mma(of, p_rest[n], dv[n][d]);
+              dk[n][d] = mma(qf, ds_rest[n], dk[n][d]);
+            }
           }
         }
       }
@@ -343,7 +351,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : 1) void attenti
 // overlap. Measured at 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of
 // 128: 338 us, against 415 with both sums in one wave (one wave a SIMD) and
 // 527 with a launch for each.
-template <typename DT, int DP, int KT, int MT, bool FAST>
+template <typename DT, int DP, int KT, int MT, bool FAST, bool REST>
 __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArgs a) {
   using S = KvShape<DT, DP, KT, 1, MT>;
   constexpr int kC = DP / 32, kDT = DP / 16, kKeys = S::kKeys, kRows = S::kRows, kLd = S::kLd;
@@ -455,14 +463,20 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArg
               for (int j = 0; j < 4; ++j) s[h][n][j] *= dp[n][j] - de[j];
           }
         }
-        Frag<DT> x[KT];
+        Frag<DT> x[KT], rest[KT];
 #pragma unroll
-        for (int n = 0; n < KT; ++n) x[n] = stack<DT>(s[0][n], s[1][n]);
+        for (int n = 0; n < KT; ++n) {
+          x[n] = stack<DT>(s[0][n], s[1][n]);
+          if constexpr (REST) rest[n] = stack_rest(s[0][n], s[1][n], x[n]);
+        }
 #pragma unroll
         for (int d = 0; d < kDT; ++d) {
           const Frag<DT> f = read_cols<DT>(lx, kLd, mt * 16, 16 * d, lane);
 #pragma unroll
-          for (int n = 0; n < KT; ++n) acc[n][d] = mma(f, x[n], acc[n][d]);
+          for (int n = 0; n < KT; ++n) {
+            acc[n][d] = mma(f, x[n], acc[n][d]);
+            if constexpr (REST) acc[n][d] = mma(f, rest[n], acc[n][d]);
+          }
         }
       }
       if (more) put(smem + (turn ^ 1) * S::kTile);
@@ -482,15 +496,38 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArg
   }
 }
 
+// p and ds are rounded to bf16 for the products of dk and dv (one rounding of
+// each value, of the relative size of the gradients' own, so that these come
+// out sqrt(2) times as far off as by their own rounding alone) where the
+// launch fills the device: with the rest of the rounding as a second product
+// dk and dv take 433 us for 346 at 1000 x 1000, 32 ragged rows, 8/2 heads of
+// 128. A launch with fewer workgroups than compute units has the time for it.
+bool keep_rest(const AttentionArgs& a, int64_t tiles) { return tiles * a.B * a.kv_heads <= a.cus; }
+
 template <typename DT, int DP, int KT, int WM, int MT>
 hipError_t run_kv(const AttentionArgs& a, bool fast, hipStream_t st) {
   using S = KvShape<DT, DP, KT, WM, MT>;
-  const auto kernel = fast ? attention_dkv_kernel<DT, DP, KT, WM, MT, true>
-                           : attention_dkv_kernel<DT, DP, KT, WM, MT, false>;
+  constexpr bool kBf = sizeof(DT) == 2;
+  const int64_t tiles = ((int64_t)a.Tk + S::kKeys - 1) / S::kKeys;
+  const bool rest = kBf && keep_rest(a, tiles);
+  const auto kernel = rest ? (fast ? attention_dkv_kernel<DT, DP, KT, WM, MT, true, kBf> : attention_dkv_kernel<DT, DP, KT, WM, MT, false, kBf>)
+                           : (fast ? attention_dkv_kernel<DT, DP, KT, WM, MT, true, false> : attention_dkv_kernel<DT, DP, KT, WM, MT, false, false>);
   const hipError_t e = allow_lds(kernel, S::kBytes);
   if (e != hipSuccess) return e;
-  const int64_t grid = work_grid(a, ((int64_t)a.Tk + S::kKeys - 1) / S::kKeys);
-  launch_kernel(kernel, dim3((unsigned)grid), dim3(kAttnThreads), S::kBytes, st, a);
+  launch_kernel(kernel, dim3((unsigned)work_grid(a, tiles)), dim3(kAttnThreads), S::kBytes, st, a);
+  return hipGetLastError();
+}
+
+template <typename DT, int DP, int KT, int MT>
+hipError_t run_kv_team(const AttentionArgs& a, bool fast, hipStream_t st) {
+  using S = KvShape<DT, DP, KT, 1, MT>;
+  const int64_t tiles = ((int64_t)a.Tk + S::kKeys - 1) / S::kKeys;
+  const bool rest = keep_rest(a, tiles);
+  const auto kernel = rest ? (fast ? attention_dkv_team_kernel<DT, DP, KT, MT, true, true> : attention_dkv_team_kernel<DT, DP, KT, MT, false, true>)
+                           : (fast ? attention_dkv_team_kernel<DT, DP, KT, MT, true, false> : attention_dkv_team_kernel<DT, DP, KT, MT, false, false>);
+  const hipError_t e = allow_lds(kernel, S::kBytes);
+  if (e != hipSuccess) return e;
+  launch_kernel(kernel, dim3((unsigned)work_grid(a, tiles)), dim3(512), S::kBytes, st, a);
   return hipGetLastError();
 }
 
@@ -502,22 +539,15 @@ hipError_t run(const AttentionArgs& a, hipStream_t st) {
   constexpr int kLdsQ = 2 * KT * 16 * (kLdT + kLdR) * (int)sizeof(DT);
   const bool fast = a.vec && a.near && a.D == DP;
   const auto dq = fast ? attention_dq_kernel<DT, DP, QT, KT, true> : attention_dq_kernel<DT, DP, QT, KT, false>;
-  hipError_t e = allow_lds(dq, kLdsQ);
+  const hipError_t e = allow_lds(dq, kLdsQ);
   if (e != hipSuccess) return e;
   launch_kernel(dq, dim3((unsigned)work_grid(a, (M + 64 * QT - 1) / (64 * QT))), dim3(kAttnThreads), kLdsQ, st, a);
-  if constexpr (sizeof(DT) == 4) {
+  if constexpr (sizeof(DT) == 4)
     return run_kv<DT, DP, 1, 1, 2>(a, fast, st);
-  } else if constexpr (DP <= 64) {
+  else if constexpr (DP <= 64)
     return run_kv<DT, DP, 2, 2, 2>(a, fast, st);
-  } else {
-    constexpr int MT = 4;
-    using S = KvShape<DT, DP, 2, 1, MT>;
-    const auto kernel = fast ? attention_dkv_team_kernel<DT, DP, 2, MT, true> : attention_dkv_team_kernel<DT, DP, 2, MT, false>;
-    e = allow_lds(kernel, S::kBytes);
-    if (e != hipSuccess) return e;
-    launch_kernel(kernel, dim3((unsigned)work_grid(a, ((int64_t)a.Tk + S::kKeys - 1) / S::kKeys)), dim3(512), S::kBytes, st, a);
-    return hipGetLastError();
-  }
+  else
+    return run_kv_team<DT, DP, 2, 4>(a, fast, st);
 }
 
 template <typename DT>

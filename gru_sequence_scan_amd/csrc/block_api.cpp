@@ -422,6 +422,7 @@ int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentio
   a.o_rest = attention_rest(desc, const_cast<void*>(reserve));
   a.delta = static_cast<float*>(workspace);
   a.xcds = xcds;
+  a.cus = kPlanCus;
   a.d_o = grads->d_o; a.dq = grads->dq; a.dk = grads->dk; a.dv = grads->dv;
   return hip_status(launch_attention_backward(a, desc->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }

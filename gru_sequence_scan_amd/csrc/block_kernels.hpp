@@ -72,7 +72,7 @@ struct AttentionArgs {
   void* o_rest;                     // training in bf16: like o, what its rounding left; else null
   int vec;                          // rows take 16-byte accesses
   int near;                         // offsets inside a (batch row, key head) of q, do and of 256 keys fit 31 bits
-  int xcds;                         // XCDs of the device
+  int xcds, cus;                    // of the device
   // split of the keys over workgroups (forward)
   int splits;
   float* part_o;                    // [splits, B, kv_heads, Tq * G, D]
