@@ -265,7 +265,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
 // end: keys go from memory straight into fragments, values through a wave's
 // own piece of LDS, which turns them. A step's keys are loaded as soon as the
 // ones before have been used, and its values likewise.
-constexpr int kStepKeys = 32, kStepThreads = 512;
+constexpr int kStepKeys = 32, kStepThreads = 256;
 template <typename DT, int DP>
 struct StepShape {
   static constexpr int kWaves = kStepThreads / 64;
@@ -378,21 +378,23 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
   for (int d = 0; d < kDT; ++d) *reinterpret_cast<f32x4*>(jo + r * kLdO + 16 * d + 4 * g) = o[d];
   if (g == 0) jm[2 * r] = mx, jm[2 * r + 1] = sum;
   __syncthreads();
-  const int m = threadIdx.x / (DP / 4), col = threadIdx.x % (DP / 4) * 4;
-  if (m >= 16 || m0 + m >= rows.M) return;
-  float top = kLowest;
+  for (int k = threadIdx.x; k < 16 * (DP / 4); k += kStepThreads) {
+    const int m = k / (DP / 4), col = k % (DP / 4) * 4;
+    if (m0 + m >= rows.M) return;
+    float top = kLowest;
 #pragma unroll
-  for (int x = 0; x < kWaves; ++x) top = __builtin_fmaxf(top, jm[2 * (x * 16 + m)]);
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  float total = 0.f;
+    for (int x = 0; x < kWaves; ++x) top = __builtin_fmaxf(top, jm[2 * (x * 16 + m)]);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    float total = 0.f;
 #pragma unroll
-  for (int x = 0; x < kWaves; ++x) {
-    const int rr = x * 16 + m;
-    const float f = __builtin_amdgcn_exp2f(jm[2 * rr] - top);
-    total += f * jm[2 * rr + 1];
-    acc += f * *reinterpret_cast<const f32x4*>(jo + rr * kLdO + col);
+    for (int x = 0; x < kWaves; ++x) {
+      const int rr = x * 16 + m;
+      const float f = __builtin_amdgcn_exp2f(jm[2 * rr] - top);
+      total += f * jm[2 * rr + 1];
+      acc += f * *reinterpret_cast<const f32x4*>(jo + rr * kLdO + col);
+    }
+    write_part<DT, FAST>(a, rows, bh, split, m0 + m, L, col, top, total, acc);
   }
-  write_part<DT, FAST>(a, rows, bh, split, m0 + m, L, col, top, total, acc);
 }
 
 // Joins the splits' partial results of one query row: a thread per split for
@@ -488,12 +490,11 @@ AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, boo
   AttentionPlan p{};
   const int wide = bf ? 128 : 64;
   const int64_t heads_all = (int64_t)B * kv_heads;
-  // Narrow also while its workgroups are at most two a compute unit and walk
-  // few steps (us, narrow / wide tiles: 500 queries, 500 keys, 16 heads of 64,
-  // bf16, 512 narrow workgroups: 9.9 / 21.8, fp32 23.7 / 29.3; 80 queries, 128
-  // heads, 640 workgroups, fp32: 44.5 / 33.8; 300 queries, 4000 keys, 8 heads
-  // of 128, bf16: 42.6 / 28.8).
-  p.narrow = M <= 16 || ((M + 15) / 16 * heads_all <= 2ll * cus && Tk <= 4 * kStepKeys * kStepThreads / 64);
+  // Narrow also while its workgroups are at most four a compute unit and walk
+  // few steps (us, narrow / wide tiles, 500 keys, heads of 64: 640 workgroups,
+  // bf16 12.3 / 24.4, fp32 27.0 / 33.8; 1280 workgroups, bf16 19.1 / 14.9;
+  // 4000 keys, 8 heads of 128, 152 workgroups, bf16: 42.6 / 28.8).
+  p.narrow = M <= 16 || ((M + 15) / 16 * heads_all <= 4ll * cus && Tk <= 8 * kStepKeys * kStepThreads / 64);
   const int rows = p.narrow ? 16 : wide;
   // A split of the keys keeps two tiles (narrow: a step of every wave) or more.
   const int keys = p.narrow ? kStepKeys * kStepThreads / 64 : bf ? 128 : 64;

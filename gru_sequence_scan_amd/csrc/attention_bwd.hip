@@ -12,6 +12,21 @@
 namespace rnnk {
 namespace {
 
+// This lane's share (eight columns) of delta.
+template <typename DT, bool FAST>
+__device__ __forceinline__ float delta_part(const AttentionArgs& a, int64_t at, int col, const Frag<DT>& dO) {
+  const Frag<DT> o = load8<DT, FAST>((const DT*)a.o + at, col, a.D, a.vec != 0);
+  float dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(o.get(j), dO.get(j), dot);
+  if constexpr (sizeof(DT) == 2) {
+    const Frag<DT> rest = load8<DT, FAST>((const DT*)a.o_rest + at, col, a.D, a.vec != 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(rest.get(j), dO.get(j), dot);
+  }
+  return dot;
+}
+
 // Query rows across (16 per wave and tile), keys down: dq^T = K^T ds^T.
 template <typename DT, int DP, int QT, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(AttentionArgs a) {
@@ -48,14 +63,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
         const int64_t at = rows.dense(a, b, hk, m);
         q[t][c] = load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m), col, a.D, vec);
         dO[t][c] = load8<DT, FAST>((const DT*)a.d_o + at, col, a.D, vec);
-        const Frag<DT> o = load8<DT, FAST>((const DT*)a.o + at, col, a.D, vec);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(o.get(j), dO[t][c].get(j), dot);
-        if (sizeof(DT) == 2) {
-          const Frag<DT> rest = load8<DT, FAST>((const DT*)a.o_rest + at, col, a.D, vec);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(rest.get(j), dO[t][c].get(j), dot);
-        }
+        dot += delta_part<DT, FAST>(a, at, col, dO[t][c]);
       }
     }
     delta[t] = col_sum(dot);
@@ -153,6 +161,122 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
   }
 }
 
+// The same for few query rows: 16 a workgroup, whose waves divide the keys, 32
+// at a time (see the forward pass): keys and values go from memory straight
+// into fragments, and a wave's keys through its own piece of LDS for the
+// product with ds.
+template <typename DT, int DP>
+struct DqStepShape {
+  static constexpr int kLdK = TileShape<DT, DP, true>::kLd, kLdO = DP + 4;
+  static constexpr int kBytesK = 4 * 32 * kLdK * (int)sizeof(DT), kBytesO = 4 * 16 * kLdO * (int)sizeof(float);
+  static constexpr int kBytes = kBytesK > kBytesO ? kBytesK : kBytesO;
+};
+template <typename DT, int DP, bool FAST>
+__global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_step_kernel(AttentionArgs a) {
+  using S = DqStepShape<DT, DP>;
+  constexpr int kC = DP / 32, kDT = DP / 16, kWaves = 4, kStep = 32, kLdK = S::kLdK, kLdO = S::kLdO;
+  extern __shared__ __align__(16) char lds[];
+  const QRows rows{a.Tq * (a.heads / a.kv_heads), a.heads / a.kv_heads};
+  const int tiles = (rows.M + 15) / 16;
+  const Work w = work_of(a, tiles);
+  if (w.tile >= tiles) return;
+  const int bh = w.bh, m0 = w.tile * 16;
+  const int b = bh / a.kv_heads, hk = bh % a.kv_heads;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
+  const bool vec = a.vec != 0;
+  const int L = key_count(a, b);
+  const DT* kb = (const DT*)a.k + b * a.k_b + hk * a.k_h;
+  const DT* vb = (const DT*)a.v + b * a.v_b + hk * a.v_h;
+  DT* lk = reinterpret_cast<DT*>(lds) + wave * kStep * kLdK;
+
+  Frag<DT> k[2][kC], v[2][kC];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int key = k0 + 16 * n + i16;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        k[n][c] = key < L ? load8<DT, FAST>(kb + key * a.k_t, 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+        v[n][c] = key < L ? load8<DT, FAST>(vb + key * a.v_t, 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+      }
+    }
+  };
+  int k0 = wave * kStep;
+  load(k0);
+  const DT* qb = (const DT*)a.q + b * a.q_b + (int64_t)hk * rows.G * a.q_h;
+  const int mine = m0 + i16;
+  const bool on = mine < rows.M;
+  Frag<DT> q[kC], dO[kC];
+  float dot = 0.f;
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    const int col = 32 * c + 8 * g;
+    q[c] = dO[c] = zero_frag<DT>();
+    if (on) {
+      const int64_t at = rows.dense(a, b, hk, mine);
+      q[c] = load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, mine), col, a.D, vec);
+      dO[c] = load8<DT, FAST>((const DT*)a.d_o + at, col, a.D, vec);
+      dot += delta_part<DT, FAST>(a, at, col, dO[c]);
+    }
+  }
+  const float delta = col_sum(dot);
+  const float lse = on && L > 0 ? a.lse[(int64_t)bh * rows.M + mine] : 0.f;
+  if (on && g == 0 && wave == 0) a.delta[(int64_t)bh * rows.M + mine] = delta;
+  f32x4 dq[kDT];
+#pragma unroll
+  for (int d = 0; d < kDT; ++d) dq[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float sl = a.scale * kLog2e;
+  for (; k0 < L; k0 += kWaves * kStep) {
+    f32x4 s[2], dp[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      s[n] = dp[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        s[n] = mma(k[n][c], q[c], s[n]);
+        dp[n] = mma(v[n][c], dO[c], dp[n]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int c = 0; c < kC; ++c) put8<DT>(lk + (16 * n + i16) * kLdK + 32 * c + 8 * g, k[n][c]);
+    load(k0 + kWaves * kStep);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j], sl, -lse));
+        s[n][j] = k0 + 16 * n + 4 * g + j < L ? p * (dp[n][j] - delta) : 0.f;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const Frag<DT> ds = stack<DT>(s[0], s[1]);
+    Frag<DT> rest;
+    if constexpr (sizeof(DT) == 2) rest = stack_rest(s[0], s[1], ds);
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) {
+      const Frag<DT> kf = read_cols<DT>(lk, kLdK, 0, 16 * d, lane);
+      dq[d] = mma(kf, ds, dq[d]);
+      if constexpr (sizeof(DT) == 2) dq[d] = mma(kf, rest, dq[d]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  // join the waves' parts of the keys, in order of their number
+  float* jo = reinterpret_cast<float*>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < kDT; ++d) *reinterpret_cast<f32x4*>(jo + (wave * 16 + i16) * kLdO + 16 * d + 4 * g) = dq[d];
+  __syncthreads();
+  for (int p = threadIdx.x; p < 16 * (DP / 4); p += kAttnThreads) {
+    const int m = p / (DP / 4), col = p % (DP / 4) * 4;
+    if (m0 + m >= rows.M) return;
+    f32x4 acc = *reinterpret_cast<const f32x4*>(jo + m * kLdO + col);
+#pragma unroll
+    for (int x = 1; x < kWaves; ++x) acc += *reinterpret_cast<const f32x4*>(jo + (x * 16 + m) * kLdO + col);
+    store4<DT, FAST>((DT*)a.dq + rows.dense(a, b, hk, m0 + m), col, a.D, vec, acc * a.scale);
+  }
+}
+
 // Keys across (KT x 16 per wave), query rows down: dv^T = do^T p, dk^T = Q^T
 // ds. The four waves are 4 / WM sets of keys times WM parts of a tile's rows,
 // whose sums are joined at the end.
@@ -167,7 +291,7 @@ struct KvShape {
 };
 
 template <typename DT, int DP, int KT, int WM, int MT, bool FAST, bool REST>
-__global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : DP <= 64 ? 3 : 1) void attention_dkv_kernel(AttentionArgs a) {
   using S = KvShape<DT, DP, KT, WM, MT>;
   constexpr int kC = DP / 32, kDT = DP / 16, kKeys = S::kKeys, kRows = S::kRows, kLd = S::kLd;
   extern __shared__ __align__(16) char lds[];
@@ -538,10 +662,19 @@ hipError_t run(const AttentionArgs& a, hipStream_t st) {
   constexpr int kLdT = TileShape<DT, DP, true>::kLd, kLdR = TileShape<DT, DP, false>::kLd;
   constexpr int kLdsQ = 2 * KT * 16 * (kLdT + kLdR) * (int)sizeof(DT);
   const bool fast = a.vec && a.near && a.D == DP;
-  const auto dq = fast ? attention_dq_kernel<DT, DP, QT, KT, true> : attention_dq_kernel<DT, DP, QT, KT, false>;
-  const hipError_t e = allow_lds(dq, kLdsQ);
-  if (e != hipSuccess) return e;
-  launch_kernel(dq, dim3((unsigned)work_grid(a, (M + 64 * QT - 1) / (64 * QT))), dim3(kAttnThreads), kLdsQ, st, a);
+  // the tiling of the query rows follows the forward pass's rule
+  if (attention_plan(a.B, a.Tq, a.Tk, a.heads, a.kv_heads, sizeof(DT) == 2, a.cus).narrow) {
+    const auto dq = fast ? attention_dq_step_kernel<DT, DP, true> : attention_dq_step_kernel<DT, DP, false>;
+    constexpr int kLds = DqStepShape<DT, DP>::kBytes;
+    const hipError_t e = allow_lds(dq, kLds);
+    if (e != hipSuccess) return e;
+    launch_kernel(dq, dim3((unsigned)work_grid(a, (M + 15) / 16)), dim3(kAttnThreads), kLds, st, a);
+  } else {
+    const auto dq = fast ? attention_dq_kernel<DT, DP, QT, KT, true> : attention_dq_kernel<DT, DP, QT, KT, false>;
+    const hipError_t e = allow_lds(dq, kLdsQ);
+    if (e != hipSuccess) return e;
+    launch_kernel(dq, dim3((unsigned)work_grid(a, (M + 64 * QT - 1) / (64 * QT))), dim3(kAttnThreads), kLdsQ, st, a);
+  }
   if constexpr (sizeof(DT) == 4)
     return run_kv<DT, DP, 1, 1, 2>(a, fast, st);
   else if constexpr (DP <= 64)

@@ -373,7 +373,9 @@ struct QueryLoad {
 // The tiles of one (batch row, key head) are cut into up to kParts parts
 // (every kParts-th tile); a part's tiles run on one XCD one after the other,
 // so that they share its L2, and the parts of a row fall on different XCDs,
-// so that rows of different lengths load the XCDs evenly.
+// so that rows of different lengths load the XCDs evenly. Each part begins
+// one tile further on than the one before it: an XCD's compute units are
+// dealt workgroups in turn too, and the last tiles of a short row are idle.
 struct Work {
   int bh, tile;  // tile < tiles, or the workgroup has none
 };
@@ -387,7 +389,7 @@ inline __host__ __device__ int part_count(const AttentionArgs& a, int tiles) {
 __device__ __forceinline__ Work work_of(const AttentionArgs& a, int tiles) {
   const int parts = part_count(a, tiles), each = (tiles + parts - 1) / parts;
   const int xcd = blockIdx.x % a.xcds, slot = blockIdx.x / a.xcds;
-  const int unit = slot / each * a.xcds + xcd, within = slot % each;
+  const int turn = slot / each, unit = turn * a.xcds + xcd, within = (slot + turn) % each;
   Work w;
   w.bh = unit / parts;
   w.tile = within * parts + unit % parts;
