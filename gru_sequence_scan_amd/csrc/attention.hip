@@ -129,9 +129,7 @@ __device__ __forceinline__ void write_part(const AttentionArgs& a, const QRows& 
   if (a.lse && col == 0) a.lse[(int64_t)bh * rows.M + m] = mx + __builtin_amdgcn_logf(sum);
 }
 
-// TRAIN: p enters the product as its rounded value and the rest, so that o is
-// exact beyond its rounding.
-template <typename DT, int DP, int QT, int KT, bool FAST, bool TRAIN>
+template <typename DT, int DP, int QT, int KT, bool FAST>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArgs a) {
   using S = Shape<DT, DP, QT, KT>;
   static_assert(KT % 2 == 0, "pairs of key tiles make a fragment");
@@ -220,11 +218,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
     }
 #pragma unroll
     for (int t = 0; t < QT; ++t) softmax_step<KT, kDT>(s[t], sl, &mx[t], &sum[t], o[t]);
-    // p is rounded to the storage type here (one rounding of each value, of
-    // the relative size of o's own); its sum keeps 32 bits
+    // p in bf16 enters the product as its rounded value and the rest of the
+    // rounding, so that o is as exact as its own rounding. With the rounded
+    // value alone 1000 x 1000, 32 ragged rows, 8/2 heads of 128 takes 146 us
+    // for 190, with o 1.4 times as far off and the backward pass's delta, a
+    // sum over o, up to 1.9 times where there are few keys.
 #pragma unroll
     for (int n = 0; n < KT; n += 2) {
-      constexpr bool kRest = TRAIN && sizeof(DT) == 2;
+      constexpr bool kRest = sizeof(DT) == 2;
       Frag<DT> p[QT], rest[QT];
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
@@ -462,9 +463,7 @@ hipError_t run(const AttentionArgs& a, const AttentionPlan& p, hipStream_t st) {
     if (e != hipSuccess) return e;
     launch_kernel(kernel, dim3((unsigned)work_grid(a, (M + 15) / 16 * a.splits)), dim3(kStepThreads), StepShape<DT, DP>::kBytes, st, a);
   } else {
-    constexpr bool kBf = sizeof(DT) == 2;
-    const auto kernel = a.lse && kBf ? (fast ? attention_kernel<DT, DP, QT, KT, true, kBf> : attention_kernel<DT, DP, QT, KT, false, kBf>)
-                                     : (fast ? attention_kernel<DT, DP, QT, KT, true, false> : attention_kernel<DT, DP, QT, KT, false, false>);
+    const auto kernel = fast ? attention_kernel<DT, DP, QT, KT, true> : attention_kernel<DT, DP, QT, KT, false>;
     const hipError_t e = allow_lds(kernel, S::kBytes);
     if (e != hipSuccess) return e;
     launch_kernel(kernel, dim3((unsigned)work_grid(a, (M + S::kRows - 1) / S::kRows * a.splits)), dim3(kAttnThreads),

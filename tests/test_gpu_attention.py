@@ -93,6 +93,33 @@ def test_cross_attention_ragged(Tq, heads, kv, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Tq,Tk,B,heads,kv,D", [
+    (50, 70, 70, 4, 4, 64), (50, 70, 70, 4, 4, 40), (37, 130, 70, 8, 4, 128), (70, 33, 70, 4, 4, 96), (65, 40, 60, 4, 4, 33),
+    (50, 65, 100, 4, 4, 32), (40, 1100, 1, 2, 1, 64), (70, 1030, 2, 2, 2, 128), (33, 1100, 1, 3, 1, 100),
+])
+def test_cross_attention_wide_tiles(Tq, Tk, B, heads, kv, D, dtype):
+    """Enough rows, or keys, for the kernels that work on wide tiles of query
+    rows, whole and ragged (a row without keys among them), and for long keys
+    that are split over workgroups."""
+    log(f"cross_attention wide Tq {Tq} Tk {Tk} B {B} heads {heads}/{kv} D {D} {dtype}")
+    q, k, v, do = _case(Tq, Tk, B, heads, kv, D, dtype, D + B)
+    _check(q, k, v, do, what="whole")
+    if B > 2:
+        lengths = [(7 * b) % (Tk + 1) for b in range(B)]
+        lengths[1] = Tk
+        dev = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+
+        def dirty(t):
+            out = t.cuda()
+            if t.shape[0] == Tk and t.shape[2] == kv:
+                for b, L in enumerate(lengths):
+                    out[L:, b] = float("nan")
+            return out
+
+        _check(q, k, v, do, lengths, dev=dev, put=dirty, what="ragged")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("D", [64, 24, 33])
 @pytest.mark.parametrize("Tq", [1, 21])
 def test_cross_attention_layouts(Tq, D, dtype):

@@ -184,6 +184,26 @@ def test_gated_scan_ragged(place, reverse, dtype):
             assert torch.equal(p, q) and torch.equal(p, r)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("reverse", [False, True], ids=["forward", "reverse"])
+def test_gated_scan_ragged_segments(reverse, dtype):
+    """Few channels over a long time: segments of the time axis, with rows
+    that end before, at and inside a segment and a chunk."""
+    T, lengths = 1700, [1700, 0, 1, 255, 256, 257, 1024, 1300, 1536]
+    for gate, H, place in ((False, 8, "dense"), (True, 5, "strided")):
+        log(f"gated_scan segments reverse {reverse} gate {gate} {dtype}")
+        case = _scan_case(T, len(lengths), H, dtype, gate, 23 + gate)
+
+        def dirty(t):
+            out = PLACE[place](t)
+            if t.dim() == 3 and t.shape[0] == T:
+                for b, L in enumerate(lengths):
+                    out[L:, b] = float("nan")
+            return out
+
+        _check_scan(*case, lengths, reverse, dirty, torch.tensor(lengths, dtype=torch.int32, device="cuda"), place)
+
+
 def test_gated_scan_nan_in_unread_gradients():
     """What lies past a row's end in dy is not read either."""
     T, lengths = 140, [3, 140, 0]
