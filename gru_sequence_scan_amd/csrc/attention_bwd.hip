@@ -172,7 +172,7 @@ struct DqStepShape {
   static constexpr int kBytes = kBytesK > kBytesO ? kBytesK : kBytesO;
 };
 template <typename DT, int DP, bool FAST>
-__global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_step_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 4 && DP > 96 ? 1 : 2) void attention_dq_step_kernel(AttentionArgs a) {
   using S = DqStepShape<DT, DP>;
   constexpr int kC = DP / 32, kDT = DP / 16, kWaves = 4, kStep = 32, kLdK = S::kLdK, kLdO = S::kLdO;
   extern __shared__ __align__(16) char lds[];

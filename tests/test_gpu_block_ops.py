@@ -82,7 +82,7 @@ def test_layer_norm_without_parameters_or_residual(dtype):
 def test_layer_norm_extreme_rows():
     """A constant row (variance 0), a row with a large mean, values near the
     type's largest, and rows with NaN or infinity, which stay in their row."""
-    x = torch.randn(6, 64, generator=torch.Generator().manual_seed(3))
+    x = torch.randn(6, 64, generator=torch.Generator().manual_seed(3), dtype=torch.float32)
     x[1] = 7.0
     x[2] += 4096.0
     x[3] *= 1e18

@@ -67,7 +67,7 @@ def test_example_gradients():
     enc = ex.encoder(B, S, 8, 12, lengths, torch.float32)
     block = ex.DecoderBlock(H, 24, heads, kv, torch.float32, seed=3)
     g = torch.Generator().manual_seed(5)
-    x, dy = torch.randn(2, T, B, H, generator=g)
+    x, dy = torch.randn(2, T, B, H, generator=g, dtype=torch.float32)
     y, saved = block.train(x.cuda(), enc, lengths)
     grads, dx, denc = block.backward(saved, dy.cuda())
     w = {k: v.double().cpu().requires_grad_(True) for k, v in block.w.items()}
