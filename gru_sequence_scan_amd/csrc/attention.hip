@@ -12,6 +12,13 @@
 // query heads that share a key head are rows of the same tile, so K and V
 // are read once for all of them; a single-token call has as many rows as
 // that group has heads.
+//
+// 1000 queries x 1000 keys, 32 rows, 8/2 heads of 128, bf16: 235 us (558
+// TFLOP/s of 4 Tq Tk D a head), ragged 189 us. Neither the matrix units (31%
+// of the SIMD cycles) nor LDS (a quarter) is full: two waves a SIMD take turns at
+// products, exponentials and LDS reads and hide only part of each other.
+// fp32 at 1000 x 1000, 8 rows, 4 heads of 64: 84 us (97 of the 154 TFLOP/s
+// that a large fp32 product reaches).
 #include "attention_common.hpp"
 
 namespace rnnk {
@@ -260,8 +267,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
 }
 
 // 16 query rows a workgroup (one token, with the heads that share a key head;
-// or a few tiles of them where wider ones would leave compute units idle):
-// for one tile bound by the reading of K and V, each used once. The waves
+// or a few tiles of them where wider ones would leave compute units idle;
+// for one tile bound by the reading of K and V, each used once: 64 requests
+// over 2000 states of 8 heads of 64, bf16, 54 us = 4.9 TB/s, the rate of a
+// large copy; over 500 ragged ones 11 us, mostly latency). The waves
 // divide the keys, 32 at a time, and never wait for each other before the
 // end: keys go from memory straight into fragments, values through a wave's
 // own piece of LDS, which turns them. A step's keys are loaded as soon as the

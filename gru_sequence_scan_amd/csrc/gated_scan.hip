@@ -29,7 +29,14 @@
 // (1 / 64 of a bf16 tensor), so y (rounded to the storage type) is not read.
 //
 // All states, products and sums are fp32; only x, f, i, dy and the outputs
-// y, dx, df, di have the storage type. Bound by memory.
+// y, dx, df, di have the storage type.
+//
+// Bound by memory. T = 1000, B = 32, H = 1024, bf16, forward: 44 us (its 197
+// MB at 4.4 TB/s); a launch per step of the method over all chunks (compose,
+// carry, run) took 80. T = 16384, B = 2, H = 1000, bf16: forward 37 (compose)
+// + 5 + 41 us, backward 30 + 5 + 72 us. T = 500, B = 64 ragged, H = 512, fp32
+// with an input gate: forward 57 us (3.0 TB/s: the longest rows' chunks follow
+// each other on few compute units), backward 72 us (4.7 TB/s).
 #include "block_kernels.hpp"
 #include "device_common.hpp"
 

@@ -12,6 +12,10 @@
 // once and the variance is taken about the row's own mean (two passes over
 // registers; no difference of large sums). Sums are fp32 and reduced in a
 // fixed order, so the results are deterministic.
+//
+// Bound by memory. 32000 x 1024 bf16 with a residual: forward 46.5 us (its
+// 262 MB at 5.6 TB/s), backward 48.4 us (5.4 TB/s) and 5.5 us for the
+// reduction; with loads only as a row is reached the backward took 82.
 #include "block_kernels.hpp"
 #include "device_common.hpp"
 
