@@ -18,6 +18,8 @@ static_assert(RNN_NORM_MAX_N == kNormMaxN, "layer norm's row limit");
 
 // A launch has at most 2^31 - 1 workgroups.
 constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+// ... and less than 2^32 threads.
+constexpr double kMaxThreads = 4294967295.0;
 
 // A named host range (roctx) around one public call, for timeline tools.
 struct Range {
@@ -86,9 +88,10 @@ int validate(const RnnGatedScanDesc* d) {
   if ((d->reverse | 1) != 1 || (d->input_gate | 1) != 1) return RNN_E_SHAPE;
   if (d->x_t < 0 || d->x_b < 0 || d->f_t < 0 || d->f_b < 0) return RNN_E_SHAPE;
   if (d->input_gate && (d->i_t < 0 || d->i_b < 0)) return RNN_E_SHAPE;
-  // at most one workgroup per 32 channels, batch row (rounded up to XCDs) and chunk
+  // at most one workgroup of 256 threads (bf16: 512 for 64 channels) per 32
+  // channels, batch row (rounded up to XCDs) and chunk
   const double groups = ((double)d->B * scan_chunks(d) + 64) * (((double)d->H + 31) / 32);
-  if (groups > (double)kMaxGrid || (double)d->B * d->H > (double)kMaxGrid * 64) return RNN_E_SHAPE;
+  if (groups * 256 > kMaxThreads) return RNN_E_SHAPE;
   return RNN_OK;
 }
 
@@ -168,11 +171,12 @@ int validate(const RnnAttentionDesc* d) {
   if (d->D > RNN_ATTENTION_MAX_D) return RNN_E_UNSUPPORTED;
   for (int64_t s : {d->q_t, d->q_b, d->q_h, d->k_t, d->k_b, d->k_h, d->v_t, d->v_b, d->v_h})
     if (s < 0) return RNN_E_SHAPE;
-  // row numbers, and the workgroups of the widest launch (16 rows each and
-  // at most 256 splits of the keys), stay 32-bit
-  const double groups = (double)d->B * d->kv_heads;
-  if (d->Tk > kMaxGrid - 1024 || query_rows(d) > kMaxGrid - 1024) return RNN_E_SHAPE;
-  if (groups * ((double)query_rows(d) / 16 + 256) > (double)kMaxGrid || groups * ((double)d->Tk / 16 + 1) > (double)kMaxGrid)
+  const double groups = (double)d->B * d->kv_heads, rows = (double)query_rows(d);
+  if (d->Tk > kMaxGrid - 1024 || rows > (double)(kMaxGrid - 1024) || groups > (double)kMaxGrid) return RNN_E_SHAPE;
+  // threads of the launches: 256 per 64 query rows and per 64 keys (bf16 takes
+  // as many for twice the rows); per 16 rows where there are at most 16
+  const double per_group = rows <= 16 ? 256.0 : 4.0 * (rows + 64.0);
+  if ((groups + 64.0) * per_group > kMaxThreads || (groups + 64.0) * 4.0 * ((double)d->Tk + 128.0) > kMaxThreads)
     return RNN_E_SHAPE;
   return RNN_OK;
 }

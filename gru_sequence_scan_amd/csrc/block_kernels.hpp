@@ -41,6 +41,7 @@ hipError_t launch_gated_scan(GatedScanArgs a, bool bf16_storage, bool backward, 
 // Layer norm (layer_norm.hip).
 struct NormArgs {
   int64_t rows; int N; float eps;
+  int64_t row0;                     // set by launch_layer_norm: a launch's first row
   const void* x; int64_t ldx;
   const void* r; int64_t ldr;       // residual or null
   const void* w; const void* b;     // [N] or null

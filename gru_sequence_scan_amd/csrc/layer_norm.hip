@@ -105,7 +105,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void norm_forward_kernel(NormArgs
   constexpr int kThreads = threads_of(TEAM);
   __shared__ float lds[kThreads / 64];
   const int lane = threadIdx.x % TEAM;
-  const int64_t row = blockIdx.x * (int64_t)(kThreads / TEAM) + threadIdx.x / TEAM;
+  const int64_t row = a.row0 + blockIdx.x * (int64_t)(kThreads / TEAM) + threadIdx.x / TEAM;
   if (row >= a.rows) return;  // whole teams
   float s[V][kE];
   load_row<DT, TEAM, V, VEC>((const DT*)a.x + row * a.ldx, a.N, lane, s);
@@ -311,13 +311,17 @@ __global__ __launch_bounds__(kReduceThreads) void norm_reduce_kernel(const float
 }
 
 template <typename DT, int TEAM, int V, bool VEC>
-void run_forward(const NormArgs& a, hipStream_t st) {
+void run_forward(NormArgs a, hipStream_t st) {
   constexpr int kThreads = threads_of(TEAM), kTeams = kThreads / TEAM;
-  const dim3 grid((unsigned)((a.rows + kTeams - 1) / kTeams)), block(kThreads);
-  if (a.r)
-    launch_kernel(norm_forward_kernel<DT, TEAM, V, VEC, true>, grid, block, 0, st, a);
-  else
-    launch_kernel(norm_forward_kernel<DT, TEAM, V, VEC, false>, grid, block, 0, st, a);
+  // a launch has less than 2^32 threads
+  constexpr int64_t kMost = (1ll << 31) / kThreads;
+  for (int64_t left = (a.rows + kTeams - 1) / kTeams; left > 0; left -= kMost, a.row0 += kMost * kTeams) {
+    const dim3 grid((unsigned)(left < kMost ? left : kMost)), block(kThreads);
+    if (a.r)
+      launch_kernel(norm_forward_kernel<DT, TEAM, V, VEC, true>, grid, block, 0, st, a);
+    else
+      launch_kernel(norm_forward_kernel<DT, TEAM, V, VEC, false>, grid, block, 0, st, a);
+  }
 }
 
 template <typename DT, int TEAM, int V, bool VEC>

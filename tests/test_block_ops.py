@@ -171,7 +171,8 @@ def _scan(**kw):
     ({"dtype": -1}, E_UNSUPPORTED), ({"T": 0}, E_SHAPE), ({"B": 0}, E_SHAPE), ({"H": -1}, E_SHAPE),
     ({"reverse": 2}, E_SHAPE), ({"reverse": -1}, E_SHAPE), ({"input_gate": 3}, E_SHAPE),
     ({"x_t": -1}, E_SHAPE), ({"f_b": -8}, E_SHAPE), ({"input_gate": 1, "i_t": -1}, E_SHAPE), ({"i_t": -1}, OK),
-    ({"T": 2147483647}, E_SHAPE), ({"T": 2000000000, "B": 2000000000}, E_SHAPE), ({"B": 2147483647, "H": 2147483647}, E_SHAPE),
+    ({"T": 2147483647}, E_SHAPE), ({"B": 1 << 20, "H": 4096}, E_SHAPE),
+    ({"T": 2000000000, "B": 2000000000}, E_SHAPE), ({"B": 2147483647, "H": 2147483647}, E_SHAPE),
 ])
 def test_scan_desc(kw, expect):
     n = ctypes.c_size_t(0)
@@ -237,6 +238,7 @@ def _attend(**kw):
     ({"B": 0}, E_SHAPE), ({"Tq": 0}, E_SHAPE), ({"Tk": -3}, E_SHAPE), ({"heads": 3}, E_SHAPE), ({"heads": 0}, E_SHAPE),
     ({"kv_heads": 0}, E_SHAPE), ({"heads": 1}, E_SHAPE), ({"D": 0}, E_SHAPE), ({"scale": float("nan")}, E_SHAPE),
     ({"scale": float("inf")}, E_SHAPE), ({"q_t": -1}, E_SHAPE), ({"k_h": -8}, E_SHAPE), ({"v_b": -1}, E_SHAPE),
+    ({"B": 1 << 20, "Tq": 1}, OK), ({"B": 1 << 20, "Tk": 1 << 12}, E_SHAPE), ({"B": 1 << 20, "Tq": 1 << 12}, E_SHAPE),
     ({"Tk": 2147483647}, E_SHAPE), ({"Tq": 2000000000}, E_SHAPE), ({"B": 2000000000, "kv_heads": 4}, E_SHAPE),
 ])
 def test_attention_desc(kw, expect):

@@ -277,3 +277,17 @@ def test_block_ops_capture_and_streams():
         torch.cuda.synchronize()
         for a, b in zip(step(), held):
             assert torch.equal(a, b)
+
+
+def test_layer_norm_more_rows_than_a_launch():
+    """More rows than one launch has teams for: the last rows are normalised
+    too, and with the same values as the same rows alone."""
+    rows = (1 << 27) + 5003          # 2^23 workgroups of 16 rows, and some
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB of free device memory")
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda")
+    tail = draw(np.random.default_rng(2), (6000, 8), torch.bfloat16).cuda()
+    x[-6000:] = tail
+    y = gss.layer_norm(x)
+    assert torch.equal(y[-6000:], gss.layer_norm(tail))
+    assert not y[:6000].any()
