@@ -120,19 +120,22 @@ __device__ __forceinline__ void write_o(const AttentionArgs& a, int64_t at, int 
   }
 }
 
-// Four elements of a query row's result (mx in base-2 units, sum over all
+// Four elements of each of N column tiles of a query row's result (mx in base-2 units, sum over all
 // lanes), or of its part where the keys are split.
-template <typename DT, bool FAST>
+template <typename DT, bool FAST, int N>
 __device__ __forceinline__ void write_part(const AttentionArgs& a, const QRows& rows, int bh, int split, int m, int L, int col,
-                                           float mx, float sum, const f32x4& o) {
+                                           float mx, float sum, const f32x4 (&o)[N]) {
   if (a.splits > 1) {
     const int64_t r = ((int64_t)split * a.B * a.kv_heads + bh) * rows.M + m;
-    store4<float, FAST>(a.part_o + r * a.D, col, a.D, a.D % 4 == 0, o);
+#pragma unroll
+    for (int d = 0; d < N; ++d) store4<float, FAST>(a.part_o + r * a.D, 16 * d + col, a.D, a.D % 4 == 0, o[d]);
     if (col == 0) a.part_ml[2 * r] = mx, a.part_ml[2 * r + 1] = sum;
     return;
   }
   const float inv = sum > 0.f ? 1.0f / sum : (L > 0 ? __builtin_nanf("") : 0.f);
-  write_o<DT, FAST>(a, rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m), col, o * inv);
+  const int64_t at = rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m);
+#pragma unroll
+  for (int d = 0; d < N; ++d) write_o<DT, FAST>(a, at, 16 * d + col, o[d] * inv);
   if (a.lse && col == 0) a.lse[(int64_t)bh * rows.M + m] = mx + __builtin_amdgcn_logf(sum);
 }
 
@@ -169,9 +172,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     const int m = m0 + (wave * QT + t) * 16 + i16;
+    const DT* row = rows.in<DT>(qb, a.q_t, a.q_h, m < rows.M ? m : 0);
 #pragma unroll
-    for (int c = 0; c < kC; ++c)
-      q[t][c] = m < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+    for (int c = 0; c < kC; ++c) {
+      q[t][c] = load8<DT, FAST>(row, 32 * c + 8 * g, a.D, vec);
+      if (m >= rows.M) q[t][c] = zero_frag<DT>();
+    }
     sl = base2_scale<DT, kC>(a.scale, q[t]);
     mx[t] = kLowest;
     sum[t] = 0.f;
@@ -260,9 +266,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
   for (int t = 0; t < QT; ++t) {
     const int m = m0 + (wave * QT + t) * 16 + i16;
     const float total = col_sum(sum[t]), top = __builtin_fmaxf(mx[t] * sl, kLowest);
-    if (m >= rows.M) continue;
-#pragma unroll
-    for (int d = 0; d < kDT; ++d) write_part<DT, FAST>(a, rows, bh, split, m, L, 16 * d + 4 * g, top, total, o[t][d]);
+    if (m < rows.M) write_part<DT, FAST, kDT>(a, rows, bh, split, m, L, 4 * g, top, total, o[t]);
   }
 }
 
@@ -329,9 +333,13 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
   Frag<DT> q[kC];
   {
     const DT* qb = (const DT*)a.q + b * a.q_b + (int64_t)hk * rows.G * a.q_h;
+    const bool on = m0 + i16 < rows.M;
+    const DT* row = rows.in<DT>(qb, a.q_t, a.q_h, on ? m0 + i16 : 0);
 #pragma unroll
-    for (int c = 0; c < kC; ++c)
-      q[c] = m0 + i16 < rows.M ? load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m0 + i16), 32 * c + 8 * g, a.D, vec) : zero_frag<DT>();
+    for (int c = 0; c < kC; ++c) {
+      q[c] = load8<DT, FAST>(row, 32 * c + 8 * g, a.D, vec);
+      if (!on) q[c] = zero_frag<DT>();
+    }
   }
   const float sl = base2_scale<DT, kC>(a.scale, q);
   f32x4 o[kDT];
@@ -394,16 +402,16 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
     float top = kLowest;
 #pragma unroll
     for (int x = 0; x < kWaves; ++x) top = __builtin_fmaxf(top, jm[2 * (x * 16 + m)]);
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
     float total = 0.f;
 #pragma unroll
     for (int x = 0; x < kWaves; ++x) {
       const int rr = x * 16 + m;
       const float f = __builtin_amdgcn_exp2f(jm[2 * rr] - top);
       total += f * jm[2 * rr + 1];
-      acc += f * *reinterpret_cast<const f32x4*>(jo + rr * kLdO + col);
+      acc[0] += f * *reinterpret_cast<const f32x4*>(jo + rr * kLdO + col);
     }
-    write_part<DT, FAST>(a, rows, bh, split, m0 + m, L, col, top, total, acc);
+    write_part<DT, FAST, 1>(a, rows, bh, split, m0 + m, L, col, top, total, acc);
   }
 }
 

@@ -59,17 +59,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
   for (int t = 0; t < QT; ++t) {
     const int m = m0 + (wave * QT + t) * 16 + i16;
     const bool on = m < rows.M;
+    const int64_t at = rows.dense(a, b, hk, on ? m : 0);
+    const DT* row = rows.in<DT>(qb, a.q_t, a.q_h, on ? m : 0);
     float dot = 0.f;
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       const int col = 32 * c + 8 * g;
-      q[t][c] = dO[t][c] = zero_frag<DT>();
-      if (on) {
-        const int64_t at = rows.dense(a, b, hk, m);
-        q[t][c] = load8<DT, FAST>(rows.in<DT>(qb, a.q_t, a.q_h, m), col, a.D, vec);
-        dO[t][c] = load8<DT, FAST>((const DT*)a.d_o + at, col, a.D, vec);
-        dot += delta_part<DT, FAST>(a, at, col, dO[t][c]);
-      }
+      q[t][c] = load8<DT, FAST>(row, col, a.D, vec);
+      dO[t][c] = load8<DT, FAST>((const DT*)a.d_o + at, col, a.D, vec);
+      if (!on) q[t][c] = dO[t][c] = zero_frag<DT>();
+      dot += delta_part<DT, FAST>(a, at, col, dO[t][c]);
     }
     delta[t] = col_sum(dot);
     lse[t] = on && L > 0 ? a.lse[(int64_t)bh * rows.M + m] : 0.f;
