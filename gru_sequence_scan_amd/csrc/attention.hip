@@ -13,11 +13,11 @@
 // are read once for all of them; a single-token call has as many rows as
 // that group has heads.
 //
-// 1000 queries x 1000 keys, 32 rows, 8/2 heads of 128, bf16: 235 us (558
-// TFLOP/s of 4 Tq Tk D a head), ragged 189 us. Neither the matrix units (31%
+// 1000 queries x 1000 keys, 32 rows, 8/2 heads of 128, bf16: 224 us (585
+// TFLOP/s of 4 Tq Tk D a head), ragged 182 us. Neither the matrix units (35%
 // of the SIMD cycles) nor LDS (a quarter) is full: two waves a SIMD take turns at
 // products, exponentials and LDS reads and hide only part of each other.
-// fp32 at 1000 x 1000, 8 rows, 4 heads of 64: 84 us (97 of the 154 TFLOP/s
+// fp32 at 1000 x 1000, 8 rows, 4 heads of 64: 82 us (100 of the 154 TFLOP/s
 // that a large fp32 product reaches).
 #include "attention_common.hpp"
 

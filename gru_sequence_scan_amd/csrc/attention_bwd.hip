@@ -8,8 +8,8 @@
 // the query rows of all heads that share them (dk, dv). So every output has
 // one owner and no sum depends on the order in which workgroups run.
 //
-// 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of 128, bf16: dq 216 us,
-// dk and dv 347 us. The latter walks 310 equal key tiles on 256 compute units,
+// 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of 128, bf16: dq 211 us,
+// dk and dv 345 us. The latter walks 310 equal key tiles on 256 compute units,
 // so it takes as long as 512 would; dq and dk/dv in one launch, the query tiles
 // filling the gap, measured 557 + 31 us (delta apart) and was not taken.
 #include "attention_common.hpp"
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : DP <= 64 ? 3 : 
 // Both form the scores (a fifth of the work more than forming them once); a
 // SIMD runs a wave of each team, whose products, exponentials and LDS reads
 // overlap. Measured at 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of
-// 128: 347 us (144 GFLOP: 415 TFLOP/s), against 415 with both sums in one wave (one wave a SIMD) and
+// 128: 345 us (144 GFLOP: 417 TFLOP/s), against 415 with both sums in one wave (one wave a SIMD) and
 // 527 with a launch for each.
 template <typename DT, int DP, int KT, int MT, bool FAST, bool REST>
 __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArgs a) {
