@@ -2,9 +2,13 @@
 //
 //   o = softmax(scale q k^T) v   over the first L_b keys of a batch row
 //
-// One pass over the keys with a running maximum m and sum l per query row
-// (in base 2: p = 2^(s - m), s = scale log2(e) q k):
-//   m' = max(m, max s),  l' = 2^(m - m') l + sum p,  o' = 2^(m - m') o + p v
+// One pass over the keys with a running reference r (the maximum, or near it)
+// and sum l per query row (in base 2: p = 2^(s - r), s = scale log2(e) q k):
+//   r' = max(r, max s),  l' = 2^(r - r') l + sum p,  o' = 2^(r - r') o + p v
+// r is a float, and everything refers to that float itself, not to the product
+// it was rounded from: the tiles before and after it moves, the waves and the
+// splits that are joined, and the log-sum-exp. So its rounding, which at large
+// scores is not small against 1, cancels in p / l.
 //
 // The scores are formed transposed, keys down and query rows across (S^T =
 // K Q^T), so that a lane keeps one query row: its statistics need two
@@ -25,10 +29,6 @@ namespace rnnk {
 namespace {
 
 constexpr int kMaxSplits = 256;
-
-// The running maximum of no scores: finite, so that subtracting it from the
-// -inf of a masked score never makes inf - inf.
-constexpr float kLowest = -3.402823466e38f;
 
 // Four waves of QT x 16 query rows share tiles of KT x 16 keys.
 template <typename DT, int DP, int QT, int KT>
@@ -57,41 +57,38 @@ __device__ __forceinline__ float base2_scale(float scale, Frag<DT> (&q)[N]) {
 }
 
 // Scores of KT tiles of keys (raw, -inf where masked) to probabilities:
-// updates the running maximum and sum of this lane's query row and rescales
-// its part of o.
+// updates the reference and the sum of this lane's query row and rescales its
+// part of o. The reference is -inf before the row's first tile and finite from
+// then on, so that a masked score never makes inf - inf.
 template <int KT, int NO>
-__device__ __forceinline__ void softmax_step(f32x4 (&s)[KT], float sl, float* mx, float* sum, f32x4 (&o)[NO]) {
+__device__ __forceinline__ void softmax_step(f32x4 (&s)[KT], float sl, float* ref, float* sum, f32x4 (&o)[NO]) {
   float top = s[0][0];
 #pragma unroll
   for (int n = 0; n < KT; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[n][j]);
-  // The maximum that is subtracted only has to keep 2^(s - m) in range: it
-  // moves when a score passes it by more than 2^kSlack, so most tiles skip
-  // the exchange between lanes and the rescaling of o.
+  // The reference only has to keep 2^(s - r) in range: it moves when a score
+  // passes it by more than 2^kSlack, so most tiles skip the exchange between
+  // lanes and the rescaling of o.
   constexpr float kSlack = 8.0f;
-  if (__any((top - *mx) * sl > kSlack)) {
-    top = __builtin_fmaxf(*mx, col_max(top));
-    const float keep = __builtin_amdgcn_exp2f((*mx - top) * sl);
-    *mx = top;
+  if (__any(!(__builtin_fmaf(top, sl, -*ref) <= kSlack))) {
+    const float next = __builtin_fmaxf(*ref, base2_score(col_max(top), sl));
+    const float keep = __builtin_amdgcn_exp2f(*ref - next);
+    *ref = next;
     *sum *= keep;
 #pragma unroll
     for (int d = 0; d < NO; ++d) o[d] *= keep;
   }
-  // s sl - m sl in one multiply-add: the rounding of m sl is the same factor
-  // in every p and in their sum. Past 2^20 that rounding is no longer small
-  // against 1, and the difference is taken first.
-  const float shift = __builtin_fmaxf(*mx * sl, kLowest);
-  if (__any(__builtin_fabsf(shift) > 1048576.0f)) {
+  if (__any(__builtin_fabsf(*ref) > kCoarse)) {
 #pragma unroll
     for (int n = 0; n < KT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[n][j] = (s[n][j] - *mx) * sl;
+      for (int j = 0; j < 4; ++j) s[n][j] = score_above(s[n][j], sl, *ref);
   } else {
 #pragma unroll
     for (int n = 0; n < KT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[n][j] = __builtin_fmaf(s[n][j], sl, -shift);
+      for (int j = 0; j < 4; ++j) s[n][j] = __builtin_fmaf(s[n][j], sl, -*ref);
   }
   float part = 0.f;
 #pragma unroll
@@ -120,23 +117,23 @@ __device__ __forceinline__ void write_o(const AttentionArgs& a, int64_t at, int 
   }
 }
 
-// Four elements of each of N column tiles of a query row's result (mx in base-2 units, sum over all
-// lanes), or of its part where the keys are split.
+// Four elements of each of N column tiles of a query row's result (sum over all lanes), or of its part
+// where the keys are split.
 template <typename DT, bool FAST, int N>
 __device__ __forceinline__ void write_part(const AttentionArgs& a, const QRows& rows, int bh, int split, int m, int L, int col,
-                                           float mx, float sum, const f32x4 (&o)[N]) {
+                                           float ref, float sum, const f32x4 (&o)[N]) {
   if (a.splits > 1) {
     const int64_t r = ((int64_t)split * a.B * a.kv_heads + bh) * rows.M + m;
 #pragma unroll
     for (int d = 0; d < N; ++d) store4<float, FAST>(a.part_o + r * a.D, 16 * d + col, a.D, a.D % 4 == 0, o[d]);
-    if (col == 0) a.part_ml[2 * r] = mx, a.part_ml[2 * r + 1] = sum;
+    if (col == 0) a.part_ml[2 * r] = ref, a.part_ml[2 * r + 1] = sum;
     return;
   }
   const float inv = sum > 0.f ? 1.0f / sum : (L > 0 ? __builtin_nanf("") : 0.f);
   const int64_t at = rows.dense(a, bh / a.kv_heads, bh % a.kv_heads, m);
 #pragma unroll
   for (int d = 0; d < N; ++d) write_o<DT, FAST>(a, at, 16 * d + col, o[d] * inv);
-  if (a.lse && col == 0) a.lse[(int64_t)bh * rows.M + m] = mx + __builtin_amdgcn_logf(sum);
+  if (a.lse && col == 0) a.lse[(int64_t)bh * rows.M + m] = ref + __builtin_amdgcn_logf(sum);
 }
 
 template <typename DT, int DP, int QT, int KT, bool FAST>
@@ -168,7 +165,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
 
   Frag<DT> q[QT][kC];
   f32x4 o[QT][kDT];
-  float mx[QT], sum[QT], sl = 0.f;
+  float ref[QT], sum[QT], sl = 0.f;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     const int m = m0 + (wave * QT + t) * 16 + i16;
@@ -179,7 +176,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
       if (m >= rows.M) q[t][c] = zero_frag<DT>();
     }
     sl = base2_scale<DT, kC>(a.scale, q[t]);
-    mx[t] = kLowest;
+    ref[t] = -__builtin_inff();
     sum[t] = 0.f;
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -230,7 +227,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
           }
     }
 #pragma unroll
-    for (int t = 0; t < QT; ++t) softmax_step<KT, kDT>(s[t], sl, &mx[t], &sum[t], o[t]);
+    for (int t = 0; t < QT; ++t) softmax_step<KT, kDT>(s[t], sl, &ref[t], &sum[t], o[t]);
     // p in bf16 enters the product as its rounded value and the rest of the
     // rounding, so that o is as exact as its own rounding. With the rounded
     // value alone 1000 x 1000, 32 ragged rows, 8/2 heads of 128 takes 146 us
@@ -265,8 +262,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     const int m = m0 + (wave * QT + t) * 16 + i16;
-    const float total = col_sum(sum[t]), top = __builtin_fmaxf(mx[t] * sl, kLowest);
-    if (m < rows.M) write_part<DT, FAST, kDT>(a, rows, bh, split, m, L, 4 * g, top, total, o[t]);
+    const float total = col_sum(sum[t]);
+    if (m < rows.M) write_part<DT, FAST, kDT>(a, rows, bh, split, m, L, 4 * g, ref[t], total, o[t]);
   }
 }
 
@@ -345,7 +342,7 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
   f32x4 o[kDT];
 #pragma unroll
   for (int d = 0; d < kDT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float mx = kLowest, sum = 0.f;
+  float ref = -__builtin_inff(), sum = 0.f;
   for (; k0 < last; k0 += kWaves * kStepKeys) {
     f32x4 s[2];
 #pragma unroll
@@ -362,7 +359,7 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
         for (int j = 0; j < 4; ++j)
           if (k0 + n * 16 + 4 * g + j >= last) s[n][j] = -__builtin_inff();
     }
-    softmax_step<2, kDT>(s, sl, &mx, &sum, o);
+    softmax_step<2, kDT>(s, sl, &ref, &sum, o);
     // the wave's own reads of the step before are done: they fed products
     // that were issued before these writes
 #pragma unroll
@@ -384,7 +381,6 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   sum = col_sum(sum);
-  mx = __builtin_fmaxf(mx * sl, kLowest);  // base-2 units, as it was subtracted
 
   // join the waves' parts, in order of their number: four elements of a row
   // per thread
@@ -394,7 +390,7 @@ __global__ __launch_bounds__(kStepThreads, 2) void attention_step_kernel(Attenti
   const int r = wave * 16 + i16;
 #pragma unroll
   for (int d = 0; d < kDT; ++d) *reinterpret_cast<f32x4*>(jo + r * kLdO + 16 * d + 4 * g) = o[d];
-  if (g == 0) jm[2 * r] = mx, jm[2 * r + 1] = sum;
+  if (g == 0) jm[2 * r] = ref, jm[2 * r + 1] = sum;
   __syncthreads();
   for (int k = threadIdx.x; k < 16 * (DP / 4); k += kStepThreads) {
     const int m = k / (DP / 4), col = k % (DP / 4) * 4;
@@ -430,7 +426,7 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttentionA
   const bool on = (int)threadIdx.x < a.splits;
   const float mine = on ? a.part_ml[2 * (threadIdx.x * n + r)] : kLowest;
   const float part = on ? a.part_ml[2 * (threadIdx.x * n + r) + 1] : 0.f;
-  float top = mine;
+  float top = __builtin_fmaxf(mine, kLowest);  // finite where every part is empty
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, k, 64));
   if (lane == 0) wtop[wave] = top;

@@ -164,6 +164,22 @@ __device__ __forceinline__ float col_sum(float v) {
   return a + b;
 }
 
+// Scores in base 2, s sl for the raw score s and sl = scale log2(e), relative
+// to a reference r: one multiply-add, exact but for its last rounding. r is
+// such a product rounded, so that even the largest score lies half a unit in
+// r's last place from it; past kCoarse (16 there, and the spacing of scores
+// 32: only equal ones share the weight) products are rounded like r instead,
+// and clamped to finite values.
+constexpr float kLowest = -3.402823466e38f, kHighest = 3.402823466e38f;
+constexpr float kCoarse = 536870912.0f;  // 2^29
+__device__ __forceinline__ float base2_score(float s, float sl) {
+  return __builtin_fmaxf(kLowest, __builtin_fminf(kHighest, s * sl));
+}
+__device__ __forceinline__ float score_above(float s, float sl, float r) {
+  if (__builtin_fabsf(r) <= kCoarse || !__builtin_isfinite(s)) return __builtin_fmaf(s, sl, -r);
+  return base2_score(s, sl) - r;
+}
+
 // Eight elements of a row in global memory from column col on; columns past D
 // are zero. `vec`: rows take 16-byte accesses and D is a multiple of them.
 // FAST kernels are for rows that do and fill their tiles (D = DP): no access
