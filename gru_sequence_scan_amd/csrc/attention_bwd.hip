@@ -8,10 +8,21 @@
 // the query rows of all heads that share them (dk, dv). So every output has
 // one owner and no sum depends on the order in which workgroups run.
 //
+// At large scores the log-sum-exp lse, a float, is rounded by more than the
+// sums can bear (2^(s - lse) is off by a factor 2^(half a unit in its last
+// place): 1e-3 at 2^13, 2 at 2^23). For such rows (large_lse) the first kernel
+// adds up their probabilities as they come out, in a pass over the keys of its
+// own, and keeps rest = log2 of the sum in delta's place; p is 2^(s - lse -
+// rest) then, and the second kernel forms delta again from do and o. A
+// workgroup without such rows does none of it; one with them takes 1.5 (fp32)
+// to 3 times (bf16) as long.
+//
 // 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of 128, bf16: dq 211 us,
 // dk and dv 345 us. The latter walks 310 equal key tiles on 256 compute units,
 // so it takes as long as 512 would; dq and dk/dv in one launch, the query tiles
 // filling the gap, measured 557 + 31 us (delta apart) and was not taken.
+#include <type_traits>
+
 #include "attention_common.hpp"
 
 namespace rnnk {
@@ -30,6 +41,93 @@ __device__ __forceinline__ float delta_part(const AttentionArgs& a, int64_t at, 
     for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(rest.get(j), dO.get(j), dot);
   }
   return dot;
+}
+
+// log2 of the sum of this lane's query row's probabilities as the kernels form
+// them from the kept log-sum-exp. Called by whole waves.
+template <typename DT, int DP, bool FAST>
+__device__ __forceinline__ float lse_rest(const AttentionArgs& a, const DT* kb, int L, const Frag<DT> (&q)[DP / 32], float sl,
+                                          float lse) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
+  float sum = 0.f;
+  for (int k0 = 0; k0 < L; k0 += 16) {
+    const int key = k0 + i16;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < DP / 32; ++c)
+      s = mma(key < L ? load8<DT, FAST>(kb + key * a.k_t, 32 * c + 8 * g, a.D, a.vec != 0) : zero_frag<DT>(), q[c], s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k0 + 4 * g + j < L) sum += __builtin_amdgcn_exp2f(score_above(s[j], sl, lse));
+  }
+  return large_lse(lse) ? __builtin_amdgcn_logf(col_sum(sum)) : 0.f;
+}
+
+// Raw scores to base 2 above their row's log-sum-exp, of one row (a lane's
+// four results belong to one) or of four. LARGE: there may be rows that need
+// their rest. The kernels have their loops twice for it: a branch inside, that
+// is never taken, costs 13% (1000 x 1000, 32 ragged rows, 8/2 heads of 128).
+template <bool LARGE>
+__device__ __forceinline__ void above_lse(f32x4& s, float sl, float lse, float rest) {
+  if (LARGE) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = score_above(s[j], sl, lse) - rest;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(s[j], sl, -lse);
+  }
+}
+template <bool LARGE>
+__device__ __forceinline__ void above_lse(f32x4& s, float sl, const f32x4& lse, const float* rest) {
+  if (LARGE) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = score_above(s[j], sl, lse[j]) - rest[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(s[j], sl, -lse[j]);
+  }
+}
+
+// Whether any thread of the workgroup has a large log-sum-exp; a barrier.
+template <int WAVES>
+__device__ __forceinline__ bool any_large(bool mine, int* flags) {
+  const int wave_has = __any(mine);
+  if ((threadIdx.x & 63) == 0) flags[threadIdx.x >> 6] = wave_has;
+  __syncthreads();
+  int any = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) any |= flags[w];
+  return __builtin_amdgcn_readfirstlane(any) != 0;
+}
+
+// For a tile of query rows some of which have a large log-sum-exp: takes their
+// rest out of delta's place and puts delta there. Called by the whole
+// workgroup of NT threads.
+template <typename DT, int kRows, int NT>
+__device__ __forceinline__ void settle_large_rows(const AttentionArgs& a, const QRows& rows, int b, int hk, int m0,
+                                                  const DT* ldo, int ld, const float* llse, float* ldelta, float* lrest) {
+  constexpr int kPer = NT / kRows;  // neighbouring threads of a row
+  static_assert(NT % kRows == 0 && 64 % kPer == 0, "a row's threads are in one wave");
+  const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
+  const bool large = large_lse(llse[r]);  // not past the last row: infinite there
+  float dot = 0.f;
+  if (large) {
+    const int64_t at = rows.dense(a, b, hk, m0 + r);
+#pragma unroll 1
+    for (int d = part; d < a.D; d += kPer) {
+      float o = to_f32<DT>(((const DT*)a.o)[at + d]);
+      if constexpr (sizeof(DT) == 2) o += to_f32<DT>(((const DT*)a.o_rest)[at + d]);
+      dot = __builtin_fmaf(o, to_f32<DT>(ldo[r * ld + d]), dot);
+    }
+  }
+#pragma unroll
+  for (int k = 1; k < kPer; k <<= 1) dot += __shfl_xor(dot, k, 64);
+  const float rest = ldelta[r];
+  if (part == 0) {
+    lrest[r] = large ? rest : 0.f;
+    if (large) ldelta[r] = dot;
+  }
+  __syncthreads();
 }
 
 // Query rows across (16 per wave and tile), keys down: dq^T = K^T ds^T.
@@ -53,7 +151,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
   const DT* vb = (const DT*)a.v + b * a.v_b + hk * a.v_h;
 
   Frag<DT> q[QT][kC], dO[QT][kC];
-  float lse[QT], delta[QT];
+  float lse[QT], delta[QT], rest_of[QT];
+  bool large = false;  // a row of this wave
+  const float sl = a.scale * kLog2e;
   f32x4 dq[QT][kDT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -72,11 +172,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
     }
     delta[t] = col_sum(dot);
     lse[t] = on && L > 0 ? a.lse[(int64_t)bh * rows.M + m] : 0.f;
-    if (on && g == 0) a.delta[(int64_t)bh * rows.M + m] = delta[t];
+    rest_of[t] = 0.f;
+    if (__any(large_lse(lse[t]))) {
+      rest_of[t] = lse_rest<DT, DP, FAST>(a, kb, L, q[t], sl, lse[t]);
+      large = true;
+    }
+    if (on && g == 0) a.delta[(int64_t)bh * rows.M + m] = large_lse(lse[t]) ? rest_of[t] : delta[t];
 #pragma unroll
     for (int d = 0; d < kDT; ++d) dq[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  const float sl = a.scale * kLog2e;
 
   TileLoad<DT, DP, kKeys, kLdK, FAST> nk;
   TileLoad<DT, DP, kKeys, kLdV, FAST> nv;
@@ -85,76 +189,81 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_dq_kernel(Attention
   nv.load(vb, a.v_t, 0, L, a.D, vec);
   nk.put(smem);
   nv.put(smem + kKeys * kLdK);
-  __syncthreads();
-  for (int k0 = 0; k0 < L; k0 += kKeys) {
-    const DT* lk = smem + (k0 / kKeys & 1) * kTile;
-    const DT* lv = lk + kKeys * kLdK;
-    const bool more = k0 + kKeys < L;
-    if (more) {
-      nk.load(kb, a.k_t, k0 + kKeys, L, a.D, vec);
-      nv.load(vb, a.v_t, k0 + kKeys, L, a.D, vec);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    f32x4 s[QT][KT], dp[QT][KT];
-#pragma unroll
-    for (int n = 0; n < KT; ++n) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t) s[t][n] = dp[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const Frag<DT> kf = read_rows<DT>(lk, kLdK, n * 16 + i16, 32 * c + 8 * g);
-        const Frag<DT> vf = read_rows<DT>(lv, kLdV, n * 16 + i16, 32 * c + 8 * g);
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          s[t][n] = mma(kf, q[t][c], s[t][n]);
-          dp[t][n] = mma(vf, dO[t][c], dp[t][n]);
-        }
+  __shared__ int flags[kAttnThreads / 64];
+  auto walk = [&](auto LARGE) {
+    for (int k0 = 0; k0 < L; k0 += kKeys) {
+      const DT* lk = smem + (k0 / kKeys & 1) * kTile;
+      const DT* lv = lk + kKeys * kLdK;
+      const bool more = k0 + kKeys < L;
+      if (more) {
+        nk.load(kb, a.k_t, k0 + kKeys, L, a.D, vec);
+        nv.load(vb, a.v_t, k0 + kKeys, L, a.D, vec);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 s[QT][KT], dp[QT][KT];
 #pragma unroll
-      for (int t = 0; t < QT; ++t)
+      for (int n = 0; n < KT; ++n) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = __builtin_amdgcn_exp2f(s[t][n][j] * sl - lse[t]);
-          s[t][n][j] = p * (dp[t][n][j] - delta[t]);
-        }
-    }
-    if (!more) {  // keys past the row's end have a p that means nothing
+        for (int t = 0; t < QT; ++t) s[t][n] = dp[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < KT; ++n)
+        for (int c = 0; c < kC; ++c) {
+          const Frag<DT> kf = read_rows<DT>(lk, kLdK, n * 16 + i16, 32 * c + 8 * g);
+          const Frag<DT> vf = read_rows<DT>(lv, kLdV, n * 16 + i16, 32 * c + 8 * g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (k0 + n * 16 + 4 * g + j >= L) {
-#pragma unroll
-            for (int t = 0; t < QT; ++t) s[t][n][j] = 0.f;
+          for (int t = 0; t < QT; ++t) {
+            s[t][n] = mma(kf, q[t][c], s[t][n]);
+            dp[t][n] = mma(vf, dO[t][c], dp[t][n]);
           }
-    }
-    // ds enters the product as its rounded value and the rest: the rounding
-    // errors of a long row's ds would add up against a sum that cancels
-#pragma unroll
-    for (int n = 0; n < KT; n += 2) {
-      Frag<DT> ds[QT], rest[QT];
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        ds[t] = stack<DT>(s[t][n], s[t][n + 1]);
-        if constexpr (sizeof(DT) == 2) rest[t] = stack_rest(s[t][n], s[t][n + 1], ds[t]);
-      }
-#pragma unroll
-      for (int d = 0; d < kDT; ++d) {
-        const Frag<DT> kf = read_cols<DT>(lk, kLdK, n * 16, 16 * d, lane);
+        }
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-          dq[t][d] = mma(kf, ds[t], dq[t][d]);
-          if constexpr (sizeof(DT) == 2) dq[t][d] = mma(kf, rest[t], dq[t][d]);
+          above_lse<LARGE()>(s[t][n], sl, lse[t], rest_of[t]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[t][n][j] = __builtin_amdgcn_exp2f(s[t][n][j]) * (dp[t][n][j] - delta[t]);
         }
       }
+      if (!more) {  // keys past the row's end have a p that means nothing
+#pragma unroll
+        for (int n = 0; n < KT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (k0 + n * 16 + 4 * g + j >= L) {
+#pragma unroll
+              for (int t = 0; t < QT; ++t) s[t][n][j] = 0.f;
+            }
+      }
+      // ds enters the product as its rounded value and the rest: the rounding
+      // errors of a long row's ds would add up against a sum that cancels
+#pragma unroll
+      for (int n = 0; n < KT; n += 2) {
+        Frag<DT> ds[QT], rest[QT];
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          ds[t] = stack<DT>(s[t][n], s[t][n + 1]);
+          if constexpr (sizeof(DT) == 2) rest[t] = stack_rest(s[t][n], s[t][n + 1], ds[t]);
+        }
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) {
+          const Frag<DT> kf = read_cols<DT>(lk, kLdK, n * 16, 16 * d, lane);
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            dq[t][d] = mma(kf, ds[t], dq[t][d]);
+            if constexpr (sizeof(DT) == 2) dq[t][d] = mma(kf, rest[t], dq[t][d]);
+          }
+        }
+      }
+      if (more) {
+        DT* dst = smem + (k0 / kKeys + 1 & 1) * kTile;
+        nk.put(dst);
+        nv.put(dst + kKeys * kLdK);
+      }
+      __syncthreads();
     }
-    if (more) {
-      DT* dst = smem + (k0 / kKeys + 1 & 1) * kTile;
-      nk.put(dst);
-      nv.put(dst + kKeys * kLdK);
-    }
-    __syncthreads();
-  }
+  };
+  if (any_large<kAttnThreads / 64>(large, flags))
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     const int m = m0 + (wave * QT + t) * 16 + i16;
@@ -225,11 +334,14 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 4 && DP > 96 ? 1 : 2) v
   }
   const float delta = col_sum(dot);
   const float lse = on && L > 0 ? a.lse[(int64_t)bh * rows.M + mine] : 0.f;
-  if (on && g == 0 && wave == 0) a.delta[(int64_t)bh * rows.M + mine] = delta;
+  const float sl = a.scale * kLog2e;
+  const bool large = __any(large_lse(lse));
+  float rest_of = 0.f;
+  if (large) rest_of = lse_rest<DT, DP, FAST>(a, kb, L, q, sl, lse);
+  if (on && g == 0 && wave == 0) a.delta[(int64_t)bh * rows.M + mine] = large_lse(lse) ? rest_of : delta;
   f32x4 dq[kDT];
 #pragma unroll
   for (int d = 0; d < kDT; ++d) dq[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const float sl = a.scale * kLog2e;
   for (; k0 < L; k0 += kWaves * kStep) {
     f32x4 s[2], dp[2];
 #pragma unroll
@@ -247,12 +359,17 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 4 && DP > 96 ? 1 : 2) v
       for (int c = 0; c < kC; ++c) put8<DT>(lk + (16 * n + i16) * kLdK + 32 * c + 8 * g, k[n][c]);
     load(k0 + kWaves * kStep);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2; ++n) {
+      if (large)
+        above_lse<true>(s[n], sl, lse, rest_of);
+      else
+        above_lse<false>(s[n], sl, lse, rest_of);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j], sl, -lse));
+        const float p = __builtin_amdgcn_exp2f(s[n][j]);
         s[n][j] = k0 + 16 * n + 4 * g + j < L ? p * (dp[n][j] - delta) : 0.f;
       }
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const Frag<DT> ds = stack<DT>(s[0], s[1]);
     Frag<DT> rest;
@@ -288,14 +405,14 @@ template <typename DT, int DP, int KT, int WM, int MT>
 struct KvShape {
   static constexpr int kKeys = 4 / WM * KT * 16, kRows = WM * MT * 16;
   static constexpr int kLd = TileShape<DT, DP, true>::kLd;
-  // a tile's query rows, their do, log-sum-exp and delta; kept twice
-  static constexpr int kTile = 2 * kRows * kLd + 2 * kRows * (int)(sizeof(float) / sizeof(DT));
+  // a tile's query rows, their do, log-sum-exp, delta and the former's rest; kept twice
+  static constexpr int kTile = 2 * kRows * kLd + 3 * kRows * (int)(sizeof(float) / sizeof(DT));
   static constexpr int kJoin = WM > 1 ? (WM - 1) * kKeys * (DP + 4) * (int)sizeof(float) : 0;
   static constexpr int kBytes = 2 * kTile * (int)sizeof(DT) > kJoin ? 2 * kTile * (int)sizeof(DT) : kJoin;
 };
 
 template <typename DT, int DP, int KT, int WM, int MT, bool FAST, bool REST>
-__global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : DP <= 64 ? 3 : 1) void attention_dkv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : DP <= 64 ? 3 : DP <= 96 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
   using S = KvShape<DT, DP, KT, WM, MT>;
   constexpr int kC = DP / 32, kDT = DP / 16, kKeys = S::kKeys, kRows = S::kRows, kLd = S::kLd;
   extern __shared__ __align__(16) char lds[];
@@ -350,77 +467,93 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : DP <= 64 ? 3 : 
     nq.start((const DT*)a.q + b * a.q_b + (int64_t)hk * rows.G * a.q_h, a.q_t, a.q_h, rows.G);
     no.start((const DT*)a.d_o + ((int64_t)b * a.heads + hk * rows.G) * a.D, (int64_t)a.B * a.heads * a.D, a.D, rows.G);
     load(0);
+    bool large = false;
+#pragma unroll 8
+    for (int m = threadIdx.x; m < rows.M; m += kAttnThreads) large |= large_lse(a.lse[(int64_t)bh * rows.M + m]);
     put(smem);
-    __syncthreads();
-    int turn = 0;
-    for (int m0 = 0; m0 < rows.M; m0 += kRows, turn ^= 1) {
-      const DT* lq = smem + turn * S::kTile;
-      const DT* ldo = lq + kRows * kLd;
-      const float* llse = reinterpret_cast<const float*>(ldo + kRows * kLd);
-      const float* ldelta = llse + kRows;
-      const bool more = m0 + kRows < rows.M;
-      if (more) {
-        nq.next(rows.G);
-        no.next(rows.G);
-        load(m0 + kRows);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+    auto ahead = [&](int m0) {
+      nq.next(rows.G);
+      no.next(rows.G);
+      load(m0 + kRows);
+    };
+    __shared__ int flags[kAttnThreads / 64];
+    auto walk = [&](auto LARGE) {
+      int turn = 0;
+      for (int m0 = 0; m0 < rows.M; m0 += kRows, turn ^= 1) {
+        const DT* lq = smem + turn * S::kTile;
+        const DT* ldo = lq + kRows * kLd;
+        const float* llse = reinterpret_cast<const float*>(ldo + kRows * kLd);
+        const float *ldelta = llse + kRows, *lrest = ldelta + kRows;
+        const bool more = m0 + kRows < rows.M;
+        if (more && !LARGE()) ahead(m0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (LARGE())
+          settle_large_rows<DT, kRows, kAttnThreads>(a, rows, b, hk, m0, ldo, kLd, llse, const_cast<float*>(ldelta),
+                                                 const_cast<float*>(lrest));
 #pragma unroll
-      for (int mt = 0; mt < MT; mt += 2) {
-        const int r0 = (wm * MT + mt) * 16;
-        f32x4 s[2][KT], dp[2][KT];
+        for (int mt = 0; mt < MT; mt += 2) {
+          const int r0 = (wm * MT + mt) * 16;
+          f32x4 s[2][KT], dp[2][KT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int n = 0; n < KT; ++n) s[h][n] = dp[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int n = 0; n < KT; ++n) s[h][n] = dp[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            const Frag<DT> qf = read_rows<DT>(lq, kLd, r0 + h * 16 + i16, 32 * c + 8 * g);
+            for (int c = 0; c < kC; ++c) {
+              const Frag<DT> qf = read_rows<DT>(lq, kLd, r0 + h * 16 + i16, 32 * c + 8 * g);
 #pragma unroll
-            for (int n = 0; n < KT; ++n) s[h][n] = mma(qf, k[n][c], s[h][n]);
-            const Frag<DT> of = read_rows<DT>(ldo, kLd, r0 + h * 16 + i16, 32 * c + 8 * g);
+              for (int n = 0; n < KT; ++n) s[h][n] = mma(qf, k[n][c], s[h][n]);
+              const Frag<DT> of = read_rows<DT>(ldo, kLd, r0 + h * 16 + i16, 32 * c + 8 * g);
 #pragma unroll
-            for (int n = 0; n < KT; ++n) dp[h][n] = mma(of, v[n][c], dp[h][n]);
-          }
-          const f32x4 lse = *reinterpret_cast<const f32x4*>(llse + r0 + h * 16 + 4 * g);
-          const f32x4 de = *reinterpret_cast<const f32x4*>(ldelta + r0 + h * 16 + 4 * g);
-#pragma unroll
-          for (int n = 0; n < KT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][n][j], sl, -lse[j]));
-              s[h][n][j] = p;
-              dp[h][n][j] = p * (dp[h][n][j] - de[j]);
+              for (int n = 0; n < KT; ++n) dp[h][n] = mma(of, v[n][c], dp[h][n]);
             }
-        }
-        Frag<DT> p[KT], ds[KT], p_rest[KT], ds_rest[KT];
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(llse + r0 + h * 16 + 4 * g);
+            const f32x4 de = *reinterpret_cast<const f32x4*>(ldelta + r0 + h * 16 + 4 * g);
+            const float* rest_of = lrest + r0 + h * 16 + 4 * g;
 #pragma unroll
-        for (int n = 0; n < KT; ++n) {
-          p[n] = stack<DT>(s[0][n], s[1][n]);
-          ds[n] = stack<DT>(dp[0][n], dp[1][n]);
-          if constexpr (REST) {
-            p_rest[n] = stack_rest(s[0][n], s[1][n], p[n]);
-            ds_rest[n] = stack_rest(dp[0][n], dp[1][n], ds[n]);
+            for (int n = 0; n < KT; ++n) {
+              above_lse<LARGE()>(s[h][n], sl, lse, rest_of);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                s[h][n][j] = __builtin_amdgcn_exp2f(s[h][n][j]);
+                dp[h][n][j] = s[h][n][j] * (dp[h][n][j] - de[j]);
+              }
+            }
           }
-        }
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          const Frag<DT> of = read_cols<DT>(ldo, kLd, r0, 16 * d, lane);
-          const Frag<DT> qf = read_cols<DT>(lq, kLd, r0, 16 * d, lane);
+          Frag<DT> p[KT], ds[KT], p_rest[KT], ds_rest[KT];
 #pragma unroll
           for (int n = 0; n < KT; ++n) {
-            dv[n][d] = mma(of, p[n], dv[n][d]);
-            dk[n][d] = mma(qf, ds[n], dk[n][d]);
+            p[n] = stack<DT>(s[0][n], s[1][n]);
+            ds[n] = stack<DT>(dp[0][n], dp[1][n]);
             if constexpr (REST) {
-              dv[n][d] = mma(of, p_rest[n], dv[n][d]);
-              dk[n][d] = mma(qf, ds_rest[n], dk[n][d]);
+              p_rest[n] = stack_rest(s[0][n], s[1][n], p[n]);
+              ds_rest[n] = stack_rest(dp[0][n], dp[1][n], ds[n]);
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < kDT; ++d) {
+            const Frag<DT> of = read_cols<DT>(ldo, kLd, r0, 16 * d, lane);
+            const Frag<DT> qf = read_cols<DT>(lq, kLd, r0, 16 * d, lane);
+#pragma unroll
+            for (int n = 0; n < KT; ++n) {
+              dv[n][d] = mma(of, p[n], dv[n][d]);
+              dk[n][d] = mma(qf, ds[n], dk[n][d]);
+              if constexpr (REST) {
+                dv[n][d] = mma(of, p_rest[n], dv[n][d]);
+                dk[n][d] = mma(qf, ds_rest[n], dk[n][d]);
+              }
             }
           }
         }
+        if (more && LARGE()) ahead(m0);  // fewer values are held meanwhile, so that the other loop has its registers
+        if (more) put(smem + (turn ^ 1) * S::kTile);
+        __syncthreads();
       }
-      if (more) put(smem + (turn ^ 1) * S::kTile);
-      __syncthreads();
-    }
+    };
+    if (any_large<kAttnThreads / 64>(large, flags))
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
     if constexpr (WM > 1) {
       // join the parts of the rows, in order of their number
       constexpr int kLdJ = DP + 4;
@@ -536,80 +669,97 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArg
     nq.start((const DT*)a.q + b * a.q_b + (int64_t)hk * rows.G * a.q_h, a.q_t, a.q_h, rows.G);
     no.start((const DT*)a.d_o + ((int64_t)b * a.heads + hk * rows.G) * a.D, (int64_t)a.B * a.heads * a.D, a.D, rows.G);
     load(0);
+    bool large = false;
+#pragma unroll 8
+    for (int m = threadIdx.x; m < rows.M; m += 512) large |= large_lse(a.lse[(int64_t)bh * rows.M + m]);
     put(smem);
-    __syncthreads();
-    int turn = 0;
-    for (int m0 = 0; m0 < rows.M; m0 += kRows, turn ^= 1) {
-      const DT* lq = smem + turn * S::kTile;
-      const DT* ldo = lq + kRows * kLd;
-      const float* llse = reinterpret_cast<const float*>(ldo + kRows * kLd);
-      const float* ldelta = llse + kRows;
-      const bool more = m0 + kRows < rows.M;
-      if (more) {
-        nq.next(rows.G);
-        no.next(rows.G);
-        load(m0 + kRows);
-      }
-      const DT* lx = for_dk ? lq : ldo;
+    auto ahead = [&](int m0) {
+      nq.next(rows.G);
+      no.next(rows.G);
+      load(m0 + kRows);
+    };
+    __shared__ int flags[512 / 64];
+    auto walk = [&](auto LARGE) {
+      int turn = 0;
+      for (int m0 = 0; m0 < rows.M; m0 += kRows, turn ^= 1) {
+        const DT* lq = smem + turn * S::kTile;
+        const DT* ldo = lq + kRows * kLd;
+        const float* llse = reinterpret_cast<const float*>(ldo + kRows * kLd);
+        const float *ldelta = llse + kRows, *lrest = ldelta + kRows;
+        const bool more = m0 + kRows < rows.M;
+        if (more && !LARGE()) ahead(m0);
+        const DT* lx = for_dk ? lq : ldo;
+        if (LARGE())
+          settle_large_rows<DT, kRows, 512>(a, rows, b, hk, m0, ldo, kLd, llse, const_cast<float*>(ldelta),
+                                                 const_cast<float*>(lrest));
 #pragma unroll
-      for (int mt = 0; mt < MT; mt += 2) {
-        f32x4 s[2][KT];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r0 = (mt + h) * 16;
-#pragma unroll
-          for (int n = 0; n < KT; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            const Frag<DT> qf = read_rows<DT>(lq, kLd, r0 + i16, 32 * c + 8 * g);
-#pragma unroll
-            for (int n = 0; n < KT; ++n) s[h][n] = mma(qf, k[n][c], s[h][n]);
-          }
-          const f32x4 lse = *reinterpret_cast<const f32x4*>(llse + r0 + 4 * g);
-#pragma unroll
-          for (int n = 0; n < KT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[h][n][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][n][j], sl, -lse[j]));
-        }
-        if (for_dk) {
+        for (int mt = 0; mt < MT; mt += 2) {
+          f32x4 s[2][KT];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r0 = (mt + h) * 16;
-            f32x4 dp[KT];
 #pragma unroll
-            for (int n = 0; n < KT; ++n) dp[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int n = 0; n < KT; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
-              const Frag<DT> of = read_rows<DT>(ldo, kLd, r0 + i16, 32 * c + 8 * g);
+              const Frag<DT> qf = read_rows<DT>(lq, kLd, r0 + i16, 32 * c + 8 * g);
 #pragma unroll
-              for (int n = 0; n < KT; ++n) dp[n] = mma(of, v[n][c], dp[n]);
+              for (int n = 0; n < KT; ++n) s[h][n] = mma(qf, k[n][c], s[h][n]);
             }
-            const f32x4 de = *reinterpret_cast<const f32x4*>(ldelta + r0 + 4 * g);
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(llse + r0 + 4 * g);
+            const float* rest_of = lrest + r0 + 4 * g;
 #pragma unroll
-            for (int n = 0; n < KT; ++n)
+            for (int n = 0; n < KT; ++n) {
+              above_lse<LARGE()>(s[h][n], sl, lse, rest_of);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) s[h][n][j] *= dp[n][j] - de[j];
+              for (int j = 0; j < 4; ++j) s[h][n][j] = __builtin_amdgcn_exp2f(s[h][n][j]);
+            }
           }
-        }
-        Frag<DT> x[KT], rest[KT];
+          if (for_dk) {
 #pragma unroll
-        for (int n = 0; n < KT; ++n) {
-          x[n] = stack<DT>(s[0][n], s[1][n]);
-          if constexpr (REST) rest[n] = stack_rest(s[0][n], s[1][n], x[n]);
-        }
+            for (int h = 0; h < 2; ++h) {
+              const int r0 = (mt + h) * 16;
+              f32x4 dp[KT];
 #pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          const Frag<DT> f = read_cols<DT>(lx, kLd, mt * 16, 16 * d, lane);
+              for (int n = 0; n < KT; ++n) dp[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int c = 0; c < kC; ++c) {
+                const Frag<DT> of = read_rows<DT>(ldo, kLd, r0 + i16, 32 * c + 8 * g);
+#pragma unroll
+                for (int n = 0; n < KT; ++n) dp[n] = mma(of, v[n][c], dp[n]);
+              }
+              const f32x4 de = *reinterpret_cast<const f32x4*>(ldelta + r0 + 4 * g);
+#pragma unroll
+              for (int n = 0; n < KT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[h][n][j] *= dp[n][j] - de[j];
+            }
+          }
+          Frag<DT> x[KT], rest[KT];
 #pragma unroll
           for (int n = 0; n < KT; ++n) {
-            acc[n][d] = mma(f, x[n], acc[n][d]);
-            if constexpr (REST) acc[n][d] = mma(f, rest[n], acc[n][d]);
+            x[n] = stack<DT>(s[0][n], s[1][n]);
+            if constexpr (REST) rest[n] = stack_rest(s[0][n], s[1][n], x[n]);
+          }
+#pragma unroll
+          for (int d = 0; d < kDT; ++d) {
+            const Frag<DT> f = read_cols<DT>(lx, kLd, mt * 16, 16 * d, lane);
+#pragma unroll
+            for (int n = 0; n < KT; ++n) {
+              acc[n][d] = mma(f, x[n], acc[n][d]);
+              if constexpr (REST) acc[n][d] = mma(f, rest[n], acc[n][d]);
+            }
           }
         }
+        if (more && LARGE()) ahead(m0);  // fewer values are held meanwhile, so that the other loop has its registers
+        if (more) put(smem + (turn ^ 1) * S::kTile);
+        __syncthreads();
       }
-      if (more) put(smem + (turn ^ 1) * S::kTile);
-      __syncthreads();
-    }
+    };
+    if (any_large<512 / 64>(large, flags))
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
   }
   const float mul = for_dk ? a.scale : 1.0f;
   DT* out = (DT*)(for_dk ? a.dk : a.dv);

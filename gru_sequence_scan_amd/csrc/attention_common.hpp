@@ -179,6 +179,12 @@ __device__ __forceinline__ float score_above(float s, float sl, float r) {
   if (__builtin_fabsf(r) <= kCoarse || !__builtin_isfinite(s)) return __builtin_fmaf(s, sl, -r);
   return base2_score(s, sl) - r;
 }
+// The kept log-sum-exp of a row is a float too. Up to 256 half a unit in its
+// last place (2^-17) is small beside what fp32 scores of that size carry
+// themselves; past it the backward pass makes up for it.
+__device__ __forceinline__ bool large_lse(float lse) {
+  return __builtin_fabsf(lse) > 256.0f && __builtin_isfinite(lse);
+}
 
 // Eight elements of a row in global memory from column col on; columns past D
 // are zero. `vec`: rows take 16-byte accesses and D is a multiple of them.

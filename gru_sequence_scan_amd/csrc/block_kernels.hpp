@@ -81,7 +81,7 @@ struct AttentionArgs {
   // backward
   const void* d_o;
   void* dq; void* dk; void* dv;
-  float* delta;                     // [B, kv_heads, Tq * G]
+  float* delta;                     // [B, kv_heads, Tq * G]; at large scores what the rounding of lse left
 };
 // How the forward pass runs: narrow (at most 16 query rows per key head, the
 // waves of a workgroup divide the keys) or in tiles of query rows, and how
