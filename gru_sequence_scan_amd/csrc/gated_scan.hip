@@ -376,7 +376,9 @@ __global__ __launch_bounds__(kScanThreads<DT>) void scan_backward_kernel(GatedSc
   }
   for (; chunk >= p.c0; --chunk) {
     const int s0 = p.step0(chunk);
-    float a[K][E], keep[K][E], w[GATE ? K : 1][E], x[K][E], dy[K][E], P[E], S[E], C[E];
+    // with a gate: slope a (1 - a) in keep's place, u = s x in x's and u (1 - s)
+    // in v; each factor 1 - s has its own accuracy (see gates_of)
+    float a[K][E], keep[K][E], w[GATE ? K : 1][E], x[K][E], v[GATE ? K : 1][E], dy[K][E], P[E], S[E], C[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) P[e] = 1.f, S[e] = 0.f, C[e] = 0.f;
 #pragma unroll
@@ -387,11 +389,17 @@ __global__ __launch_bounds__(kScanThreads<DT>) void scan_backward_kernel(GatedSc
         gates_of(to_f32<DT>(in.f[k].v[e]), &av, &kv);
         const bool on = s0 + k < p.L;
         a[k][e] = on ? av : 1.f;
-        keep[k][e] = on ? kv : 0.f;
-        if (GATE) w[k][e] = on ? sigma(to_f32<DT>(in.i[GATE ? k : 0].v[e])) : 0.f;
+        keep[k][e] = on ? (GATE ? av * kv : kv) : 0.f;
         x[k][e] = on ? to_f32<DT>(in.x[k].v[e]) : 0.f;
         dy[k][e] = on ? to_f32<DT>(in.dy[k].v[e]) : 0.f;
-        S[e] = __builtin_fmaf(a[k][e], S[e], (GATE ? w[GATE ? k : 0][e] : keep[k][e]) * x[k][e]);
+        if (GATE) {
+          float open, shut;
+          gates_of(to_f32<DT>(in.i[GATE ? k : 0].v[e]), &open, &shut);
+          w[k][e] = on ? open : 0.f;
+          x[k][e] *= w[k][e];
+          v[k][e] = x[k][e] * shut;
+        }
+        S[e] = __builtin_fmaf(a[k][e], S[e], GATE ? x[k][e] : keep[k][e] * x[k][e]);
         P[e] *= a[k][e];
       }
 #pragma unroll
@@ -420,7 +428,7 @@ __global__ __launch_bounds__(kScanThreads<DT>) void scan_backward_kernel(GatedSc
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           hp[k][e] = h[e];
-          h[e] = __builtin_fmaf(a[k][e], h[e], (GATE ? w[GATE ? k : 0][e] : keep[k][e]) * x[k][e]);
+          h[e] = __builtin_fmaf(a[k][e], h[e], GATE ? x[k][e] : keep[k][e] * x[k][e]);
         }
 #pragma unroll
       for (int k = K - 1; k >= 0; --k) {
@@ -430,13 +438,17 @@ __global__ __launch_bounds__(kScanThreads<DT>) void scan_backward_kernel(GatedSc
         for (int e = 0; e < E; ++e) {
           const float gt = dy[k][e] + cc[e];
           cc[e] = a[k][e] * gt;
-          // past the row's end a = 1 carries c on, and keep = 0 (w = 0) ends the rest
-          const float ga = gt * a[k][e] * keep[k][e];
-          const float wv = GATE ? w[GATE ? k : 0][e] : keep[k][e];
-          dx[e] = gt * wv;
-          df[e] = ga * (GATE ? hp[k][e] : hp[k][e] - x[k][e]);
-          di[e] = GATE ? gt * x[k][e] * wv * (1.0f - wv) : 0.f;
-          if (s >= p.L) dx[e] = df[e] = di[e] = 0.f;
+          // past the row's end a = 1 carries c on, and keep = 0 (w = v = 0) ends the rest
+          if (GATE) {
+            dx[e] = gt * w[GATE ? k : 0][e];
+            df[e] = gt * keep[k][e] * hp[k][e];
+            di[e] = gt * v[GATE ? k : 0][e];
+          } else {
+            dx[e] = gt * keep[k][e];
+            df[e] = gt * a[k][e] * keep[k][e] * (hp[k][e] - x[k][e]);
+          }
+          if (s >= p.L) dx[e] = df[e] = 0.f;
+          if (GATE && s >= p.L) di[e] = 0.f;
         }
         if (s < g.T) {
           const int64_t o = (s < p.L ? p.time(g, s) : s) * d_t + (int64_t)p.b * g.H + p.h;
