@@ -88,10 +88,9 @@ int validate(const RnnGatedScanDesc* d) {
   if ((d->reverse | 1) != 1 || (d->input_gate | 1) != 1) return RNN_E_SHAPE;
   if (d->x_t < 0 || d->x_b < 0 || d->f_t < 0 || d->f_b < 0) return RNN_E_SHAPE;
   if (d->input_gate && (d->i_t < 0 || d->i_b < 0)) return RNN_E_SHAPE;
-  // at most one workgroup of 256 threads (bf16: 512 for 64 channels) per 32
-  // channels, batch row (rounded up to XCDs) and chunk
-  const double groups = ((double)d->B * scan_chunks(d) + 64) * (((double)d->H + 31) / 32);
-  if (groups * 256 > kMaxThreads) return RNN_E_SHAPE;
+  // a workgroup per tile of channels and batch row (rounded up to XCDs); the
+  // time axis is cut only while there are fewer of them than fill the device
+  if (((double)d->B + 64) * gated_scan_row_threads(d->H, d->dtype == RNN_DTYPE_BF16) > kMaxThreads) return RNN_E_SHAPE;
   return RNN_OK;
 }
 

@@ -35,6 +35,7 @@ struct GatedScanArgs {
   int xcds;                         // XCDs of the device
   int tiles;                        // set by launch_gated_scan
 };
+double gated_scan_row_threads(int H, bool bf16_storage);  // of a launch, for one batch row and segment
 int gated_scan_segments(int T, int B, int H, bool bf16_storage, int cus, int* seg_chunks);
 hipError_t launch_gated_scan(GatedScanArgs a, bool bf16_storage, bool backward, hipStream_t stream);
 

@@ -534,6 +534,11 @@ hipError_t run_gate(const GatedScanArgs& a, bool back, hipStream_t st) {
 
 }  // namespace
 
+double gated_scan_row_threads(int H, bool bf) {
+  const int lanes = bf ? kScanLanes<bf16> : kScanLanes<float>, threads = bf ? kScanThreads<bf16> : kScanThreads<float>;
+  return (double)(((int64_t)H + lanes - 1) / lanes) * threads;
+}
+
 // Segments so that the walks fill the compute units' threads about once,
 // each over two chunks at least.
 int gated_scan_segments(int T, int B, int H, bool bf, int cus, int* seg_chunks) {
