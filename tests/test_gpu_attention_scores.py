@@ -50,7 +50,9 @@ def _unit(dtype):
     log2 e, beside what the reference's rounding leaves (16 at most) and the
     log of the sum, it carries 2^-24 of 32 where the probability counts, the
     exponentials and the sum 2^-22. In bf16 a value and the rest of its
-    rounding hold it to 2^-18, p and ds in the sums and o in delta."""
+    rounding, each rounded by 2^-8 at most, hold it to 2^-16, p and ds in the
+    sums and o in delta; half of that is allowed, since the errors of a sum's
+    terms differ in sign."""
     return (2.0 ** -19 + 2.0 ** -17, 2.0 ** -8) if dtype == torch.bfloat16 else (2.0 ** -19, 0.0)
 
 
