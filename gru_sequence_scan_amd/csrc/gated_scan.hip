@@ -539,13 +539,21 @@ double gated_scan_row_threads(int H, bool bf) {
   return (double)(((int64_t)H + lanes - 1) / lanes) * threads;
 }
 
-// Segments so that the walks fill the compute units' threads about once,
-// each over two chunks at least.
+// Segments so that the walks fill the compute units' threads about once, each
+// over two chunks at least; only while the tiles are fewer than half the
+// compute units and the time has eight chunks: cutting it costs two launches
+// and a second read of the inputs. Measured (us forward + backward, cut /
+// whole): bf16, T = 4096, 96 tiles 161 / 171, 128 tiles 173 / 188, 160 tiles
+// 215 / 196, 256 tiles 351 / 226; T = 2048, 128 tiles 98 / 91; T = 1024, 32
+// tiles 34 / 47, T = 512 33 / 26. fp32, T = 4096, 96 tiles 113 / 137, 128
+// tiles 156 / 154, 160 tiles 237 / 169; T = 1024, 32 tiles 31 / 38, T = 512
+// 31 / 22.
 int gated_scan_segments(int T, int B, int H, bool bf, int cus, int* seg_chunks) {
   const int lanes = bf ? kScanLanes<bf16> : kScanLanes<float>, threads = bf ? kScanThreads<bf16> : kScanThreads<float>;
   const int64_t tiles = (int64_t)B * ((H + lanes - 1) / lanes);
   const int chunks = (T + kGatedScanChunk - 1) / kGatedScanChunk;
-  int64_t want = (1024 / threads) * (int64_t)cus / tiles;
+  int64_t want = 1;
+  if (2 * tiles < cus && chunks >= 8) want = (1024 / threads) * (int64_t)cus / tiles;
   if (want > chunks / 2) want = chunks / 2;
   if (want < 1) want = 1;
   *seg_chunks = (int)((chunks + want - 1) / want);

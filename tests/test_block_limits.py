@@ -43,3 +43,18 @@ def test_scan_long_time_is_no_launch_limit():
 @pytest.mark.parametrize("B,H", [(9_000_000, 8), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 1), (1, 2 ** 31 - 1)])
 def test_scan_sizes_past_a_launch(B, H):
     assert _status(1, 9, B, H) == E_SHAPE
+
+
+@pytest.mark.parametrize("dtype,lanes", [(0, 32), (1, 64)], ids=["f32", "bf16"])
+def test_scan_cuts_time_only_for_few_tiles_and_long_times(dtype, lanes):
+    """The workspace holds the maps of the time's segments: none where the
+    tiles reach half of 256 compute units, or the time is short."""
+    n = ctypes.c_size_t(0)
+
+    def cut(T, tiles):
+        d = gss.RnnGatedScanDesc(dtype, T, 1, tiles * lanes, 0, 0, 8192, 0, 8192, 0, 0, 0)
+        assert ops._lib().rnn_gated_scan_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == OK
+        return n.value > 0
+
+    assert cut(1024, 1) and cut(1024, 32) and cut(4096, 96) and cut(16384, 127)
+    assert not (cut(512, 1) or cut(512, 127) or cut(4096, 128) or cut(16384, 160) or cut(16384, 512))
