@@ -502,11 +502,16 @@ AttentionPlan attention_plan(int B, int Tq, int Tk, int heads, int kv_heads, boo
   AttentionPlan p{};
   const int wide = bf ? 128 : 64;
   const int64_t heads_all = (int64_t)B * kv_heads;
-  // Narrow also while its workgroups are at most four a compute unit and walk
-  // few steps (us, narrow / wide tiles, 500 keys, heads of 64: 640 workgroups,
-  // bf16 12.3 / 24.4, fp32 27.0 / 33.8; 1280 workgroups, bf16 19.1 / 14.9;
-  // 4000 keys, 8 heads of 128, 152 workgroups, bf16: 42.6 / 28.8).
-  p.narrow = M <= 16 || ((M + 15) / 16 * heads_all <= 4ll * cus && Tk <= 8 * kStepKeys * kStepThreads / 64);
+  // Narrow also while its workgroups are at most three a compute unit and walk
+  // few steps. Measured (us, narrow / wide tiles, 4 heads), forward at 500
+  // keys: heads of 64, 512 workgroups, bf16 10.4 / 23.5, fp32 19.3 / 30.0; 768:
+  // 12.5 / 16.2, 25.5 / 30.7; 992: 15.2 / 16.3, 31.5 / 31.5; heads of 128, 768:
+  // 21.5 / 22.5, 50.5 / 49.5; 992: 26.5 / 23.1, 64.2 / 52.0. Backward, whose dq
+  // follows the same rule (1000 keys): heads of 64, 512 workgroups, bf16 47.8 /
+  // 56.4, fp32 99 / 130; 768: 67.7 / 69.5, 139 / 151; 992: 85.0 / 78.5, 178 /
+  // 178; heads of 128, 768: 130 / 126, 351 / 363; 992: 168 / 151, 464 / 426.
+  // 4000 keys, 8 heads of 128, 152 workgroups, bf16, forward: 42.6 / 28.8.
+  p.narrow = M <= 16 || ((M + 15) / 16 * heads_all <= 3ll * cus && Tk <= 8 * kStepKeys * kStepThreads / 64);
   const int rows = p.narrow ? 16 : wide;
   // A split of the keys keeps two tiles (narrow: a step of every wave) or more.
   const int keys = p.narrow ? kStepKeys * kStepThreads / 64 : bf ? 128 : 64;
