@@ -264,8 +264,8 @@ def layer_norm(x, weight=None, bias=None, *, residual=None, eps=1e-5):
 def layer_norm_train(x, weight=None, bias=None, *, residual=None, eps=1e-5):
     """layer_norm that also keeps each row's fp32 statistics. Returns
     ((y, sum), ctx), sum None without a residual; pass ctx to
-    layer_norm_backward. ctx holds x (or the sum): do not change it in
-    place before the backward pass."""
+    layer_norm_backward. ctx holds x (or the sum) and the weight: do not
+    change them in place before the backward pass."""
     return _layer_norm(x, weight, bias, residual, eps, True)
 
 
@@ -339,8 +339,9 @@ def gated_scan(x, f, i=None, *, h0=None, lengths=None, reverse=False):
 
 def gated_scan_train(x, f, i=None, *, h0=None, lengths=None, reverse=False):
     """gated_scan that also keeps the fp32 state at every 128th step. Returns
-    ((y, h_n), ctx); pass ctx to gated_scan_backward. ctx holds x, f and i:
-    do not change them in place before the backward pass."""
+    ((y, h_n), ctx); pass ctx to gated_scan_backward. ctx holds x, f, i and a
+    device tensor of lengths: do not change them in place before the backward
+    pass (a lengths buffer that is used again neither)."""
     return _gated_scan(x, f, i, h0, lengths, reverse, True)
 
 
@@ -415,14 +416,18 @@ def cross_attention(q, k, v, *, lengths=None, scale=None):
 def cross_attention_train(q, k, v, *, lengths=None, scale=None):
     """cross_attention that also keeps the fp32 log-sum-exp of every query's
     scores. Returns (o, ctx); pass ctx to cross_attention_backward. ctx holds
-    q, k, v and o: do not change them in place before the backward pass."""
+    q, k, v, o and a device tensor of lengths: do not change them in place
+    before the backward pass (a lengths buffer that is used again neither)."""
     return _cross_attention(q, k, v, lengths, scale, True)
 
 
 def cross_attention_backward(ctx, do):
     """Gradients of cross_attention_train, given do (shape and dtype of o).
     Returns dense (dq, dk, dv); dk and dv are summed over the query heads of
-    a key head and zero past a row's length."""
+    a key head and zero past a row's length. In bf16, o and dq are as exact as
+    their own rounding; dk and dv too for small calls, and sqrt(2) times as far
+    off where ceil(Tk / (64 if D <= 64 else 128)) * B * kv_heads passes 256
+    (probabilities and score gradients are rounded once there)."""
     o, device = ctx.o, ctx.device
     do = _plain(do, "do", o.shape, o.dtype, device)
     dq = torch.empty_like(o)

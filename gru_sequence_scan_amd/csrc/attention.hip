@@ -17,12 +17,12 @@
 // are read once for all of them; a single-token call has as many rows as
 // that group has heads.
 //
-// 1000 queries x 1000 keys, 32 rows, 8/2 heads of 128, bf16: 224 us (585
-// TFLOP/s of 4 Tq Tk D a head), ragged 182 us. Neither the matrix units (35%
-// of the SIMD cycles) nor LDS (a quarter) is full: two waves a SIMD take turns at
-// products, exponentials and LDS reads and hide only part of each other.
-// fp32 at 1000 x 1000, 8 rows, 4 heads of 64: 82 us (100 of the 154 TFLOP/s
-// that a large fp32 product reaches).
+// 1000 queries x 1000 keys, 32 rows, 8/2 heads of 128, bf16, launches back to
+// back: 197 us (665 TFLOP/s of 4 Tq Tk D a head), ragged in training 157 us.
+// Neither the matrix units (34% of the SIMD cycles) nor LDS (a quarter) is full:
+// two waves a SIMD take turns at products, exponentials and LDS reads and hide
+// only part of each other. fp32 at 1000 x 1000, 8 rows, 4 heads of 64: 79 us
+// (104 of the 154 TFLOP/s that a large fp32 product reaches).
 #include "attention_common.hpp"
 
 namespace rnnk {
@@ -230,8 +230,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
     for (int t = 0; t < QT; ++t) softmax_step<KT, kDT>(s[t], sl, &ref[t], &sum[t], o[t]);
     // p in bf16 enters the product as its rounded value and the rest of the
     // rounding, so that o is as exact as its own rounding. With the rounded
-    // value alone 1000 x 1000, 32 ragged rows, 8/2 heads of 128 takes 146 us
-    // for 190, with o 1.4 times as far off and the backward pass's delta, a
+    // value alone 1000 x 1000, 32 ragged rows, 8/2 heads of 128 takes 133 us
+    // for 157, with o 1.4 times as far off and the backward pass's delta, a
     // sum over o, up to 1.9 times where there are few keys.
 #pragma unroll
     for (int n = 0; n < KT; n += 2) {
@@ -270,8 +270,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttentionArg
 // 16 query rows a workgroup (one token, with the heads that share a key head;
 // or a few tiles of them where wider ones would leave compute units idle;
 // for one tile bound by the reading of K and V, each used once: 64 requests
-// over 2000 states of 8 heads of 64, bf16, 54 us = 4.9 TB/s, the rate of a
-// large copy; over 500 ragged ones 11 us, mostly latency). The waves
+// over 2000 states of 8 heads of 64, bf16, 44 to 47 us = 5.6 to 6 TB/s, more
+// than a large copy; over 500 ragged ones 10 us, mostly latency; fp32, 2000
+// states, 97 us = 5.4 TB/s). The waves
 // divide the keys, 32 at a time, and never wait for each other before the
 // end: keys go from memory straight into fragments, values through a wave's
 // own piece of LDS, which turns them. A step's keys are loaded as soon as the

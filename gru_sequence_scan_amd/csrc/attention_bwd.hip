@@ -17,10 +17,11 @@
 // workgroup without such rows does none of it; one with them takes 1.5 (fp32)
 // to 3 times (bf16) as long.
 //
-// 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of 128, bf16: dq 211 us,
-// dk and dv 345 us. The latter walks 310 equal key tiles on 256 compute units,
-// so it takes as long as 512 would; dq and dk/dv in one launch, the query tiles
-// filling the gap, measured 557 + 31 us (delta apart) and was not taken.
+// 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of 128, bf16, launches
+// back to back: dq 188 us, dk and dv 292 us. The latter walks 310 equal key
+// tiles on 256 compute units, so it takes as long as 512 would; dq and dk/dv in
+// one launch, the query tiles filling the gap, took 4% more than apart (with
+// delta's own launch) and was not taken.
 #include <type_traits>
 
 #include "attention_common.hpp"
@@ -607,11 +608,11 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(DT) == 2 ? 2 : DP <= 64 ? 3 : 
 // The same for wide bf16 heads, where a wave cannot hold the sums of both
 // gradients and two waves a SIMD at once: two teams of four waves own the same
 // keys, one summing dv and one dk, and share the tiles of Q and do in LDS.
-// Both form the scores (a fifth of the work more than forming them once); a
+// Both form the scores (a quarter of the work more than forming them once); a
 // SIMD runs a wave of each team, whose products, exponentials and LDS reads
 // overlap. Measured at 1000 queries x 1000 keys, 32 ragged rows, 8/2 heads of
-// 128: 345 us (144 GFLOP: 417 TFLOP/s), against 415 with both sums in one wave (one wave a SIMD) and
-// 527 with a launch for each.
+// 128: 292 us (144 GFLOP: 493 TFLOP/s); both sums in one wave (one wave a SIMD)
+// took 1.2 and a launch for each 1.5 times as long.
 template <typename DT, int DP, int KT, int MT, bool FAST, bool REST>
 __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArgs a) {
   using S = KvShape<DT, DP, KT, 1, MT>;
@@ -778,8 +779,9 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_team_kernel(AttentionArg
 // each value, of the relative size of the gradients' own, so that these come
 // out sqrt(2) times as far off as by their own rounding alone) where the
 // launch fills the device: with the rest of the rounding as a second product
-// dk and dv take 433 us for 346 at 1000 x 1000, 32 ragged rows, 8/2 heads of
+// dk and dv take 372 us for 292 at 1000 x 1000, 32 ragged rows, 8/2 heads of
 // 128. A launch with fewer workgroups than compute units has the time for it.
+// include/rnn.h states the rule, which is part of what a caller gets.
 bool keep_rest(const AttentionArgs& a, int64_t tiles) { return tiles * a.B * a.kv_heads <= a.cus; }
 
 template <typename DT, int DP, int KT, int WM, int MT>

@@ -27,16 +27,18 @@
 // c runs the same way from the far end. h_{t-1} is computed again in fp32
 // from the state at every chunk's beginning, which the training forward kept
 // (1 / 64 of a bf16 tensor), so y (rounded to the storage type) is not read.
+// Every 1 - s is formed as sigma of the negative, not by a difference.
 //
 // All states, products and sums are fp32; only x, f, i, dy and the outputs
 // y, dx, df, di have the storage type.
 //
-// Bound by memory. T = 1000, B = 32, H = 1024, bf16, forward: 44 us (its 197
-// MB at 4.4 TB/s); a launch per step of the method over all chunks (compose,
-// carry, run) took 80. T = 16384, B = 2, H = 1000, bf16: forward 37 (compose)
-// + 5 + 41 us, backward 30 + 5 + 72 us. T = 500, B = 64 ragged, H = 512, fp32
+// Bound by memory. T = 1000, B = 32, H = 1024, bf16, forward: 46 us (its 197
+// MB at 4.3 TB/s); a launch per step of the method over all chunks (compose,
+// carry, run) took 80. T = 16384, B = 2, H = 1000, bf16: forward 36 (compose)
+// + 5 + 39 us, backward 29 + 5 + 69 us. T = 500, B = 64 ragged, H = 512, fp32
 // with an input gate: forward 57 us (3.0 TB/s: the longest rows' chunks follow
-// each other on few compute units), backward 72 us (4.7 TB/s).
+// each other on few compute units, and a row's tiles on one XCD), backward 71
+// us (4.8 TB/s).
 #include "block_kernels.hpp"
 #include "device_common.hpp"
 
@@ -61,7 +63,9 @@ struct Tile {
 };
 
 // a = sigma(f) and 1 - a = sigma(-f), each with its own relative accuracy:
-// exp of -|f| cannot overflow and neither value is formed by a difference.
+// exp of -|f| cannot overflow and neither value is formed by a difference. The
+// exponent is a rounded product, so the smaller one carries about |f| / 2 units
+// in its last place (5e-6 at |f| = 80).
 __device__ __forceinline__ void gates_of(float f, float* a, float* keep) {
   const float e = fexp(-__builtin_fabsf(f));
   const float r = __builtin_amdgcn_rcpf(1.0f + e);

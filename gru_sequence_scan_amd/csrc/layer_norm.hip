@@ -13,8 +13,8 @@
 // registers; no difference of large sums). Sums are fp32 and reduced in a
 // fixed order, so the results are deterministic.
 //
-// Bound by memory. 32000 x 1024 bf16 with a residual: forward 46.5 us (its
-// 262 MB at 5.6 TB/s), backward 48.4 us (5.4 TB/s) and 5.5 us for the
+// Bound by memory. 32000 x 1024 bf16 with a residual: forward 45.6 us (its
+// 262 MB at 5.7 TB/s), backward 47.4 us (5.5 TB/s) and 5.4 us for the
 // reduction; with loads only as a row is reached the backward took 82.
 #include "block_kernels.hpp"
 #include "device_common.hpp"
@@ -331,9 +331,11 @@ void run_backward(const NormArgs& a, hipStream_t st) {
 }
 
 // The team of a row: as few threads as hold it in 8 or 16 elements each (the
-// backward pass keeps about ten registers an element: with 32 it would spill).
-// 16 threads up to 128 elements, a wave up to 1024, then a workgroup of 256
-// or 512.
+// backward pass keeps about ten registers an element). 16 threads up to 128
+// elements, a wave up to 1024, then a workgroup of 256 or 512. Past 8192
+// elements a thread holds 32, and the backward pass spills: up to 26 registers
+// with 16-byte accesses (16384: 3.2 to 3.7 TB/s, 8192: 3.4 to 4.3) and 195 to
+// 303 without (16377: 0.5 to 1.2 TB/s).
 template <typename DT, bool VEC, bool BACK>
 void pick(const NormArgs& a, hipStream_t st) {
 #define NORM_RUN(TEAM, V) return BACK ? run_backward<DT, TEAM, V, VEC>(a, st) : run_forward<DT, TEAM, V, VEC>(a, st)

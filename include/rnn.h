@@ -477,8 +477,8 @@ int rnn_layer_norm_backward_workspace_bytes(const RnnNormDesc* desc, size_t* byt
 /* Gradients for the row tensor that was normalised (`s`: x, or `sum` with
  * x_ld = N when there was a residual) and the parameters. dy [rows, N];
  * dsum: NULL, or the gradient that reaches the sum by another way (the
- * residual stream), added to dx. dx [rows, N] is the gradient of s, hence of
- * x and of residual alike. dweight, dbias: fp32 [N], both or neither (NULL =
+ * residual stream), added to dx. s and weight as the forward read them. dx
+ * [rows, N] is the gradient of s, hence of x and of residual alike. dweight, dbias: fp32 [N], both or neither (NULL =
  * skip; no workspace is needed then); written, not accumulated. */
 int rnn_layer_norm_backward(const RnnNormDesc* desc, const void* s, const void* weight, const float* stats,
                             const void* dy, const void* dsum, void* dx, float* dweight, float* dbias,
@@ -528,8 +528,8 @@ int rnn_gated_scan(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io, void*
                    void* stream);
 int rnn_gated_scan_train(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io, void* reserve,
                          size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream);
-/* io as for rnn_gated_scan_train (x, f, i and lengths are read; y, h0 and
- * h_n are not). */
+/* io as for rnn_gated_scan_train (x, f, i and lengths are read, unchanged
+ * since; y, h0 and h_n are not). */
 int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* io,
                             const RnnGatedScanGrads* grads, const void* reserve, size_t reserve_bytes,
                             void* workspace, size_t ws_bytes, void* stream);
@@ -537,7 +537,18 @@ int rnn_gated_scan_backward(const RnnGatedScanDesc* desc, const RnnGatedScanIO* 
 /* Cross attention: every query of [Tq, B, heads, D] attends the first L_b
  * states of its batch row in [Tk, B, kv_heads, D]; query head h reads key
  * head h / (heads / kv_heads):
- *   o = softmax(scale q k^T) v, zero when L_b = 0                             */
+ *   o = softmax(scale q k^T) v, zero when L_b = 0
+ * Scores may be as large as fp32 holds: a probability depends on their
+ * distance from the row's largest, which is formed without loss up to 3e8
+ * (past that scores within a rounding of each other count as equal). The
+ * backward pass takes 1.5 to 3 times as long where scores pass about 180.
+ *
+ * bf16: the probabilities and the score gradients enter the sums of o and dq
+ * as two bf16 numbers (16 bits), so that o and dq are as exact as their own
+ * rounding. Those of dk and dv do too while the launch, of
+ * ceil(Tk / (D <= 64 ? 64 : 128)) B kv_heads workgroups, has at most 256 of
+ * them; beyond that they are rounded once, and dk and dv are sqrt(2) times as
+ * far off as by their own rounding alone. */
 typedef struct RnnAttentionDesc {
   int32_t dtype;         /* RnnDtype                                           */
   int32_t B, Tq, Tk;     /* >= 1                                               */
@@ -576,7 +587,7 @@ int rnn_cross_attention(const RnnAttentionDesc* desc, const RnnAttentionIO* io, 
                         void* stream);
 int rnn_cross_attention_train(const RnnAttentionDesc* desc, const RnnAttentionIO* io, void* reserve,
                               size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream);
-/* io as for rnn_cross_attention_train, with the o it wrote. */
+/* io as for rnn_cross_attention_train, unchanged since, with the o it wrote. */
 int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentionIO* io,
                                  const RnnAttentionGrads* grads, const void* reserve, size_t reserve_bytes,
                                  void* workspace, size_t ws_bytes, void* stream);
