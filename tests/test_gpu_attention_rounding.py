@@ -21,7 +21,7 @@ REST, ONCE = 2.0 ** -16, 2.0 ** -8   # a value with its rest: two roundings of 2
 CASES = [
     (1, 40, 3, 4, 2, 64, True), (20, 150, 4, 4, 2, 64, True), (33, 70, 8, 4, 4, 40, True), (20, 300, 4, 4, 2, 128, True),
     (70, 200, 3, 4, 2, 96, True), (9, 1100, 1, 4, 1, 32, True), (50, 70, 64, 2, 2, 64, True),
-    (50, 70, 70, 4, 4, 64, False), (37, 130, 70, 8, 4, 128, False),
+    (50, 70, 70, 4, 4, 64, False), (37, 130, 70, 8, 4, 128, False), (20, 70, 100, 3, 3, 33, False),
 ]
 
 
