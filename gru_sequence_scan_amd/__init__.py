@@ -14,6 +14,9 @@ rnn_forward_train and rnn_backward (fp32 LSTM / LSTMP / GRU).
 
 Operators of a decoder block: layer_norm (with the residual add), gated_scan (a gated linear recurrence) and
 cross_attention (over an encoder's states), each with a _train form that also returns a context and a _backward that takes it.
+
+Operators of a state-space block, in the same manner: causal_conv (short, one filter per channel, with its state),
+selective_scan (a recurrence with a state of N numbers per channel and an input-dependent step) and feed_forward (gated).
 """
 
 from .binding import (  # noqa: F401
@@ -26,4 +29,7 @@ from .block_ops import (  # noqa: F401
     RnnNormDesc, RnnGatedScanDesc, RnnGatedScanIO, RnnGatedScanGrads, BlockContext,
     layer_norm, layer_norm_train, layer_norm_backward, gated_scan, gated_scan_train, gated_scan_backward,
     RnnAttentionDesc, RnnAttentionIO, RnnAttentionGrads, cross_attention, cross_attention_train, cross_attention_backward,
+)
+from .state_block_ops import (  # noqa: F401
+    RnnCausalConvDesc, RnnCausalConvIO, RnnCausalConvGrads, causal_conv, causal_conv_train, causal_conv_backward,
 )

@@ -592,6 +592,64 @@ int rnn_cross_attention_backward(const RnnAttentionDesc* desc, const RnnAttentio
                                  const RnnAttentionGrads* grads, const void* reserve, size_t reserve_bytes,
                                  void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a state-space block: the short causal convolution, the
+ * selective scan and the gated feed-forward. Conventions as for the decoder
+ * block's operators above.
+ * ------------------------------------------------------------------------- */
+
+/* What is applied to a convolution's or a projection's result. */
+typedef enum RnnActivation {
+  RNN_ACT_NONE = 0,
+  RNN_ACT_SILU = 1,      /* v sigma(v)                                         */
+  RNN_ACT_GELU_TANH = 2, /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))      */
+  RNN_ACT_SIGMOID = 3    /* sigma(v)                                           */
+} RnnActivation;
+
+#define RNN_CONV_MAX_W 8
+
+/* Causal convolution over time with one filter of W taps per channel, for
+ * t < L_b:
+ *   p_t = bias + sum_k weight[k] x'_{t - W + 1 + k},   y_t = p_t or silu(p_t)
+ * where x'_s is x_s, and before the row's first step the state: x'_{-1} is
+ * its last row. state_n is the state to go on with: x'_{L_b - W + 1} ..
+ * x'_{L_b - 1} (of the old state where the row has fewer steps). */
+typedef struct RnnCausalConvDesc {
+  int32_t dtype;         /* RnnDtype of every tensor but dweight and dbias     */
+  int32_t T, B, C;       /* >= 1                                               */
+  int32_t W;             /* 2 .. RNN_CONV_MAX_W                                */
+  int32_t activation;    /* RNN_ACT_NONE or RNN_ACT_SILU                       */
+  int64_t x_t, x_b;      /* elements between time steps and batch rows of x    */
+} RnnCausalConvDesc;
+
+typedef struct RnnCausalConvIO {
+  const void* x;           /* [T, B, C]                                        */
+  const void* weight;      /* [C, W], the tap of the newest input last         */
+  const void* bias;        /* [C], NULL = zeros                                */
+  const int32_t* lengths;  /* device [B], NULL = every row has T steps         */
+  const void* state;       /* [W - 1, B, C], the newest input last; NULL =
+                              zeros                                            */
+  void* y;                 /* [T, B, C]                                        */
+  void* state_n;           /* [W - 1, B, C], not the memory of state; NULL =
+                              skip                                             */
+} RnnCausalConvIO;
+
+typedef struct RnnCausalConvGrads {
+  const void* dy;          /* [T, B, C]                                        */
+  const void* dstate_n;    /* [W - 1, B, C], NULL = zeros                      */
+  void* dx;                /* [T, B, C]                                        */
+  float* dweight;          /* fp32 [C, W]                                      */
+  float* dbias;            /* fp32 [C], NULL = skip                            */
+  void* dstate;            /* [W - 1, B, C], NULL = skip                       */
+} RnnCausalConvGrads;
+
+/* The forward needs no workspace and keeps nothing for the backward pass. */
+int rnn_causal_conv(const RnnCausalConvDesc* desc, const RnnCausalConvIO* io, void* stream);
+int rnn_causal_conv_backward_workspace_bytes(const RnnCausalConvDesc* desc, size_t* bytes);
+/* io as for rnn_causal_conv, unchanged since (y and state_n are not read). */
+int rnn_causal_conv_backward(const RnnCausalConvDesc* desc, const RnnCausalConvIO* io,
+                             const RnnCausalConvGrads* grads, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -48,4 +48,7 @@ from .block import (  # noqa: F401
     layer_norm, layer_norm_backward, gated_scan, gated_scan_backward,
     cross_attention, cross_attention_backward, attention_bounds,
 )
+from .state_block import (  # noqa: F401
+    causal_conv, causal_conv_backward, selective_scan, selective_scan_backward, feed_forward, feed_forward_backward,
+)
 from .rssm import rssm_prior_step, rssm_prior_unroll, actor_mlp, rssm_actor_unroll  # noqa: F401

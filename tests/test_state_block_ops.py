@@ -1,0 +1,167 @@
+"""The state-space block's operators on the CPU: the float64 definitions
+against torch and against differences, and the refusals of the C entry points
+and of the Python calls, which all come before anything touches a device."""
+
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+gss = pytest.importorskip("gru_sequence_scan_amd")
+ops = gss.block_ops
+
+OK, E_NULL, E_SHAPE, E_UNSUPPORTED, E_WORKSPACE, E_ALIGN, E_DEVICE = 0, -1, -2, -3, -5, -6, -7
+ADDR = 4096
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _differences(fn, v, eps=1e-6):
+    """d fn / d v by central differences, fn a scalar function."""
+    g = np.zeros_like(v)
+    for k in np.ndindex(v.shape):
+        keep = v[k]
+        v[k] = keep + eps
+        up = fn()
+        v[k] = keep - eps
+        down = fn()
+        v[k] = keep
+        g[k] = (up - down) / (2 * eps)
+    return g
+
+
+def _layouts(tmp_path, names):
+    """The structs' sizes and offsets in C are those of their ctypes mirrors."""
+    lines = [f'  printf("%zu", sizeof({n}));' + "".join(f' printf(" %zu", offsetof({n}, {f[0]}));'
+                                                       for f in getattr(gss, n)._fields_) + ' printf("\\n");' for n in names]
+    src = tmp_path / "layout.c"
+    src.write_text("#include <stdio.h>\n#include <stddef.h>\n#include \"rnn.h\"\nint main(void) {\n" + "\n".join(lines) +
+                   "\n  return 0;\n}\n")
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(tmp_path / "layout")], check=True)
+    out = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.splitlines()
+    for n, line in zip(names, out):
+        t = getattr(gss, n)
+        assert [int(v) for v in line.split()] == [ctypes.sizeof(t)] + [getattr(t, f[0]).offset for f in t._fields_]
+
+
+
+
+# ---------------------------------------------------------------------------
+# Causal convolution
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("activation", [None, "silu"])
+@pytest.mark.parametrize("W", [2, 4, 5])
+def test_causal_conv_definition(W, activation):
+    rng = np.random.default_rng(1)
+    T, B, C = 5, 4, 3
+    x, dy = rng.standard_normal((2, T, B, C))
+    w, b = rng.standard_normal((C, W)), rng.standard_normal(C)
+    state, ds = rng.standard_normal((2, W - 1, B, C))
+    lens = [5, 0, 1, 4]
+    y, last = oracle.causal_conv(x, w, b, state, lens, activation)
+    ref = torch.nn.functional.conv1d(torch.tensor(np.concatenate([state, x])).permute(1, 2, 0), torch.tensor(w)[:, None],
+                                     torch.tensor(b), groups=C).permute(2, 0, 1)
+    ref = torch.nn.functional.silu(ref) if activation else ref
+    for row, L in enumerate(lens):
+        assert np.allclose(y[:L, row], ref[:L, row].numpy(), atol=1e-12) and (y[L:, row] == 0).all()
+        assert np.array_equal(last[:, row], np.concatenate([state[:, row], x[:L, row]])[L:])
+
+    def loss():
+        y, last = oracle.causal_conv(x, w, b, state, lens, activation)
+        return float((y * dy).sum() + (last * ds).sum())
+
+    grads = oracle.causal_conv_backward(x, w, b, dy, ds, state, lens, activation)
+    for got, v in zip(grads, (x, w, b, state)):
+        assert np.allclose(got, _differences(loss, v), atol=1e-7)
+
+
+def test_causal_conv_in_parts_is_the_whole():
+    rng = np.random.default_rng(2)
+    x, w = rng.standard_normal((9, 2, 3)), rng.standard_normal((3, 4))
+    whole, last = oracle.causal_conv(x, w)
+    state, parts = None, []
+    for a, b in ((0, 1), (1, 6), (6, 9)):
+        y, state = oracle.causal_conv(x[a:b], w, None, state)
+        parts.append(y)
+    assert np.allclose(np.concatenate(parts), whole, atol=1e-13) and np.array_equal(state, last)
+
+
+def test_conv_layout(tmp_path):
+    _layouts(tmp_path, ["RnnCausalConvDesc", "RnnCausalConvIO", "RnnCausalConvGrads"])
+
+
+def _conv(**kw):
+    v = dict(dtype=0, T=30, B=4, C=8, W=4, activation=1, x_t=32, x_b=8)
+    v.update(kw)
+    return gss.RnnCausalConvDesc(*v.values())
+
+
+@pytest.mark.parametrize("kw,expect", [
+    ({}, OK), ({"dtype": 1}, OK), ({"W": 2}, OK), ({"W": 8}, OK), ({"activation": 0}, OK), ({"x_b": 0}, OK),
+    ({"dtype": 2}, E_UNSUPPORTED), ({"W": 1}, E_UNSUPPORTED), ({"W": 9}, E_UNSUPPORTED), ({"W": 0}, E_SHAPE),
+    ({"activation": 2}, E_UNSUPPORTED), ({"activation": -1}, E_UNSUPPORTED),
+    ({"T": 0}, E_SHAPE), ({"B": 0}, E_SHAPE), ({"C": 0}, E_SHAPE), ({"x_t": -1}, E_SHAPE), ({"x_b": -8}, E_SHAPE),
+    ({"T": 2147483647}, E_SHAPE), ({"T": 160000, "B": 1 << 19, "C": 4096}, E_SHAPE),
+    ({"T": 1 << 20, "B": 1 << 10, "C": 63}, OK), ({"T": 1 << 20, "B": 1 << 10, "C": 64}, E_SHAPE),
+    ({"T": 1, "B": 1, "C": 2147483647}, E_SHAPE), ({"T": 8, "B": 2147483647, "C": 1}, E_SHAPE),
+])
+def test_conv_desc(kw, expect):
+    n = ctypes.c_size_t(0)
+    assert ops._lib().rnn_causal_conv_backward_workspace_bytes(ctypes.byref(_conv(**kw)), ctypes.byref(n)) == expect
+    if expect == OK:
+        assert n.value >= 5 * 4 or kw.get("W") == 2
+
+
+def test_conv_pointers():
+    L = ops._lib()
+    d = ctypes.byref(_conv())
+    n = ctypes.c_size_t(0)
+    assert L.rnn_causal_conv_backward_workspace_bytes(d, ctypes.byref(n)) == OK
+    assert L.rnn_causal_conv_backward_workspace_bytes(d, None) == E_NULL
+
+    def io(**kw):
+        v = dict(x=ADDR, weight=ADDR, bias=ADDR, lengths=None, state=None, y=ADDR, state_n=ADDR)
+        v.update(kw)
+        return gss.RnnCausalConvIO(*v.values())
+
+    def fwd(desc=d, **kw):
+        return L.rnn_causal_conv(desc, ctypes.byref(io(**kw)), None)
+
+    assert fwd(desc=None) == E_NULL and L.rnn_causal_conv(d, None, None) == E_NULL
+    for k in ("x", "weight", "y"):
+        assert fwd(**{k: None}) == E_NULL, k
+    for k in ("x", "weight", "bias", "lengths", "state", "y", "state_n"):
+        assert fwd(**{k: ADDR + 2}) == E_ALIGN, k
+
+    def bwd(ws=ADDR, size=n.value, **kw):
+        v = dict(dy=ADDR, dstate_n=None, dx=ADDR, dweight=ADDR, dbias=ADDR, dstate=None)
+        v.update(kw)
+        return L.rnn_causal_conv_backward(d, ctypes.byref(io()), ctypes.byref(gss.RnnCausalConvGrads(*v.values())), ws, size,
+                                          None)
+
+    for k in ("dy", "dx", "dweight"):
+        assert bwd(**{k: None}) == E_NULL, k
+    for k in ("dy", "dstate_n", "dx", "dweight", "dbias", "dstate"):
+        assert bwd(**{k: ADDR + 1}) == E_ALIGN, k
+    assert bwd(ws=None) == E_WORKSPACE and bwd(size=n.value - 1) == E_WORKSPACE and bwd(ws=ADDR + 4) == E_ALIGN
+    assert L.rnn_causal_conv_backward(d, ctypes.byref(io()), None, ADDR, n.value, None) == E_NULL
+    if not torch.cuda.is_available():
+        assert fwd() == E_DEVICE and fwd(state_n=None, bias=None) == E_DEVICE and bwd() == E_DEVICE
+        assert bwd(dbias=None) == E_DEVICE
+
+
+def test_conv_python_refusals():
+    x, w = torch.zeros(4, 2, 8), torch.zeros(8, 4)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        gss.causal_conv(x, w)
+    with pytest.raises(ValueError, match="activation"):
+        gss.causal_conv(x, w, activation="gelu_tanh")
+    with pytest.raises(ValueError, match="dimensions"):
+        gss.causal_conv(x[0], w)
+    with pytest.raises(ValueError, match="dtype"):
+        gss.causal_conv(x.half(), w)
