@@ -32,4 +32,6 @@ from .block_ops import (  # noqa: F401
 )
 from .state_block_ops import (  # noqa: F401
     RnnCausalConvDesc, RnnCausalConvIO, RnnCausalConvGrads, causal_conv, causal_conv_train, causal_conv_backward,
+    RnnSelectiveScanDesc, RnnSelectiveScanIO, RnnSelectiveScanGrads, selective_scan, selective_scan_train,
+    selective_scan_backward,
 )

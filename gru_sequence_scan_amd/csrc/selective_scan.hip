@@ -1,0 +1,270 @@
+// Selective scan: a linear recurrence with a state of N numbers per channel
+// and a step length of its own at every time.
+//
+//   d_t = softplus(dt_t + bias)  (or dt_t + bias)
+//   h_t[n] = exp(d_t A[n]) h_{t-1}[n] + d_t x_t B_t[n]
+//   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)
+//
+// per channel of [T, B, H]; B and C are shared by a group's channels.
+//
+// Bound by the vector units: a state's step is an exponential (a quarter of
+// the rate) and four products or sums, 32 clocks of a SIMD for 64 states,
+// while a channel's step moves 8 bytes in bf16. So the states stay in
+// registers for the whole time, four lanes a channel; the time is walked in
+// tiles of 32 steps, staged through LDS with the next tile's loads in flight,
+// and what is formed once a channel and step (step length, gate) is formed by
+// one lane in four.
+//
+// Where that gives few workgroups the time is cut into segments: a first
+// launch finds what each adds to the state and the sum of its steps (its
+// decay is exp(A sum d)), a second runs the state through the segments, and
+// the walk starts from there.
+//
+// All states, products and sums are fp32; x, dt, z, B, C and y have the
+// storage type.
+#include "selective_scan_common.hpp"
+
+namespace rnnk {
+namespace {
+
+constexpr int kSteps = 32;
+
+template <typename DT, int J, bool VEC, bool COMPOSE>
+__global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanArgs a) {
+  constexpr int NP = 4 * J;
+  using Tile = SelTile<DT, kSteps, VEC>;
+  __shared__ __attribute__((aligned(16))) DT lds_x[kSteps * Tile::kLd], lds_d[kSteps * Tile::kLd];
+  __shared__ __attribute__((aligned(16))) DT lds_z[COMPOSE ? 1 : kSteps * Tile::kLd], lds_y[COMPOSE ? 1 : kSteps * Tile::kLd];
+  __shared__ __attribute__((aligned(16))) float lds_b[kSteps * NP], lds_c[COMPOSE ? 1 : kSteps * NP];
+  const SelPlace p(a);
+  if (p.seg >= a.segs) return;
+  const int lane = threadIdx.x & 63, q = lane & 3, ch = (threadIdx.x >> 6) * 16 + (lane >> 2);
+  const bool live = ch < p.live;
+  const int hc = p.c0 + (live ? ch : 0);
+  const int64_t cell = (int64_t)p.b * a.H + hc, cells = (int64_t)a.B * a.H;
+  float A2[J], h[J];
+  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, A2);
+#pragma unroll
+  for (int j = 0; j < J; ++j) A2[j] *= kLog2e;
+  if (COMPOSE) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) h[j] = 0.f;
+  } else if (a.segs > 1) {
+    read_states<J>(a.map_s + (p.seg * cells + cell) * NP + q * J, h);
+  } else {
+    load_row<J>(a.h0 ? a.h0 + cell * a.N : nullptr, q * J, a.N, h);
+  }
+  const float bias = a.dt_bias ? a.dt_bias[hc] : 0.f, D = a.D ? a.D[hc] : 0.f;
+  const DT* x = (const DT*)a.x + p.b * a.x_b;
+  const DT* dt = (const DT*)a.dt + p.b * a.dt_b;
+  const DT* z = a.z ? (const DT*)a.z + p.b * a.z_b : nullptr;
+  const DT* Bm = (const DT*)a.Bm + p.b * a.B_b + p.group * a.B_g;
+  const DT* Cm = (const DT*)a.Cm + p.b * a.C_b + p.group * a.C_g;
+  DT* y = (DT*)a.y + (int64_t)p.b * a.H;
+  const int64_t y_t = cells;
+  const int end = p.t1 < p.L ? p.t1 : p.L;  // steps there are
+  float sum_d = 0.f;
+  Tile tx, td, tz;
+  SelRows<DT, kSteps, NP> tb, tc;
+  auto load = [&](int t) {
+    tx.load(x, a.x_t, t, p.L - 1, p.c0, p.live);
+    td.load(dt, a.dt_t, t, p.L - 1, p.c0, p.live);
+    tb.load(Bm, a.B_t, t, p.L - 1, a.N);
+    if (!COMPOSE) {
+      if (z) tz.load(z, a.z_t, t, p.L - 1, p.c0, p.live);
+      tc.load(Cm, a.C_t, t, p.L - 1, a.N);
+    }
+  };
+  if (p.t0 < end) load(p.t0);
+  int t = p.t0;
+  for (; t < end; t += kSteps) {
+    tx.put(lds_x);
+    td.put(lds_d);
+    tb.put(lds_b, t, p.L, a.N);
+    if (!COMPOSE) {
+      if (z) tz.put(lds_z);
+      tc.put(lds_c, t, p.L, a.N);
+    }
+    lds_barrier();
+    if (t + kSteps < end) load(t + kSteps);
+#pragma unroll 1
+    for (int g = 0; g < kSteps / 4; ++g) {
+      if (!COMPOSE && a.keep && g % (kSelKeep / 4) == 0 && live && t + 4 * g < end)
+        write_states<J>(a.keep + ((t / kSelKeep + g / (kSelKeep / 4)) * cells + cell) * NP + q * J, h);
+      const int at = (4 * g + q) * Tile::kLd + ch;
+      const bool on = t + 4 * g + q < p.L;  // a step past the row's end has no length
+      const float xv = on ? to_f32<DT>(lds_x[at]) : 0.f;
+      const float d = on ? step_length(to_f32<DT>(lds_d[at]) + bias, a.softplus) : 0.f;
+      const float dx = d * xv;
+      if (COMPOSE) sum_d += d;
+      float acc[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float ds = quad_from(d, s), dxs = quad_from(dx, s);
+        float bv[J], cv[J];
+        read_states<J>(lds_b + (4 * g + s) * NP + q * J, bv);
+        if (!COMPOSE) read_states<J>(lds_c + (4 * g + s) * NP + q * J, cv);
+        acc[s] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * A2[j]), h[j], dxs * bv[j]);
+          if (!COMPOSE) acc[s] = __builtin_fmaf(h[j], cv[j], acc[s]);
+        }
+      }
+      if (!COMPOSE) {
+        float v = __builtin_fmaf(D, xv, quad_scatter(acc, q));
+        if (z) {
+          const float zv = to_f32<DT>(lds_z[at]);
+          v *= zv * fsigmoid(zv);
+        }
+        lds_y[at] = from_f32<DT>(v);
+      }
+    }
+    lds_barrier();
+    if (!COMPOSE) Tile::store(lds_y, y, y_t, t, p.t1, p.L, p.c0, p.live);
+  }
+  if (COMPOSE) {
+    if (live) write_states<J>(a.map_s + (p.seg * cells + cell) * NP + q * J, h);
+    sum_d = quad_sum(sum_d);
+    if (live && q == 0) a.map_d[p.seg * cells + cell] = sum_d;
+    return;
+  }
+  // steps past the row's end
+  for (; t < p.t1; t += kSteps) Tile::store(lds_y, y, y_t, t, p.t1, p.L, p.c0, p.live);
+  if (a.h_n && live && p.seg == a.segs - 1) store_row<J>(a.h_n + cell * a.N, q * J, a.N, h);
+}
+
+// The states that enter the segments, one thread per state: in the place of
+// what the segments add. Forward from h_0, backward from dh_n and the last
+// segment.
+__global__ __launch_bounds__(256) void sel_carry_kernel(SelectiveScanArgs a, const float* __restrict__ first, int NP, int back) {
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x, cells = (int64_t)a.B * a.H;
+  if (i >= cells * NP) return;
+  const int n = (int)(i % NP);
+  const int64_t cell = i / NP;
+  const bool on = n < a.N;
+  const float A2 = on ? a.A[cell % a.H * a.N + n] * kLog2e : 0.f;
+  float h = on && first ? first[cell * a.N + n] : 0.f;
+  constexpr int kBatch = 8;
+  for (int k0 = 0; k0 < a.segs; k0 += kBatch) {
+    float s[kBatch], d[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int c = k0 + k < a.segs ? k0 + k : a.segs - 1;
+      const int64_t o = (back ? a.segs - 1 - c : c) * cells + cell;
+      s[k] = a.map_s[o * NP + n];
+      d[k] = a.map_d[o];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k < a.segs) {
+        const int64_t o = (back ? a.segs - 1 - (k0 + k) : k0 + k) * cells + cell;
+        a.map_s[o * NP + n] = h;
+        h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * d[k]), h, s[k]);
+      }
+  }
+}
+
+// A few steps (one, where a model answers token by token): the same lanes
+// without the tiles. Bound by the states' way in and out.
+constexpr int kShort = 8;
+template <typename DT, int J>
+__global__ __launch_bounds__(kSelThreads) void sel_short_kernel(SelectiveScanArgs a) {
+  constexpr int NP = 4 * J;
+  const int64_t id = blockIdx.x * (int64_t)kSelThreads + threadIdx.x, cells = (int64_t)a.B * a.H;
+  const int q = threadIdx.x & 3;
+  const bool live = (id >> 2) < cells;
+  const int64_t cell = live ? id >> 2 : 0;
+  const int b = (int)(cell / a.H), hc = (int)(cell % a.H), group = hc / (a.H / a.G);
+  const int len = a.lengths ? a.lengths[b] : a.T, L = len < 0 ? 0 : (len > a.T ? a.T : len);
+  float A2[J], h[J];
+  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, A2);
+#pragma unroll
+  for (int j = 0; j < J; ++j) A2[j] *= kLog2e;
+  load_row<J>(a.h0 ? a.h0 + cell * a.N : nullptr, q * J, a.N, h);
+  if (a.keep && live) write_states<J>(a.keep + cell * NP + q * J, h);
+  const float bias = a.dt_bias ? a.dt_bias[hc] : 0.f, D = a.D ? a.D[hc] : 0.f;
+  for (int t = 0; t < a.T; ++t) {
+    float v = 0.f;
+    if (t < L) {
+      const float xv = to_f32<DT>(((const DT*)a.x)[t * a.x_t + b * a.x_b + hc]);
+      const float d = step_length(to_f32<DT>(((const DT*)a.dt)[t * a.dt_t + b * a.dt_b + hc]) + bias, a.softplus);
+      const DT* Bm = (const DT*)a.Bm + t * a.B_t + b * a.B_b + group * a.B_g;
+      const DT* Cm = (const DT*)a.Cm + t * a.C_t + b * a.C_b + group * a.C_g;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const bool on = q * J + j < a.N;
+        const float bv = on ? to_f32<DT>(Bm[q * J + j]) : 0.f, cv = on ? to_f32<DT>(Cm[q * J + j]) : 0.f;
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], d * xv * bv);
+        v = __builtin_fmaf(h[j], cv, v);
+      }
+      v = __builtin_fmaf(D, xv, quad_sum(v));
+      if (a.z) {
+        const float zv = to_f32<DT>(((const DT*)a.z)[t * a.z_t + b * a.z_b + hc]);
+        v *= zv * fsigmoid(zv);
+      }
+    }
+    if (live && q == 0) ((DT*)a.y)[t * cells + cell] = from_f32<DT>(v);
+  }
+  if (a.h_n && live) store_row<J>(a.h_n + cell * a.N, q * J, a.N, h);
+}
+
+template <typename DT, int J, bool VEC>
+hipError_t run(const SelectiveScanArgs& a, hipStream_t st) {
+  if (a.segs > 1) {
+    launch_kernel(sel_forward_kernel<DT, J, VEC, true>, sel_grid(a), dim3(kSelThreads), 0, st, a);
+    const hipError_t e = launch_sel_carry(a, a.h0, 4 * J, false, st);
+    if (e != hipSuccess) return e;
+  }
+  launch_kernel(sel_forward_kernel<DT, J, VEC, false>, sel_grid(a), dim3(kSelThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename DT, int J>
+hipError_t run_width(const SelectiveScanArgs& a, hipStream_t st) {
+  if (a.T <= kShort) {
+    const int64_t n = (int64_t)a.B * a.H * 4;
+    launch_kernel(sel_short_kernel<DT, J>, dim3((unsigned)((n + kSelThreads - 1) / kSelThreads)), dim3(kSelThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  return a.vec ? run<DT, J, true>(a, st) : run<DT, J, false>(a, st);
+}
+
+template <typename DT>
+hipError_t run_states(const SelectiveScanArgs& a, hipStream_t st) {
+  switch (sel_padded(a.N)) {
+    case 4: return run_width<DT, 1>(a, st);
+    case 8: return run_width<DT, 2>(a, st);
+    case 16: return run_width<DT, 4>(a, st);
+    case 32: return run_width<DT, 8>(a, st);
+    default: return run_width<DT, 16>(a, st);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_sel_carry(const SelectiveScanArgs& a, const float* first, int NP, bool back, hipStream_t st) {
+  const int64_t n = (int64_t)a.B * a.H * NP;
+  launch_kernel(sel_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a, first, NP, (int)back);
+  return hipGetLastError();
+}
+
+// Segments so that about two workgroups a compute unit are at work, each over
+// 64 steps at least.
+int sel_segments(int T, int B, int H, int G, int cus, int* seg_steps) {
+  const int64_t tiles = (int64_t)B * sel_group_tiles(H, G) * G;
+  const int chunks = (T + 63) / 64;
+  int64_t want = 1;
+  if (2 * tiles <= cus) want = 2 * (int64_t)cus / tiles;
+  if (want > chunks / 2) want = chunks / 2;
+  if (want < 1) want = 1;
+  *seg_steps = (int)((chunks + want - 1) / want) * 64;
+  return (T + *seg_steps - 1) / *seg_steps;
+}
+
+hipError_t launch_selective_scan(SelectiveScanArgs a, bool bf, hipStream_t st) {
+  sel_tiles(a);
+  return bf ? run_states<bf16>(a, st) : run_states<float>(a, st);
+}
+
+}  // namespace rnnk

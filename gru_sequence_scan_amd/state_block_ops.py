@@ -32,7 +32,30 @@ class RnnCausalConvGrads(ctypes.Structure):
     _fields_ = [("dy", _P), ("dstate_n", _P), ("dx", _P), ("dweight", _P), ("dbias", _P), ("dstate", _P)]
 
 
+class RnnSelectiveScanDesc(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("T", _I32), ("B", _I32), ("H", _I32), ("N", _I32), ("G", _I32), ("softplus", _I32),
+                ("gate", _I32), ("x_t", _I64), ("x_b", _I64), ("dt_t", _I64), ("dt_b", _I64), ("z_t", _I64), ("z_b", _I64),
+                ("B_t", _I64), ("B_b", _I64), ("B_g", _I64), ("C_t", _I64), ("C_b", _I64), ("C_g", _I64)]
+
+
+class RnnSelectiveScanIO(ctypes.Structure):
+    _fields_ = [("x", _P), ("dt", _P), ("z", _P), ("Bm", _P), ("Cm", _P), ("A", _P), ("D", _P), ("dt_bias", _P),
+                ("lengths", _P), ("h0", _P), ("y", _P), ("h_n", _P)]
+
+
+class RnnSelectiveScanGrads(ctypes.Structure):
+    _fields_ = [("dy", _P), ("dh_n", _P), ("dx", _P), ("ddt", _P), ("dz", _P), ("dB", _P), ("dC", _P), ("dA", _P),
+                ("dD", _P), ("ddt_bias", _P), ("dh0", _P)]
+
+
+_SCAN = [_REF(RnnSelectiveScanDesc), _REF(RnnSelectiveScanIO)]
 block_ops._SIGNATURES.update({
+    "rnn_selective_scan_workspace_bytes": [_REF(RnnSelectiveScanDesc), _REF(_SZ)],
+    "rnn_selective_scan_reserve_bytes": [_REF(RnnSelectiveScanDesc), _REF(_SZ)],
+    "rnn_selective_scan_backward_workspace_bytes": [_REF(RnnSelectiveScanDesc), _REF(_SZ)],
+    "rnn_selective_scan": _SCAN + [_P, _SZ, _P],
+    "rnn_selective_scan_train": _SCAN + [_P, _SZ, _P, _SZ, _P],
+    "rnn_selective_scan_backward": _SCAN + [_REF(RnnSelectiveScanGrads), _P, _SZ, _P, _SZ, _P],
     "rnn_causal_conv": [_REF(RnnCausalConvDesc), _REF(RnnCausalConvIO), _P],
     "rnn_causal_conv_backward_workspace_bytes": [_REF(RnnCausalConvDesc), _REF(_SZ)],
     "rnn_causal_conv_backward": [_REF(RnnCausalConvDesc), _REF(RnnCausalConvIO), _REF(RnnCausalConvGrads), _P, _SZ, _P],
@@ -113,3 +136,98 @@ def causal_conv_backward(ctx, dy, dstate_n=None):
     ctx._use(ctx.x, ctx.weight, ctx.bias, ctx.lengths, ctx.state)
     _call("rnn_causal_conv_backward", device, ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ws), size)
     return dx, dw, db, dstate
+
+
+# ---------------------------------------------------------------------------
+# Selective scan
+# ---------------------------------------------------------------------------
+
+def _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, train):
+    _tensor(x, "x", 3)
+    _tensor(B, "B", 4)
+    _tensor(A, "A", 2)
+    T, rows, H = x.shape
+    G, N = B.shape[2:]
+    device, dtype, shape = x.device, x.dtype, x.shape
+    x = _strided(x, "x", shape, x)
+    dt = _strided(dt, "dt", shape, x)
+    z = None if z is None else _strided(z, "z", shape, x)
+    B = _strided(B, "B", (T, rows, G, N), x)
+    C = _strided(C, "C", (T, rows, G, N), x)
+    A = _plain(A, "A", (H, N), torch.float32, device)
+    D = _plain(D, "D", (H,), torch.float32, device)
+    dt_bias = _plain(dt_bias, "dt_bias", (H,), torch.float32, device)
+    h0 = _plain(h0, "h0", (rows, H, N), torch.float32, device)
+    lengths = _lengths(lengths, rows, T, device)
+    y = _dense_like(x)
+    h_n = torch.empty((rows, H, N), dtype=torch.float32, device=device)
+    desc = RnnSelectiveScanDesc(DTYPES[dtype], T, rows, H, N, G, 1 if softplus else 0, 0 if z is None else 1, *x.stride()[:2],
+                                *dt.stride()[:2], *((0, 0) if z is None else z.stride()[:2]), *B.stride()[:3],
+                                *C.stride()[:3])
+    io = RnnSelectiveScanIO(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D),
+                            _ptr(dt_bias), _ptr(lengths), _ptr(h0), y.data_ptr(), h_n.data_ptr())
+    size = _bytes("rnn_selective_scan_workspace_bytes", desc)
+    ws = _buffer(size, device)
+    if not train:
+        _call("rnn_selective_scan", device, ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size)
+        return y, h_n
+    rsize = _bytes("rnn_selective_scan_reserve_bytes", desc)
+    reserve = _buffer(rsize, device)
+    stream = _call("rnn_selective_scan_train", device, ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws),
+                   size)
+    return (y, h_n), BlockContext(device, stream, desc=desc, x=x, dt=dt, z=z, B=B, C=C, A=A, D=D, dt_bias=dt_bias,
+                                  lengths=lengths, reserve=reserve)
+
+
+def selective_scan(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=True, h0=None, lengths=None):
+    """Linear recurrence with a state of N numbers per channel and a step
+    length of its own at every time:
+
+        d_t = softplus(dt_t + dt_bias)                  (softplus=False: dt_t + dt_bias)
+        h_t = exp(d_t A) h_{t-1} + d_t x_t B_t          (h: [H, N])
+        y_t = (sum_n C_t h_t + D x_t) silu(z_t)         (z None: no factor)
+
+    x, dt, z: [T, B, H], B, C: [T, B, G, N] (float32 or bfloat16; may be
+    slices of projections: only the last dimension has to be contiguous).
+    Channel h reads group h // (H // G); N is at most 64. A: fp32 [H, N],
+    finite; D, dt_bias: fp32 [H]; h0: fp32 [B, H, N]. lengths: B row lengths
+    in [0, T], a device int32 tensor or host values (which are copied).
+    Returns (y [T, B, H] with zeros past a row's length, h_n fp32 [B, H, N]).
+    A serving step is T = 1 with the last call's h_n as h0."""
+    return _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, False)
+
+
+def selective_scan_train(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=True, h0=None, lengths=None):
+    """selective_scan that also keeps the fp32 state at every 16th step.
+    Returns ((y, h_n), ctx); pass ctx to selective_scan_backward. ctx holds the
+    inputs (a device tensor of lengths among them): do not change them in place
+    before the backward pass."""
+    return _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, True)
+
+
+def selective_scan_backward(ctx, dy, dh_n=None):
+    """Gradients of selective_scan_train, given dy (shape and dtype of y) and
+    optionally dh_n (fp32 [B, H, N]). Returns them by the inputs' names: "x",
+    "dt", "z", "B", "C" in x's dtype, "A", "D", "dt_bias", "h0" in fp32; None
+    for z, D and dt_bias where they were not given."""
+    d, device, dtype = ctx.desc, ctx.device, ctx.x.dtype
+    dy = _plain(dy, "dy", (d.T, d.B, d.H), dtype, device)
+    dh_n = _plain(dh_n, "dh_n", (d.B, d.H, d.N), torch.float32, device)
+
+    def f32(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=device)
+
+    g = {"x": _dense_like(dy), "dt": _dense_like(dy), "z": None if ctx.z is None else _dense_like(dy),
+         "B": dy.new_empty(ctx.B.shape), "C": dy.new_empty(ctx.B.shape), "A": f32(d.H, d.N),
+         "D": None if ctx.D is None else f32(d.H), "dt_bias": None if ctx.dt_bias is None else f32(d.H),
+         "h0": f32(d.B, d.H, d.N)}
+    io = RnnSelectiveScanIO(ctx.x.data_ptr(), ctx.dt.data_ptr(), _ptr(ctx.z), ctx.B.data_ptr(), ctx.C.data_ptr(),
+                            ctx.A.data_ptr(), _ptr(ctx.D), _ptr(ctx.dt_bias), _ptr(ctx.lengths), None, None, None)
+    grads = RnnSelectiveScanGrads(dy.data_ptr(), _ptr(dh_n), *(_ptr(g[k]) for k in ("x", "dt", "z", "B", "C", "A", "D",
+                                                                                    "dt_bias", "h0")))
+    size = _bytes("rnn_selective_scan_backward_workspace_bytes", d)
+    ws = _buffer(size, device)
+    ctx._use(ctx.x, ctx.dt, ctx.z, ctx.B, ctx.C, ctx.A, ctx.D, ctx.dt_bias, ctx.lengths, ctx.reserve)
+    _call("rnn_selective_scan_backward", device, ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ctx.reserve),
+          ctx.reserve.numel(), _ptr(ws), size)
+    return g

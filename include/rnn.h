@@ -650,6 +650,72 @@ int rnn_causal_conv_backward_workspace_bytes(const RnnCausalConvDesc* desc, size
 int rnn_causal_conv_backward(const RnnCausalConvDesc* desc, const RnnCausalConvIO* io,
                              const RnnCausalConvGrads* grads, void* workspace, size_t ws_bytes, void* stream);
 
+#define RNN_SELECTIVE_MAX_N 64
+
+/* Selective scan: a linear recurrence with a state of N numbers for each of H
+ * channels and a step length of its own at every time, for t < L_b:
+ *   d_t = softplus(dt_t + dt_bias)                    (or dt_t + dt_bias)
+ *   h_t[n] = exp(d_t A[n]) h_{t-1}[n] + d_t x_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)     (without z: no factor)
+ * Channel h reads B and C of group h / (H / G). A must be finite. */
+typedef struct RnnSelectiveScanDesc {
+  int32_t dtype;         /* RnnDtype of x, dt, z, B, C, y and their gradients  */
+  int32_t T, B, H;       /* >= 1                                               */
+  int32_t N;             /* 1 .. RNN_SELECTIVE_MAX_N                           */
+  int32_t G;             /* groups, a divisor of H                             */
+  int32_t softplus;      /* 0 or 1: whether d_t is a softplus                  */
+  int32_t gate;          /* 0 or 1: whether z is given                         */
+  int64_t x_t, x_b;      /* elements between time steps and batch rows         */
+  int64_t dt_t, dt_b;
+  int64_t z_t, z_b;
+  int64_t B_t, B_b, B_g; /* ... and groups                                     */
+  int64_t C_t, C_b, C_g;
+} RnnSelectiveScanDesc;
+
+typedef struct RnnSelectiveScanIO {
+  const void* x;           /* [T, B, H]                                        */
+  const void* dt;          /* [T, B, H]                                        */
+  const void* z;           /* [T, B, H] with gate                              */
+  const void* Bm;          /* [T, B, G, N]                                     */
+  const void* Cm;          /* [T, B, G, N]                                     */
+  const float* A;          /* fp32 [H, N]                                      */
+  const float* D;          /* fp32 [H], NULL = zeros                           */
+  const float* dt_bias;    /* fp32 [H], NULL = zeros                           */
+  const int32_t* lengths;  /* device [B], NULL = every row has T steps         */
+  const float* h0;         /* fp32 [B, H, N], NULL = zeros                     */
+  void* y;                 /* [T, B, H]                                        */
+  float* h_n;              /* fp32 [B, H, N] state after each row's last step;
+                              NULL = skip                                      */
+} RnnSelectiveScanIO;
+
+typedef struct RnnSelectiveScanGrads {
+  const void* dy;          /* [T, B, H]                                        */
+  const float* dh_n;       /* fp32 [B, H, N], NULL = zeros                     */
+  void* dx;                /* [T, B, H]                                        */
+  void* ddt;               /* [T, B, H]                                        */
+  void* dz;                /* [T, B, H] with gate                              */
+  void* dB;                /* [T, B, G, N], summed over a group's channels     */
+  void* dC;                /* [T, B, G, N]                                     */
+  float* dA;               /* fp32 [H, N]                                      */
+  float* dD;               /* fp32 [H], NULL = skip                            */
+  float* ddt_bias;         /* fp32 [H], NULL = skip                            */
+  float* dh0;              /* fp32 [B, H, N], NULL = skip                      */
+} RnnSelectiveScanGrads;
+
+/* The reserve between the passes is the fp32 state at every 16th step. */
+int rnn_selective_scan_workspace_bytes(const RnnSelectiveScanDesc* desc, size_t* bytes);
+int rnn_selective_scan_reserve_bytes(const RnnSelectiveScanDesc* desc, size_t* bytes);
+int rnn_selective_scan_backward_workspace_bytes(const RnnSelectiveScanDesc* desc, size_t* bytes);
+int rnn_selective_scan(const RnnSelectiveScanDesc* desc, const RnnSelectiveScanIO* io, void* workspace,
+                       size_t ws_bytes, void* stream);
+int rnn_selective_scan_train(const RnnSelectiveScanDesc* desc, const RnnSelectiveScanIO* io, void* reserve,
+                             size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream);
+/* io as for rnn_selective_scan_train, unchanged since (y, h0 and h_n are not
+ * read). */
+int rnn_selective_scan_backward(const RnnSelectiveScanDesc* desc, const RnnSelectiveScanIO* io,
+                                const RnnSelectiveScanGrads* grads, const void* reserve, size_t reserve_bytes,
+                                void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

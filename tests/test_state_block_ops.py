@@ -165,3 +165,159 @@ def test_conv_python_refusals():
         gss.causal_conv(x[0], w)
     with pytest.raises(ValueError, match="dtype"):
         gss.causal_conv(x.half(), w)
+
+
+# ---------------------------------------------------------------------------
+# Selective scan
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("full", [True, False])
+def test_selective_scan_definition(full, G):
+    rng = np.random.default_rng(4)
+    T, B, H, N = 4, 3, 4, 3
+    x, dt, z, dy = rng.standard_normal((4, T, B, H))
+    Bm, Cm = rng.standard_normal((2, T, B, G, N))
+    A = -np.exp(rng.standard_normal((H, N)))
+    D, bias = rng.standard_normal((2, H))
+    h0, dhn = rng.standard_normal((2, B, H, N))
+    lens = [4, 0, 2]
+    opt = dict(z=z, dt_bias=bias, soft=True) if full else dict(z=None, dt_bias=None, soft=False)
+    D = D if full else None
+
+    def loss():
+        y, hn, _ = oracle.selective_scan(x, dt, A, Bm, Cm, D, h0=h0, lengths=lens, **opt)
+        return float((y * dy).sum() + (hn * dhn).sum())
+
+    g = oracle.selective_scan_backward(x, dt, A, Bm, Cm, D, dy, dhn, h0=h0, lengths=lens, **opt)
+    # A difference of two losses of size |loss|, each rounded to 2^-53 of its
+    # terms, over 2 eps = 2e-6 is off by up to |loss| 2^-52 / 2e-6 and as much
+    # again for the sums' own roundings. (Steps may be negative here without
+    # softplus: a state that grows by exp(-d A) reaches 1e9.)
+    noise = abs(loss()) * 2.0 ** -52 / 1e-6
+    for name, v in (("x", x), ("dt", dt), ("A", A), ("B", Bm), ("C", Cm), ("D", D), ("z", opt["z"]),
+                    ("dt_bias", opt["dt_bias"]), ("h0", h0)):
+        if v is not None:
+            assert np.allclose(g[name], _differences(loss, v), atol=2e-7 + noise), name
+    # a row without steps passes its state and its gradient through
+    assert np.array_equal(oracle.selective_scan(x, dt, A, Bm, Cm, D, h0=h0, lengths=lens, **opt)[1][1], h0[1])
+    assert np.array_equal(g["h0"][1], dhn[1])
+
+
+def test_selective_scan_of_one_state_is_a_gated_scan():
+    """N = 1, A = -1, B = C = 1 and unit-free inputs: h = a h + u with
+    a = sigma(f) for d = -log sigma(f), u = (1 - sigma(f)) x."""
+    rng = np.random.default_rng(5)
+    T, B, H = 6, 2, 3
+    x, f = rng.standard_normal((2, T, B, H))
+    d = np.log1p(np.exp(-f))
+    one = np.ones((T, B, 1, 1))
+    u = x * (1 - np.exp(-d)) / d
+    assert np.allclose(oracle.selective_scan(u, d, -np.ones((H, 1)), one, one, soft=False)[0],
+                       oracle.gated_scan(x, f)[0], atol=1e-12)
+
+
+def test_selective_layout(tmp_path):
+    _layouts(tmp_path, ["RnnSelectiveScanDesc", "RnnSelectiveScanIO", "RnnSelectiveScanGrads"])
+
+
+def _selective(**kw):
+    v = dict(dtype=0, T=300, B=4, H=8, N=16, G=2, softplus=1, gate=1, x_t=32, x_b=8, dt_t=32, dt_b=8, z_t=32, z_b=8,
+             B_t=128, B_b=32, B_g=16, C_t=128, C_b=32, C_g=16)
+    v.update(kw)
+    return gss.RnnSelectiveScanDesc(*v.values())
+
+
+_SEL_SIZES = ("rnn_selective_scan_workspace_bytes", "rnn_selective_scan_reserve_bytes",
+              "rnn_selective_scan_backward_workspace_bytes")
+
+
+@pytest.mark.parametrize("kw,expect", [
+    ({}, OK), ({"dtype": 1}, OK), ({"N": 1}, OK), ({"N": 64}, OK), ({"G": 8}, OK), ({"softplus": 0, "gate": 0}, OK),
+    ({"gate": 0, "z_t": -1}, OK), ({"x_b": 0}, OK),
+    ({"dtype": 3}, E_UNSUPPORTED), ({"N": 65}, E_UNSUPPORTED), ({"N": 0}, E_SHAPE), ({"G": 3}, E_SHAPE), ({"G": 0}, E_SHAPE),
+    ({"softplus": 2}, E_SHAPE), ({"gate": -1}, E_SHAPE), ({"z_t": -1}, E_SHAPE), ({"B_g": -1}, E_SHAPE), ({"C_t": -8}, E_SHAPE),
+    ({"x_t": -1}, E_SHAPE), ({"dt_b": -1}, E_SHAPE), ({"T": 0}, E_SHAPE), ({"B": 0}, E_SHAPE), ({"H": 0}, E_SHAPE),
+    ({"T": 2147483647}, E_SHAPE), ({"B": 1 << 20, "H": 4096, "G": 1}, E_SHAPE), ({"B": 2147483647}, E_SHAPE),
+    ({"B": 1, "H": 1 << 26, "G": 1, "N": 64}, E_SHAPE), ({"T": 1 << 24, "B": 4, "G": 2}, E_SHAPE),
+    ({"T": 2147483000, "H": 2147483640, "G": 1, "B": 2147483647}, E_SHAPE),
+])
+def test_selective_desc(kw, expect):
+    n = ctypes.c_size_t(0)
+    for fn in _SEL_SIZES:
+        assert getattr(ops._lib(), fn)(ctypes.byref(_selective(**kw)), ctypes.byref(n)) == expect
+    if expect == OK:
+        for fn in _SEL_SIZES:
+            assert getattr(ops._lib(), fn)(ctypes.byref(_selective(**kw)), None) == E_NULL
+
+
+def test_selective_sizes():
+    def size(fn, **kw):
+        n = ctypes.c_size_t(0)
+        assert getattr(ops._lib(), fn)(ctypes.byref(_selective(**kw)), ctypes.byref(n)) == OK
+        return n.value
+
+    # the reserve: a state (N rounded up to 4, 8, 16, 32 or 64) at every 16th step
+    assert size(_SEL_SIZES[1]) == 19 * 4 * 8 * 16 * 4 and size(_SEL_SIZES[1], T=16, N=17) == 4 * 8 * 32 * 4
+    # one tile of channels over a long time is cut into segments; a few steps are not
+    assert size(_SEL_SIZES[0], T=20000) > 0 and size(_SEL_SIZES[0], T=100) == 0
+    assert size(_SEL_SIZES[0], T=20000, B=64, H=2048, G=1) == 0
+
+
+def test_selective_pointers():
+    L = ops._lib()
+    d = _selective(T=20000)
+    sizes = []
+    for fn in _SEL_SIZES:
+        n = ctypes.c_size_t(0)
+        assert getattr(L, fn)(ctypes.byref(d), ctypes.byref(n)) == OK and n.value > 0
+        sizes.append(n.value)
+    ws, rs, bs = sizes
+
+    def io(**kw):
+        v = dict(x=ADDR, dt=ADDR, z=ADDR, Bm=ADDR, Cm=ADDR, A=ADDR, D=ADDR, dt_bias=ADDR, lengths=None, h0=None, y=ADDR,
+                 h_n=ADDR)
+        v.update(kw)
+        return ctypes.byref(gss.RnnSelectiveScanIO(*v.values()))
+
+    def fwd(ptr=ADDR, size=ws, **kw):
+        return L.rnn_selective_scan(ctypes.byref(d), io(**kw), ptr, size, None)
+
+    for k in ("x", "dt", "z", "Bm", "Cm", "A", "y"):
+        assert fwd(**{k: None}) == E_NULL, k
+    for k in ("x", "dt", "z", "Bm", "Cm", "A", "D", "dt_bias", "lengths", "h0", "y", "h_n"):
+        assert fwd(**{k: ADDR + 2}) == E_ALIGN, k
+    assert fwd(ptr=None) == E_WORKSPACE and fwd(size=ws - 1) == E_WORKSPACE and fwd(ptr=ADDR + 8) == E_ALIGN
+    assert L.rnn_selective_scan(ctypes.byref(d), None, ADDR, ws, None) == E_NULL
+    assert L.rnn_selective_scan(None, io(), ADDR, ws, None) == E_NULL
+
+    def train(ptr=ADDR, size=rs):
+        return L.rnn_selective_scan_train(ctypes.byref(d), io(), ptr, size, ADDR, ws, None)
+
+    assert train(ptr=None) == E_WORKSPACE and train(size=rs - 1) == E_WORKSPACE
+
+    def bwd(ptr=ADDR, size=bs, rptr=ADDR, rsize=rs, **kw):
+        v = dict(dy=ADDR, dh_n=None, dx=ADDR, ddt=ADDR, dz=ADDR, dB=ADDR, dC=ADDR, dA=ADDR, dD=ADDR, ddt_bias=ADDR, dh0=ADDR)
+        v.update(kw)
+        return L.rnn_selective_scan_backward(ctypes.byref(d), io(), ctypes.byref(gss.RnnSelectiveScanGrads(*v.values())), rptr,
+                                             rsize, ptr, size, None)
+
+    for k in ("dy", "dx", "ddt", "dz", "dB", "dC", "dA"):
+        assert bwd(**{k: None}) == E_NULL, k
+    for k in ("dy", "dh_n", "dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0"):
+        assert bwd(**{k: ADDR + 1}) == E_ALIGN, k
+    assert bwd(ptr=None) == E_WORKSPACE and bwd(size=bs - 1) == E_WORKSPACE and bwd(rsize=rs - 1) == E_WORKSPACE
+    assert L.rnn_selective_scan_backward(ctypes.byref(d), io(), None, ADDR, rs, ADDR, bs, None) == E_NULL
+    if not torch.cuda.is_available():
+        assert fwd() == E_DEVICE and train() == E_DEVICE and bwd() == E_DEVICE
+        assert bwd(dD=None, ddt_bias=None, dh0=None) == E_DEVICE and fwd(D=None, dt_bias=None, h_n=None) == E_DEVICE
+
+
+def test_selective_python_refusals():
+    x, A, B = torch.zeros(4, 2, 8), torch.zeros(8, 4), torch.zeros(4, 2, 1, 4)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        gss.selective_scan(x, x, A, B, B)
+    with pytest.raises(ValueError, match="dimensions"):
+        gss.selective_scan(x[0], x, A, B, B)
+    with pytest.raises(ValueError, match="must be a tensor"):
+        gss.selective_scan(None, x, A, B, B)
