@@ -34,4 +34,5 @@ from .state_block_ops import (  # noqa: F401
     RnnCausalConvDesc, RnnCausalConvIO, RnnCausalConvGrads, causal_conv, causal_conv_train, causal_conv_backward,
     RnnSelectiveScanDesc, RnnSelectiveScanIO, RnnSelectiveScanGrads, selective_scan, selective_scan_train,
     selective_scan_backward,
+    RnnFeedForwardDesc, RnnFeedForwardIO, RnnFeedForwardGrads, feed_forward, feed_forward_train, feed_forward_backward,
 )

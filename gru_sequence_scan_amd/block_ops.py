@@ -14,7 +14,7 @@ import torch
 from . import binding
 from .binding import DTYPES, RnnError, _check, _dense
 
-_P, _I32, _I64, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
 class RnnNormDesc(ctypes.Structure):

@@ -1,0 +1,252 @@
+// Gated feed-forward: how its products are tiled and split, the kernels for
+// few rows, and the copies and sums around the products
+// (feed_forward_gemm.hpp).
+//
+//   g | u = x W_in^T,  h = act(g) u,  y = h W_out^T (+ residual)
+//
+//   dh = dy W_out,  dg = dh u act'(g),  du = dh act(g)
+//   dx = [dg du] W_in,  dW_in = [dg du]^T x,  dW_out = dy^T h
+//
+// g and u meet in the first product's accumulators and dg and du come out of
+// dh's: neither g and u (in the forward alone) nor dh is ever in memory. h, dg
+// and du are rounded to the storage type once, where they leave the
+// accumulators: they are operands of matrix instructions of that type. So y,
+// dx and the weights' gradients carry one rounding of their terms beside
+// their own, sqrt(2) times the latter alone. Training keeps g and u in fp32
+// (8 bytes a hidden unit and row): rounded, they would put two more roundings
+// into every gradient.
+#include <cmath>
+
+#include "attention_common.hpp"
+#include "feed_forward_gemm.hpp"
+
+namespace rnnk {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Few rows. The weights' way from memory is what counts: a workgroup takes 16
+// hidden units (32 rows of W_in), or 16 outputs, over all rows of x, its waves
+// divide the summed dimension, and their sums meet in LDS. The weights are the
+// first operand of the 16x16 instructions and go straight from memory into
+// registers; a result lane holds four neighbouring hidden units of one row.
+// ---------------------------------------------------------------------------
+constexpr int kInWaves = 8, kOutWaves = 16;
+
+template <typename DT>
+__device__ __forceinline__ void store4(DT* p, const f32x4& v, int n) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (r < n) p[r] = from_f32<DT>(v[r]);
+}
+
+// acc[w][t] += the weights' rows (w of 16 each) times 16 rows of x (t), over
+// this wave's share of the steps of 32.
+template <typename DT, int NW, int MT, int WAVES, int DEEP>
+__device__ __forceinline__ void few_product(f32x4 (&acc)[NW][MT], const DT* (&wrow)[NW], const DT* (&xrow)[MT], int K, int KX,
+                                            bool wvec, bool xvec, int wave, int group) {
+  const int steps = (K + 31) / 32;
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[w][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = wave; s0 < steps; s0 += WAVES * DEEP) {
+    Frag<DT> fw[DEEP][NW], fx[DEEP][MT];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      const int col = (s0 + d * WAVES) * 32 + 8 * group;  // past K: zeros
+#pragma unroll
+      for (int w = 0; w < NW; ++w) fw[d][w] = load8<DT, false>(wrow[w], col, K, wvec);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) fx[d][t] = load8<DT, false>(xrow[t], col, KX, xvec);
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[w][t] = mma(fw[d][w], fx[d][t], acc[w][t]);
+  }
+}
+
+template <typename DT, int MT>
+__global__ __launch_bounds__(kInWaves * 64) void feed_few_in_kernel(FeedFewArgs a) {
+  __shared__ f32x4 sums[kInWaves][2 * MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, group = lane >> 4;
+  const int f0 = blockIdx.x * 16;
+  const DT *wrow[2], *xrow[MT];
+  const int f = f0 + i < a.F ? f0 + i : a.F - 1;
+  wrow[0] = (const DT*)a.w_in + (int64_t)f * a.ld_in;
+  wrow[1] = (const DT*)a.w_in + ((int64_t)a.F + f) * a.ld_in;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = 16 * t + i < a.rows ? 16 * t + i : a.rows - 1;
+    xrow[t] = (const DT*)a.x + m * a.ldx;
+  }
+  f32x4 acc[2][MT];
+  few_product<DT, 2, MT, kInWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.n, a.n, a.vec, a.vec, wave, group);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    sums[wave][t][lane] = acc[0][t];
+    sums[wave][MT + t][lane] = acc[1][t];
+  }
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 g = sums[0][wave][lane], u = sums[0][MT + wave][lane];
+#pragma unroll
+  for (int k = 1; k < kInWaves; ++k) {
+    g += sums[k][wave][lane];
+    u += sums[k][MT + wave][lane];
+  }
+  const int m = 16 * wave + i, fo = f0 + 4 * group;
+  f32x4 h;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) h[r] = fo + r < a.F ? activate(g[r], a.act).act * u[r] : 0.f;
+  if (m < a.rows) store4((DT*)a.h + (int64_t)m * a.Fp + fo, h, a.Fp - fo);
+}
+
+template <typename DT, int MT>
+__global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArgs a) {
+  __shared__ f32x4 sums[kOutWaves][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, group = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const DT *wrow[1], *xrow[MT];
+  wrow[0] = (const DT*)a.w_out + (int64_t)(n0 + i < a.n_out ? n0 + i : a.n_out - 1) * a.ld_out;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = 16 * t + i < a.rows ? 16 * t + i : a.rows - 1;
+    xrow[t] = (const DT*)a.h + (int64_t)m * a.Fp;
+  }
+  f32x4 acc[1][MT];
+  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, a.vec, true, wave, group);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) sums[wave][t][lane] = acc[0][t];
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 y = sums[0][wave][lane];
+#pragma unroll
+  for (int k = 1; k < kOutWaves; ++k) y += sums[k][wave][lane];
+  const int m = 16 * wave + i, n = n0 + 4 * group;
+  if (m >= a.rows) return;
+  if (a.residual) {
+    const DT* r = (const DT*)a.residual + m * a.ldr + n;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + k < a.n_out) y[k] += to_f32<DT>(r[k]);
+  }
+  store4((DT*)a.y + (int64_t)m * a.n_out + n, y, a.n_out - n);
+}
+
+template <typename DT, int MT>
+hipError_t few(const FeedFewArgs& a, hipStream_t st) {
+  launch_kernel(feed_few_in_kernel<DT, MT>, dim3((unsigned)((a.Fp + 15) / 16)), dim3(kInWaves * 64), 0, st, a);
+  launch_kernel(feed_few_out_kernel<DT, MT>, dim3((unsigned)((a.n_out + 15) / 16)), dim3(kOutWaves * 64), 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename DT>
+hipError_t few_rows(const FeedFewArgs& a, hipStream_t st) {
+  return a.rows <= 16 ? few<DT, 1>(a, st) : a.rows <= 32 ? few<DT, 2>(a, st) : few<DT, 4>(a, st);
+}
+
+// ---------------------------------------------------------------------------
+// Copies and sums around the products
+// ---------------------------------------------------------------------------
+template <typename DT>
+__global__ __launch_bounds__(256) void feed_pack_kernel(const DT* from, int64_t ld, int64_t rows, int cols, DT* to, int pitch) {
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    for (int c = threadIdx.x; c < pitch; c += 256) to[row * pitch + c] = c < cols ? from[row * ld + c] : (DT)0.f;
+}
+
+// out = residual + the partial products, in their order: four columns a
+// thread, or one where rows are not multiples of four.
+template <typename DT, int E>
+__global__ __launch_bounds__(256) void feed_join_kernel(FeedArgs a) {
+  const int64_t plane = (int64_t)a.M * a.N, count = plane / E;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i * E / a.N, n = i * E % a.N;
+    int64_t row = m;
+    if (a.rows_split) {
+      const bool second = m >= a.rows_split;
+      row = second ? m - a.rows_split + a.F : m;
+      if (row >= (second ? 2 * (int64_t)a.F : a.F)) continue;
+    }
+    float sum[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+      const float* p = a.part + s * plane + i * E;
+      if constexpr (E == 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += v[e];
+      } else {
+        sum[0] += p[0];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (a.residual) sum[e] += to_f32<DT>(((const DT*)a.residual)[row * a.ldr + n + e]);
+      ((DT*)a.out)[row * a.ldo + n + e] = from_f32<DT>(sum[e]);
+    }
+  }
+}
+
+template <typename DT>
+hipError_t join(const FeedArgs& a, hipStream_t st) {
+  const bool four = a.N % 4 == 0;
+  const int64_t blocks = ((int64_t)a.M * a.N / (four ? 4 : 1) + 255) / 256;
+  const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
+  if (four)
+    launch_kernel(feed_join_kernel<DT, 4>, grid, dim3(256), 0, st, a);
+  else
+    launch_kernel(feed_join_kernel<DT, 1>, grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
+  const double rows = p.big ? 256 : 128, cols = op == kFeedIn ? rows / 2 : rows;
+  return std::ceil((double)M / rows) * std::ceil((double)N / cols);
+}
+
+// The tile and the split with the shortest expected time: rounds of the
+// workgroups that the device holds, times steps, plus the partial products'
+// way through memory. Products whose results are used on the way out of the
+// accumulators are not split.
+FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, int cus) {
+  FeedPlan best{0, 1};
+  double least = 0.0;
+  for (int big = 0; big < 2; ++big) {
+    FeedPlan p{big, 1};
+    const double tiles = feed_tiles(p, M, N, op), resident = big ? cus : 2.0 * cus;
+    for (int want = 1; want <= (op == kFeedIn || op == kFeedDh ? 1 : 32) && want <= steps; ++want) {
+      const int each = (steps + want - 1) / want;
+      p.splits = (steps + each - 1) / each;
+      if (p.splits != want) continue;
+      const double rounds = std::ceil(tiles * want / resident);
+      double us = rounds * (each * (big ? 1.7 : 1.1) + (big ? 5.0 : 3.0));
+      if (want > 1) us += 4.0 + (double)want * M * N * 8.0 / 4e6;
+      if (least == 0.0 || us < least) {
+        least = us;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
+hipError_t launch_feed_few(const FeedFewArgs& a, bool bf, hipStream_t st) { return bf ? few_rows<bf16>(a, st) : few_rows<float>(a, st); }
+
+hipError_t launch_feed_pack(const void* from, int64_t ld, int64_t rows, int cols, void* to, int pitch, bool bf, hipStream_t st) {
+  const dim3 grid((unsigned)(rows < 8192 ? rows : 8192));
+  if (bf)
+    launch_kernel(feed_pack_kernel<bf16>, grid, dim3(256), 0, st, (const bf16*)from, ld, rows, cols, (bf16*)to, pitch);
+  else
+    launch_kernel(feed_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)from, ld, rows, cols, (float*)to, pitch);
+  return hipGetLastError();
+}
+
+hipError_t launch_feed_join(const FeedArgs& a, bool bf, hipStream_t st) { return bf ? join<bf16>(a, st) : join<float>(a, st); }
+
+}  // namespace rnnk

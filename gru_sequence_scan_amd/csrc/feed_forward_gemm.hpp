@@ -1,0 +1,392 @@
+// The products of the gated feed-forward, one kernel template.
+//
+// C[m, n] = sum_k A[m, k] B[n, k]: an operand lies with k running along its
+// rows, or across them. A workgroup makes a tile of 256 x 256 (eight waves of
+// 128 x 64) or 128 x 128 (four of 64 x 64) outputs on the 32x32 matrix
+// instructions, k in steps of 128 bytes. A step's operands go straight from
+// memory into LDS (16 bytes a lane), two steps deep: while one is multiplied
+// the next is on its way, and one barrier a step says that it has arrived and
+// that the other half may be overwritten.
+//
+// In LDS an operand that runs along k is [rows][128 bytes], the 16-byte chunk
+// c of row r at c ^ (r & 7), so that eight neighbouring rows' reads of a chunk
+// fall on different banks. One that runs across is [k][tile columns]; bf16
+// takes it through the transposing read (4 x 16 blocks), whose 32-byte columns
+// lie at u ^ kTurn(k & 3) for the same reason. The order of k inside a step is
+// the same for both operands, which is all that a product asks of it.
+//
+// What is behind a row's end along k is zero in LDS: the last step of such an
+// operand goes through registers. Rows and columns behind the output's are
+// some row or column again and are not stored.
+//
+// Workgroups stay for several tiles: the first step of the next one is
+// fetched while the last of this one is multiplied and its results are
+// stored. Neighbouring tiles (8 rows of tiles, then the next column) go to one
+// XCD at a time, whose L2 they share.
+#pragma once
+
+#include "../../include/rnn.h"
+#include "device_common.hpp"
+#include "state_block_kernels.hpp"
+
+namespace rnnk {
+namespace {
+
+typedef short feed_s16x4 __attribute__((ext_vector_type(4)));
+typedef short feed_s16x8 __attribute__((ext_vector_type(8)));
+
+// act(g) and its slope. gelu(g) = g (1 + tanh(u)) / 2 = g sigma(2 u).
+struct Activated {
+  float act, slope;
+};
+__device__ __forceinline__ Activated activate(float g, int kind) {
+  Activated r;
+  if (kind == RNN_ACT_GELU_TANH) {
+    constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float g2 = g * g, u = c * g * __builtin_fmaf(0.044715f, g2, 1.0f);
+    const float s = fsigmoid(u), no = fsigmoid(-u);
+    r.act = g * s;
+    r.slope = __builtin_fmaf(g * s * no, c * __builtin_fmaf(3.0f * 0.044715f, g2, 1.0f), s);
+  } else {
+    const float s = fsigmoid(g), no = fsigmoid(-g);
+    r.act = kind == RNN_ACT_SIGMOID ? s : g * s;
+    r.slope = kind == RNN_ACT_SIGMOID ? s * no : __builtin_fmaf(g * s, no, s);
+  }
+  return r;
+}
+
+template <int BIG>
+struct FeedTile {
+  static constexpr int kRows = BIG ? 256 : 128;       // of either operand
+  static constexpr int kThreads = BIG ? 512 : 256;
+  static constexpr int kWavesN = BIG ? 4 : 2;         // waves across, two waves down
+  static constexpr int MI = BIG ? 4 : 2;              // 32-row blocks of a wave; two across
+  static constexpr int kBytes = kRows * 128;          // one operand's step
+  static constexpr int kLds = 2 * 2 * kBytes;
+  static constexpr int kTimes = kBytes / 16 / kThreads;  // 16-byte loads of a thread: 4
+};
+
+// 16-byte loads that bring an operand's step into LDS.
+template <typename DT, int BIG, bool ALONG>
+struct Operand {
+  using T = FeedTile<BIG>;
+  static constexpr int E = 16 / (int)sizeof(DT);              // elements of a chunk
+  static constexpr int kStep = 128 / (int)sizeof(DT);         // k of a step
+  static constexpr int kChunks = T::kRows / E;                // of a k row (across)
+  static constexpr int kSweep = ALONG ? T::kThreads / 8 : T::kThreads / kChunks;  // rows between a thread's loads
+  const DT* src[ALONG ? T::kTimes : 1];
+  int chunk;                                                  // first k (along) or k row (across) of this thread in a step
+  // 32-byte column u of k row k is at u ^ turn(k): four rows on different
+  // banks, also where two neighbouring columns are read at once
+  static __device__ __forceinline__ int turn(int k) { return (k & 3) ^ ((k & 1) << 2); }
+
+  // The tile's rows from row0 on, `rows` there are; PAIRS: 32 of them, then 32
+  // that are `apart` rows behind those, then the next 32 and so on.
+  template <bool PAIRS>
+  __device__ __forceinline__ void place_along(const void* base, int64_t ld, int row0, int rows, int apart) {
+    const int t = threadIdx.x, r0 = t >> 3, c = (t & 7) ^ (r0 & 7);
+    chunk = c * E;
+#pragma unroll
+    for (int i = 0; i < T::kTimes; ++i) {
+      const int r = r0 + i * kSweep, at = row0 + (PAIRS ? (r >> 6) * 32 + (r & 31) : r);
+      const int row = (at < rows ? at : rows - 1) + (PAIRS && (r & 32) ? apart : 0);
+      src[ALONG ? i : 0] = (const DT*)base + (int64_t)row * ld + chunk;
+    }
+  }
+  // The tile's columns from col0 on, `cols` there are in memory.
+  __device__ __forceinline__ void place_across(const void* base, int64_t ld, int col0, int cols) {
+    const int t = threadIdx.x, k = t / kChunks, pos = t % kChunks;
+    const int c = sizeof(DT) == 2 ? ((pos >> 1) ^ turn(k)) * 2 + (pos & 1) : pos;
+    chunk = k;
+    const int at = col0 + c * E;
+    src[0] = (const DT*)base + (int64_t)k * ld + (at + E <= cols ? at : cols - E);
+  }
+
+  __device__ __forceinline__ void fetch(char* lds, int k0, int64_t row0, int limit, int64_t ld) const {
+    // k0: the step's first k; row0: the operand's row of it (across); limit: how far k goes
+    char* wave_lds = lds + (threadIdx.x >> 6) * 1024;
+    if (k0 + kStep <= limit) {
+#pragma unroll
+      for (int i = 0; i < T::kTimes; ++i) {
+        const DT* p = ALONG ? src[ALONG ? i : 0] + k0 : src[0] + (row0 + i * kSweep) * ld;
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know LDS pointers and drops kernels over them
+        __builtin_amdgcn_global_load_lds(p, wave_lds + i * T::kThreads * 16, 16, 0, 0);
+#endif
+      }
+    } else {
+      u32x4 v[T::kTimes];
+#pragma unroll
+      for (int i = 0; i < T::kTimes; ++i) {
+        const int k = k0 + chunk + (ALONG ? 0 : i * kSweep);
+        v[i] = u32x4{0u, 0u, 0u, 0u};
+        if (k < limit) v[i] = *reinterpret_cast<const u32x4*>(ALONG ? src[ALONG ? i : 0] + k0 : src[0] + (row0 + i * kSweep) * ld);
+      }
+#pragma unroll
+      for (int i = 0; i < T::kTimes; ++i) *reinterpret_cast<u32x4*>(lds + (i * T::kThreads + threadIdx.x) * 16) = v[i];
+    }
+  }
+};
+
+// A wave's fragment of 32 rows for part s of a step (a quarter in both types).
+template <typename DT>
+struct FeedFrag;
+template <>
+struct FeedFrag<bf16> {
+  bf16x8 v;
+};
+template <>
+struct FeedFrag<float> {
+  float v[4];
+};
+
+template <bool ALONG, int ROWS>
+__device__ __forceinline__ void read_frag(FeedFrag<bf16>& f, const char* lds, int r0, int s, int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
+  if constexpr (ALONG) {
+    f.v = *reinterpret_cast<const bf16x8*>(lds + (r0 + l32) * 128 + (((2 * s + half) ^ (l32 & 7)) << 4));
+  } else {
+    typedef __attribute__((address_space(3))) feed_s16x4* LdsPtr;
+    const int i = lane & 15, unit = (r0 >> 4) + ((lane >> 4) & 1), k = 16 * s + 8 * half + (i >> 2);
+    const char* p = lds + k * (ROWS * 2) + ((unit ^ Operand<bf16, 1, false>::turn(k)) << 5) + ((i & 3) << 3);
+    const feed_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p));
+    const feed_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 4 * ROWS * 2));
+    f.v = __builtin_bit_cast(bf16x8, (feed_s16x8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+}
+template <bool ALONG, int ROWS>
+__device__ __forceinline__ void read_frag(FeedFrag<float>& f, const char* lds, int r0, int s, int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
+  if constexpr (ALONG) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(lds + (r0 + l32) * 128 + (((2 * s + half) ^ (l32 & 7)) << 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = v[e];
+  } else {
+    const float* p = reinterpret_cast<const float*>(lds) + (4 * (2 * s + half)) * ROWS + r0 + l32;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = p[e * ROWS];
+  }
+}
+
+__device__ __forceinline__ f32x16 feed_mma(const FeedFrag<bf16>& a, const FeedFrag<bf16>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 feed_mma(const FeedFrag<float>& a, const FeedFrag<float>& b, f32x16 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[e], b.v[e], c, 0, 0, 0);
+  return c;
+}
+
+// Waits for everything this wave has asked for, then for the other waves.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int OP>
+struct FeedShape {
+  static constexpr bool kAlongA = OP == kFeedIn || OP == kFeedOut || OP == kFeedDh || OP == kFeedDx;
+  static constexpr bool kAlongB = OP == kFeedIn || OP == kFeedOut;
+};
+
+// One piece of work: a tile of the output and a range of steps.
+struct FeedItem {
+  int m0, n0, split, k0, k1;
+};
+template <int BIG, int OP>
+__device__ __forceinline__ FeedItem feed_item(const FeedArgs& a, int tiles_m, int tiles_n, int id) {
+  constexpr int kRows = FeedTile<BIG>::kRows, kCols = OP == kFeedIn ? kRows / 2 : kRows;
+  const int tiles = tiles_m * tiles_n;
+  FeedItem w;
+  w.split = id / tiles;
+  int t = id % tiles;
+  constexpr int kGroup = 8;
+  const int per = kGroup * tiles_n, group = t / per, first = group * kGroup;
+  const int down = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+  t -= group * per;
+  w.m0 = (first + t % down) * kRows;
+  w.n0 = t / down * kCols;
+  const int each = (a.steps + a.splits - 1) / a.splits;
+  w.k0 = w.split * each;
+  w.k1 = a.steps - w.k0 < each ? a.steps : w.k0 + each;
+  return w;
+}
+
+template <typename DT, int BIG, int OP>
+__global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedArgs a, int tiles_m, int tiles_n) {
+  using T = FeedTile<BIG>;
+  using S = FeedShape<OP>;
+  constexpr int kStep = 128 / (int)sizeof(DT), MI = T::MI;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / T::kWavesN, wn = wave % T::kWavesN;
+  const int items = tiles_m * tiles_n * a.splits;
+  // this round's items of one XCD are neighbours
+  const int grid = gridDim.x, whole = grid / 8 * 8;
+  const int mine = (int)blockIdx.x < whole ? (blockIdx.x % 8) * (whole / 8) + blockIdx.x / 8 : blockIdx.x;
+  if (mine >= items) return;
+
+  Operand<DT, BIG, S::kAlongA> oa;
+  Operand<DT, BIG, S::kAlongB> ob;
+  auto place = [&](const FeedItem& w) {
+    if (S::kAlongA)
+      oa.template place_along<false>(a.A, a.lda, w.m0, a.M, 0);
+    else
+      oa.place_across(a.A, a.lda, w.m0, a.cols_a);
+    if (S::kAlongB)
+      ob.template place_along<OP == kFeedIn>(a.B, a.ldb, w.n0, OP == kFeedIn ? a.F : a.N, a.F);
+    else
+      ob.place_across(a.B, a.ldb, w.n0, a.cols_b);
+  };
+  auto fetch = [&](int kt, int half) {
+    char* at = lds + half * 2 * T::kBytes;
+    const int k = kt * kStep;
+    oa.fetch(at, k, k, a.KA, a.lda);
+    if constexpr (OP == kFeedDx) {  // rows of the gate's and of its partner's weights, F each
+      const bool second = k >= a.Fp;
+      ob.fetch(at + T::kBytes, second ? k - a.Fp : k, second ? k - a.Fp + a.F : k, a.F, a.ldb);
+    } else {
+      ob.fetch(at + T::kBytes, k, k, a.KB, a.ldb);
+    }
+  };
+
+  FeedItem w = feed_item<BIG, OP>(a, tiles_m, tiles_n, mine);
+  int half = 0;
+  place(w);
+  fetch(w.k0, 0);
+  for (int id = mine; id < items; id += grid) {
+    f32x16 acc[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    FeedItem next = w;
+    for (int kt = w.k0; kt < w.k1; ++kt) {
+      step_barrier();
+      if (kt + 1 < w.k1) {
+        fetch(kt + 1, half ^ 1);
+      } else if (id + grid < items) {
+        next = feed_item<BIG, OP>(a, tiles_m, tiles_n, id + grid);
+        place(next);
+        fetch(next.k0, half ^ 1);
+      }
+      const char* at = lds + half * 2 * T::kBytes;
+      FeedFrag<DT> fa[2][MI], fb[2][2];
+      auto read = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) read_frag<S::kAlongA, T::kRows>(fa[s & 1][i], at, wm * MI * 32 + i * 32, s, lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) read_frag<S::kAlongB, T::kRows>(fb[s & 1][j], at + T::kBytes, wn * 64 + j * 32, s, lane);
+      };
+      read(0);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s < 3) read(s + 1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = feed_mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+      }
+      half ^= 1;
+    }
+
+    // A lane holds column lane % 32 and rows 8 (v / 4) + 4 (lane / 32) + v % 4 of each block.
+    const int l32 = lane & 31, up = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int mb = w.m0 + wm * MI * 32 + i * 32 + 4 * up;
+      if constexpr (OP == kFeedIn) {
+        const int f = w.n0 + wn * 32 + l32;
+        if (f < a.Fp) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int64_t m = mb + 8 * (v >> 2) + (v & 3);
+            if (m < a.M) {
+              const bool on = f < a.F;
+              const float g = on ? acc[i][0][v] : 0.f, u = on ? acc[i][1][v] : 0.f;
+              ((DT*)a.out)[m * a.ldo + f] = from_f32<DT>(activate(g, a.act).act * u);
+              if (a.gu) {
+                a.gu[m * 2 * a.Fp + f] = g;
+                a.gu[m * 2 * a.Fp + a.Fp + f] = u;
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int n = w.n0 + wn * 64 + j * 32 + l32;
+          if (n >= a.N) continue;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int m = mb + 8 * (v >> 2) + (v & 3);
+            if (m >= a.M) continue;
+            const float val = acc[i][j][v];
+            if constexpr (OP == kFeedDh) {
+              const float* gu = a.gu + (int64_t)m * 2 * a.Fp + n;
+              const float g = gu[0], u = gu[a.Fp];
+              const Activated r = activate(g, a.act);
+              const bool on = n < a.F;
+              DT* out = (DT*)a.out + m * a.ldo + n;
+              out[0] = from_f32<DT>(on ? val * u * r.slope : 0.f);
+              out[a.Fp] = from_f32<DT>(on ? val * r.act : 0.f);
+            } else if (a.splits > 1) {
+              a.part[((int64_t)w.split * a.M + m) * a.N + n] = val;
+            } else {
+              int row = m;
+              if (OP == kFeedDwIn) {
+                const bool second = m >= a.Fp;
+                row = second ? m - a.Fp + a.F : m;
+                if (row >= (second ? 2 * a.F : a.F)) continue;
+              }
+              const float more = OP == kFeedOut && a.residual ? to_f32<DT>(((const DT*)a.residual)[row * a.ldr + n]) : 0.f;
+              ((DT*)a.out)[row * a.ldo + n] = from_f32<DT>(val + more);
+            }
+          }
+        }
+      }
+    }
+    w = next;
+  }
+}
+
+template <typename DT, int BIG, int OP>
+hipError_t launch_feed_op(const FeedArgs& a, hipStream_t st) {
+  using T = FeedTile<BIG>;
+  constexpr int kCols = OP == kFeedIn ? T::kRows / 2 : T::kRows;
+  const int tiles_m = (a.M + T::kRows - 1) / T::kRows, tiles_n = (a.N + kCols - 1) / kCols;
+  const int64_t items = (int64_t)tiles_m * tiles_n * a.splits;
+  constexpr int kResident = BIG ? 256 : 512;  // workgroups that a device of 256 compute units holds
+  auto kernel = feed_kernel<DT, BIG, OP>;
+  if (T::kLds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    if (e != hipSuccess) return e;
+  }
+  launch_kernel(kernel, dim3((unsigned)(items < kResident ? items : kResident)), dim3(T::kThreads), T::kLds, st, a, tiles_m,
+                tiles_n);
+  if (a.splits > 1) return launch_feed_join(a, sizeof(DT) == 2, st);
+  return hipGetLastError();
+}
+
+template <typename DT, int BIG>
+hipError_t launch_feed_tile(int op, const FeedArgs& a, hipStream_t st) {
+  switch (op) {
+    case kFeedIn: return launch_feed_op<DT, BIG, kFeedIn>(a, st);
+    case kFeedOut: return launch_feed_op<DT, BIG, kFeedOut>(a, st);
+    case kFeedDh: return launch_feed_op<DT, BIG, kFeedDh>(a, st);
+    case kFeedDx: return launch_feed_op<DT, BIG, kFeedDx>(a, st);
+    case kFeedDwIn: return launch_feed_op<DT, BIG, kFeedDwIn>(a, st);
+    default: return launch_feed_op<DT, BIG, kFeedDwOut>(a, st);
+  }
+}
+
+template <typename DT>
+hipError_t launch_feed_type(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t st) {
+  return p.big ? launch_feed_tile<DT, 1>(op, a, st) : launch_feed_tile<DT, 0>(op, a, st);
+}
+
+}  // namespace
+}  // namespace rnnk

@@ -154,6 +154,239 @@ int sel_forward(const RnnSelectiveScanDesc* d, const RnnSelectiveScanIO* io, voi
   return hip_status(launch_selective_scan(a, d->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------------------
+// Gated feed-forward
+// ---------------------------------------------------------------------------
+int validate(const RnnFeedForwardDesc* d) {
+  if (!d) return RNN_E_NULL;
+  if (!dtype_ok(d->dtype)) return RNN_E_UNSUPPORTED;
+  if (d->activation != RNN_ACT_SILU && d->activation != RNN_ACT_GELU_TANH && d->activation != RNN_ACT_SIGMOID)
+    return RNN_E_UNSUPPORTED;
+  if (d->rows < 1 || d->N < 1 || d->F < 1 || d->N_out < 1 || (d->aligned | 1) != 1) return RNN_E_SHAPE;
+  if (d->x_ld < d->N || d->in_ld < d->N || d->out_ld < d->F) return RNN_E_SHAPE;
+  // rows, columns and steps of the products are counted in 32 bits, and so are their tiles
+  constexpr int64_t most = 1 << 30;
+  if (d->rows > most || d->N > most || d->F > most / 2 - 64 || d->N_out > most) return RNN_E_SHAPE;
+  auto tiles = [](double m, double n) { return (m / 128.0 + 1.0) * (n / 64.0 + 1.0) * 32.0; };
+  const double r = (double)d->rows, n = d->N, f = 2.0 * d->F + 128.0, o = d->N_out;
+  if (std::fmax(std::fmax(tiles(r, f), tiles(r, o)), std::fmax(tiles(f, n), std::fmax(tiles(r, n), tiles(o, f)))) > 2147483647.0)
+    return RNN_E_SHAPE;
+  return RNN_OK;
+}
+
+struct FeedSizes {
+  int64_t m;                       // elements of 16 bytes
+  int Np, Fm, Op, Fp;              // N, F and N_out in whole 16 bytes; F in whole steps of 128 bytes
+  bool pack_x, pack_in, pack_out, pack_dy;
+  explicit FeedSizes(const RnnFeedForwardDesc* d) {
+    m = 16 / (int64_t)esize_of(d->dtype);
+    auto up = [](int64_t v, int64_t to) { return (int)((v + to - 1) / to * to); };
+    Np = up(d->N, m);
+    Fm = up(d->F, m);
+    Op = up(d->N_out, m);
+    Fp = up(d->F, 8 * m);
+    pack_x = !d->aligned || d->N % m || d->x_ld % m;
+    pack_in = !d->aligned || d->N % m || d->in_ld % m;
+    pack_out = !d->aligned || d->F % m || d->out_ld % m;
+    pack_dy = !d->aligned || d->N_out % m;
+  }
+  int steps(int64_t k) const { return (int)((k + 8 * m - 1) / (8 * m)); }
+};
+
+bool feed_few(const RnnFeedForwardDesc* d) { return d->rows <= kFeedFewRows; }
+
+// Where things lie in a workspace, one after the other.
+struct Layout {
+  size_t bytes = 0;
+  size_t take(size_t n) {
+    const size_t at = bytes;
+    bytes += round16(n);
+    return at;
+  }
+};
+
+struct FeedSpace {
+  size_t x, in, out, dy, h, dp, part, bytes;
+};
+
+FeedPlan feed_plan_of(const RnnFeedForwardDesc* d, const FeedSizes& s, int op) {
+  switch (op) {
+    case kFeedIn: return feed_plan(op, d->rows, s.Fp, s.steps(s.Np), kPlanCus);
+    case kFeedOut: return feed_plan(op, d->rows, d->N_out, s.steps(s.Fm), kPlanCus);
+    case kFeedDh: return feed_plan(op, d->rows, s.Fp, s.steps(s.Op), kPlanCus);
+    case kFeedDx: return feed_plan(op, d->rows, d->N, s.steps(2 * (int64_t)s.Fp), kPlanCus);
+    case kFeedDwIn: return feed_plan(op, 2 * (int64_t)s.Fp, d->N, s.steps(d->rows), kPlanCus);
+    default: return feed_plan(op, d->N_out, d->F, s.steps(d->rows), kPlanCus);
+  }
+}
+size_t feed_part(const FeedPlan& p, size_t M, size_t N) { return p.splits > 1 ? p.splits * M * N * sizeof(float) : 0; }
+
+// The forward (serving or training) or the backward pass.
+FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
+  const FeedSizes s(d);
+  const size_t e = (size_t)esize_of(d->dtype), rows = (size_t)d->rows;
+  Layout l;
+  FeedSpace a{};
+  if (!train && !back && feed_few(d)) {  // any alignment is taken there
+    a.h = l.take(rows * s.Fp * e);
+    a.bytes = l.bytes;
+    return a;
+  }
+  if (s.pack_x) a.x = l.take(rows * s.Np * e);
+  if (s.pack_in) a.in = l.take(2 * (size_t)d->F * s.Np * e);
+  if (s.pack_out) a.out = l.take((size_t)d->N_out * s.Fm * e);
+  size_t part = 0;
+  if (back) {
+    if (s.pack_dy) a.dy = l.take(rows * s.Op * e);
+    a.dp = l.take(rows * 2 * s.Fp * e);
+    part = feed_part(feed_plan_of(d, s, kFeedDx), rows, d->N);
+    const size_t in = feed_part(feed_plan_of(d, s, kFeedDwIn), 2 * (size_t)s.Fp, d->N);
+    const size_t out = feed_part(feed_plan_of(d, s, kFeedDwOut), d->N_out, d->F);
+    if (part < in) part = in;
+    if (part < out) part = out;
+  } else {
+    if (!train) a.h = l.take(rows * s.Fp * e);
+    part = feed_part(feed_plan_of(d, s, kFeedOut), rows, d->N_out);
+  }
+  a.part = l.take(part);
+  a.bytes = l.bytes;
+  return a;
+}
+
+// g and u, then h.
+size_t feed_gu_bytes(const RnnFeedForwardDesc* d) { return (size_t)d->rows * 2 * FeedSizes(d).Fp * sizeof(float); }
+size_t feed_reserve(const RnnFeedForwardDesc* d) {
+  return feed_gu_bytes(d) + round16((size_t)d->rows * FeedSizes(d).Fp * esize_of(d->dtype));
+}
+
+// One pass over the rows of the operands that the kernels cannot take as they are.
+struct FeedOperand {
+  const void* p;
+  int64_t ld;
+};
+hipError_t feed_packed(FeedOperand* o, bool pack, int64_t rows, int cols, int pitch, void* to, bool bf, hipStream_t st) {
+  if (!pack) return hipSuccess;
+  const hipError_t e = launch_feed_pack(o->p, o->ld, rows, cols, to, pitch, bf, st);
+  o->p = to;
+  o->ld = pitch;
+  return e;
+}
+
+int feed_io(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io) {
+  const size_t e = d->aligned ? 16 : (size_t)esize_of(d->dtype);
+  if (!io) return RNN_E_NULL;
+  RETURN_IF_BAD(need(io->x, e));
+  RETURN_IF_BAD(need(io->w_in, e));
+  return need(io->w_out, e);
+}
+
+#define RETURN_IF_HIP(expr)                   \
+  do {                                        \
+    if ((expr) != hipSuccess) return RNN_E_HIP; \
+  } while (0)
+
+int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* reserve, void* ws, size_t ws_bytes, void* stream) {
+  RETURN_IF_BAD(feed_io(d, io));
+  const size_t e = (size_t)esize_of(d->dtype);
+  RETURN_IF_BAD(optional(io->residual, e));
+  if (io->residual && d->residual_ld < d->N_out) return RNN_E_SHAPE;
+  RETURN_IF_BAD(need(io->y, e));
+  const FeedSpace at = feed_space(d, reserve != nullptr, false);
+  RETURN_IF_BAD(need_memory(ws, ws_bytes, at.bytes));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
+  const FeedSizes s(d);
+  const bool bf = d->dtype == RNN_DTYPE_BF16;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  char* mem = static_cast<char*>(ws);
+  if (!reserve && feed_few(d)) {
+    FeedFewArgs f{};
+    f.rows = (int)d->rows; f.n = d->N; f.F = d->F; f.n_out = d->N_out; f.act = d->activation;
+    f.x = io->x; f.ldx = d->x_ld; f.w_in = io->w_in; f.ld_in = d->in_ld; f.w_out = io->w_out; f.ld_out = d->out_ld;
+    f.residual = io->residual; f.ldr = io->residual ? d->residual_ld : 0;
+    f.h = mem + at.h; f.Fp = s.Fp; f.y = io->y;
+    f.vec = !s.pack_x && !s.pack_in && !s.pack_out;
+    return hip_status(launch_feed_few(f, bf, st));
+  }
+  FeedOperand x{io->x, d->x_ld}, in{io->w_in, d->in_ld}, out{io->w_out, d->out_ld};
+  RETURN_IF_HIP(feed_packed(&x, s.pack_x, d->rows, d->N, s.Np, mem + at.x, bf, st));
+  RETURN_IF_HIP(feed_packed(&in, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in, bf, st));
+  RETURN_IF_HIP(feed_packed(&out, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out, bf, st));
+  void* h = reserve ? static_cast<char*>(reserve) + feed_gu_bytes(d) : mem + at.h;
+  auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
+  FeedArgs a{};
+  a.F = d->F; a.Fp = s.Fp; a.act = d->activation;
+  a.M = (int)d->rows; a.N = s.Fp;
+  a.A = x.p; a.lda = x.ld; a.KA = s.Np;
+  a.B = in.p; a.ldb = in.ld; a.KB = s.Np;
+  a.steps = s.steps(s.Np);
+  a.out = h; a.ldo = s.Fp; a.gu = static_cast<float*>(reserve);
+  FeedPlan p = feed_plan_of(d, s, kFeedIn);
+  a.splits = p.splits;
+  RETURN_IF_HIP(launch(kFeedIn, a, p, st));
+  a.N = d->N_out;
+  a.A = h; a.lda = s.Fp; a.KA = s.Fm;
+  a.B = out.p; a.ldb = out.ld; a.KB = s.Fm;
+  a.steps = s.steps(s.Fm);
+  a.out = io->y; a.ldo = d->N_out; a.gu = nullptr;
+  a.residual = io->residual; a.ldr = io->residual ? d->residual_ld : 0;
+  p = feed_plan_of(d, s, kFeedOut);
+  a.splits = p.splits; a.part = reinterpret_cast<float*>(mem + at.part);
+  return hip_status(launch(kFeedOut, a, p, st));
+}
+
+int feed_backward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, const RnnFeedForwardGrads* g, const void* reserve,
+                  char* mem, const FeedSpace& at, hipStream_t st) {
+  const FeedSizes s(d);
+  const bool bf = d->dtype == RNN_DTYPE_BF16;
+  const int rows = (int)d->rows;
+  FeedOperand x{io->x, d->x_ld}, in{io->w_in, d->in_ld}, out{io->w_out, d->out_ld}, dy{g->dy, d->N_out};
+  RETURN_IF_HIP(feed_packed(&x, s.pack_x, d->rows, d->N, s.Np, mem + at.x, bf, st));
+  RETURN_IF_HIP(feed_packed(&in, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in, bf, st));
+  RETURN_IF_HIP(feed_packed(&out, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out, bf, st));
+  RETURN_IF_HIP(feed_packed(&dy, s.pack_dy, d->rows, d->N_out, s.Op, mem + at.dy, bf, st));
+  auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
+  void* dp = mem + at.dp;
+  const void* h = static_cast<const char*>(reserve) + feed_gu_bytes(d);
+  FeedArgs base{};
+  base.F = d->F; base.Fp = s.Fp; base.act = d->activation;
+  base.part = reinterpret_cast<float*>(mem + at.part);
+  auto run = [&](int op, FeedArgs& a) {
+    const FeedPlan p = feed_plan_of(d, s, op);
+    a.splits = p.splits;
+    return launch(op, a, p, st);
+  };
+  FeedArgs a = base;  // [dg, du]
+  a.M = rows; a.N = s.Fp;
+  a.A = dy.p; a.lda = dy.ld; a.KA = s.Op;
+  a.B = out.p; a.ldb = out.ld; a.KB = d->N_out; a.cols_b = s.Fm;
+  a.steps = s.steps(s.Op);
+  a.out = dp; a.ldo = 2 * (int64_t)s.Fp;
+  a.gu = const_cast<float*>(static_cast<const float*>(reserve));
+  RETURN_IF_HIP(run(kFeedDh, a));
+  a = base;           // dx
+  a.M = rows; a.N = d->N;
+  a.A = dp; a.lda = 2 * (int64_t)s.Fp; a.KA = 2 * s.Fp;
+  a.B = in.p; a.ldb = in.ld; a.KB = d->F; a.cols_b = s.Np;
+  a.steps = s.steps(2 * (int64_t)s.Fp);
+  a.out = g->dx; a.ldo = d->N;
+  RETURN_IF_HIP(run(kFeedDx, a));
+  a = base;           // dw_in
+  a.M = 2 * s.Fp; a.N = d->N;
+  a.A = dp; a.lda = 2 * (int64_t)s.Fp; a.KA = rows; a.cols_a = 2 * s.Fp;
+  a.B = x.p; a.ldb = x.ld; a.KB = rows; a.cols_b = s.Np;
+  a.steps = s.steps(rows);
+  a.out = g->dw_in; a.ldo = d->N; a.rows_split = s.Fp;
+  RETURN_IF_HIP(run(kFeedDwIn, a));
+  a = base;           // dw_out
+  a.M = d->N_out; a.N = d->F;
+  a.A = dy.p; a.lda = dy.ld; a.KA = rows; a.cols_a = s.Op;
+  a.B = h; a.ldb = s.Fp; a.KB = rows; a.cols_b = s.Fp;
+  a.steps = s.steps(rows);
+  a.out = g->dw_out; a.ldo = d->F;
+  return hip_status(run(kFeedDwOut, a));
+}
+
 }  // namespace
 
 extern "C" {
@@ -278,6 +511,68 @@ int rnn_selective_scan_backward(const RnnSelectiveScanDesc* desc, const RnnSelec
   for (const void* p : {a.dy, (const void*)a.dx, (const void*)a.ddt, (const void*)a.dz})
     if (!aligned(p, 16)) a.vec = 0;
   return hip_status(launch_selective_scan_backward(a, desc->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int rnn_feed_forward_workspace_bytes(const RnnFeedForwardDesc* desc, size_t* bytes) {
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = feed_space(desc, false, false).bytes;
+  return RNN_OK;
+}
+
+int rnn_feed_forward_train_workspace_bytes(const RnnFeedForwardDesc* desc, size_t* bytes) {
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = feed_space(desc, true, false).bytes;
+  return RNN_OK;
+}
+
+int rnn_feed_forward_backward_workspace_bytes(const RnnFeedForwardDesc* desc, size_t* bytes) {
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = feed_space(desc, true, true).bytes;
+  return RNN_OK;
+}
+
+int rnn_feed_forward_reserve_bytes(const RnnFeedForwardDesc* desc, size_t* bytes) {
+  RETURN_IF_BAD(validate(desc));
+  if (!bytes) return RNN_E_NULL;
+  *bytes = feed_reserve(desc);
+  return RNN_OK;
+}
+
+int rnn_feed_forward(const RnnFeedForwardDesc* desc, const RnnFeedForwardIO* io, void* workspace, size_t ws_bytes, void* stream) {
+  Range range("rnn_feed_forward");
+  RETURN_IF_BAD(validate(desc));
+  return feed_forward(desc, io, nullptr, workspace, ws_bytes, stream);
+}
+
+int rnn_feed_forward_train(const RnnFeedForwardDesc* desc, const RnnFeedForwardIO* io, void* reserve, size_t reserve_bytes,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  Range range("rnn_feed_forward_train");
+  RETURN_IF_BAD(validate(desc));
+  if (!io) return RNN_E_NULL;
+  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, feed_reserve(desc)));
+  return feed_forward(desc, io, reserve, workspace, ws_bytes, stream);
+}
+
+int rnn_feed_forward_backward(const RnnFeedForwardDesc* desc, const RnnFeedForwardIO* io, const RnnFeedForwardGrads* grads,
+                              const void* reserve, size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream) {
+  Range range("rnn_feed_forward_backward");
+  RETURN_IF_BAD(validate(desc));
+  if (!io || !grads) return RNN_E_NULL;
+  RETURN_IF_BAD(feed_io(desc, io));
+  const size_t e = (size_t)esize_of(desc->dtype);
+  RETURN_IF_BAD(need(grads->dy, desc->aligned ? 16 : e));
+  RETURN_IF_BAD(need(grads->dx, e));
+  RETURN_IF_BAD(need(grads->dw_in, e));
+  RETURN_IF_BAD(need(grads->dw_out, e));
+  RETURN_IF_BAD(need_memory(reserve, reserve_bytes, feed_reserve(desc)));
+  const FeedSpace at = feed_space(desc, true, true);
+  RETURN_IF_BAD(need_memory(workspace, ws_bytes, at.bytes));
+  int xcds;
+  RETURN_IF_BAD(on_device(&xcds));
+  return feed_backward(desc, io, grads, reserve, static_cast<char*>(workspace), at, reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -72,4 +72,53 @@ int sel_segments(int T, int B, int H, int G, int cus, int* seg_steps);
 hipError_t launch_selective_scan(SelectiveScanArgs a, bool bf16_storage, hipStream_t stream);
 hipError_t launch_selective_scan_backward(SelectiveScanArgs a, bool bf16_storage, hipStream_t stream);
 
+// Gated feed-forward (feed_forward.hip and its instances).
+// A product's output is [M, N]; its operands are given by rows of the summed
+// dimension's neighbours ("along": [M, K]) or by rows of the outputs'
+// neighbours ("across": [K, M]).
+enum FeedOp { kFeedIn, kFeedOut, kFeedDh, kFeedDx, kFeedDwIn, kFeedDwOut, kFeedOps };
+struct FeedArgs {
+  int M, N;                         // the output's rows and columns, padding of F included
+  const void* A; int64_t lda; int KA;  // KA: how far the operand goes along the summed dimension
+  const void* B; int64_t ldb; int KB;
+  int cols_a, cols_b;               // columns of an operand that lies across, in memory
+  int steps;                        // of the summed dimension, 128 bytes (64 bf16, 32 fp32) each
+  int F, Fp;                        // hidden size, and rounded up to whole steps
+  int act;                          // RnnActivation
+  // outputs
+  void* out; int64_t ldo;           // kFeedIn: h; kFeedDh: [dg, du]
+  const void* residual; int64_t ldr;
+  float* gu;                        // [M, 2 Fp] the two projections in fp32: kFeedIn writes it (or null), kFeedDh reads it
+  int rows_split;                   // output rows from here on (padded) belong after the first F; 0: one block of rows
+  float* part; int splits;          // splits > 1: partial products [splits, M, N]
+};
+// Tile and split of one product.
+struct FeedPlan {
+  int big;                          // 256 x 256 tiles, else 128 x 128
+  int splits;
+};
+FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, int cus);
+double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op);
+hipError_t launch_feed_f32(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
+hipError_t launch_feed_bf16(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
+// Few rows: both projections and the activation, then the projection back.
+constexpr int kFeedFewRows = 64;
+struct FeedFewArgs {
+  int rows, n, F, n_out, act;
+  const void* x; int64_t ldx;
+  const void* w_in; int64_t ld_in;
+  const void* w_out; int64_t ld_out;
+  const void* residual; int64_t ldr;
+  void* h;                          // [rows, Fp] (workspace)
+  int Fp;
+  void* y;
+  int vec;                          // rows take 16-byte accesses
+};
+hipError_t launch_feed_few(const FeedFewArgs& a, bool bf16_storage, hipStream_t stream);
+// Rows of a tensor copied to a pitch of whole 16 bytes, zeros behind each.
+hipError_t launch_feed_pack(const void* from, int64_t ld, int64_t rows, int cols, void* to, int pitch, bool bf16_storage,
+                            hipStream_t stream);
+// out = residual + the sum of the partial products.
+hipError_t launch_feed_join(const FeedArgs& a, bool bf16_storage, hipStream_t stream);
+
 }  // namespace rnnk

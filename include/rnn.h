@@ -716,6 +716,57 @@ int rnn_selective_scan_backward(const RnnSelectiveScanDesc* desc, const RnnSelec
                                 const RnnSelectiveScanGrads* grads, const void* reserve, size_t reserve_bytes,
                                 void* workspace, size_t ws_bytes, void* stream);
 
+/* Gated feed-forward over rows:
+ *   g = x w_in[:F]^T,  u = x w_in[F:]^T,  h = act(g) u
+ *   y = h w_out^T (+ residual)
+ * h (and, backward, the gradients of g and u) are rounded to the storage type
+ * where they enter the next product; everything else is fp32 up to the
+ * results' own rounding. */
+typedef struct RnnFeedForwardDesc {
+  int32_t dtype;         /* RnnDtype of every tensor                           */
+  int32_t activation;    /* RNN_ACT_SILU, RNN_ACT_GELU_TANH or RNN_ACT_SIGMOID */
+  int64_t rows;          /* >= 1                                               */
+  int32_t N, F, N_out;   /* widths of x, h and y, >= 1                         */
+  int32_t aligned;       /* 1: x, w_in, w_out and dy are multiples of 16 bytes
+                            (else RNN_E_ALIGN). 0: they need not be; they are
+                            copied to the workspace, as are (in either case)
+                            those whose rows are not                           */
+  int64_t x_ld;          /* elements between rows of x (>= N)                  */
+  int64_t in_ld;         /* ... of w_in (>= N)                                 */
+  int64_t out_ld;        /* ... of w_out (>= F)                                */
+  int64_t residual_ld;   /* ... of residual (>= N_out; ignored without one)    */
+} RnnFeedForwardDesc;
+
+typedef struct RnnFeedForwardIO {
+  const void* x;           /* [rows, N]                                        */
+  const void* w_in;        /* [2 F, N], the gate's rows first                  */
+  const void* w_out;       /* [N_out, F]                                       */
+  const void* residual;    /* [rows, N_out], NULL = none                       */
+  void* y;                 /* [rows, N_out]                                    */
+} RnnFeedForwardIO;
+
+typedef struct RnnFeedForwardGrads {
+  const void* dy;          /* [rows, N_out]; also the residual's gradient      */
+  void* dx;                /* [rows, N]                                        */
+  void* dw_in;             /* [2 F, N]                                         */
+  void* dw_out;            /* [N_out, F]                                       */
+} RnnFeedForwardGrads;
+
+int rnn_feed_forward_workspace_bytes(const RnnFeedForwardDesc* desc, size_t* bytes);
+int rnn_feed_forward_train_workspace_bytes(const RnnFeedForwardDesc* desc, size_t* bytes);
+int rnn_feed_forward_backward_workspace_bytes(const RnnFeedForwardDesc* desc, size_t* bytes);
+/* The reserve between the passes: g and u in fp32, and h. */
+int rnn_feed_forward_reserve_bytes(const RnnFeedForwardDesc* desc, size_t* bytes);
+int rnn_feed_forward(const RnnFeedForwardDesc* desc, const RnnFeedForwardIO* io, void* workspace, size_t ws_bytes,
+                     void* stream);
+int rnn_feed_forward_train(const RnnFeedForwardDesc* desc, const RnnFeedForwardIO* io, void* reserve,
+                           size_t reserve_bytes, void* workspace, size_t ws_bytes, void* stream);
+/* io as for rnn_feed_forward_train, unchanged since (residual and y are not
+ * read). */
+int rnn_feed_forward_backward(const RnnFeedForwardDesc* desc, const RnnFeedForwardIO* io,
+                              const RnnFeedForwardGrads* grads, const void* reserve, size_t reserve_bytes,
+                              void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -321,3 +321,128 @@ def test_selective_python_refusals():
         gss.selective_scan(x[0], x, A, B, B)
     with pytest.raises(ValueError, match="must be a tensor"):
         gss.selective_scan(None, x, A, B, B)
+
+
+# ---------------------------------------------------------------------------
+# Gated feed-forward
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh", "sigmoid"])
+def test_feed_forward_definition(kind):
+    rng = np.random.default_rng(7)
+    rows, n, F, n_out = 4, 3, 5, 2
+    x, w_in, w_out = rng.standard_normal((rows, n)), rng.standard_normal((2 * F, n)), rng.standard_normal((n_out, F))
+    r, dy = rng.standard_normal((2, rows, n_out))
+    y = oracle.feed_forward(x, w_in, w_out, r, kind)
+    t = torch.tensor(x @ w_in[:F].T)
+    act = {"silu": torch.nn.functional.silu(t), "sigmoid": torch.sigmoid(t),
+           "gelu_tanh": torch.nn.functional.gelu(t, approximate="tanh")}[kind].numpy()
+    assert np.allclose(y, (act * (x @ w_in[F:].T)) @ w_out.T + r, atol=1e-12)
+    loss = lambda: float((oracle.feed_forward(x, w_in, w_out, r, kind) * dy).sum())  # noqa: E731
+    for got, v in zip(oracle.feed_forward_backward(x, w_in, w_out, dy, kind), (x, w_in, w_out)):
+        assert np.allclose(got, _differences(loss, v), atol=1e-7)
+
+
+def test_feed_layout(tmp_path):
+    _layouts(tmp_path, ["RnnFeedForwardDesc", "RnnFeedForwardIO", "RnnFeedForwardGrads"])
+
+
+def _feed(**kw):
+    v = dict(dtype=1, activation=1, rows=300, N=64, F=96, N_out=64, aligned=1, x_ld=64, in_ld=64, out_ld=96, residual_ld=64)
+    v.update(kw)
+    return gss.RnnFeedForwardDesc(*v.values())
+
+
+_FEED_SIZES = tuple(f"rnn_feed_forward_{k}_bytes" for k in ("workspace", "train_workspace", "backward_workspace", "reserve"))
+
+
+def _feed_size(fn, **kw):
+    n = ctypes.c_size_t(0)
+    assert getattr(ops._lib(), fn)(ctypes.byref(_feed(**kw)), ctypes.byref(n)) == OK
+    return n.value
+
+
+@pytest.mark.parametrize("kw,expect", [
+    ({}, OK), ({"dtype": 0}, OK), ({"activation": 2}, OK), ({"activation": 3}, OK), ({"aligned": 0}, OK), ({"rows": 1}, OK),
+    ({"N": 1, "F": 1, "N_out": 1}, OK), ({"x_ld": 1 << 40}, OK), ({"residual_ld": 0}, OK), ({"rows": 1 << 20}, OK),
+    ({"dtype": 2}, E_UNSUPPORTED), ({"activation": 0}, E_UNSUPPORTED), ({"activation": 4}, E_UNSUPPORTED),
+    ({"rows": 0}, E_SHAPE), ({"rows": -1}, E_SHAPE), ({"N": 0}, E_SHAPE), ({"F": 0}, E_SHAPE), ({"N_out": 0}, E_SHAPE),
+    ({"aligned": 2}, E_SHAPE), ({"x_ld": 63}, E_SHAPE), ({"in_ld": 63}, E_SHAPE), ({"out_ld": 95}, E_SHAPE),
+    ({"rows": 1 << 40}, E_SHAPE), ({"F": 2147483647, "out_ld": 1 << 40}, E_SHAPE),
+    ({"rows": 1 << 30, "F": 1 << 20, "out_ld": 1 << 20}, E_SHAPE), ({"N": 2147483647, "x_ld": 1 << 40, "in_ld": 1 << 40}, E_SHAPE),
+])
+def test_feed_desc(kw, expect):
+    n = ctypes.c_size_t(0)
+    for fn in _FEED_SIZES:
+        assert getattr(ops._lib(), fn)(ctypes.byref(_feed(**kw)), ctypes.byref(n)) == expect
+        if expect == OK:
+            assert getattr(ops._lib(), fn)(ctypes.byref(_feed(**kw)), None) == E_NULL
+
+
+def test_feed_sizes():
+    # the reserve: two fp32 numbers and a hidden value each, F in whole steps of 128 bytes
+    assert _feed_size(_FEED_SIZES[3]) == 300 * 128 * (2 * 4 + 2)
+    assert _feed_size(_FEED_SIZES[3], dtype=0) == 300 * 96 * 3 * 4
+    # few rows keep the hidden values alone, whatever the alignment
+    assert _feed_size(_FEED_SIZES[0], rows=64) == _feed_size(_FEED_SIZES[0], rows=64, aligned=0, x_ld=65) == 64 * 128 * 2
+    # operands whose rows are not whole 16 bytes are copied
+    for kw, more in (({"x_ld": 65}, 300 * 64 * 2), ({"in_ld": 65}, 2 * 96 * 64 * 2), ({"out_ld": 97}, 64 * 96 * 2),
+                     ({"aligned": 0}, (300 * 64 + 2 * 96 * 64 + 64 * 96) * 2)):
+        for fn in _FEED_SIZES[:2]:
+            assert _feed_size(fn, **kw) == _feed_size(fn) + more, kw
+    assert _feed_size(_FEED_SIZES[2], aligned=0) > _feed_size(_FEED_SIZES[2])
+
+
+def test_feed_pointers():
+    L = ops._lib()
+    d = _feed(aligned=0)
+    ws, ts, bs, rs = (_feed_size(fn, aligned=0) for fn in _FEED_SIZES)
+
+    def io(**kw):
+        v = dict(x=ADDR, w_in=ADDR, w_out=ADDR, residual=ADDR, y=ADDR)
+        v.update(kw)
+        return ctypes.byref(gss.RnnFeedForwardIO(*v.values()))
+
+    def fwd(ptr=ADDR, size=ws, desc=d, **kw):
+        return L.rnn_feed_forward(ctypes.byref(desc), io(**kw), ptr, size, None)
+
+    for k in ("x", "w_in", "w_out", "y"):
+        assert fwd(**{k: None}) == E_NULL, k
+    for k in ("x", "w_in", "w_out", "residual", "y"):
+        assert fwd(**{k: ADDR + 1}) == E_ALIGN, k
+    for k in ("x", "w_in", "w_out"):       # promised to be multiples of 16 bytes
+        assert fwd(desc=_feed(), **{k: ADDR + 2}) == E_ALIGN, k
+    assert fwd(desc=_feed(residual_ld=63)) == E_SHAPE
+    assert fwd(ptr=None) == E_WORKSPACE and fwd(size=ws - 1) == E_WORKSPACE and fwd(ptr=ADDR + 8) == E_ALIGN
+    assert L.rnn_feed_forward(ctypes.byref(d), None, ADDR, ws, None) == E_NULL
+    assert L.rnn_feed_forward(None, io(), ADDR, ws, None) == E_NULL
+
+    def train(ptr=ADDR, size=rs, wptr=ADDR, wsize=ts):
+        return L.rnn_feed_forward_train(ctypes.byref(d), io(), ptr, size, wptr, wsize, None)
+
+    assert train(ptr=None) == E_WORKSPACE and train(size=rs - 1) == E_WORKSPACE and train(wsize=ts - 1) == E_WORKSPACE
+
+    def bwd(ptr=ADDR, size=bs, rsize=rs, desc=d, **kw):
+        v = dict(dy=ADDR, dx=ADDR, dw_in=ADDR, dw_out=ADDR)
+        v.update(kw)
+        return L.rnn_feed_forward_backward(ctypes.byref(desc), io(), ctypes.byref(gss.RnnFeedForwardGrads(*v.values())), ADDR,
+                                           rsize, ptr, size, None)
+
+    for k in ("dy", "dx", "dw_in", "dw_out"):
+        assert bwd(**{k: None}) == E_NULL, k
+        assert bwd(**{k: ADDR + 1}) == E_ALIGN, k
+    assert bwd(desc=_feed(), dy=ADDR + 2) == E_ALIGN
+    assert bwd(ptr=None) == E_WORKSPACE and bwd(size=bs - 1) == E_WORKSPACE and bwd(rsize=rs - 1) == E_WORKSPACE
+    assert L.rnn_feed_forward_backward(ctypes.byref(d), io(), None, ADDR, rs, ADDR, bs, None) == E_NULL
+    if not torch.cuda.is_available():
+        assert fwd() == E_DEVICE and fwd(residual=None) == E_DEVICE and train() == E_DEVICE and bwd() == E_DEVICE
+
+
+def test_feed_python_refusals():
+    x, w_in, w_out = torch.zeros(4, 8), torch.zeros(32, 8), torch.zeros(8, 16)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        gss.feed_forward(x, w_in, w_out)
+    with pytest.raises(ValueError, match="activation"):
+        gss.feed_forward(x, w_in, w_out, activation=None)
+    with pytest.raises(ValueError, match="tensor of at least one"):
+        gss.feed_forward(None, w_in, w_out)
