@@ -214,7 +214,7 @@ double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
 // workgroups that the device holds, times steps, plus the partial products'
 // way through memory. Products whose results are used on the way out of the
 // accumulators are not split.
-FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, int cus) {
+FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus) {
   FeedPlan best{0, 1};
   double least = 0.0;
   for (int big = 0; big < 2; ++big) {
@@ -225,7 +225,8 @@ FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, int cus) {
       p.splits = (steps + each - 1) / each;
       if (p.splits != want) continue;
       const double rounds = std::ceil(tiles * want / resident);
-      double us = rounds * (each * (big ? 1.7 : 1.1) + (big ? 5.0 : 3.0));
+      const double step = bf16_storage ? (big ? 2.2 : 1.4) : (big ? 7.6 : 3.9);  // us, both workgroups of a unit at work
+      double us = rounds * (each * step + (big ? 12.0 : 6.0));
       if (want > 1) us += 4.0 + (double)want * M * N * 8.0 / 4e6;
       if (least == 0.0 || us < least) {
         least = us;

@@ -104,11 +104,11 @@ struct Operand {
 
   __device__ __forceinline__ void fetch(char* lds, int k0, int64_t row0, int limit, int64_t ld) const {
     // k0: the step's first k; row0: the operand's row of it (across); limit: how far k goes
-    char* wave_lds = lds + (threadIdx.x >> 6) * 1024;
+    [[maybe_unused]] char* wave_lds = lds + (threadIdx.x >> 6) * 1024;
     if (k0 + kStep <= limit) {
 #pragma unroll
       for (int i = 0; i < T::kTimes; ++i) {
-        const DT* p = ALONG ? src[ALONG ? i : 0] + k0 : src[0] + (row0 + i * kSweep) * ld;
+        [[maybe_unused]] const DT* p = ALONG ? src[ALONG ? i : 0] + k0 : src[0] + (row0 + i * kSweep) * ld;
 #ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know LDS pointers and drops kernels over them
         __builtin_amdgcn_global_load_lds(p, wave_lds + i * T::kThreads * 16, 16, 0, 0);
 #endif
@@ -213,6 +213,159 @@ __device__ __forceinline__ FeedItem feed_item(const FeedArgs& a, int tiles_m, in
   return w;
 }
 
+// Eight results of a lane: column n, rows 8 (v / 4) + v % 4 of `out`, where
+// half a 32 x 32 block begins. In bf16 lanes change every other row's result
+// with their neighbour, so that each stores two columns at a time (PAIRS: rows
+// and n allow it).
+template <typename DT, bool PAIRS>
+__device__ __forceinline__ void store_half(DT* out, int64_t ld, const float (&val)[8], int lane) {
+  if constexpr (PAIRS && sizeof(DT) == 2) {
+    const bool odd = lane & 1;
+    bf16* p = out + (odd ? ld - 1 : 0);
+#pragma unroll
+    for (int v = 0; v < 8; v += 2) {
+      const float keep = odd ? val[v + 1] : val[v], give = odd ? val[v] : val[v + 1];
+      const float got = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, give), 0xB1, 0xF, 0xF, true));
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      *reinterpret_cast<bf16x2*>(p + (8 * (v >> 2) + (v & 3)) * ld) = bf16x2{(bf16)(odd ? got : keep), (bf16)(odd ? keep : got)};
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) out[(8 * (v >> 2) + (v & 3)) * ld] = from_f32<DT>(val[v]);
+  }
+}
+template <typename DT>
+__device__ __forceinline__ void store_half(DT* out, int64_t ld, const float (&val)[8], int lane, bool pairs) {
+  if (pairs)
+    store_half<DT, true>(out, ld, val, lane);
+  else
+    store_half<DT, false>(out, ld, val, lane);
+}
+
+// A tile's way out of the accumulators. A lane holds column lane % 32 and rows
+// 8 (v / 4) + 4 (lane / 32) + v % 4 of each 32 x 32 block. WHOLE: every row
+// and column of the tile exists; it leaves in halves of a block, and what a
+// half needs from memory is asked for while the one before it is worked on.
+template <typename DT, int BIG, int OP, bool WHOLE>
+__device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& w, const f32x16 (&acc)[FeedTile<BIG>::MI][2], int wm,
+                                             int wn, int lane) {
+  constexpr int MI = FeedTile<BIG>::MI, kAcross = OP == kFeedIn ? 1 : 2, kBlocks = kAcross * MI;
+  const int m_base = w.m0 + wm * MI * 32 + 4 * (lane >> 5), n_base = w.n0 + wn * (OP == kFeedIn ? 32 : 64) + (lane & 31);
+  if constexpr (WHOLE) {
+    const bool pairs = sizeof(DT) == 2 && a.ldo % 2 == 0 && ((uintptr_t)a.out & 3) == 0;
+    const bool add = OP == kFeedOut && a.residual && a.splits == 1;
+    float more[2][8], more_u[OP == kFeedDh ? 2 : 1][8];
+    auto ask = [&](int k) {
+      const int64_t m = m_base + k / (2 * kAcross) * 32 + k % 2 * 16, n = n_base + k / 2 % kAcross * 32;
+      if constexpr (OP == kFeedDh) {
+        const float* p = a.gu + m * 2 * a.Fp + n;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float* q = p + (int64_t)(8 * (v >> 2) + (v & 3)) * 2 * a.Fp;
+          more[k & 1][v] = q[0];
+          more_u[k & 1][v] = q[a.Fp];
+        }
+      } else if (add) {
+        const DT* p = (const DT*)a.residual + m * a.ldr + n;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) more[k & 1][v] = to_f32<DT>(p[(8 * (v >> 2) + (v & 3)) * a.ldr]);
+      }
+    };
+    if (OP == kFeedDh || OP == kFeedOut) ask(0);
+#pragma unroll
+    for (int k = 0; k < 2 * kBlocks; ++k) {
+      const int i = k / (2 * kAcross), j = k / 2 % kAcross, v0 = k % 2 * 8;
+      const int64_t m = m_base + i * 32 + k % 2 * 16, n = n_base + j * 32;
+      if ((OP == kFeedDh || OP == kFeedOut) && k + 1 < 2 * kBlocks) ask(k + 1);
+      float val[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) val[v] = acc[i][j][v0 + v];
+      if constexpr (OP == kFeedIn) {
+        float u[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) u[v] = acc[i][1][v0 + v];
+        if (a.gu) {
+          float* p = a.gu + m * 2 * a.Fp + n;
+          store_half<float, false>(p, 2 * (int64_t)a.Fp, val, lane);
+          store_half<float, false>(p + a.Fp, 2 * (int64_t)a.Fp, u, lane);
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v) u[v] *= activate(val[v], a.act).act;
+        store_half<DT>((DT*)a.out + m * a.ldo + n, a.ldo, u, lane, pairs);
+      } else if constexpr (OP == kFeedDh) {
+        float du[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const Activated r = activate(more[k & 1][v], a.act);
+          du[v] = val[v] * r.act;
+          val[v] *= more_u[k & 1][v] * r.slope;
+        }
+        DT* out = (DT*)a.out + m * a.ldo + n;
+        store_half<DT>(out, a.ldo, val, lane, pairs);
+        store_half<DT>(out + a.Fp, a.ldo, du, lane, pairs);
+      } else if (a.splits > 1) {
+        store_half<float, false>(a.part + ((int64_t)w.split * a.M + m) * a.N + n, a.N, val, lane);
+      } else {
+        // a block's rows lie on one side of the gate's last (padded) one
+        const bool second = OP == kFeedDwIn && m >= a.Fp;
+        const int64_t f = second ? m - a.Fp : m, row = second ? f + a.F : m;
+        DT* out = (DT*)a.out + row * a.ldo + n;
+        if (add) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v) val[v] += more[k & 1][v];
+        }
+        if (OP == kFeedDwIn && f + 16 > a.F) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            if (f + 8 * (v >> 2) + (v & 3) < a.F) out[(8 * (v >> 2) + (v & 3)) * a.ldo] = from_f32<DT>(val[v]);
+        } else {
+          store_half<DT>(out, a.ldo, val, lane, pairs);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      const int i = k / kAcross, j = k % kAcross;
+      const int n = n_base + j * 32;
+      if (n >= (OP == kFeedIn ? a.Fp : a.N)) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t m = m_base + i * 32 + 8 * (v >> 2) + (v & 3);
+        if (m >= a.M) continue;
+        const float val = acc[i][j][v];
+        if constexpr (OP == kFeedIn) {
+          const bool on = n < a.F;
+          const float g = on ? val : 0.f, u = on ? acc[i][1][v] : 0.f;
+          ((DT*)a.out)[m * a.ldo + n] = from_f32<DT>(activate(g, a.act).act * u);
+          if (a.gu) {
+            a.gu[m * 2 * a.Fp + n] = g;
+            a.gu[m * 2 * a.Fp + a.Fp + n] = u;
+          }
+        } else if constexpr (OP == kFeedDh) {
+          const float* gu = a.gu + m * 2 * a.Fp + n;
+          const Activated r = activate(gu[0], a.act);
+          const bool on = n < a.F;
+          DT* out = (DT*)a.out + m * a.ldo + n;
+          out[0] = from_f32<DT>(on ? val * gu[a.Fp] * r.slope : 0.f);
+          out[a.Fp] = from_f32<DT>(on ? val * r.act : 0.f);
+        } else if (a.splits > 1) {
+          a.part[((int64_t)w.split * a.M + m) * a.N + n] = val;
+        } else {
+          int64_t row = m;
+          if (OP == kFeedDwIn) {
+            const bool second = m >= a.Fp;
+            row = second ? m - a.Fp + a.F : m;
+            if (row >= (second ? 2 * (int64_t)a.F : a.F)) continue;
+          }
+          const float more = OP == kFeedOut && a.residual ? to_f32<DT>(((const DT*)a.residual)[row * a.ldr + n]) : 0.f;
+          ((DT*)a.out)[row * a.ldo + n] = from_f32<DT>(val + more);
+        }
+      }
+    }
+  }
+}
+
 template <typename DT, int BIG, int OP>
 __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedArgs a, int tiles_m, int tiles_n) {
   using T = FeedTile<BIG>;
@@ -290,65 +443,26 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[i][j] = feed_mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
       }
-      half ^= 1;
-    }
-
-    // A lane holds column lane % 32 and rows 8 (v / 4) + 4 (lane / 32) + v % 4 of each block.
-    const int l32 = lane & 31, up = lane >> 5;
+      if constexpr (sizeof(DT) == 2) {
+        // the reads of a quarter go out between the products of the one before
+        constexpr int kReads = MI * (S::kAlongA ? 1 : 2) + 2 * (S::kAlongB ? 1 : 2), kEach = (kReads + 2 * MI - 1) / (2 * MI);
+        __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int mb = w.m0 + wm * MI * 32 + i * 32 + 4 * up;
-      if constexpr (OP == kFeedIn) {
-        const int f = w.n0 + wn * 32 + l32;
-        if (f < a.Fp) {
+        for (int s = 0; s < 4; ++s) {
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int64_t m = mb + 8 * (v >> 2) + (v & 3);
-            if (m < a.M) {
-              const bool on = f < a.F;
-              const float g = on ? acc[i][0][v] : 0.f, u = on ? acc[i][1][v] : 0.f;
-              ((DT*)a.out)[m * a.ldo + f] = from_f32<DT>(activate(g, a.act).act * u);
-              if (a.gu) {
-                a.gu[m * 2 * a.Fp + f] = g;
-                a.gu[m * 2 * a.Fp + a.Fp + f] = u;
-              }
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = w.n0 + wn * 64 + j * 32 + l32;
-          if (n >= a.N) continue;
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int m = mb + 8 * (v >> 2) + (v & 3);
-            if (m >= a.M) continue;
-            const float val = acc[i][j][v];
-            if constexpr (OP == kFeedDh) {
-              const float* gu = a.gu + (int64_t)m * 2 * a.Fp + n;
-              const float g = gu[0], u = gu[a.Fp];
-              const Activated r = activate(g, a.act);
-              const bool on = n < a.F;
-              DT* out = (DT*)a.out + m * a.ldo + n;
-              out[0] = from_f32<DT>(on ? val * u * r.slope : 0.f);
-              out[a.Fp] = from_f32<DT>(on ? val * r.act : 0.f);
-            } else if (a.splits > 1) {
-              a.part[((int64_t)w.split * a.M + m) * a.N + n] = val;
-            } else {
-              int row = m;
-              if (OP == kFeedDwIn) {
-                const bool second = m >= a.Fp;
-                row = second ? m - a.Fp + a.F : m;
-                if (row >= (second ? 2 * a.F : a.F)) continue;
-              }
-              const float more = OP == kFeedOut && a.residual ? to_f32<DT>(((const DT*)a.residual)[row * a.ldr + n]) : 0.f;
-              ((DT*)a.out)[row * a.ldo + n] = from_f32<DT>(val + more);
-            }
+          for (int m = 0; m < 2 * MI; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (s < 3 && m * kEach < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
           }
         }
       }
+      half ^= 1;
     }
+    const bool whole = w.m0 + T::kRows <= a.M && w.n0 + (OP == kFeedIn ? T::kRows / 2 : T::kRows) <= (OP == kFeedIn || OP == kFeedDh ? a.F : a.N);
+    if (whole)
+      feed_results<DT, BIG, OP, true>(a, w, acc, wm, wn, lane);
+    else
+      feed_results<DT, BIG, OP, false>(a, w, acc, wm, wn, lane);
     w = next;
   }
 }

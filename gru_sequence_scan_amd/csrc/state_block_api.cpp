@@ -211,12 +211,12 @@ struct FeedSpace {
 
 FeedPlan feed_plan_of(const RnnFeedForwardDesc* d, const FeedSizes& s, int op) {
   switch (op) {
-    case kFeedIn: return feed_plan(op, d->rows, s.Fp, s.steps(s.Np), kPlanCus);
-    case kFeedOut: return feed_plan(op, d->rows, d->N_out, s.steps(s.Fm), kPlanCus);
-    case kFeedDh: return feed_plan(op, d->rows, s.Fp, s.steps(s.Op), kPlanCus);
-    case kFeedDx: return feed_plan(op, d->rows, d->N, s.steps(2 * (int64_t)s.Fp), kPlanCus);
-    case kFeedDwIn: return feed_plan(op, 2 * (int64_t)s.Fp, d->N, s.steps(d->rows), kPlanCus);
-    default: return feed_plan(op, d->N_out, d->F, s.steps(d->rows), kPlanCus);
+    case kFeedIn: return feed_plan(op, d->rows, s.Fp, s.steps(s.Np), d->dtype == RNN_DTYPE_BF16, kPlanCus);
+    case kFeedOut: return feed_plan(op, d->rows, d->N_out, s.steps(s.Fm), d->dtype == RNN_DTYPE_BF16, kPlanCus);
+    case kFeedDh: return feed_plan(op, d->rows, s.Fp, s.steps(s.Op), d->dtype == RNN_DTYPE_BF16, kPlanCus);
+    case kFeedDx: return feed_plan(op, d->rows, d->N, s.steps(2 * (int64_t)s.Fp), d->dtype == RNN_DTYPE_BF16, kPlanCus);
+    case kFeedDwIn: return feed_plan(op, 2 * (int64_t)s.Fp, d->N, s.steps(d->rows), d->dtype == RNN_DTYPE_BF16, kPlanCus);
+    default: return feed_plan(op, d->N_out, d->F, s.steps(d->rows), d->dtype == RNN_DTYPE_BF16, kPlanCus);
   }
 }
 size_t feed_part(const FeedPlan& p, size_t M, size_t N) { return p.splits > 1 ? p.splits * M * N * sizeof(float) : 0; }

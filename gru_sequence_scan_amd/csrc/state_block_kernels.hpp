@@ -97,7 +97,7 @@ struct FeedPlan {
   int big;                          // 256 x 256 tiles, else 128 x 128
   int splits;
 };
-FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, int cus);
+FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus);
 double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op);
 hipError_t launch_feed_f32(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
 hipError_t launch_feed_bf16(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
