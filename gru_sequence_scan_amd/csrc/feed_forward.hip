@@ -211,9 +211,13 @@ double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
 }
 
 // The tile and the split with the shortest expected time: rounds of the
-// workgroups that the device holds, times steps, plus the partial products'
-// way through memory. Products whose results are used on the way out of the
-// accumulators are not split.
+// workgroups that the device holds, times steps, plus the results' way out and
+// the partial products' way through memory. Products whose results are used on
+// the way out of the accumulators are not split. dh reads and writes 16 bytes
+// a result there (fp32; 12 in bf16), which two workgroups a compute unit hide
+// better than one: 32000 x 2816 bf16 422 us in small tiles and 450 in large
+// ones, 19334 x 1368 fp32 356 and 501; without that traffic large ones win
+// (dx of the same in bf16: 411 and 480 us).
 FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus) {
   FeedPlan best{0, 1};
   double least = 0.0;
@@ -226,7 +230,7 @@ FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, i
       if (p.splits != want) continue;
       const double rounds = std::ceil(tiles * want / resident);
       const double step = bf16_storage ? (big ? 2.2 : 1.4) : (big ? 7.6 : 3.9);  // us, both workgroups of a unit at work
-      double us = rounds * (each * step + (big ? 12.0 : 6.0));
+      double us = rounds * (each * step + (big ? (op == kFeedDh ? 90.0 : 12.0) : 6.0));
       if (want > 1) us += 4.0 + (double)want * M * N * 8.0 / 4e6;
       if (least == 0.0 || us < least) {
         least = us;

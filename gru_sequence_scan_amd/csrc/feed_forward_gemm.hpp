@@ -2,28 +2,32 @@
 //
 // C[m, n] = sum_k A[m, k] B[n, k]: an operand lies with k running along its
 // rows, or across them. A workgroup makes a tile of 256 x 256 (eight waves of
-// 128 x 64) or 128 x 128 (four of 64 x 64) outputs on the 32x32 matrix
-// instructions, k in steps of 128 bytes. A step's operands go straight from
-// memory into LDS (16 bytes a lane), two steps deep: while one is multiplied
-// the next is on its way, and one barrier a step says that it has arrived and
-// that the other half may be overwritten.
+// 128 x 64, one workgroup a compute unit) or 128 x 128 (four of 64 x 64, two
+// workgroups) outputs on the 32x32 matrix instructions, k in steps of 128
+// bytes. A step's operands go straight from memory into LDS (16 bytes a lane),
+// in five places that hold one operand's step each: while a step is multiplied
+// one operand of the next is there, the other and one more are on their way,
+// issued between the products. One barrier a step says that the next step has
+// arrived and that this one's places are free.
 //
 // In LDS an operand that runs along k is [rows][128 bytes], the 16-byte chunk
-// c of row r at c ^ (r & 7), so that eight neighbouring rows' reads of a chunk
-// fall on different banks. One that runs across is [k][tile columns]; bf16
-// takes it through the transposing read (4 x 16 blocks), whose 32-byte columns
-// lie at u ^ kTurn(k & 3) for the same reason. The order of k inside a step is
-// the same for both operands, which is all that a product asks of it.
+// c of row r at c ^ ((r >> 1) & 7), so that 16 neighbouring rows' reads of a
+// chunk fall on different banks. One that runs across is [k][tile columns];
+// bf16 takes it through the transposing read (4 x 16 blocks), whose 32-byte
+// columns u lie at u ^ turn(k) for the same reason. The order of k inside a
+// step is the same for both operands, which is all that a product asks of it.
 //
 // What is behind a row's end along k is zero in LDS: the last step of such an
 // operand goes through registers. Rows and columns behind the output's are
 // some row or column again and are not stored.
 //
-// Workgroups stay for several tiles: the first step of the next one is
-// fetched while the last of this one is multiplied and its results are
+// Workgroups stay for several tiles: the first steps of the next one are
+// fetched while the last of this one are multiplied and its results are
 // stored. Neighbouring tiles (8 rows of tiles, then the next column) go to one
 // XCD at a time, whose L2 they share.
 #pragma once
+
+#include <type_traits>
 
 #include "../../include/rnn.h"
 #include "device_common.hpp"
@@ -62,11 +66,12 @@ struct FeedTile {
   static constexpr int kWavesN = BIG ? 4 : 2;         // waves across, two waves down
   static constexpr int MI = BIG ? 4 : 2;              // 32-row blocks of a wave; two across
   static constexpr int kBytes = kRows * 128;          // one operand's step
-  static constexpr int kLds = 2 * 2 * kBytes;
+  static constexpr int kSlots = 5, kLds = kSlots * kBytes;
   static constexpr int kTimes = kBytes / 16 / kThreads;  // 16-byte loads of a thread: 4
 };
 
-// 16-byte loads that bring an operand's step into LDS.
+// 16-byte loads that bring an operand's step into LDS. A thread's addresses
+// are 32-bit distances from the step's, which is the same for all.
 template <typename DT, int BIG, bool ALONG>
 struct Operand {
   using T = FeedTile<BIG>;
@@ -74,53 +79,75 @@ struct Operand {
   static constexpr int kStep = 128 / (int)sizeof(DT);         // k of a step
   static constexpr int kChunks = T::kRows / E;                // of a k row (across)
   static constexpr int kSweep = ALONG ? T::kThreads / 8 : T::kThreads / kChunks;  // rows between a thread's loads
-  const DT* src[ALONG ? T::kTimes : 1];
-  int chunk;                                                  // first k (along) or k row (across) of this thread in a step
+  const char* base;                                           // the tile's first element (the same for a wave)
+  int64_t partner;                                            // ... and how far from it the other rows of pairs are
+  uint32_t at[ALONG ? T::kTimes : 1];
   // 32-byte column u of k row k is at u ^ turn(k): four rows on different
   // banks, also where two neighbouring columns are read at once
   static __device__ __forceinline__ int turn(int k) { return (k & 3) ^ ((k & 1) << 2); }
+  // first k (along) or k row (across) of this thread in a step
+  static __device__ __forceinline__ int chunk() {
+    const int t = threadIdx.x;
+    return ALONG ? ((t & 7) ^ ((t >> 4) & 7)) * E : t / kChunks;
+  }
 
   // The tile's rows from row0 on, `rows` there are; PAIRS: 32 of them, then 32
   // that are `apart` rows behind those, then the next 32 and so on.
   template <bool PAIRS>
-  __device__ __forceinline__ void place_along(const void* base, int64_t ld, int row0, int rows, int apart) {
-    const int t = threadIdx.x, r0 = t >> 3, c = (t & 7) ^ (r0 & 7);
-    chunk = c * E;
+  __device__ __forceinline__ void place_along(const void* p, int64_t ld, int row0, int rows, int apart) {
+    base = (const char*)p + row0 * ld * (int64_t)sizeof(DT);
+    partner = PAIRS ? apart * ld * (int64_t)sizeof(DT) : 0;
+    if (BIG) {  // a wave's rows are all on one side: 8 of every 64
+      if (__builtin_amdgcn_readfirstlane(threadIdx.x) & 256) base += partner;
+      partner = 0;
+    }
 #pragma unroll
     for (int i = 0; i < T::kTimes; ++i) {
-      const int r = r0 + i * kSweep, at = row0 + (PAIRS ? (r >> 6) * 32 + (r & 31) : r);
-      const int row = (at < rows ? at : rows - 1) + (PAIRS && (r & 32) ? apart : 0);
-      src[ALONG ? i : 0] = (const DT*)base + (int64_t)row * ld + chunk;
+      const int r = (threadIdx.x >> 3) + i * kSweep, n = PAIRS ? (r >> 6) * 32 + (r & 31) : r;
+      const int row = row0 + n < rows ? n : rows - 1 - row0;
+      at[ALONG ? i : 0] = (uint32_t)((row * ld + chunk()) * (int64_t)sizeof(DT));
     }
   }
   // The tile's columns from col0 on, `cols` there are in memory.
-  __device__ __forceinline__ void place_across(const void* base, int64_t ld, int col0, int cols) {
+  __device__ __forceinline__ void place_across(const void* p, int64_t ld, int col0, int cols) {
     const int t = threadIdx.x, k = t / kChunks, pos = t % kChunks;
-    const int c = sizeof(DT) == 2 ? ((pos >> 1) ^ turn(k)) * 2 + (pos & 1) : pos;
-    chunk = k;
-    const int at = col0 + c * E;
-    src[0] = (const DT*)base + (int64_t)k * ld + (at + E <= cols ? at : cols - E);
+    const int c = (sizeof(DT) == 2 ? ((pos >> 1) ^ turn(k)) * 2 + (pos & 1) : pos) * E;
+    base = (const char*)p + (int64_t)col0 * (int64_t)sizeof(DT);
+    partner = 0;
+    at[0] = (uint32_t)((k * ld + (col0 + c + E <= cols ? c : cols - E - col0)) * (int64_t)sizeof(DT));
   }
 
+  // Load i of a step whose first k is k0 and (across) first row row0.
+  __device__ __forceinline__ const char* from(int i, int k0, int64_t row0, int64_t ld) const {
+    const char* step = base + (ALONG ? (int64_t)k0 : (row0 + i * kSweep) * ld) * (int64_t)sizeof(DT);
+    if (!BIG && ALONG && i % 2) step += partner;  // every other 32 rows
+    return step + at[ALONG ? i : 0];
+  }
+  // ... that is there as a whole
+  __device__ __forceinline__ void load(char* lds, int i, int k0, int64_t row0, int64_t ld) const {
+    [[maybe_unused]] char* to = lds + (threadIdx.x >> 6) * 1024 + i * T::kThreads * 16;
+    [[maybe_unused]] const char* p = from(i, k0, row0, ld);
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know LDS pointers and drops kernels over them
+    __builtin_amdgcn_global_load_lds(p, to, 16, 0, 0);
+#endif
+  }
   __device__ __forceinline__ void fetch(char* lds, int k0, int64_t row0, int limit, int64_t ld) const {
-    // k0: the step's first k; row0: the operand's row of it (across); limit: how far k goes
-    [[maybe_unused]] char* wave_lds = lds + (threadIdx.x >> 6) * 1024;
     if (k0 + kStep <= limit) {
 #pragma unroll
-      for (int i = 0; i < T::kTimes; ++i) {
-        [[maybe_unused]] const DT* p = ALONG ? src[ALONG ? i : 0] + k0 : src[0] + (row0 + i * kSweep) * ld;
-#ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know LDS pointers and drops kernels over them
-        __builtin_amdgcn_global_load_lds(p, wave_lds + i * T::kThreads * 16, 16, 0, 0);
-#endif
-      }
+      for (int i = 0; i < T::kTimes; ++i) load(lds, i, k0, row0, ld);
     } else {
       u32x4 v[T::kTimes];
+      const int c = chunk();
 #pragma unroll
       for (int i = 0; i < T::kTimes; ++i) {
-        const int k = k0 + chunk + (ALONG ? 0 : i * kSweep);
+        const int k = k0 + c + (ALONG ? 0 : i * kSweep);
         v[i] = u32x4{0u, 0u, 0u, 0u};
-        if (k < limit) v[i] = *reinterpret_cast<const u32x4*>(ALONG ? src[ALONG ? i : 0] + k0 : src[0] + (row0 + i * kSweep) * ld);
+        if (k < limit) v[i] = *reinterpret_cast<const u32x4*>(from(i, k0, row0, ld));
       }
+      // A wave none of whose rows are left has loaded nothing here: without a
+      // wait of its own the loads that step_barrier counts could be older ones.
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int i = 0; i < T::kTimes; ++i) *reinterpret_cast<u32x4*>(lds + (i * T::kThreads + threadIdx.x) * 16) = v[i];
     }
@@ -143,7 +170,7 @@ template <bool ALONG, int ROWS>
 __device__ __forceinline__ void read_frag(FeedFrag<bf16>& f, const char* lds, int r0, int s, int lane) {
   const int half = lane >> 5, l32 = lane & 31;
   if constexpr (ALONG) {
-    f.v = *reinterpret_cast<const bf16x8*>(lds + (r0 + l32) * 128 + (((2 * s + half) ^ (l32 & 7)) << 4));
+    f.v = *reinterpret_cast<const bf16x8*>(lds + (r0 + l32) * 128 + (((2 * s + half) ^ ((l32 >> 1) & 7)) << 4));
   } else {
     typedef __attribute__((address_space(3))) feed_s16x4* LdsPtr;
     const int i = lane & 15, unit = (r0 >> 4) + ((lane >> 4) & 1), k = 16 * s + 8 * half + (i >> 2);
@@ -157,7 +184,7 @@ template <bool ALONG, int ROWS>
 __device__ __forceinline__ void read_frag(FeedFrag<float>& f, const char* lds, int r0, int s, int lane) {
   const int half = lane >> 5, l32 = lane & 31;
   if constexpr (ALONG) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(lds + (r0 + l32) * 128 + (((2 * s + half) ^ (l32 & 7)) << 4));
+    const f32x4 v = *reinterpret_cast<const f32x4*>(lds + (r0 + l32) * 128 + (((2 * s + half) ^ ((l32 >> 1) & 7)) << 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) f.v[e] = v[e];
   } else {
@@ -176,10 +203,13 @@ __device__ __forceinline__ f32x16 feed_mma(const FeedFrag<float>& a, const FeedF
   return c;
 }
 
-// Waits for everything this wave has asked for, then for the other waves.
+// Waits until all but the last LATER loads have arrived (loads and stores end
+// in order), then for the other waves.
+template <int LATER>
 __device__ __forceinline__ void step_barrier() {
+  static_assert(LATER < 16, "vmcnt's low bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_waitcnt(0x0070 | LATER);  // vmcnt(LATER), lgkmcnt(0), expcnt at its maximum
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -366,49 +396,105 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
   }
 }
 
+// One operand's loads, which run ahead of the products.
+template <typename DT, int BIG, int OP, bool IS_A>
+struct FeedStream {
+  static constexpr bool kAlong = IS_A ? FeedShape<OP>::kAlongA : FeedShape<OP>::kAlongB;
+  static constexpr int kStep = 128 / (int)sizeof(DT);
+  Operand<DT, BIG, kAlong> op;
+  int id, kt, end, slot;  // the next step to fetch and where it goes
+  __device__ __forceinline__ void place(const FeedArgs& a, int tiles_m, int tiles_n) {
+    const FeedItem w = feed_item<BIG, OP>(a, tiles_m, tiles_n, id);
+    kt = w.k0;
+    end = w.k1;
+    if (IS_A) {
+      if (kAlong)
+        op.template place_along<false>(a.A, a.lda, w.m0, a.M, 0);
+      else
+        op.place_across(a.A, a.lda, w.m0, a.cols_a);
+    } else {
+      if (kAlong)
+        op.template place_along<OP == kFeedIn>(a.B, a.ldb, w.n0, OP == kFeedIn ? a.F : a.N, a.F);
+      else
+        op.place_across(a.B, a.ldb, w.n0, a.cols_b);
+    }
+  }
+  // Goes on to the next item where this one's steps are all fetched; whether
+  // there is a step left.
+  __device__ __forceinline__ bool ready(const FeedArgs& a, int tiles_m, int tiles_n, int items) {
+    if (kt == end && id < items) {
+      id += gridDim.x;
+      if (id < items) place(a, tiles_m, tiles_n);
+    }
+    return id < items;
+  }
+  // The step's first k, how far k goes and the operand's row (across): those
+  // of the gate's weights and of its partner's, F each, follow each other.
+  __device__ __forceinline__ void where(const FeedArgs& a, int* k, int* row, int* limit) const {
+    *k = *row = kt * kStep;
+    *limit = IS_A ? a.KA : a.KB;
+    if (OP == kFeedDx && !IS_A) {
+      *limit = a.F;
+      if (*k >= a.Fp) {
+        *k -= a.Fp;
+        *row = *k + a.F;
+      }
+    }
+  }
+  __device__ __forceinline__ bool whole(const FeedArgs& a) const {
+    int k, row, limit;
+    where(a, &k, &row, &limit);
+    return k + kStep <= limit;
+  }
+  __device__ __forceinline__ char* to(char* lds) const { return lds + slot * FeedTile<BIG>::kBytes; }
+  __device__ __forceinline__ void load(const FeedArgs& a, char* lds, int i) const {
+    int k, row, limit;
+    where(a, &k, &row, &limit);
+    op.load(to(lds), i, k, row, IS_A ? a.lda : a.ldb);
+  }
+  __device__ __forceinline__ void next() {
+    ++kt;
+    slot = slot < 3 ? slot + 2 : slot - 3;
+  }
+  __device__ __forceinline__ void fetch(const FeedArgs& a, char* lds) {
+    int k, row, limit;
+    where(a, &k, &row, &limit);
+    op.fetch(to(lds), k, row, limit, IS_A ? a.lda : a.ldb);
+    next();
+  }
+};
+
 template <typename DT, int BIG, int OP>
 __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedArgs a, int tiles_m, int tiles_n) {
   using T = FeedTile<BIG>;
   using S = FeedShape<OP>;
-  constexpr int kStep = 128 / (int)sizeof(DT), MI = T::MI;
+  constexpr int MI = T::MI;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / T::kWavesN, wn = wave % T::kWavesN;
   const int items = tiles_m * tiles_n * a.splits;
   // this round's items of one XCD are neighbours
-  const int grid = gridDim.x, whole = grid / 8 * 8;
-  const int mine = (int)blockIdx.x < whole ? (blockIdx.x % 8) * (whole / 8) + blockIdx.x / 8 : blockIdx.x;
+  const int grid = gridDim.x, whole_grid = grid / 8 * 8;
+  const int mine = (int)blockIdx.x < whole_grid ? (blockIdx.x % 8) * (whole_grid / 8) + blockIdx.x / 8 : blockIdx.x;
   if (mine >= items) return;
 
-  Operand<DT, BIG, S::kAlongA> oa;
-  Operand<DT, BIG, S::kAlongB> ob;
-  auto place = [&](const FeedItem& w) {
-    if (S::kAlongA)
-      oa.template place_along<false>(a.A, a.lda, w.m0, a.M, 0);
-    else
-      oa.place_across(a.A, a.lda, w.m0, a.cols_a);
-    if (S::kAlongB)
-      ob.template place_along<OP == kFeedIn>(a.B, a.ldb, w.n0, OP == kFeedIn ? a.F : a.N, a.F);
-    else
-      ob.place_across(a.B, a.ldb, w.n0, a.cols_b);
-  };
-  auto fetch = [&](int kt, int half) {
-    char* at = lds + half * 2 * T::kBytes;
-    const int k = kt * kStep;
-    oa.fetch(at, k, k, a.KA, a.lda);
-    if constexpr (OP == kFeedDx) {  // rows of the gate's and of its partner's weights, F each
-      const bool second = k >= a.Fp;
-      ob.fetch(at + T::kBytes, second ? k - a.Fp : k, second ? k - a.Fp + a.F : k, a.F, a.ldb);
-    } else {
-      ob.fetch(at + T::kBytes, k, k, a.KB, a.ldb);
-    }
-  };
-
-  FeedItem w = feed_item<BIG, OP>(a, tiles_m, tiles_n, mine);
-  int half = 0;
-  place(w);
-  fetch(w.k0, 0);
+  // Slots of LDS are taken in turn: A 0, B 0, A 1, B 1, ... While step t is
+  // multiplied, A t + 1 is there, B t + 1 and A t + 2 go to the two places that
+  // step t - 1 left.
+  FeedStream<DT, BIG, OP, true> sa;
+  FeedStream<DT, BIG, OP, false> sb;
+  sa.id = sb.id = mine;
+  sa.slot = 0;
+  sb.slot = 1;
+  sa.place(a, tiles_m, tiles_n);
+  sb.place(a, tiles_m, tiles_n);
+  sa.fetch(a, lds);
+  sb.fetch(a, lds);
+  if (sa.ready(a, tiles_m, tiles_n, items)) sa.fetch(a, lds);
+  step_barrier<0>();
+  int slot = 0;
   for (int id = mine; id < items; id += grid) {
+    const FeedItem w = feed_item<BIG, OP>(a, tiles_m, tiles_n, id);
     f32x16 acc[MI][2];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -416,35 +502,37 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    FeedItem next = w;
-    for (int kt = w.k0; kt < w.k1; ++kt) {
-      step_barrier();
-      if (kt + 1 < w.k1) {
-        fetch(kt + 1, half ^ 1);
-      } else if (id + grid < items) {
-        next = feed_item<BIG, OP>(a, tiles_m, tiles_n, id + grid);
-        place(next);
-        fetch(next.k0, half ^ 1);
-      }
-      const char* at = lds + half * 2 * T::kBytes;
+    // One step: its products, and between them the loads (FETCH) and the next
+    // quarter's reads.
+    auto multiply = [&](auto fetch_tag) {
+      constexpr bool FETCH = decltype(fetch_tag)::value;
+      const char *at_a = lds + slot * T::kBytes, *at_b = lds + (slot == T::kSlots - 1 ? 0 : slot + 1) * T::kBytes;
       FeedFrag<DT> fa[2][MI], fb[2][2];
       auto read = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) read_frag<S::kAlongA, T::kRows>(fa[s & 1][i], at, wm * MI * 32 + i * 32, s, lane);
+        for (int j = 0; j < 2; ++j) read_frag<S::kAlongB, T::kRows>(fb[s & 1][j], at_b, wn * 64 + j * 32, s, lane);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) read_frag<S::kAlongB, T::kRows>(fb[s & 1][j], at + T::kBytes, wn * 64 + j * 32, s, lane);
+        for (int i = 0; i < MI; ++i) read_frag<S::kAlongA, T::kRows>(fa[s & 1][i], at_a, wm * MI * 32 + i * 32, s, lane);
       };
       read(0);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if (s < 3) read(s + 1);
+        if constexpr (FETCH) {
+          if (s < 2) {
+            sb.load(a, lds, 2 * s);
+            sb.load(a, lds, 2 * s + 1);
+          } else {
+            sa.load(a, lds, 2 * s - 4);
+            sa.load(a, lds, 2 * s - 3);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[i][j] = feed_mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
       }
       if constexpr (sizeof(DT) == 2) {
-        // the reads of a quarter go out between the products of the one before
         constexpr int kReads = MI * (S::kAlongA ? 1 : 2) + 2 * (S::kAlongB ? 1 : 2), kEach = (kReads + 2 * MI - 1) / (2 * MI);
         __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
 #pragma unroll
@@ -453,17 +541,43 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
           for (int m = 0; m < 2 * MI; ++m) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             if (s < 3 && m * kEach < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+            if (FETCH && m >= 2 * MI - 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
           }
         }
       }
-      half ^= 1;
+    };
+    // What the next step needs has arrived where the steps end: a tile's stores
+    // are behind that wait.
+    for (int kt = w.k0; kt < w.k1;) {
+      bool fast = true;
+      for (; kt < w.k1 && fast; ++kt) {
+        const bool more_b = sb.ready(a, tiles_m, tiles_n, items), more_a = sa.ready(a, tiles_m, tiles_n, items);
+        fast = more_a && more_b && sa.whole(a) && sb.whole(a);
+        if (!fast) break;
+        multiply(std::true_type{});
+        sb.next();
+        sa.next();
+        step_barrier<T::kTimes>();
+        slot = slot < 3 ? slot + 2 : slot - 3;
+      }
+      if (kt < w.k1) {
+        if (sb.id < items) sb.fetch(a, lds);
+        const bool counted = sa.id < items && sa.whole(a);
+        if (sa.id < items) sa.fetch(a, lds);
+        multiply(std::false_type{});
+        if (counted)
+          step_barrier<T::kTimes>();
+        else
+          step_barrier<0>();
+        slot = slot < 3 ? slot + 2 : slot - 3;
+        ++kt;
+      }
     }
     const bool whole = w.m0 + T::kRows <= a.M && w.n0 + (OP == kFeedIn ? T::kRows / 2 : T::kRows) <= (OP == kFeedIn || OP == kFeedDh ? a.F : a.N);
     if (whole)
       feed_results<DT, BIG, OP, true>(a, w, acc, wm, wn, lane);
     else
       feed_results<DT, BIG, OP, false>(a, w, acc, wm, wn, lane);
-    w = next;
   }
 }
 

@@ -157,6 +157,8 @@ int sel_forward(const RnnSelectiveScanDesc* d, const RnnSelectiveScanIO* io, voi
 // ---------------------------------------------------------------------------
 // Gated feed-forward
 // ---------------------------------------------------------------------------
+constexpr int64_t kFeedMostWidth = 1 << 21;  // 256 rows of fp32 are 2 GiB
+
 int validate(const RnnFeedForwardDesc* d) {
   if (!d) return RNN_E_NULL;
   if (!dtype_ok(d->dtype)) return RNN_E_UNSUPPORTED;
@@ -164,9 +166,9 @@ int validate(const RnnFeedForwardDesc* d) {
     return RNN_E_UNSUPPORTED;
   if (d->rows < 1 || d->N < 1 || d->F < 1 || d->N_out < 1 || (d->aligned | 1) != 1) return RNN_E_SHAPE;
   if (d->x_ld < d->N || d->in_ld < d->N || d->out_ld < d->F) return RNN_E_SHAPE;
-  // rows, columns and steps of the products are counted in 32 bits, and so are their tiles
-  constexpr int64_t most = 1 << 30;
-  if (d->rows > most || d->N > most || d->F > most / 2 - 64 || d->N_out > most) return RNN_E_SHAPE;
+  // rows, columns and steps of the products are counted in 32 bits, and so are
+  // their tiles and the bytes of a tile's 256 rows
+  if (d->rows > 1 << 30 || d->N > kFeedMostWidth || d->F > kFeedMostWidth / 2 || d->N_out > kFeedMostWidth) return RNN_E_SHAPE;
   auto tiles = [](double m, double n) { return (m / 128.0 + 1.0) * (n / 64.0 + 1.0) * 32.0; };
   const double r = (double)d->rows, n = d->N, f = 2.0 * d->F + 128.0, o = d->N_out;
   if (std::fmax(std::fmax(tiles(r, f), tiles(r, o)), std::fmax(tiles(f, n), std::fmax(tiles(r, n), tiles(o, f)))) > 2147483647.0)
@@ -185,9 +187,9 @@ struct FeedSizes {
     Fm = up(d->F, m);
     Op = up(d->N_out, m);
     Fp = up(d->F, 8 * m);
-    pack_x = !d->aligned || d->N % m || d->x_ld % m;
-    pack_in = !d->aligned || d->N % m || d->in_ld % m;
-    pack_out = !d->aligned || d->F % m || d->out_ld % m;
+    pack_x = !d->aligned || d->N % m || d->x_ld % m || d->x_ld > kFeedMostWidth;
+    pack_in = !d->aligned || d->N % m || d->in_ld % m || d->in_ld > kFeedMostWidth;
+    pack_out = !d->aligned || d->F % m || d->out_ld % m || d->out_ld > kFeedMostWidth;
     pack_dy = !d->aligned || d->N_out % m;
   }
   int steps(int64_t k) const { return (int)((k + 8 * m - 1) / (8 * m)); }
