@@ -38,6 +38,7 @@ struct alignas(sizeof(DT) * E) Vec {
 };
 template <typename DT>
 constexpr int kWide = 16 / (int)sizeof(DT);
+constexpr int kBackWide = 4;  // channels of a thread backward
 
 template <typename DT, int E>
 __device__ __forceinline__ Vec<DT, E> zero_vec() {
@@ -51,8 +52,8 @@ __device__ __forceinline__ Vec<DT, E> zero_vec() {
 // sigma of the negative.
 __device__ __forceinline__ float silu(float p) { return p * fsigmoid(p); }
 __device__ __forceinline__ float silu_slope(float p) {
-  const float s = fsigmoid(p);
-  return __builtin_fmaf(p * s, fsigmoid(-p), s);
+  const SigmoidPair g = fsigmoid_pair(p);
+  return __builtin_fmaf(p * g.s, g.no, g.s);
 }
 
 __device__ __forceinline__ int row_length(const CausalConvArgs& a, int b) {
@@ -247,7 +248,7 @@ __device__ __forceinline__ void backward_run(const CausalConvArgs& a, int c, int
 }
 
 template <typename DT, int E, int KW>
-__global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(CausalConvArgs a) {
+__global__ __launch_bounds__(kConvThreads, KW <= 4 ? 2 : 1) void conv_backward_kernel(CausalConvArgs a) {
   __shared__ float lds[kConvThreads * E];
   const int groups = a.C / E, lanes = channel_lanes(groups), slots = kConvThreads / lanes;
   const int lane = threadIdx.x % lanes, slot = threadIdx.x / lanes;
@@ -327,19 +328,29 @@ hipError_t backward(const CausalConvArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename DT, int E>
-hipError_t run(const CausalConvArgs& a, bool back, hipStream_t st) {
-  switch (a.W) {
-    case 2: return back ? backward<DT, E, 2>(a, st) : forward<DT, E, 2>(a, st);
-    case 3: return back ? backward<DT, E, 3>(a, st) : forward<DT, E, 3>(a, st);
-    case 4: return back ? backward<DT, E, 4>(a, st) : forward<DT, E, 4>(a, st);
-    default: return back ? backward<DT, E, 8>(a, st) : forward<DT, E, 8>(a, st);
+template <typename DT, int E, bool BACK>
+hipError_t run(const CausalConvArgs& a, hipStream_t st) {
+  if constexpr (BACK) {
+    switch (a.W) {
+      case 2: return backward<DT, E, 2>(a, st);
+      case 3: return backward<DT, E, 3>(a, st);
+      case 4: return backward<DT, E, 4>(a, st);
+      default: return backward<DT, E, 8>(a, st);
+    }
+  } else {
+    switch (a.W) {
+      case 2: return forward<DT, E, 2>(a, st);
+      case 3: return forward<DT, E, 3>(a, st);
+      case 4: return forward<DT, E, 4>(a, st);
+      default: return forward<DT, E, 8>(a, st);
+    }
   }
 }
 
 template <typename DT>
 hipError_t run_width(const CausalConvArgs& a, bool back, hipStream_t st) {
-  return a.vec ? run<DT, kWide<DT>>(a, back, st) : run<DT, 1>(a, back, st);
+  if (back) return a.vec ? run<DT, kBackWide, true>(a, st) : run<DT, 1, true>(a, st);
+  return a.vec ? run<DT, kWide<DT>, false>(a, st) : run<DT, 1, false>(a, st);
 }
 
 }  // namespace
@@ -347,7 +358,7 @@ hipError_t run_width(const CausalConvArgs& a, bool back, hipStream_t st) {
 // About four workgroups a compute unit over all channel tiles, fewer where
 // the runs do not fill them.
 int conv_parts(int T, int B, int C, bool bf, int cus) {
-  const int E = bf ? kWide<bf16> : kWide<float>, groups = (C + E - 1) / E, lanes = channel_lanes(groups);
+  const int E = kBackWide, groups = (C + E - 1) / E, lanes = channel_lanes(groups);
   const int64_t tiles = (groups + lanes - 1) / lanes, slots = kConvThreads / lanes;
   const int64_t units = (int64_t)((T + kRun - 1) / kRun) * B;
   int64_t parts = 4 * (int64_t)cus / tiles;

@@ -187,6 +187,18 @@ __device__ __forceinline__ float clampf(float x, float lo, float hi) { return x 
 // large argument gives +inf and rcp(inf) = 0, so both tails are exact.
 __device__ __forceinline__ float fsigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + fexp(-x)); }
 
+// sigma(x) and sigma(-x) = 1 - sigma(x), each with its own relative accuracy,
+// for one exponential and one reciprocal: exp of -|x| cannot overflow and
+// neither value is formed by a difference.
+struct SigmoidPair {
+  float s, no;
+};
+__device__ __forceinline__ SigmoidPair fsigmoid_pair(float x) {
+  const float e = fexp(-__builtin_fabsf(x));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  return x >= 0.f ? SigmoidPair{r, er} : SigmoidPair{er, r};
+}
+
 // tanh(x) = sign(x) (1 - e) / (1 + e) with e = exp(-2|x|) in (0, 1]; near
 // zero the absolute error stays at the fp32 rounding level of 1.
 __device__ __forceinline__ float ftanh(float x) {

@@ -39,21 +39,21 @@ __device__ __forceinline__ void store4(DT* p, const f32x4& v, int n) {
     if (r < n) p[r] = from_f32<DT>(v[r]);
 }
 
-// acc[w][t] += the weights' rows (w of 16 each) times 16 rows of x (t), over
-// this wave's share of the steps of 32.
+// acc[w][t] = the weights' rows (w of 16 each) times 16 rows of x (t), over
+// this wave's share of the steps [first, steps) of 32.
 template <typename DT, int NW, int MT, int WAVES, int DEEP>
 __device__ __forceinline__ void few_product(f32x4 (&acc)[NW][MT], const DT* (&wrow)[NW], const DT* (&xrow)[MT], int K, int KX,
-                                            bool wvec, bool xvec, int wave, int group) {
-  const int steps = (K + 31) / 32;
+                                            bool wvec, bool xvec, int first, int steps, int wave, int group) {
 #pragma unroll
   for (int w = 0; w < NW; ++w)
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[w][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int s0 = wave; s0 < steps; s0 += WAVES * DEEP) {
+  for (int s0 = first + wave; s0 < steps; s0 += WAVES * DEEP) {
     Frag<DT> fw[DEEP][NW], fx[DEEP][MT];
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
-      const int col = (s0 + d * WAVES) * 32 + 8 * group;  // past K: zeros
+      const int step = s0 + d * WAVES;
+      const int col = step < steps ? step * 32 + 8 * group : K > KX ? K : KX;  // past the end: zeros
 #pragma unroll
       for (int w = 0; w < NW; ++w) fw[d][w] = load8<DT, false>(wrow[w], col, K, wvec);
 #pragma unroll
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kInWaves * 64) void feed_few_in_kernel(FeedFewArgs 
     xrow[t] = (const DT*)a.x + m * a.ldx;
   }
   f32x4 acc[2][MT];
-  few_product<DT, 2, MT, kInWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.n, a.n, a.vec, a.vec, wave, group);
+  few_product<DT, 2, MT, kInWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.n, a.n, a.vec, a.vec, 0, (a.n + 31) / 32, wave, group);
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     sums[wave][t][lane] = acc[0][t];
@@ -109,6 +109,7 @@ __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArg
   __shared__ f32x4 sums[kOutWaves][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, group = lane >> 4;
   const int n0 = blockIdx.x * 16;
+  const int steps = (a.F + 31) / 32, each = (steps + a.splits - 1) / a.splits, first = blockIdx.y * each;
   const DT *wrow[1], *xrow[MT];
   wrow[0] = (const DT*)a.w_out + (int64_t)(n0 + i < a.n_out ? n0 + i : a.n_out - 1) * a.ld_out;
 #pragma unroll
@@ -117,7 +118,8 @@ __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArg
     xrow[t] = (const DT*)a.h + (int64_t)m * a.Fp;
   }
   f32x4 acc[1][MT];
-  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, a.vec, true, wave, group);
+  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, a.vec, true, first, steps - first < each ? steps : first + each, wave,
+                                                                 group);
 #pragma unroll
   for (int t = 0; t < MT; ++t) sums[wave][t][lane] = acc[0][t];
   __syncthreads();
@@ -127,6 +129,10 @@ __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArg
   for (int k = 1; k < kOutWaves; ++k) y += sums[k][wave][lane];
   const int m = 16 * wave + i, n = n0 + 4 * group;
   if (m >= a.rows) return;
+  if (a.splits > 1) {
+    store4(a.part + ((int64_t)blockIdx.y * a.rows + m) * a.n_out + n, y, a.n_out - n);
+    return;
+  }
   if (a.residual) {
     const DT* r = (const DT*)a.residual + m * a.ldr + n;
 #pragma unroll
@@ -139,8 +145,13 @@ __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArg
 template <typename DT, int MT>
 hipError_t few(const FeedFewArgs& a, hipStream_t st) {
   launch_kernel(feed_few_in_kernel<DT, MT>, dim3((unsigned)((a.Fp + 15) / 16)), dim3(kInWaves * 64), 0, st, a);
-  launch_kernel(feed_few_out_kernel<DT, MT>, dim3((unsigned)((a.n_out + 15) / 16)), dim3(kOutWaves * 64), 0, st, a);
-  return hipGetLastError();
+  launch_kernel(feed_few_out_kernel<DT, MT>, dim3((unsigned)((a.n_out + 15) / 16), (unsigned)a.splits), dim3(kOutWaves * 64), 0,
+                st, a);
+  if (a.splits == 1) return hipGetLastError();
+  FeedArgs j{};
+  j.M = a.rows; j.N = a.n_out; j.splits = a.splits; j.part = a.part;
+  j.out = a.y; j.ldo = a.n_out; j.residual = a.residual; j.ldr = a.ldr;
+  return launch_feed_join(j, sizeof(DT) == 2, st);
 }
 
 template <typename DT>
@@ -239,6 +250,21 @@ FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, i
     }
   }
   return best;
+}
+
+// A workgroup of the second product reads all hidden values (F of each row)
+// beside its 16 rows of weights: with more than 16 rows that is what bounds it,
+// so the summed dimension is divided over as many workgroups as the device has
+// compute units, and a third launch adds up. 64 rows, F = 4096, 1024 outputs,
+// bf16: 21 us undivided; with 16 rows and less the launch would cost more.
+int feed_few_splits(int64_t rows, int F, int n_out, int cus) {
+  if (rows <= 16) return 1;
+  const int tiles = (n_out + 15) / 16, steps = (F + 31) / 32;
+  int want = cus / tiles;
+  if (want > steps / 16) want = steps / 16;  // a step for every wave
+  if (want < 2) return 1;
+  const int each = (steps + want - 1) / want;
+  return (steps + each - 1) / each;
 }
 
 hipError_t launch_feed_few(const FeedFewArgs& a, bool bf, hipStream_t st) { return bf ? few_rows<bf16>(a, st) : few_rows<float>(a, st); }

@@ -48,13 +48,13 @@ __device__ __forceinline__ Activated activate(float g, int kind) {
   if (kind == RNN_ACT_GELU_TANH) {
     constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     const float g2 = g * g, u = c * g * __builtin_fmaf(0.044715f, g2, 1.0f);
-    const float s = fsigmoid(u), no = fsigmoid(-u);
-    r.act = g * s;
-    r.slope = __builtin_fmaf(g * s * no, c * __builtin_fmaf(3.0f * 0.044715f, g2, 1.0f), s);
+    const SigmoidPair p = fsigmoid_pair(u);
+    r.act = g * p.s;
+    r.slope = __builtin_fmaf(g * p.s * p.no, c * __builtin_fmaf(3.0f * 0.044715f, g2, 1.0f), p.s);
   } else {
-    const float s = fsigmoid(g), no = fsigmoid(-g);
-    r.act = kind == RNN_ACT_SIGMOID ? s : g * s;
-    r.slope = kind == RNN_ACT_SIGMOID ? s * no : __builtin_fmaf(g * s, no, s);
+    const SigmoidPair p = fsigmoid_pair(g);
+    r.act = kind == RNN_ACT_SIGMOID ? p.s : g * p.s;
+    r.slope = kind == RNN_ACT_SIGMOID ? p.s * p.no : __builtin_fmaf(g * p.s, p.no, p.s);
   }
   return r;
 }

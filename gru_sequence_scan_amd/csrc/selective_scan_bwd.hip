@@ -231,9 +231,10 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
             for (int j = 0; j < J; ++j) acc[s] = __builtin_fmaf(hs[4 * g + s + 1][j], cv[j], acc[s]);
           }
           const float yv = __builtin_fmaf(D, xv, quad_scatter(acc, q));
-          const float zv = to_f32<DT>(lds_z[at]), sig = fsigmoid(zv);
-          lds_z[at] = from_f32<DT>(on ? v * yv * __builtin_fmaf(zv * sig, fsigmoid(-zv), sig) : 0.f);
-          v = on ? v * (zv * sig) : 0.f;
+          const float zv = to_f32<DT>(lds_z[at]);
+          const SigmoidPair g = fsigmoid_pair(zv);
+          lds_z[at] = from_f32<DT>(on ? v * yv * __builtin_fmaf(zv * g.s, g.no, g.s) : 0.f);
+          v = on ? v * (zv * g.s) : 0.f;
         }
         sum_D = __builtin_fmaf(v, xv, sum_D);
         float sum_w[4], sum_g[4];

@@ -231,6 +231,8 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
   FeedSpace a{};
   if (!train && !back && feed_few(d)) {  // any alignment is taken there
     a.h = l.take(rows * s.Fp * e);
+    const size_t splits = (size_t)feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
+    a.part = l.take(splits > 1 ? splits * rows * d->N_out * sizeof(float) : 0);
     a.bytes = l.bytes;
     return a;
   }
@@ -307,6 +309,8 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
     f.x = io->x; f.ldx = d->x_ld; f.w_in = io->w_in; f.ld_in = d->in_ld; f.w_out = io->w_out; f.ld_out = d->out_ld;
     f.residual = io->residual; f.ldr = io->residual ? d->residual_ld : 0;
     f.h = mem + at.h; f.Fp = s.Fp; f.y = io->y;
+    f.part = reinterpret_cast<float*>(mem + at.part);
+    f.splits = feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
     f.vec = !s.pack_x && !s.pack_in && !s.pack_out;
     return hip_status(launch_feed_few(f, bf, st));
   }

@@ -112,8 +112,10 @@ struct FeedFewArgs {
   void* h;                          // [rows, Fp] (workspace)
   int Fp;
   void* y;
+  float* part; int splits;          // splits > 1: partial second products [splits, rows, n_out] (workspace)
   int vec;                          // rows take 16-byte accesses
 };
+int feed_few_splits(int64_t rows, int F, int n_out, int cus);
 hipError_t launch_feed_few(const FeedFewArgs& a, bool bf16_storage, hipStream_t stream);
 // Rows of a tensor copied to a pitch of whole 16 bytes, zeros behind each.
 hipError_t launch_feed_pack(const void* from, int64_t ld, int64_t rows, int cols, void* to, int pitch, bool bf16_storage,
