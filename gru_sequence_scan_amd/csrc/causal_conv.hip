@@ -62,22 +62,38 @@ __device__ __forceinline__ int row_length(const CausalConvArgs& a, int b) {
 }
 
 // x'_s for any s (past the row's end: some step of the row, which the caller
-// does not use; in front of the state: zero).
+// does not use; in front of the state: zero). The load itself has no
+// condition, so that many of them are on their way at once.
 template <typename DT, int E>
 __device__ __forceinline__ Vec<DT, E> input_at(const CausalConvArgs& a, const DT* x, const DT* state, int s, int L) {
-  if (s >= 0) {
-    if (L == 0) return zero_vec<DT, E>();
-    return *reinterpret_cast<const Vec<DT, E>*>(x + (int64_t)(s < L ? s : L - 1) * a.x_t);
-  }
-  const int j = s + a.W - 1;
-  if (!state || j < 0) return zero_vec<DT, E>();
-  return *reinterpret_cast<const Vec<DT, E>*>(state + (int64_t)j * a.B * a.C);
+  const int j = s + a.W - 1, last = L > 0 ? L - 1 : 0;
+  const bool front = s < 0 && state;
+  const DT* p = front ? state + (int64_t)(j > 0 ? j : 0) * a.B * a.C : x + (int64_t)(s < 0 ? 0 : s < last ? s : last) * a.x_t;
+  const Vec<DT, E> v = *reinterpret_cast<const Vec<DT, E>*>(p);
+  return (s >= 0 ? L > 0 : front && j >= 0) ? v : zero_vec<DT, E>();
 }
 
 // The taps of E channels, the oldest first; a filter shorter than KW has
-// zeros in front, whose inputs are never read.
+// zeros in front, whose inputs are never used.
 template <typename DT, int E, int KW>
 __device__ __forceinline__ void load_taps(const CausalConvArgs& a, int c, float (&w)[KW][E], float (&bias)[E]) {
+  if constexpr (KW <= 4 && E > 1) {
+    if (a.wvec) {  // whole filters, 8 bytes an access
+      constexpr int M = 8 / (int)sizeof(DT);
+      Vec<DT, M> r[E * KW / M], rb[E / M];
+#pragma unroll
+      for (int i = 0; i < E * KW / M; ++i) r[i] = reinterpret_cast<const Vec<DT, M>*>((const DT*)a.w + (int64_t)c * KW)[i];
+#pragma unroll
+      for (int i = 0; i < E / M; ++i) rb[i] = reinterpret_cast<const Vec<DT, M>*>((const DT*)(a.bias ? a.bias : a.w) + c)[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+#pragma unroll
+        for (int k = 0; k < KW; ++k) w[k][e] = to_f32<DT>(r[(e * KW + k) / M].v[(e * KW + k) % M]);
+        bias[e] = a.bias ? to_f32<DT>(rb[e / M].v[e % M]) : 0.f;
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
 #pragma unroll
@@ -104,8 +120,12 @@ __global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(CausalConvAr
   const DT* x = (const DT*)a.x + b * a.x_b + c;
   const DT* state = a.state ? (const DT*)a.state + cell : nullptr;
   if (t0 == 0 && a.state_n) {
-    for (int j = 0; j < a.W - 1; ++j)
-      *reinterpret_cast<Vec<DT, E>*>((DT*)a.state_n + j * y_t + cell) = input_at<DT, E>(a, x, state, L - a.W + 1 + j, L);
+    Vec<DT, E> last[KW - 1];
+#pragma unroll
+    for (int j = 0; j < KW - 1; ++j) last[j] = input_at<DT, E>(a, x, state, L - a.W + 1 + j, L);
+#pragma unroll
+    for (int j = 0; j < KW - 1; ++j)
+      if (j < a.W - 1) *reinterpret_cast<Vec<DT, E>*>((DT*)a.state_n + j * y_t + cell) = last[j];
   }
   DT* y = (DT*)a.y + cell;
   if (t0 >= L) {

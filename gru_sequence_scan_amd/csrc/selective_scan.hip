@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanA
   const int hc = p.c0 + (live ? ch : 0);
   const int64_t cell = (int64_t)p.b * a.H + hc, cells = (int64_t)a.B * a.H;
   float A2[J], h[J];
-  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, A2);
+  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, a.svec, A2);
 #pragma unroll
   for (int j = 0; j < J; ++j) A2[j] *= kLog2e;
   if (COMPOSE) {
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanA
   } else if (a.segs > 1) {
     read_states<J>(a.map_s + (p.seg * cells + cell) * NP + q * J, h);
   } else {
-    load_row<J>(a.h0 ? a.h0 + cell * a.N : nullptr, q * J, a.N, h);
+    load_row<J>(a.h0 ? a.h0 + cell * a.N : nullptr, q * J, a.N, a.svec, h);
   }
   const float bias = a.dt_bias ? a.dt_bias[hc] : 0.f, D = a.D ? a.D[hc] : 0.f;
   const DT* x = (const DT*)a.x + p.b * a.x_b;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanA
   }
   // steps past the row's end
   for (; t < p.t1; t += kSteps) Tile::store(lds_y, y, y_t, t, p.t1, p.L, p.c0, p.live);
-  if (a.h_n && live && p.seg == a.segs - 1) store_row<J>(a.h_n + cell * a.N, q * J, a.N, h);
+  if (a.h_n && live && p.seg == a.segs - 1) store_row<J>(a.h_n + cell * a.N, q * J, a.N, a.svec, h);
 }
 
 // The states that enter the segments, one thread per state: in the place of
@@ -178,35 +178,54 @@ __global__ __launch_bounds__(kSelThreads) void sel_short_kernel(SelectiveScanArg
   const int b = (int)(cell / a.H), hc = (int)(cell % a.H), group = hc / (a.H / a.G);
   const int len = a.lengths ? a.lengths[b] : a.T, L = len < 0 ? 0 : (len > a.T ? a.T : len);
   float A2[J], h[J];
-  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, A2);
+  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, a.svec, A2);
 #pragma unroll
   for (int j = 0; j < J; ++j) A2[j] *= kLog2e;
-  load_row<J>(a.h0 ? a.h0 + cell * a.N : nullptr, q * J, a.N, h);
+  load_row<J>(a.h0 ? a.h0 + cell * a.N : nullptr, q * J, a.N, a.svec, h);
   if (a.keep && live) write_states<J>(a.keep + cell * NP + q * J, h);
   const float bias = a.dt_bias ? a.dt_bias[hc] : 0.f, D = a.D ? a.D[hc] : 0.f;
+  // the next step's inputs are on their way while one is worked on; past the
+  // row's end they are some step of it
+  struct {
+    DT x, dt, z, b[J], c[J];
+  } in, next;
+  auto load = [&](auto& to, int t) {
+    t = t < L ? t : L > 0 ? L - 1 : 0;
+    to.x = ((const DT*)a.x)[t * a.x_t + b * a.x_b + hc];
+    to.dt = ((const DT*)a.dt)[t * a.dt_t + b * a.dt_b + hc];
+    if (a.z) to.z = ((const DT*)a.z)[t * a.z_t + b * a.z_b + hc];
+    const DT* Bm = (const DT*)a.Bm + t * a.B_t + b * a.B_b + group * a.B_g;
+    const DT* Cm = (const DT*)a.Cm + t * a.C_t + b * a.C_b + group * a.C_g;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int n = q * J + j < a.N ? q * J + j : a.N - 1;
+      to.b[j] = Bm[n];
+      to.c[j] = Cm[n];
+    }
+  };
+  load(in, 0);
   for (int t = 0; t < a.T; ++t) {
+    if (t + 1 < a.T) load(next, t + 1);
     float v = 0.f;
     if (t < L) {
-      const float xv = to_f32<DT>(((const DT*)a.x)[t * a.x_t + b * a.x_b + hc]);
-      const float d = step_length(to_f32<DT>(((const DT*)a.dt)[t * a.dt_t + b * a.dt_b + hc]) + bias, a.softplus);
-      const DT* Bm = (const DT*)a.Bm + t * a.B_t + b * a.B_b + group * a.B_g;
-      const DT* Cm = (const DT*)a.Cm + t * a.C_t + b * a.C_b + group * a.C_g;
+      const float xv = to_f32<DT>(in.x);
+      const float d = step_length(to_f32<DT>(in.dt) + bias, a.softplus);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const bool on = q * J + j < a.N;
-        const float bv = on ? to_f32<DT>(Bm[q * J + j]) : 0.f, cv = on ? to_f32<DT>(Cm[q * J + j]) : 0.f;
-        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], d * xv * bv);
-        v = __builtin_fmaf(h[j], cv, v);
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], on ? d * xv * to_f32<DT>(in.b[j]) : 0.f);
+        v = __builtin_fmaf(h[j], on ? to_f32<DT>(in.c[j]) : 0.f, v);
       }
       v = __builtin_fmaf(D, xv, quad_sum(v));
       if (a.z) {
-        const float zv = to_f32<DT>(((const DT*)a.z)[t * a.z_t + b * a.z_b + hc]);
+        const float zv = to_f32<DT>(in.z);
         v *= zv * fsigmoid(zv);
       }
     }
     if (live && q == 0) ((DT*)a.y)[t * cells + cell] = from_f32<DT>(v);
+    in = next;
   }
-  if (a.h_n && live) store_row<J>(a.h_n + cell * a.N, q * J, a.N, h);
+  if (a.h_n && live) store_row<J>(a.h_n + cell * a.N, q * J, a.N, a.svec, h);
 }
 
 template <typename DT, int J, bool VEC>

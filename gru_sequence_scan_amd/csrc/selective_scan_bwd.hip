@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kSelThreads) void sel_compose_back_kernel(Selective
   const int hc = p.c0 + (live ? ch : 0);
   const int64_t cell = (int64_t)p.b * a.H + hc, cells = (int64_t)a.B * a.H;
   float A2[J], c[J];
-  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, A2);
+  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, a.svec, A2);
 #pragma unroll
   for (int j = 0; j < J; ++j) A2[j] *= kLog2e, c[j] = 0.f;
   const float bias = a.dt_bias ? a.dt_bias[hc] : 0.f;
@@ -119,11 +119,11 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
   const int hc = p.c0 + (live ? ch : 0);
   const int64_t cell = (int64_t)p.b * a.H + hc, cells = (int64_t)a.B * a.H;
   float A2[J], c[J], dA[J];
-  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, A2);
+  load_row<J>(a.A + (int64_t)hc * a.N, q * J, a.N, a.svec, A2);
   if (a.segs > 1)
     read_states<J>(a.map_s + (p.seg * cells + cell) * NP + q * J, c);
   else
-    load_row<J>(a.dh_n ? a.dh_n + cell * a.N : nullptr, q * J, a.N, c);
+    load_row<J>(a.dh_n ? a.dh_n + cell * a.N : nullptr, q * J, a.N, a.svec, c);
 #pragma unroll
   for (int j = 0; j < J; ++j) A2[j] *= kLog2e, dA[j] = 0.f;
   const float bias = a.dt_bias ? a.dt_bias[hc] : 0.f, D = a.D ? a.D[hc] : 0.f;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
     }
     lds_barrier();
   }
-  if (a.dh0 && live && p.seg == 0) store_row<J>(a.dh0 + cell * a.N, q * J, a.N, c);
+  if (a.dh0 && live && p.seg == 0) store_row<J>(a.dh0 + cell * a.N, q * J, a.N, a.svec, c);
   if (live) write_states<J>(a.part_a + (p.seg * cells + cell) * NP + q * J, dA);
   sum_D = quad_sum(sum_D);
   sum_bias = quad_sum(sum_bias);

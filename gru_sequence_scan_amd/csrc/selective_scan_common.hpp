@@ -214,17 +214,31 @@ __device__ __forceinline__ void write_states(float* p, const float (&v)[J]) {
     *reinterpret_cast<SelVec<float, W>*>(p + j) = r;
   }
 }
-// The same of a tensor [.., N] whose rows may be shorter than the lanes hold.
+// The same of a tensor [.., N] whose rows may be shorter than the lanes hold
+// (vec: they are not, and aligned); zeros behind N and without a tensor.
 template <int J>
-__device__ __forceinline__ void load_row(const float* row, int n0, int N, float (&v)[J]) {
+__device__ __forceinline__ void load_row(const float* row, int n0, int N, bool vec, float (&v)[J]) {
+  if (!row) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) v[j] = row && n0 + j < N ? row[n0 + j] : 0.f;
+    for (int j = 0; j < J; ++j) v[j] = 0.f;
+  } else if (vec) {
+    read_states<J>(row + n0, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = row[n0 + j < N ? n0 + j : N - 1];
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = n0 + j < N ? v[j] : 0.f;
+  }
 }
 template <int J>
-__device__ __forceinline__ void store_row(float* row, int n0, int N, const float (&v)[J]) {
+__device__ __forceinline__ void store_row(float* row, int n0, int N, bool vec, const float (&v)[J]) {
+  if (vec) {
+    write_states<J>(row + n0, v);
+  } else {
 #pragma unroll
-  for (int j = 0; j < J; ++j)
-    if (n0 + j < N) row[n0 + j] = v[j];
+    for (int j = 0; j < J; ++j)
+      if (n0 + j < N) row[n0 + j] = v[j];
+  }
 }
 
 // The grid of a launch over (row, segment)s and tiles of channels.

@@ -49,6 +49,7 @@ int conv_args(const RnnCausalConvDesc* d, const RnnCausalConvIO* io, CausalConvA
   a->w = io->weight; a->bias = io->bias; a->lengths = io->lengths; a->state = io->state;
   const int64_t m = 16 / (int64_t)e;
   a->vec = d->C % m == 0 && d->x_t % m == 0 && d->x_b % m == 0 && aligned(io->x, 16) && aligned(io->state, 16);
+  a->wvec = aligned(io->weight, 8) && aligned(io->bias, 8);
   return RNN_OK;
 }
 
@@ -133,6 +134,7 @@ int sel_args(const RnnSelectiveScanDesc* d, const RnnSelectiveScanIO* io, void* 
   const int64_t m = 16 / (int64_t)e;
   auto fits = [&](const void* p, int64_t t, int64_t b) { return aligned(p, 16) && t % m == 0 && b % m == 0; };
   a->vec = d->H / d->G % m == 0 && fits(a->x, a->x_t, a->x_b) && fits(a->dt, a->dt_t, a->dt_b) && fits(a->z, a->z_t, a->z_b);
+  a->svec = d->N == sel_padded(d->N) && aligned(a->A, 16) && aligned(a->h0, 16);
   return RNN_OK;
 }
 
@@ -150,6 +152,7 @@ int sel_forward(const RnnSelectiveScanDesc* d, const RnnSelectiveScanIO* io, voi
   a.y = io->y;
   a.h_n = io->h_n;
   if (!aligned(a.y, 16)) a.vec = 0;
+  if (!aligned(a.h_n, 16)) a.svec = 0;
   a.keep = static_cast<float*>(reserve);
   return hip_status(launch_selective_scan(a, d->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
@@ -516,6 +519,7 @@ int rnn_selective_scan_backward(const RnnSelectiveScanDesc* desc, const RnnSelec
   a.part_a = reinterpret_cast<float*>(static_cast<char*>(workspace) + sel_workspace(desc) + sel_bc_bytes(desc));
   for (const void* p : {a.dy, (const void*)a.dx, (const void*)a.ddt, (const void*)a.dz})
     if (!aligned(p, 16)) a.vec = 0;
+  if (!aligned(a.dh_n, 16) || !aligned(a.dh0, 16)) a.svec = 0;
   return hip_status(launch_selective_scan_backward(a, desc->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 

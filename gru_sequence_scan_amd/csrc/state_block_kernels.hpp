@@ -25,6 +25,7 @@ struct CausalConvArgs {
   float* part;                      // [parts, W + 1, C] partial sums of dw and db (workspace)
   int parts;
   int vec;                          // rows take 16-byte accesses
+  int wvec;                         // the filters and the bias take 8-byte accesses
 };
 // Workgroups along time and batch of the backward pass, each with one partial sum.
 int conv_parts(int T, int B, int C, bool bf16_storage, int cus);
@@ -62,6 +63,7 @@ struct SelectiveScanArgs {
   float* part_bc;                              // [tiles of a group, T, B, G, 2, NP]
   float* part_a;                               // [segs, B, H, NP + 2]: dA, then dD and dbias
   int vec;                                     // rows take vector accesses
+  int svec;                                    // ... and so do the states' ([.., N], N as the kernels hold it) and A's
   int xcds;
   int tiles, group_tiles;                      // of 64 channels: in all, and of a group of channels
 };
