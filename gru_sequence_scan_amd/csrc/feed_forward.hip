@@ -217,7 +217,7 @@ hipError_t join(const FeedArgs& a, hipStream_t st) {
 }  // namespace
 
 double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
-  const double rows = p.big ? 256 : 128, cols = op == kFeedIn ? rows / 2 : rows;
+  const double rows = p.tile == kTileBig ? 256 : 128, cols = op == kFeedIn ? rows / 2 : rows;
   return std::ceil((double)M / rows) * std::ceil((double)N / cols);
 }
 
@@ -230,18 +230,20 @@ double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
 // ones, 19334 x 1368 fp32 356 and 501; without that traffic large ones win
 // (dx of the same in bf16: 411 and 480 us).
 FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus) {
-  FeedPlan best{0, 1};
+  FeedPlan best{kTileSmall, 1};
   double least = 0.0;
-  for (int big = 0; big < 2; ++big) {
-    FeedPlan p{big, 1};
-    const double tiles = feed_tiles(p, M, N, op), resident = big ? cus : 2.0 * cus;
+  for (int tile : {kTileSmall, kTileBig, kTileDeep}) {
+    FeedPlan p{tile, 1};
+    const bool big = tile == kTileBig;
+    const double tiles = feed_tiles(p, M, N, op), resident = tile == kTileSmall ? 2.0 * cus : cus;
+    // us of a step, with all workgroups that the device holds at work, and of a tile's results
+    const double step = bf16_storage ? (big ? 2.2 : tile == kTileDeep ? 0.8 : 1.4) : (big ? 7.6 : tile == kTileDeep ? 2.2 : 3.9);
+    const double results = big ? (op == kFeedDh ? 90.0 : 12.0) : 6.0;
     for (int want = 1; want <= (op == kFeedIn || op == kFeedDh ? 1 : 32) && want <= steps; ++want) {
       const int each = (steps + want - 1) / want;
       p.splits = (steps + each - 1) / each;
       if (p.splits != want) continue;
-      const double rounds = std::ceil(tiles * want / resident);
-      const double step = bf16_storage ? (big ? 2.2 : 1.4) : (big ? 7.6 : 3.9);  // us, both workgroups of a unit at work
-      double us = rounds * (each * step + (big ? (op == kFeedDh ? 90.0 : 12.0) : 6.0));
+      double us = std::ceil(tiles * want / resident) * (each * step + results);
       if (want > 1) us += 4.0 + (double)want * M * N * 8.0 / 4e6;
       if (least == 0.0 || us < least) {
         least = us;

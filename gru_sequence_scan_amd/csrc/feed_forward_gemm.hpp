@@ -59,22 +59,28 @@ __device__ __forceinline__ Activated activate(float g, int kind) {
   return r;
 }
 
-template <int BIG>
+// Tiles: kTileBig; kTileSmall, two workgroups a compute unit; kTileDeep, small
+// ones alone on their compute unit, with eight waves (of 32 x 64) and more
+// steps on their way, for products with few tiles.
+template <int TILE>
 struct FeedTile {
-  static constexpr int kRows = BIG ? 256 : 128;       // of either operand
-  static constexpr int kThreads = BIG ? 512 : 256;
-  static constexpr int kWavesN = BIG ? 4 : 2;         // waves across, two waves down
-  static constexpr int MI = BIG ? 4 : 2;              // 32-row blocks of a wave; two across
+  static constexpr bool kBig = TILE == kTileBig;
+  static constexpr int kRows = kBig ? 256 : 128;      // of either operand
+  static constexpr int kThreads = TILE == kTileSmall ? 256 : 512;
+  static constexpr int kWavesN = kRows / 64;          // waves across
+  static constexpr int MI = kRows / 32 * kWavesN / (kThreads / 64);  // 32-row blocks of a wave; two across
   static constexpr int kBytes = kRows * 128;          // one operand's step
-  static constexpr int kSlots = 5, kLds = kSlots * kBytes;
-  static constexpr int kTimes = kBytes / 16 / kThreads;  // 16-byte loads of a thread: 4
+  static constexpr int kAhead = TILE == kTileDeep ? 4 : 2;  // steps that A's loads run ahead; B's one less
+  static constexpr int kSlots = 2 * kAhead + 1, kLds = kSlots * kBytes;
+  static constexpr int kTimes = kBytes / 16 / kThreads;     // 16-byte loads of a thread
+  static constexpr int kResident = TILE == kTileSmall ? 512 : 256;  // workgroups that a device of 256 compute units holds
 };
 
 // 16-byte loads that bring an operand's step into LDS. A thread's addresses
 // are 32-bit distances from the step's, which is the same for all.
-template <typename DT, int BIG, bool ALONG>
+template <typename DT, int TILE, bool ALONG>
 struct Operand {
-  using T = FeedTile<BIG>;
+  using T = FeedTile<TILE>;
   static constexpr int E = 16 / (int)sizeof(DT);              // elements of a chunk
   static constexpr int kStep = 128 / (int)sizeof(DT);         // k of a step
   static constexpr int kChunks = T::kRows / E;                // of a k row (across)
@@ -97,7 +103,7 @@ struct Operand {
   __device__ __forceinline__ void place_along(const void* p, int64_t ld, int row0, int rows, int apart) {
     base = (const char*)p + row0 * ld * (int64_t)sizeof(DT);
     partner = PAIRS ? apart * ld * (int64_t)sizeof(DT) : 0;
-    if (BIG) {  // a wave's rows are all on one side: 8 of every 64
+    if (T::kThreads == 512) {  // a wave's rows are all on one side: 8 of every 64
       if (__builtin_amdgcn_readfirstlane(threadIdx.x) & 256) base += partner;
       partner = 0;
     }
@@ -120,7 +126,7 @@ struct Operand {
   // Load i of a step whose first k is k0 and (across) first row row0.
   __device__ __forceinline__ const char* from(int i, int k0, int64_t row0, int64_t ld) const {
     const char* step = base + (ALONG ? (int64_t)k0 : (row0 + i * kSweep) * ld) * (int64_t)sizeof(DT);
-    if (!BIG && ALONG && i % 2) step += partner;  // every other 32 rows
+    if (T::kThreads == 256 && ALONG && i % 2) step += partner;  // every other 32 rows
     return step + at[ALONG ? i : 0];
   }
   // ... that is there as a whole
@@ -174,7 +180,7 @@ __device__ __forceinline__ void read_frag(FeedFrag<bf16>& f, const char* lds, in
   } else {
     typedef __attribute__((address_space(3))) feed_s16x4* LdsPtr;
     const int i = lane & 15, unit = (r0 >> 4) + ((lane >> 4) & 1), k = 16 * s + 8 * half + (i >> 2);
-    const char* p = lds + k * (ROWS * 2) + ((unit ^ Operand<bf16, 1, false>::turn(k)) << 5) + ((i & 3) << 3);
+    const char* p = lds + k * (ROWS * 2) + ((unit ^ Operand<bf16, kTileBig, false>::turn(k)) << 5) + ((i & 3) << 3);
     const feed_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p));
     const feed_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 4 * ROWS * 2));
     f.v = __builtin_bit_cast(bf16x8, (feed_s16x8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -207,9 +213,9 @@ __device__ __forceinline__ f32x16 feed_mma(const FeedFrag<float>& a, const FeedF
 // in order), then for the other waves.
 template <int LATER>
 __device__ __forceinline__ void step_barrier() {
-  static_assert(LATER < 16, "vmcnt's low bits");
+  static_assert(LATER < 64, "vmcnt has six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | LATER);  // vmcnt(LATER), lgkmcnt(0), expcnt at its maximum
+  __builtin_amdgcn_s_waitcnt(0x0070 | (LATER & 15) | LATER >> 4 << 14);  // vmcnt(LATER), lgkmcnt(0), expcnt at its maximum
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -224,9 +230,9 @@ struct FeedShape {
 struct FeedItem {
   int m0, n0, split, k0, k1;
 };
-template <int BIG, int OP>
+template <int TILE, int OP>
 __device__ __forceinline__ FeedItem feed_item(const FeedArgs& a, int tiles_m, int tiles_n, int id) {
-  constexpr int kRows = FeedTile<BIG>::kRows, kCols = OP == kFeedIn ? kRows / 2 : kRows;
+  constexpr int kRows = FeedTile<TILE>::kRows, kCols = OP == kFeedIn ? kRows / 2 : kRows;
   const int tiles = tiles_m * tiles_n;
   FeedItem w;
   w.split = id / tiles;
@@ -276,10 +282,10 @@ __device__ __forceinline__ void store_half(DT* out, int64_t ld, const float (&va
 // 8 (v / 4) + 4 (lane / 32) + v % 4 of each 32 x 32 block. WHOLE: every row
 // and column of the tile exists; it leaves in halves of a block, and what a
 // half needs from memory is asked for while the one before it is worked on.
-template <typename DT, int BIG, int OP, bool WHOLE>
-__device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& w, const f32x16 (&acc)[FeedTile<BIG>::MI][2], int wm,
+template <typename DT, int TILE, int OP, bool WHOLE>
+__device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& w, const f32x16 (&acc)[FeedTile<TILE>::MI][2], int wm,
                                              int wn, int lane) {
-  constexpr int MI = FeedTile<BIG>::MI, kAcross = OP == kFeedIn ? 1 : 2, kBlocks = kAcross * MI;
+  constexpr int MI = FeedTile<TILE>::MI, kAcross = OP == kFeedIn ? 1 : 2, kBlocks = kAcross * MI;
   const int m_base = w.m0 + wm * MI * 32 + 4 * (lane >> 5), n_base = w.n0 + wn * (OP == kFeedIn ? 32 : 64) + (lane & 31);
   if constexpr (WHOLE) {
     const bool pairs = sizeof(DT) == 2 && a.ldo % 2 == 0 && ((uintptr_t)a.out & 3) == 0;
@@ -397,14 +403,14 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
 }
 
 // One operand's loads, which run ahead of the products.
-template <typename DT, int BIG, int OP, bool IS_A>
+template <typename DT, int TILE, int OP, bool IS_A>
 struct FeedStream {
   static constexpr bool kAlong = IS_A ? FeedShape<OP>::kAlongA : FeedShape<OP>::kAlongB;
   static constexpr int kStep = 128 / (int)sizeof(DT);
-  Operand<DT, BIG, kAlong> op;
+  Operand<DT, TILE, kAlong> op;
   int id, kt, end, slot;  // the next step to fetch and where it goes
   __device__ __forceinline__ void place(const FeedArgs& a, int tiles_m, int tiles_n) {
-    const FeedItem w = feed_item<BIG, OP>(a, tiles_m, tiles_n, id);
+    const FeedItem w = feed_item<TILE, OP>(a, tiles_m, tiles_n, id);
     kt = w.k0;
     end = w.k1;
     if (IS_A) {
@@ -446,7 +452,7 @@ struct FeedStream {
     where(a, &k, &row, &limit);
     return k + kStep <= limit;
   }
-  __device__ __forceinline__ char* to(char* lds) const { return lds + slot * FeedTile<BIG>::kBytes; }
+  __device__ __forceinline__ char* to(char* lds) const { return lds + slot * FeedTile<TILE>::kBytes; }
   __device__ __forceinline__ void load(const FeedArgs& a, char* lds, int i) const {
     int k, row, limit;
     where(a, &k, &row, &limit);
@@ -454,7 +460,7 @@ struct FeedStream {
   }
   __device__ __forceinline__ void next() {
     ++kt;
-    slot = slot < 3 ? slot + 2 : slot - 3;
+    slot = slot + 2 < FeedTile<TILE>::kSlots ? slot + 2 : slot + 2 - FeedTile<TILE>::kSlots;
   }
   __device__ __forceinline__ void fetch(const FeedArgs& a, char* lds) {
     int k, row, limit;
@@ -464,9 +470,9 @@ struct FeedStream {
   }
 };
 
-template <typename DT, int BIG, int OP>
-__global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedArgs a, int tiles_m, int tiles_n) {
-  using T = FeedTile<BIG>;
+template <typename DT, int TILE, int OP>
+__global__ __launch_bounds__(FeedTile<TILE>::kThreads, 2) void feed_kernel(FeedArgs a, int tiles_m, int tiles_n) {
+  using T = FeedTile<TILE>;
   using S = FeedShape<OP>;
   constexpr int MI = T::MI;
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -479,22 +485,25 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
   if (mine >= items) return;
 
   // Slots of LDS are taken in turn: A 0, B 0, A 1, B 1, ... While step t is
-  // multiplied, A t + 1 is there, B t + 1 and A t + 2 go to the two places that
-  // step t - 1 left.
-  FeedStream<DT, BIG, OP, true> sa;
-  FeedStream<DT, BIG, OP, false> sb;
+  // multiplied, B t + kAhead - 1 and A t + kAhead go to the two places that
+  // step t - 1 left; what lies between is there or on its way.
+  FeedStream<DT, TILE, OP, true> sa;
+  FeedStream<DT, TILE, OP, false> sb;
   sa.id = sb.id = mine;
   sa.slot = 0;
   sb.slot = 1;
   sa.place(a, tiles_m, tiles_n);
   sb.place(a, tiles_m, tiles_n);
-  sa.fetch(a, lds);
-  sb.fetch(a, lds);
-  if (sa.ready(a, tiles_m, tiles_n, items)) sa.fetch(a, lds);
+#pragma unroll
+  for (int i = 0; i < T::kAhead; ++i) {
+    if (sa.ready(a, tiles_m, tiles_n, items)) sa.fetch(a, lds);
+    if (i < T::kAhead - 1 && sb.ready(a, tiles_m, tiles_n, items)) sb.fetch(a, lds);
+  }
   step_barrier<0>();
+  constexpr int kLater = T::kTimes * (2 * T::kAhead - 3);
   int slot = 0;
   for (int id = mine; id < items; id += grid) {
-    const FeedItem w = feed_item<BIG, OP>(a, tiles_m, tiles_n, id);
+    const FeedItem w = feed_item<TILE, OP>(a, tiles_m, tiles_n, id);
     f32x16 acc[MI][2];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -519,12 +528,12 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
       for (int s = 0; s < 4; ++s) {
         if (s < 3) read(s + 1);
         if constexpr (FETCH) {
-          if (s < 2) {
-            sb.load(a, lds, 2 * s);
-            sb.load(a, lds, 2 * s + 1);
-          } else {
-            sa.load(a, lds, 2 * s - 4);
-            sa.load(a, lds, 2 * s - 3);
+#pragma unroll
+          for (int i = 0; i < T::kTimes / 2; ++i) {
+            if (s < 2)
+              sb.load(a, lds, s * (T::kTimes / 2) + i);
+            else
+              sa.load(a, lds, (s - 2) * (T::kTimes / 2) + i);
           }
         }
 #pragma unroll
@@ -541,7 +550,7 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
           for (int m = 0; m < 2 * MI; ++m) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             if (s < 3 && m * kEach < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
-            if (FETCH && m >= 2 * MI - 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            if (FETCH && m >= 2 * MI - T::kTimes / 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
           }
         }
       }
@@ -557,63 +566,71 @@ __global__ __launch_bounds__(FeedTile<BIG>::kThreads, 2) void feed_kernel(FeedAr
         multiply(std::true_type{});
         sb.next();
         sa.next();
-        step_barrier<T::kTimes>();
-        slot = slot < 3 ? slot + 2 : slot - 3;
+        step_barrier<kLater>();
+        slot = slot + 2 < T::kSlots ? slot + 2 : slot + 2 - T::kSlots;
       }
       if (kt < w.k1) {
+        // Loads that are newer than the next step's: those of the steps behind
+        // it, where all of them are counted.
+        const bool end = sa.id >= items && sb.id >= items;
+        const bool counted = sa.id < items && sb.id < items && sa.whole(a) && sb.whole(a);
         if (sb.id < items) sb.fetch(a, lds);
-        const bool counted = sa.id < items && sa.whole(a);
         if (sa.id < items) sa.fetch(a, lds);
         multiply(std::false_type{});
         if (counted)
-          step_barrier<T::kTimes>();
+          step_barrier<kLater>();
+        else if (T::kAhead > 2 && end && w.k1 - 2 - kt >= 2)
+          step_barrier<(T::kAhead > 2 ? 4 * T::kTimes : 0)>();
+        else if (T::kAhead > 2 && end && w.k1 - 2 - kt == 1)
+          step_barrier<(T::kAhead > 2 ? 2 * T::kTimes : 0)>();
         else
           step_barrier<0>();
-        slot = slot < 3 ? slot + 2 : slot - 3;
+        slot = slot + 2 < T::kSlots ? slot + 2 : slot + 2 - T::kSlots;
         ++kt;
       }
     }
     const bool whole = w.m0 + T::kRows <= a.M && w.n0 + (OP == kFeedIn ? T::kRows / 2 : T::kRows) <= (OP == kFeedIn || OP == kFeedDh ? a.F : a.N);
     if (whole)
-      feed_results<DT, BIG, OP, true>(a, w, acc, wm, wn, lane);
+      feed_results<DT, TILE, OP, true>(a, w, acc, wm, wn, lane);
     else
-      feed_results<DT, BIG, OP, false>(a, w, acc, wm, wn, lane);
+      feed_results<DT, TILE, OP, false>(a, w, acc, wm, wn, lane);
   }
 }
 
-template <typename DT, int BIG, int OP>
+template <typename DT, int TILE, int OP>
 hipError_t launch_feed_op(const FeedArgs& a, hipStream_t st) {
-  using T = FeedTile<BIG>;
+  using T = FeedTile<TILE>;
   constexpr int kCols = OP == kFeedIn ? T::kRows / 2 : T::kRows;
   const int tiles_m = (a.M + T::kRows - 1) / T::kRows, tiles_n = (a.N + kCols - 1) / kCols;
   const int64_t items = (int64_t)tiles_m * tiles_n * a.splits;
-  constexpr int kResident = BIG ? 256 : 512;  // workgroups that a device of 256 compute units holds
-  auto kernel = feed_kernel<DT, BIG, OP>;
+  auto kernel = feed_kernel<DT, TILE, OP>;
   if (T::kLds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
     if (e != hipSuccess) return e;
   }
-  launch_kernel(kernel, dim3((unsigned)(items < kResident ? items : kResident)), dim3(T::kThreads), T::kLds, st, a, tiles_m,
+  launch_kernel(kernel, dim3((unsigned)(items < T::kResident ? items : T::kResident)), dim3(T::kThreads), T::kLds, st, a, tiles_m,
                 tiles_n);
   if (a.splits > 1) return launch_feed_join(a, sizeof(DT) == 2, st);
   return hipGetLastError();
 }
 
-template <typename DT, int BIG>
+template <typename DT, int TILE>
 hipError_t launch_feed_tile(int op, const FeedArgs& a, hipStream_t st) {
   switch (op) {
-    case kFeedIn: return launch_feed_op<DT, BIG, kFeedIn>(a, st);
-    case kFeedOut: return launch_feed_op<DT, BIG, kFeedOut>(a, st);
-    case kFeedDh: return launch_feed_op<DT, BIG, kFeedDh>(a, st);
-    case kFeedDx: return launch_feed_op<DT, BIG, kFeedDx>(a, st);
-    case kFeedDwIn: return launch_feed_op<DT, BIG, kFeedDwIn>(a, st);
-    default: return launch_feed_op<DT, BIG, kFeedDwOut>(a, st);
+    case kFeedIn: return launch_feed_op<DT, TILE, kFeedIn>(a, st);
+    case kFeedOut: return launch_feed_op<DT, TILE, kFeedOut>(a, st);
+    case kFeedDh: return launch_feed_op<DT, TILE, kFeedDh>(a, st);
+    case kFeedDx: return launch_feed_op<DT, TILE, kFeedDx>(a, st);
+    case kFeedDwIn: return launch_feed_op<DT, TILE, kFeedDwIn>(a, st);
+    default: return launch_feed_op<DT, TILE, kFeedDwOut>(a, st);
   }
 }
 
 template <typename DT>
 hipError_t launch_feed_type(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t st) {
-  return p.big ? launch_feed_tile<DT, 1>(op, a, st) : launch_feed_tile<DT, 0>(op, a, st);
+  return p.tile == kTileBig    ? launch_feed_tile<DT, kTileBig>(op, a, st)
+         : p.tile == kTileDeep ? launch_feed_tile<DT, kTileDeep>(op, a, st)
+                               : launch_feed_tile<DT, kTileSmall>(op, a, st);
 }
 
 }  // namespace

@@ -95,8 +95,9 @@ struct FeedArgs {
   float* part; int splits;          // splits > 1: partial products [splits, M, N]
 };
 // Tile and split of one product.
+enum FeedTileKind { kTileSmall, kTileBig, kTileDeep };  // 128 x 128, 256 x 256, 128 x 128 with more loads in flight
 struct FeedPlan {
-  int big;                          // 256 x 256 tiles, else 128 x 128
+  int tile;
   int splits;
 };
 FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus);
