@@ -237,7 +237,7 @@ FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, i
     const bool big = tile == kTileBig;
     const double tiles = feed_tiles(p, M, N, op), resident = tile == kTileSmall ? 2.0 * cus : cus;
     // us of a step, with all workgroups that the device holds at work, and of a tile's results
-    const double step = bf16_storage ? (big ? 2.2 : tile == kTileDeep ? 0.8 : 1.4) : (big ? 7.6 : tile == kTileDeep ? 2.2 : 3.9);
+    const double step = bf16_storage ? (big ? 2.0 : tile == kTileDeep ? 0.8 : 1.3) : (big ? 7.6 : tile == kTileDeep ? 2.6 : 3.9);
     const double results = big ? (op == kFeedDh ? 90.0 : 12.0) : 6.0;
     for (int want = 1; want <= (op == kFeedIn || op == kFeedDh ? 1 : 32) && want <= steps; ++want) {
       const int each = (steps + want - 1) / want;
