@@ -147,8 +147,8 @@ def test_steps_from_nothing_to_huge(soft):
     steps keep their own relative accuracy."""
     T, B, H, N = 24, 1, 16, 4
     c = _case(T, B, H, N, 1, torch.float32, 21)
-    raw = torch.linspace(-80, 80, T)[:, None, None].expand(T, B, H).contiguous() if soft else \
-        torch.cat([torch.zeros(8), torch.full((8,), 1e4), torch.full((8,), 1e-6)])[:, None, None].expand(T, B, H).contiguous()
+    raw = torch.linspace(-80, 80, T, dtype=torch.float32)[:, None, None].expand(T, B, H).contiguous() if soft else \
+        torch.tensor([0.0] * 8 + [1e4] * 8 + [1e-6] * 8, dtype=torch.float32)[:, None, None].expand(T, B, H).contiguous()
     c["dt"], c["dt_bias"], c["z"], c["D"] = raw, None, None, None
     # large steps make large inputs: compare where the state is of order one
     c["x"] = c["x"] / (1 + raw.clamp(min=0))
@@ -223,8 +223,8 @@ def test_refusals():
         gss.selective_scan(*args, h0=c["h0"][:1])
     with pytest.raises(ValueError, match="lengths"):
         gss.selective_scan(*args, lengths=[6, 1])
-    big = torch.zeros(5, 2, 2, 65, device="cuda")
+    big = torch.zeros(5, 2, 2, 65, device="cuda", dtype=torch.float32)
     with pytest.raises(gss.RnnError):
-        gss.selective_scan(c["x"], c["dt"], torch.zeros(8, 65, device="cuda"), big, big)
+        gss.selective_scan(c["x"], c["dt"], torch.zeros(8, 65, device="cuda", dtype=torch.float32), big, big)
     with pytest.raises(gss.RnnError):      # 8 channels in 3 groups
-        gss.selective_scan(c["x"], c["dt"], c["A"], *(torch.zeros(5, 2, 3, 4, device="cuda"),) * 2)
+        gss.selective_scan(c["x"], c["dt"], c["A"], *(torch.zeros(5, 2, 3, 4, device="cuda", dtype=torch.float32),) * 2)

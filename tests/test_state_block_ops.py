@@ -156,7 +156,7 @@ def test_conv_pointers():
 
 
 def test_conv_python_refusals():
-    x, w = torch.zeros(4, 2, 8), torch.zeros(8, 4)
+    x, w = torch.zeros(4, 2, 8, dtype=torch.float32), torch.zeros(8, 4, dtype=torch.float32)
     with pytest.raises(ValueError, match="GPU tensor"):
         gss.causal_conv(x, w)
     with pytest.raises(ValueError, match="activation"):
@@ -314,7 +314,7 @@ def test_selective_pointers():
 
 
 def test_selective_python_refusals():
-    x, A, B = torch.zeros(4, 2, 8), torch.zeros(8, 4), torch.zeros(4, 2, 1, 4)
+    x, A, B = torch.zeros(4, 2, 8, dtype=torch.float32), torch.zeros(8, 4, dtype=torch.float32), torch.zeros(4, 2, 1, 4, dtype=torch.float32)
     with pytest.raises(ValueError, match="GPU tensor"):
         gss.selective_scan(x, x, A, B, B)
     with pytest.raises(ValueError, match="dimensions"):
@@ -439,7 +439,7 @@ def test_feed_pointers():
 
 
 def test_feed_python_refusals():
-    x, w_in, w_out = torch.zeros(4, 8), torch.zeros(32, 8), torch.zeros(8, 16)
+    x, w_in, w_out = torch.zeros(4, 8, dtype=torch.float32), torch.zeros(32, 8, dtype=torch.float32), torch.zeros(8, 16, dtype=torch.float32)
     with pytest.raises(ValueError, match="GPU tensor"):
         gss.feed_forward(x, w_in, w_out)
     with pytest.raises(ValueError, match="activation"):
