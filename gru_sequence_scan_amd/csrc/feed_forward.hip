@@ -163,9 +163,11 @@ hipError_t few_rows(const FeedFewArgs& a, hipStream_t st) {
 // Copies and sums around the products
 // ---------------------------------------------------------------------------
 template <typename DT>
-__global__ __launch_bounds__(256) void feed_pack_kernel(const DT* from, int64_t ld, int64_t rows, int cols, DT* to, int pitch) {
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    for (int c = threadIdx.x; c < pitch; c += 256) to[row * pitch + c] = c < cols ? from[row * ld + c] : (DT)0.f;
+__global__ __launch_bounds__(256) void feed_pack_kernel(FeedPackArgs a) {
+  const auto t = a.t[blockIdx.y];
+  for (int64_t row = blockIdx.x; row < t.rows; row += gridDim.x)
+    for (int c = threadIdx.x; c < t.pitch; c += 256)
+      ((DT*)t.to)[row * t.pitch + c] = c < t.cols ? ((const DT*)t.from)[row * t.ld + c] : (DT)0.f;
 }
 
 // out = residual + the partial products, in their order: four columns a
@@ -244,7 +246,7 @@ FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, i
       p.splits = (steps + each - 1) / each;
       if (p.splits != want) continue;
       double us = std::ceil(tiles * want / resident) * (each * step + results);
-      if (want > 1) us += 4.0 + (double)want * M * N * 8.0 / 4e6;
+      if (want > 1) us += 8.0 + (double)want * M * N * 8.0 / 4e6;
       if (least == 0.0 || us < least) {
         least = us;
         best = p;
@@ -271,12 +273,14 @@ int feed_few_splits(int64_t rows, int F, int n_out, int cus) {
 
 hipError_t launch_feed_few(const FeedFewArgs& a, bool bf, hipStream_t st) { return bf ? few_rows<bf16>(a, st) : few_rows<float>(a, st); }
 
-hipError_t launch_feed_pack(const void* from, int64_t ld, int64_t rows, int cols, void* to, int pitch, bool bf, hipStream_t st) {
-  const dim3 grid((unsigned)(rows < 8192 ? rows : 8192));
+hipError_t launch_feed_pack(const FeedPackArgs& a, bool bf, hipStream_t st) {
+  int64_t rows = 1;
+  for (int i = 0; i < a.count; ++i) rows = rows > a.t[i].rows ? rows : a.t[i].rows;
+  const dim3 grid((unsigned)(rows < 8192 ? rows : 8192), (unsigned)a.count);
   if (bf)
-    launch_kernel(feed_pack_kernel<bf16>, grid, dim3(256), 0, st, (const bf16*)from, ld, rows, cols, (bf16*)to, pitch);
+    launch_kernel(feed_pack_kernel<bf16>, grid, dim3(256), 0, st, a);
   else
-    launch_kernel(feed_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)from, ld, rows, cols, (float*)to, pitch);
+    launch_kernel(feed_pack_kernel<float>, grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

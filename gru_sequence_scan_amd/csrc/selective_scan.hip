@@ -268,17 +268,29 @@ hipError_t launch_sel_carry(const SelectiveScanArgs& a, const float* first, int 
   return hipGetLastError();
 }
 
-// Segments so that about two workgroups a compute unit are at work, each over
-// 64 steps at least.
-int sel_segments(int T, int B, int H, int G, int cus, int* seg_steps) {
-  const int64_t tiles = (int64_t)B * sel_group_tiles(H, G) * G;
+// The time is cut where that is expected to be faster: into segments of whole
+// 64 steps, up to two workgroups a compute unit. A step of the walk takes 130
+// ns (N = 16) with one workgroup a compute unit, whose waves then wait for
+// their own results, and 185 with two; in the launch that composes a segment
+// 85 and 130; the two launches more cost about 14 us.
+int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps) {
+  const double tiles = (double)B * sel_group_tiles(H, G) * G, states = sel_padded(N) / 16.0, scale = states < 0.7 ? 0.7 : states;
   const int chunks = (T + 63) / 64;
-  int64_t want = 1;
-  if (2 * tiles <= cus) want = 2 * (int64_t)cus / tiles;
-  if (want > chunks / 2) want = chunks / 2;
-  if (want < 1) want = 1;
-  *seg_steps = (int)((chunks + want - 1) / want) * 64;
-  return (T + *seg_steps - 1) / *seg_steps;
+  int best = 1;
+  double least = T * 0.13 * scale;
+  for (int want = 2; want <= chunks && want * tiles <= 2.0 * cus; ++want) {
+    const int each = (chunks + want - 1) / want;
+    if ((chunks + each - 1) / each != want) continue;
+    const double load = want * tiles / cus;
+    const double step = load <= 1.0 ? 0.215 : 0.215 + 0.1 * (load - 1.0);
+    const double us = each * 64 * step * scale + 14.0;
+    if (us < least) {
+      least = us;
+      best = want;
+    }
+  }
+  *seg_steps = best == 1 ? chunks * 64 : (chunks + best - 1) / best * 64;
+  return best;
 }
 
 hipError_t launch_selective_scan(SelectiveScanArgs a, bool bf, hipStream_t st) {

@@ -76,7 +76,7 @@ int validate(const RnnSelectiveScanDesc* d) {
 }
 
 int sel_segments_of(const RnnSelectiveScanDesc* d, int* steps) {
-  return sel_segments(d->T, d->B, d->H, d->G, kPlanCus, steps);
+  return sel_segments(d->T, d->B, d->H, d->N, d->G, kPlanCus, steps);
 }
 
 size_t sel_cells(const RnnSelectiveScanDesc* d) { return (size_t)d->B * d->H; }
@@ -266,18 +266,22 @@ size_t feed_reserve(const RnnFeedForwardDesc* d) {
   return feed_gu_bytes(d) + round16((size_t)d->rows * FeedSizes(d).Fp * esize_of(d->dtype));
 }
 
-// One pass over the rows of the operands that the kernels cannot take as they are.
+// Operands as the kernels take them; those that they cannot take as they are
+// go through one pass over all their rows.
 struct FeedOperand {
   const void* p;
   int64_t ld;
 };
-hipError_t feed_packed(FeedOperand* o, bool pack, int64_t rows, int cols, int pitch, void* to, bool bf, hipStream_t st) {
-  if (!pack) return hipSuccess;
-  const hipError_t e = launch_feed_pack(o->p, o->ld, rows, cols, to, pitch, bf, st);
-  o->p = to;
-  o->ld = pitch;
-  return e;
-}
+struct FeedPacks {
+  FeedPackArgs a{};
+  FeedOperand add(const void* p, int64_t ld, bool pack, int64_t rows, int cols, int pitch, void* to) {
+    if (!pack) return {p, ld};
+    auto& t = a.t[a.count++];
+    t.from = p; t.ld = ld; t.rows = rows; t.cols = cols; t.to = to; t.pitch = pitch;
+    return {to, pitch};
+  }
+  hipError_t launch(bool bf, hipStream_t st) const { return a.count ? launch_feed_pack(a, bf, st) : hipSuccess; }
+};
 
 int feed_io(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io) {
   const size_t e = d->aligned ? 16 : (size_t)esize_of(d->dtype);
@@ -317,10 +321,11 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
     f.vec = !s.pack_x && !s.pack_in && !s.pack_out;
     return hip_status(launch_feed_few(f, bf, st));
   }
-  FeedOperand x{io->x, d->x_ld}, in{io->w_in, d->in_ld}, out{io->w_out, d->out_ld};
-  RETURN_IF_HIP(feed_packed(&x, s.pack_x, d->rows, d->N, s.Np, mem + at.x, bf, st));
-  RETURN_IF_HIP(feed_packed(&in, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in, bf, st));
-  RETURN_IF_HIP(feed_packed(&out, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out, bf, st));
+  FeedPacks packs;
+  const FeedOperand x = packs.add(io->x, d->x_ld, s.pack_x, d->rows, d->N, s.Np, mem + at.x);
+  const FeedOperand in = packs.add(io->w_in, d->in_ld, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
+  const FeedOperand out = packs.add(io->w_out, d->out_ld, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out);
+  RETURN_IF_HIP(packs.launch(bf, st));
   void* h = reserve ? static_cast<char*>(reserve) + feed_gu_bytes(d) : mem + at.h;
   auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
   FeedArgs a{};
@@ -349,11 +354,12 @@ int feed_backward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, const
   const FeedSizes s(d);
   const bool bf = d->dtype == RNN_DTYPE_BF16;
   const int rows = (int)d->rows;
-  FeedOperand x{io->x, d->x_ld}, in{io->w_in, d->in_ld}, out{io->w_out, d->out_ld}, dy{g->dy, d->N_out};
-  RETURN_IF_HIP(feed_packed(&x, s.pack_x, d->rows, d->N, s.Np, mem + at.x, bf, st));
-  RETURN_IF_HIP(feed_packed(&in, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in, bf, st));
-  RETURN_IF_HIP(feed_packed(&out, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out, bf, st));
-  RETURN_IF_HIP(feed_packed(&dy, s.pack_dy, d->rows, d->N_out, s.Op, mem + at.dy, bf, st));
+  FeedPacks packs;
+  const FeedOperand x = packs.add(io->x, d->x_ld, s.pack_x, d->rows, d->N, s.Np, mem + at.x);
+  const FeedOperand in = packs.add(io->w_in, d->in_ld, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
+  const FeedOperand out = packs.add(io->w_out, d->out_ld, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out);
+  const FeedOperand dy = packs.add(g->dy, d->N_out, s.pack_dy, d->rows, d->N_out, s.Op, mem + at.dy);
+  RETURN_IF_HIP(packs.launch(bf, st));
   auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
   void* dp = mem + at.dp;
   const void* h = static_cast<const char*>(reserve) + feed_gu_bytes(d);

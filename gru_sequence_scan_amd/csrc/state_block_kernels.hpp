@@ -70,7 +70,7 @@ struct SelectiveScanArgs {
 // The state's length as the kernels hold it: 4, 8, 16, 32 or 64.
 inline int sel_padded(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 inline int sel_group_tiles(int H, int G) { return (H / G + kSelTile - 1) / kSelTile; }
-int sel_segments(int T, int B, int H, int G, int cus, int* seg_steps);
+int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps);
 hipError_t launch_selective_scan(SelectiveScanArgs a, bool bf16_storage, hipStream_t stream);
 hipError_t launch_selective_scan_backward(SelectiveScanArgs a, bool bf16_storage, hipStream_t stream);
 
@@ -120,9 +120,17 @@ struct FeedFewArgs {
 };
 int feed_few_splits(int64_t rows, int F, int n_out, int cus);
 hipError_t launch_feed_few(const FeedFewArgs& a, bool bf16_storage, hipStream_t stream);
-// Rows of a tensor copied to a pitch of whole 16 bytes, zeros behind each.
-hipError_t launch_feed_pack(const void* from, int64_t ld, int64_t rows, int cols, void* to, int pitch, bool bf16_storage,
-                            hipStream_t stream);
+// Rows of up to four tensors copied to a pitch of whole 16 bytes, zeros behind
+// each, in one launch.
+struct FeedPackArgs {
+  struct {
+    const void* from; int64_t ld;
+    int64_t rows; int cols;
+    void* to; int pitch;
+  } t[4];
+  int count;
+};
+hipError_t launch_feed_pack(const FeedPackArgs& a, bool bf16_storage, hipStream_t stream);
 // out = residual + the sum of the partial products.
 hipError_t launch_feed_join(const FeedArgs& a, bool bf16_storage, hipStream_t stream);
 

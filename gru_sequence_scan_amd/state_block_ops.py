@@ -2,18 +2,22 @@
 short causal convolution, the selective scan and the gated feed-forward.
 
 As in block_ops.py, only argument marshalling happens here, and nothing
-synchronises, so the calls can be captured into a graph.
+synchronises, so the calls can be captured into a graph. The C structs are
+packed as bytes (a serving step's kernels take as long as filling the ctypes
+classes would; those are there for callers of the C functions), and the sizes
+of workspaces, which depend on the descriptor alone, are asked for once.
 """
 
 import ctypes
+import functools
+import struct
 
 import torch
 
 from . import block_ops
 from .binding import DTYPES
 from .block_ops import (
-    _I32, _I64, _P, _REF, _SZ, BlockContext, _buffer, _bytes, _call, _dense_like, _lengths, _plain, _ptr, _rows,
-    _strided, _tensor,
+    _I32, _I64, _P, _REF, _SZ, BlockContext, _buffer, _call, _dense_like, _lengths, _lib, _ok, _plain, _rows, _strided, _tensor,
 )
 
 ACTIVATIONS = {None: 0, "silu": 1, "gelu_tanh": 2, "sigmoid": 3}
@@ -61,26 +65,42 @@ class RnnFeedForwardGrads(ctypes.Structure):
     _fields_ = [("dy", _P), ("dx", _P), ("dw_in", _P), ("dw_out", _P)]
 
 
-_FEED = [_REF(RnnFeedForwardDesc), _REF(RnnFeedForwardIO)]
-_SCAN = [_REF(RnnSelectiveScanDesc), _REF(RnnSelectiveScanIO)]
+# descriptor, pointers and gradients are taken as bytes or by reference
+_SIZE = [_P, _REF(_SZ)]
 block_ops._SIGNATURES.update({
-    "rnn_selective_scan_workspace_bytes": [_REF(RnnSelectiveScanDesc), _REF(_SZ)],
-    "rnn_selective_scan_reserve_bytes": [_REF(RnnSelectiveScanDesc), _REF(_SZ)],
-    "rnn_selective_scan_backward_workspace_bytes": [_REF(RnnSelectiveScanDesc), _REF(_SZ)],
-    "rnn_feed_forward_workspace_bytes": [_REF(RnnFeedForwardDesc), _REF(_SZ)],
-    "rnn_feed_forward_train_workspace_bytes": [_REF(RnnFeedForwardDesc), _REF(_SZ)],
-    "rnn_feed_forward_backward_workspace_bytes": [_REF(RnnFeedForwardDesc), _REF(_SZ)],
-    "rnn_feed_forward_reserve_bytes": [_REF(RnnFeedForwardDesc), _REF(_SZ)],
-    "rnn_feed_forward": _FEED + [_P, _SZ, _P],
-    "rnn_feed_forward_train": _FEED + [_P, _SZ, _P, _SZ, _P],
-    "rnn_feed_forward_backward": _FEED + [_REF(RnnFeedForwardGrads), _P, _SZ, _P, _SZ, _P],
-    "rnn_selective_scan": _SCAN + [_P, _SZ, _P],
-    "rnn_selective_scan_train": _SCAN + [_P, _SZ, _P, _SZ, _P],
-    "rnn_selective_scan_backward": _SCAN + [_REF(RnnSelectiveScanGrads), _P, _SZ, _P, _SZ, _P],
-    "rnn_causal_conv": [_REF(RnnCausalConvDesc), _REF(RnnCausalConvIO), _P],
-    "rnn_causal_conv_backward_workspace_bytes": [_REF(RnnCausalConvDesc), _REF(_SZ)],
-    "rnn_causal_conv_backward": [_REF(RnnCausalConvDesc), _REF(RnnCausalConvIO), _REF(RnnCausalConvGrads), _P, _SZ, _P],
+    "rnn_causal_conv": [_P, _P, _P],
+    "rnn_causal_conv_backward_workspace_bytes": _SIZE,
+    "rnn_causal_conv_backward": [_P, _P, _P, _P, _SZ, _P],
+    "rnn_selective_scan_workspace_bytes": _SIZE,
+    "rnn_selective_scan_reserve_bytes": _SIZE,
+    "rnn_selective_scan_backward_workspace_bytes": _SIZE,
+    "rnn_selective_scan": [_P, _P, _P, _SZ, _P],
+    "rnn_selective_scan_train": [_P, _P, _P, _SZ, _P, _SZ, _P],
+    "rnn_selective_scan_backward": [_P, _P, _P, _P, _SZ, _P, _SZ, _P],
+    "rnn_feed_forward_workspace_bytes": _SIZE,
+    "rnn_feed_forward_train_workspace_bytes": _SIZE,
+    "rnn_feed_forward_backward_workspace_bytes": _SIZE,
+    "rnn_feed_forward_reserve_bytes": _SIZE,
+    "rnn_feed_forward": [_P, _P, _P, _SZ, _P],
+    "rnn_feed_forward_train": [_P, _P, _P, _SZ, _P, _SZ, _P],
+    "rnn_feed_forward_backward": [_P, _P, _P, _P, _SZ, _P, _SZ, _P],
 })
+
+# the structs above, in the order of their fields
+_CONV_DESC, _CONV_IO, _CONV_GRADS = struct.Struct("6i2q").pack, struct.Struct("7Q").pack, struct.Struct("6Q").pack
+_SCAN_DESC, _SCAN_IO, _SCAN_GRADS = struct.Struct("8i12q").pack, struct.Struct("12Q").pack, struct.Struct("11Q").pack
+_FEED_DESC, _FEED_IO, _FEED_GRADS = struct.Struct("2iq4i4q").pack, struct.Struct("5Q").pack, struct.Struct("4Q").pack
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(fn, desc):
+    n = _SZ(0)
+    _ok(getattr(_lib(), fn)(desc, ctypes.byref(n)), fn)
+    return n.value
 
 
 def _activation(name, allowed):
@@ -108,13 +128,13 @@ def _causal_conv(x, weight, bias, state, lengths, activation, train):
     y = _dense_like(x)
     state_n = x.new_empty((W - 1, B, C))
     xt, xb, _ = x.stride()
-    desc = RnnCausalConvDesc(DTYPES[dtype], T, B, C, W, act, xt, xb)
-    io = RnnCausalConvIO(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(lengths), _ptr(state), y.data_ptr(),
+    desc = _CONV_DESC(DTYPES[dtype], T, B, C, W, act, xt, xb)
+    io = _CONV_IO(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(lengths), _ptr(state), y.data_ptr(),
                          state_n.data_ptr())
-    stream = _call("rnn_causal_conv", device, ctypes.byref(desc), ctypes.byref(io))
+    stream = _call("rnn_causal_conv", device, desc, io)
     if not train:
         return y, state_n
-    return (y, state_n), BlockContext(device, stream, desc=desc, x=x, weight=weight, bias=bias, lengths=lengths, state=state)
+    return (y, state_n), BlockContext(device, stream, desc=desc, shape=(T, B, C, W), x=x, weight=weight, bias=bias, lengths=lengths, state=state)
 
 
 def causal_conv(x, weight, bias=None, *, state=None, lengths=None, activation=None):
@@ -144,18 +164,19 @@ def causal_conv_backward(ctx, dy, dstate_n=None):
     optionally dstate_n. Returns (dx, dweight, dbias, dstate): dweight and
     dbias fp32, dbias None without a bias, dstate in x's dtype."""
     d, device, dtype = ctx.desc, ctx.device, ctx.x.dtype
-    dy = _plain(dy, "dy", (d.T, d.B, d.C), dtype, device)
-    dstate_n = _plain(dstate_n, "dstate_n", (d.W - 1, d.B, d.C), dtype, device)
+    T, B, C, W = ctx.shape
+    dy = _plain(dy, "dy", (T, B, C), dtype, device)
+    dstate_n = _plain(dstate_n, "dstate_n", (W - 1, B, C), dtype, device)
     dx = _dense_like(dy)
-    dw = torch.empty((d.C, d.W), dtype=torch.float32, device=device)
-    db = None if ctx.bias is None else torch.empty((d.C,), dtype=torch.float32, device=device)
-    dstate = dy.new_empty((d.W - 1, d.B, d.C))
-    io = RnnCausalConvIO(ctx.x.data_ptr(), ctx.weight.data_ptr(), _ptr(ctx.bias), _ptr(ctx.lengths), _ptr(ctx.state), None, None)
-    grads = RnnCausalConvGrads(dy.data_ptr(), _ptr(dstate_n), dx.data_ptr(), dw.data_ptr(), _ptr(db), dstate.data_ptr())
+    dw = torch.empty((C, W), dtype=torch.float32, device=device)
+    db = None if ctx.bias is None else torch.empty((C,), dtype=torch.float32, device=device)
+    dstate = dy.new_empty((W - 1, B, C))
+    io = _CONV_IO(ctx.x.data_ptr(), ctx.weight.data_ptr(), _ptr(ctx.bias), _ptr(ctx.lengths), _ptr(ctx.state), 0, 0)
+    grads = _CONV_GRADS(dy.data_ptr(), _ptr(dstate_n), dx.data_ptr(), dw.data_ptr(), _ptr(db), dstate.data_ptr())
     size = _bytes("rnn_causal_conv_backward_workspace_bytes", d)
     ws = _buffer(size, device)
     ctx._use(ctx.x, ctx.weight, ctx.bias, ctx.lengths, ctx.state)
-    _call("rnn_causal_conv_backward", device, ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ws), size)
+    _call("rnn_causal_conv_backward", device, d, io, grads, _ptr(ws), size)
     return dx, dw, db, dstate
 
 
@@ -182,21 +203,21 @@ def _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, train)
     lengths = _lengths(lengths, rows, T, device)
     y = _dense_like(x)
     h_n = torch.empty((rows, H, N), dtype=torch.float32, device=device)
-    desc = RnnSelectiveScanDesc(DTYPES[dtype], T, rows, H, N, G, 1 if softplus else 0, 0 if z is None else 1, *x.stride()[:2],
+    desc = _SCAN_DESC(DTYPES[dtype], T, rows, H, N, G, 1 if softplus else 0, 0 if z is None else 1, *x.stride()[:2],
                                 *dt.stride()[:2], *((0, 0) if z is None else z.stride()[:2]), *B.stride()[:3],
                                 *C.stride()[:3])
-    io = RnnSelectiveScanIO(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D),
+    io = _SCAN_IO(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D),
                             _ptr(dt_bias), _ptr(lengths), _ptr(h0), y.data_ptr(), h_n.data_ptr())
     size = _bytes("rnn_selective_scan_workspace_bytes", desc)
     ws = _buffer(size, device)
     if not train:
-        _call("rnn_selective_scan", device, ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size)
+        _call("rnn_selective_scan", device, desc, io, _ptr(ws), size)
         return y, h_n
     rsize = _bytes("rnn_selective_scan_reserve_bytes", desc)
     reserve = _buffer(rsize, device)
-    stream = _call("rnn_selective_scan_train", device, ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws),
+    stream = _call("rnn_selective_scan_train", device, desc, io, _ptr(reserve), rsize, _ptr(ws),
                    size)
-    return (y, h_n), BlockContext(device, stream, desc=desc, x=x, dt=dt, z=z, B=B, C=C, A=A, D=D, dt_bias=dt_bias,
+    return (y, h_n), BlockContext(device, stream, desc=desc, shape=(T, rows, H, N), x=x, dt=dt, z=z, B=B, C=C, A=A, D=D, dt_bias=dt_bias,
                                   lengths=lengths, reserve=reserve)
 
 
@@ -232,24 +253,25 @@ def selective_scan_backward(ctx, dy, dh_n=None):
     "dt", "z", "B", "C" in x's dtype, "A", "D", "dt_bias", "h0" in fp32; None
     for z, D and dt_bias where they were not given."""
     d, device, dtype = ctx.desc, ctx.device, ctx.x.dtype
-    dy = _plain(dy, "dy", (d.T, d.B, d.H), dtype, device)
-    dh_n = _plain(dh_n, "dh_n", (d.B, d.H, d.N), torch.float32, device)
+    T, rows, H, N = ctx.shape
+    dy = _plain(dy, "dy", (T, rows, H), dtype, device)
+    dh_n = _plain(dh_n, "dh_n", (rows, H, N), torch.float32, device)
 
     def f32(*shape):
         return torch.empty(shape, dtype=torch.float32, device=device)
 
     g = {"x": _dense_like(dy), "dt": _dense_like(dy), "z": None if ctx.z is None else _dense_like(dy),
-         "B": dy.new_empty(ctx.B.shape), "C": dy.new_empty(ctx.B.shape), "A": f32(d.H, d.N),
-         "D": None if ctx.D is None else f32(d.H), "dt_bias": None if ctx.dt_bias is None else f32(d.H),
-         "h0": f32(d.B, d.H, d.N)}
-    io = RnnSelectiveScanIO(ctx.x.data_ptr(), ctx.dt.data_ptr(), _ptr(ctx.z), ctx.B.data_ptr(), ctx.C.data_ptr(),
-                            ctx.A.data_ptr(), _ptr(ctx.D), _ptr(ctx.dt_bias), _ptr(ctx.lengths), None, None, None)
-    grads = RnnSelectiveScanGrads(dy.data_ptr(), _ptr(dh_n), *(_ptr(g[k]) for k in ("x", "dt", "z", "B", "C", "A", "D",
+         "B": dy.new_empty(ctx.B.shape), "C": dy.new_empty(ctx.B.shape), "A": f32(H, N),
+         "D": None if ctx.D is None else f32(H), "dt_bias": None if ctx.dt_bias is None else f32(H),
+         "h0": f32(rows, H, N)}
+    io = _SCAN_IO(ctx.x.data_ptr(), ctx.dt.data_ptr(), _ptr(ctx.z), ctx.B.data_ptr(), ctx.C.data_ptr(),
+                            ctx.A.data_ptr(), _ptr(ctx.D), _ptr(ctx.dt_bias), _ptr(ctx.lengths), 0, 0, 0)
+    grads = _SCAN_GRADS(dy.data_ptr(), _ptr(dh_n), *(_ptr(g[k]) for k in ("x", "dt", "z", "B", "C", "A", "D",
                                                                                     "dt_bias", "h0")))
     size = _bytes("rnn_selective_scan_backward_workspace_bytes", d)
     ws = _buffer(size, device)
     ctx._use(ctx.x, ctx.dt, ctx.z, ctx.B, ctx.C, ctx.A, ctx.D, ctx.dt_bias, ctx.lengths, ctx.reserve)
-    _call("rnn_selective_scan_backward", device, ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ctx.reserve),
+    _call("rnn_selective_scan_backward", device, d, io, grads, _ptr(ctx.reserve),
           ctx.reserve.numel(), _ptr(ws), size)
     return g
 
@@ -287,19 +309,20 @@ def _feed_forward(x, w_in, w_out, residual, activation, train):
         residual, r_ld = _rows(_strided(residual, "residual", shape, x))
     y = x.new_empty(shape)
     aligned = (x.data_ptr() | w_in.data_ptr() | w_out.data_ptr()) % 16 == 0
-    desc = RnnFeedForwardDesc(DTYPES[dtype], act, rows, n, F, n_out, 1 if aligned else 0, x_ld, in_ld, out_ld, r_ld)
-    io = RnnFeedForwardIO(x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), _ptr(residual), y.data_ptr())
+    fields = (DTYPES[dtype], act, rows, n, F, n_out, 1 if aligned else 0, x_ld, in_ld, out_ld, r_ld)
+    desc = _FEED_DESC(*fields)
+    io = _FEED_IO(x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), _ptr(residual), y.data_ptr())
     if not train:
         size = _bytes("rnn_feed_forward_workspace_bytes", desc)
         ws = _buffer(size, device)
-        _call("rnn_feed_forward", device, ctypes.byref(desc), ctypes.byref(io), _ptr(ws), size)
+        _call("rnn_feed_forward", device, desc, io, _ptr(ws), size)
         return y
     size = _bytes("rnn_feed_forward_train_workspace_bytes", desc)
     ws = _buffer(size, device)
     rsize = _bytes("rnn_feed_forward_reserve_bytes", desc)
     reserve = _buffer(rsize, device)
-    stream = _call("rnn_feed_forward_train", device, ctypes.byref(desc), ctypes.byref(io), _ptr(reserve), rsize, _ptr(ws), size)
-    return y, BlockContext(device, stream, desc=desc, x=x, w_in=w_in, w_out=w_out, reserve=reserve, shape=shape)
+    stream = _call("rnn_feed_forward_train", device, desc, io, _ptr(reserve), rsize, _ptr(ws), size)
+    return y, BlockContext(device, stream, fields=fields, x=x, w_in=w_in, w_out=w_out, reserve=reserve, shape=shape)
 
 
 def feed_forward(x, w_in, w_out, *, residual=None, activation="silu"):
@@ -330,17 +353,17 @@ def feed_forward_backward(ctx, dy):
     Returns (dx, dw_in, dw_out) in x's dtype; the residual's gradient is dy."""
     x, device = ctx.x, ctx.device
     dy = _plain(dy, "dy", ctx.shape, x.dtype, device)
-    d = ctx.desc
-    if d.aligned and dy.data_ptr() % 16:
-        d = RnnFeedForwardDesc.from_buffer_copy(d)
-        d.aligned = 0
-    dx = dy.new_empty(ctx.shape[:-1] + (d.N,))
-    dw_in, dw_out = dy.new_empty((2 * d.F, d.N)), dy.new_empty((d.N_out, d.F))
-    io = RnnFeedForwardIO(x.data_ptr(), ctx.w_in.data_ptr(), ctx.w_out.data_ptr(), None, None)
-    grads = RnnFeedForwardGrads(dy.data_ptr(), dx.data_ptr(), dw_in.data_ptr(), dw_out.data_ptr())
+    _, _, _, n, F, n_out, aligned = ctx.fields[:7]
+    if dy.data_ptr() % 16:
+        aligned = 0
+    d = _FEED_DESC(*ctx.fields[:6], aligned, *ctx.fields[7:])
+    dx = dy.new_empty(ctx.shape[:-1] + (n,))
+    dw_in, dw_out = dy.new_empty((2 * F, n)), dy.new_empty((n_out, F))
+    io = _FEED_IO(x.data_ptr(), ctx.w_in.data_ptr(), ctx.w_out.data_ptr(), 0, 0)
+    grads = _FEED_GRADS(dy.data_ptr(), dx.data_ptr(), dw_in.data_ptr(), dw_out.data_ptr())
     size = _bytes("rnn_feed_forward_backward_workspace_bytes", d)
     ws = _buffer(size, device)
     ctx._use(x, ctx.w_in, ctx.w_out, ctx.reserve)
-    _call("rnn_feed_forward_backward", device, ctypes.byref(d), ctypes.byref(io), ctypes.byref(grads), _ptr(ctx.reserve),
+    _call("rnn_feed_forward_backward", device, d, io, grads, _ptr(ctx.reserve),
           ctx.reserve.numel(), _ptr(ws), size)
     return dx, dw_in, dw_out

@@ -50,6 +50,19 @@ def _layouts(tmp_path, names):
 
 
 
+@pytest.mark.parametrize("pack,name", [
+    ("_CONV_DESC", "RnnCausalConvDesc"), ("_CONV_IO", "RnnCausalConvIO"), ("_CONV_GRADS", "RnnCausalConvGrads"),
+    ("_SCAN_DESC", "RnnSelectiveScanDesc"), ("_SCAN_IO", "RnnSelectiveScanIO"), ("_SCAN_GRADS", "RnnSelectiveScanGrads"),
+    ("_FEED_DESC", "RnnFeedForwardDesc"), ("_FEED_IO", "RnnFeedForwardIO"), ("_FEED_GRADS", "RnnFeedForwardGrads"),
+])
+def test_packed_structs_are_the_ctypes_ones(pack, name):
+    t = getattr(gss, name)
+    data = getattr(gss.state_block_ops, pack)(*range(1, len(t._fields_) + 1))
+    assert len(data) == ctypes.sizeof(t)
+    s = t.from_buffer_copy(data)
+    assert [getattr(s, f[0]) for f in t._fields_] == list(range(1, len(t._fields_) + 1))
+
+
 # ---------------------------------------------------------------------------
 # Causal convolution
 # ---------------------------------------------------------------------------
