@@ -151,7 +151,7 @@ hipError_t few(const FeedFewArgs& a, hipStream_t st) {
   FeedArgs j{};
   j.M = a.rows; j.N = a.n_out; j.splits = a.splits; j.part = a.part;
   j.out = a.y; j.ldo = a.n_out; j.residual = a.residual; j.ldr = a.ldr;
-  return launch_feed_join(j, sizeof(DT) == 2, st);
+  return launch_feed_join(kFeedOut, j, sizeof(DT) == 2, st);
 }
 
 template <typename DT>
@@ -204,8 +204,57 @@ __global__ __launch_bounds__(256) void feed_join_kernel(FeedArgs a) {
   }
 }
 
+// The same for the products whose results go through the activation: four
+// hidden units a thread.
+template <typename DT, bool BACK>
+__global__ __launch_bounds__(256) void feed_join_act_kernel(FeedArgs a) {
+  const int per = a.Fp / 4;
+  const int64_t count = (int64_t)a.M * per, plane = (int64_t)a.M * a.Fp * (BACK ? 1 : 2);
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / per;
+    const int f = (int)(i % per) * 4;
+    const float* p = a.part + m * a.Fp * (BACK ? 1 : 2) + f;
+    f32x4 g = {0.f, 0.f, 0.f, 0.f}, u = g, dh = g;
+    for (int s = 0; s < a.splits; ++s, p += plane) {
+      if (BACK) {
+        dh += *reinterpret_cast<const f32x4*>(p);
+      } else {
+        g += *reinterpret_cast<const f32x4*>(p);
+        u += *reinterpret_cast<const f32x4*>(p + a.Fp);
+      }
+    }
+    float* gu = a.gu ? a.gu + m * 2 * a.Fp + f : nullptr;
+    if (BACK) {
+      g = *reinterpret_cast<const f32x4*>(gu);
+      u = *reinterpret_cast<const f32x4*>(gu + a.Fp);
+    }
+    DT* out = (DT*)a.out + m * a.ldo + f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool on = f + e < a.F;
+      if (!on) g[e] = u[e] = dh[e] = 0.f;
+      const Activated r = activate(g[e], a.act);
+      out[e] = from_f32<DT>(BACK ? dh[e] * u[e] * r.slope : r.act * u[e]);
+      if (BACK) out[a.Fp + e] = from_f32<DT>(dh[e] * r.act);
+    }
+    if (!BACK && gu) {
+      *reinterpret_cast<f32x4*>(gu) = g;
+      *reinterpret_cast<f32x4*>(gu + a.Fp) = u;
+    }
+  }
+}
+
 template <typename DT>
-hipError_t join(const FeedArgs& a, hipStream_t st) {
+hipError_t join(int op, const FeedArgs& a, hipStream_t st) {
+  if (op == kFeedIn || op == kFeedDh) {
+    const int64_t n = ((int64_t)a.M * (a.Fp / 4) + 255) / 256;
+    const dim3 blocks((unsigned)(n < 4096 ? n : 4096));
+    if (op == kFeedDh)
+      launch_kernel(feed_join_act_kernel<DT, true>, blocks, dim3(256), 0, st, a);
+    else
+      launch_kernel(feed_join_act_kernel<DT, false>, blocks, dim3(256), 0, st, a);
+    return hipGetLastError();
+  }
   const bool four = a.N % 4 == 0;
   const int64_t blocks = ((int64_t)a.M * a.N / (four ? 4 : 1) + 255) / 256;
   const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
@@ -225,8 +274,7 @@ double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
 
 // The tile and the split with the shortest expected time: rounds of the
 // workgroups that the device holds, times steps, plus the results' way out and
-// the partial products' way through memory. Products whose results are used on
-// the way out of the accumulators are not split. dh reads and writes 16 bytes
+// the partial products' way through memory. dh reads and writes 16 bytes
 // a result there (fp32; 12 in bf16), which two workgroups a compute unit hide
 // better than one: 32000 x 2816 bf16 422 us in small tiles and 450 in large
 // ones, 19334 x 1368 fp32 356 and 501; without that traffic large ones win
@@ -241,12 +289,12 @@ FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, i
     // us of a step, with all workgroups that the device holds at work, and of a tile's results
     const double step = bf16_storage ? (big ? 2.0 : tile == kTileDeep ? 0.8 : 1.3) : (big ? 7.6 : tile == kTileDeep ? 2.6 : 3.9);
     const double results = big ? (op == kFeedDh ? 90.0 : 12.0) : 6.0;
-    for (int want = 1; want <= (op == kFeedIn || op == kFeedDh ? 1 : 32) && want <= steps; ++want) {
+    for (int want = 1; want <= 32 && want <= steps; ++want) {
       const int each = (steps + want - 1) / want;
       p.splits = (steps + each - 1) / each;
       if (p.splits != want) continue;
       double us = std::ceil(tiles * want / resident) * (each * step + results);
-      if (want > 1) us += 8.0 + (double)want * M * N * 8.0 / 4e6;
+      if (want > 1) us += 8.0 + (double)want * M * N * (op == kFeedIn ? 16.0 : 8.0) / 4e6;
       if (least == 0.0 || us < least) {
         least = us;
         best = p;
@@ -284,6 +332,8 @@ hipError_t launch_feed_pack(const FeedPackArgs& a, bool bf, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_feed_join(const FeedArgs& a, bool bf, hipStream_t st) { return bf ? join<bf16>(a, st) : join<float>(a, st); }
+hipError_t launch_feed_join(int op, const FeedArgs& a, bool bf, hipStream_t st) {
+  return bf ? join<bf16>(op, a, st) : join<float>(op, a, st);
+}
 
 }  // namespace rnnk

@@ -301,18 +301,19 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
           more[k & 1][v] = q[0];
           more_u[k & 1][v] = q[a.Fp];
         }
-      } else if (add) {
+      } else if constexpr (OP == kFeedOut) {
         const DT* p = (const DT*)a.residual + m * a.ldr + n;
 #pragma unroll
         for (int v = 0; v < 8; ++v) more[k & 1][v] = to_f32<DT>(p[(8 * (v >> 2) + (v & 3)) * a.ldr]);
       }
     };
-    if (OP == kFeedDh || OP == kFeedOut) ask(0);
+    const bool asks = OP == kFeedDh ? a.splits == 1 : add;
+    if (asks) ask(0);
 #pragma unroll
     for (int k = 0; k < 2 * kBlocks; ++k) {
       const int i = k / (2 * kAcross), j = k / 2 % kAcross, v0 = k % 2 * 8;
       const int64_t m = m_base + i * 32 + k % 2 * 16, n = n_base + j * 32;
-      if ((OP == kFeedDh || OP == kFeedOut) && k + 1 < 2 * kBlocks) ask(k + 1);
+      if (asks && k + 1 < 2 * kBlocks) ask(k + 1);
       float val[8];
 #pragma unroll
       for (int v = 0; v < 8; ++v) val[v] = acc[i][j][v0 + v];
@@ -320,6 +321,12 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
         float u[8];
 #pragma unroll
         for (int v = 0; v < 8; ++v) u[v] = acc[i][1][v0 + v];
+        if (a.splits > 1) {
+          float* p = a.part + ((int64_t)w.split * a.M + m) * 2 * a.Fp + n;
+          store_half<float, false>(p, 2 * (int64_t)a.Fp, val, lane);
+          store_half<float, false>(p + a.Fp, 2 * (int64_t)a.Fp, u, lane);
+          continue;
+        }
         if (a.gu) {
           float* p = a.gu + m * 2 * a.Fp + n;
           store_half<float, false>(p, 2 * (int64_t)a.Fp, val, lane);
@@ -328,6 +335,8 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
 #pragma unroll
         for (int v = 0; v < 8; ++v) u[v] *= activate(val[v], a.act).act;
         store_half<DT>((DT*)a.out + m * a.ldo + n, a.ldo, u, lane, pairs);
+      } else if (a.splits > 1) {
+        store_half<float, false>(a.part + ((int64_t)w.split * a.M + m) * a.N + n, a.N, val, lane);
       } else if constexpr (OP == kFeedDh) {
         float du[8];
 #pragma unroll
@@ -339,8 +348,6 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
         DT* out = (DT*)a.out + m * a.ldo + n;
         store_half<DT>(out, a.ldo, val, lane, pairs);
         store_half<DT>(out + a.Fp, a.ldo, du, lane, pairs);
-      } else if (a.splits > 1) {
-        store_half<float, false>(a.part + ((int64_t)w.split * a.M + m) * a.N + n, a.N, val, lane);
       } else {
         // a block's rows lie on one side of the gate's last (padded) one
         const bool second = OP == kFeedDwIn && m >= a.Fp;
@@ -370,7 +377,15 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
         const int64_t m = m_base + i * 32 + 8 * (v >> 2) + (v & 3);
         if (m >= a.M) continue;
         const float val = acc[i][j][v];
-        if constexpr (OP == kFeedIn) {
+        if (a.splits > 1) {
+          if constexpr (OP == kFeedIn) {
+            float* p = a.part + ((int64_t)w.split * a.M + m) * 2 * a.Fp + n;
+            p[0] = val;
+            p[a.Fp] = acc[i][1][v];
+          } else {
+            a.part[((int64_t)w.split * a.M + m) * a.N + n] = val;
+          }
+        } else if constexpr (OP == kFeedIn) {
           const bool on = n < a.F;
           const float g = on ? val : 0.f, u = on ? acc[i][1][v] : 0.f;
           ((DT*)a.out)[m * a.ldo + n] = from_f32<DT>(activate(g, a.act).act * u);
@@ -385,8 +400,6 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
           DT* out = (DT*)a.out + m * a.ldo + n;
           out[0] = from_f32<DT>(on ? val * gu[a.Fp] * r.slope : 0.f);
           out[a.Fp] = from_f32<DT>(on ? val * r.act : 0.f);
-        } else if (a.splits > 1) {
-          a.part[((int64_t)w.split * a.M + m) * a.N + n] = val;
         } else {
           int64_t row = m;
           if (OP == kFeedDwIn) {
@@ -610,7 +623,7 @@ hipError_t launch_feed_op(const FeedArgs& a, hipStream_t st) {
   }
   launch_kernel(kernel, dim3((unsigned)(items < T::kResident ? items : T::kResident)), dim3(T::kThreads), T::kLds, st, a, tiles_m,
                 tiles_n);
-  if (a.splits > 1) return launch_feed_join(a, sizeof(DT) == 2, st);
+  if (a.splits > 1) return launch_feed_join(OP, a, sizeof(DT) == 2, st);
   return hipGetLastError();
 }
 

@@ -247,6 +247,8 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
     if (s.pack_dy) a.dy = l.take(rows * s.Op * e);
     a.dp = l.take(rows * 2 * s.Fp * e);
     part = feed_part(feed_plan_of(d, s, kFeedDx), rows, d->N);
+    const size_t dh = feed_part(feed_plan_of(d, s, kFeedDh), rows, s.Fp);
+    if (part < dh) part = dh;
     const size_t in = feed_part(feed_plan_of(d, s, kFeedDwIn), 2 * (size_t)s.Fp, d->N);
     const size_t out = feed_part(feed_plan_of(d, s, kFeedDwOut), d->N_out, d->F);
     if (part < in) part = in;
@@ -254,6 +256,8 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
   } else {
     if (!train) a.h = l.take(rows * s.Fp * e);
     part = feed_part(feed_plan_of(d, s, kFeedOut), rows, d->N_out);
+    const size_t in = feed_part(feed_plan_of(d, s, kFeedIn), rows, 2 * (size_t)s.Fp);
+    if (part < in) part = in;
   }
   a.part = l.take(part);
   a.bytes = l.bytes;
@@ -336,7 +340,7 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   a.steps = s.steps(s.Np);
   a.out = h; a.ldo = s.Fp; a.gu = static_cast<float*>(reserve);
   FeedPlan p = feed_plan_of(d, s, kFeedIn);
-  a.splits = p.splits;
+  a.splits = p.splits; a.part = reinterpret_cast<float*>(mem + at.part);
   RETURN_IF_HIP(launch(kFeedIn, a, p, st));
   a.N = d->N_out;
   a.A = h; a.lda = s.Fp; a.KA = s.Fm;
@@ -345,7 +349,7 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   a.out = io->y; a.ldo = d->N_out; a.gu = nullptr;
   a.residual = io->residual; a.ldr = io->residual ? d->residual_ld : 0;
   p = feed_plan_of(d, s, kFeedOut);
-  a.splits = p.splits; a.part = reinterpret_cast<float*>(mem + at.part);
+  a.splits = p.splits;
   return hip_status(launch(kFeedOut, a, p, st));
 }
 

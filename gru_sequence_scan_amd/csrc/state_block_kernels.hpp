@@ -92,7 +92,7 @@ struct FeedArgs {
   const void* residual; int64_t ldr;
   float* gu;                        // [M, 2 Fp] the two projections in fp32: kFeedIn writes it (or null), kFeedDh reads it
   int rows_split;                   // output rows from here on (padded) belong after the first F; 0: one block of rows
-  float* part; int splits;          // splits > 1: partial products [splits, M, N]
+  float* part; int splits;          // splits > 1: partial products [splits, M, N] (kFeedIn: 2 Fp for N)
 };
 // Tile and split of one product.
 enum FeedTileKind { kTileSmall, kTileBig, kTileDeep };  // 128 x 128, 256 x 256, 128 x 128 with more loads in flight
@@ -131,7 +131,7 @@ struct FeedPackArgs {
   int count;
 };
 hipError_t launch_feed_pack(const FeedPackArgs& a, bool bf16_storage, hipStream_t stream);
-// out = residual + the sum of the partial products.
-hipError_t launch_feed_join(const FeedArgs& a, bool bf16_storage, hipStream_t stream);
+// What a product's results would have become, from the sums of its partial products.
+hipError_t launch_feed_join(int op, const FeedArgs& a, bool bf16_storage, hipStream_t stream);
 
 }  // namespace rnnk
