@@ -118,8 +118,8 @@ __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArg
     xrow[t] = (const DT*)a.h + (int64_t)m * a.Fp;
   }
   f32x4 acc[1][MT];
-  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, a.vec, true, first, steps - first < each ? steps : first + each, wave,
-                                                                 group);
+  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, a.vec, true, first,
+                                                     steps - first < each ? steps : first + each, wave, group);
 #pragma unroll
   for (int t = 0; t < MT; ++t) sums[wave][t][lane] = acc[0][t];
   __syncthreads();
@@ -319,7 +319,9 @@ int feed_few_splits(int64_t rows, int F, int n_out, int cus) {
   return (steps + each - 1) / each;
 }
 
-hipError_t launch_feed_few(const FeedFewArgs& a, bool bf, hipStream_t st) { return bf ? few_rows<bf16>(a, st) : few_rows<float>(a, st); }
+hipError_t launch_feed_few(const FeedFewArgs& a, bool bf, hipStream_t st) {
+  return bf ? few_rows<bf16>(a, st) : few_rows<float>(a, st);
+}
 
 hipError_t launch_feed_pack(const FeedPackArgs& a, bool bf, hipStream_t st) {
   int64_t rows = 1;

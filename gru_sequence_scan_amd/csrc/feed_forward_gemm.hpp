@@ -261,7 +261,8 @@ __device__ __forceinline__ void store_half(DT* out, int64_t ld, const float (&va
 #pragma unroll
     for (int v = 0; v < 8; v += 2) {
       const float keep = odd ? val[v + 1] : val[v], give = odd ? val[v] : val[v + 1];
-      const float got = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, give), 0xB1, 0xF, 0xF, true));
+      const int there = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, give), 0xB1, 0xF, 0xF, true);
+      const float got = __builtin_bit_cast(float, there);
       typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
       *reinterpret_cast<bf16x2*>(p + (8 * (v >> 2) + (v & 3)) * ld) = bf16x2{(bf16)(odd ? got : keep), (bf16)(odd ? keep : got)};
     }
@@ -283,8 +284,8 @@ __device__ __forceinline__ void store_half(DT* out, int64_t ld, const float (&va
 // and column of the tile exists; it leaves in halves of a block, and what a
 // half needs from memory is asked for while the one before it is worked on.
 template <typename DT, int TILE, int OP, bool WHOLE>
-__device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& w, const f32x16 (&acc)[FeedTile<TILE>::MI][2], int wm,
-                                             int wn, int lane) {
+__device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& w,
+                                             const f32x16 (&acc)[FeedTile<TILE>::MI][2], int wm, int wn, int lane) {
   constexpr int MI = FeedTile<TILE>::MI, kAcross = OP == kFeedIn ? 1 : 2, kBlocks = kAcross * MI;
   const int m_base = w.m0 + wm * MI * 32 + 4 * (lane >> 5), n_base = w.n0 + wn * (OP == kFeedIn ? 32 : 64) + (lane & 31);
   if constexpr (WHOLE) {
@@ -602,7 +603,8 @@ __global__ __launch_bounds__(FeedTile<TILE>::kThreads, 2) void feed_kernel(FeedA
         ++kt;
       }
     }
-    const bool whole = w.m0 + T::kRows <= a.M && w.n0 + (OP == kFeedIn ? T::kRows / 2 : T::kRows) <= (OP == kFeedIn || OP == kFeedDh ? a.F : a.N);
+    const int last = OP == kFeedIn || OP == kFeedDh ? a.F : a.N;
+    const bool whole = w.m0 + T::kRows <= a.M && w.n0 + (OP == kFeedIn ? T::kRows / 2 : T::kRows) <= last;
     if (whole)
       feed_results<DT, TILE, OP, true>(a, w, acc, wm, wn, lane);
     else

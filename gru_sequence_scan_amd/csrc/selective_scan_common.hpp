@@ -114,7 +114,8 @@ struct SelPlace {
 // a channel past the last one the first.
 template <typename DT, int STEPS, bool VEC>
 struct SelTile {
-  static constexpr int E = kSelTile * STEPS / kSelThreads < 16 / (int)sizeof(DT) ? kSelTile * STEPS / kSelThreads : 16 / (int)sizeof(DT);
+  static constexpr int kShare = kSelTile * STEPS / kSelThreads, kWide = 16 / (int)sizeof(DT);  // of a thread, of an access
+  static constexpr int E = kShare < kWide ? kShare : kWide;
   static constexpr int kPer = kSelTile / E;                               // accesses of a step
   static constexpr int kTimes = STEPS * kPer / kSelThreads;               // accesses of a thread
   static constexpr int kLd = kSelTile + 16;                               // a step's row in LDS: four steps fall on different banks

@@ -109,6 +109,18 @@ def _activation(name, allowed):
     return ACTIVATIONS[name]
 
 
+def _view(t, name, shape, like):
+    """(t, its strides) where t's last dimension is contiguous, else of a dense copy."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.shape == shape and t.dtype is like.dtype and t.device == like.device:
+        s = t.stride()
+        if s[-1] == 1:
+            return t, s
+    t = _strided(t, name, shape, like)
+    return t, t.stride()
+
+
 # ---------------------------------------------------------------------------
 # Short causal convolution
 # ---------------------------------------------------------------------------
@@ -119,22 +131,23 @@ def _causal_conv(x, weight, bias, state, lengths, activation, train):
     _tensor(weight, "weight", 2)
     T, B, C = x.shape
     W = weight.shape[1]
+    if W < 1:
+        raise ValueError("weight: a filter has at least one tap")
     device, dtype = x.device, x.dtype
-    x = _strided(x, "x", x.shape, x)
+    x, (xt, xb, _) = _view(x, "x", x.shape, x)
     weight = _plain(weight, "weight", (C, W), dtype, device)
     bias = _plain(bias, "bias", (C,), dtype, device)
     state = _plain(state, "state", (W - 1, B, C), dtype, device)
     lengths = _lengths(lengths, B, T, device)
     y = _dense_like(x)
     state_n = x.new_empty((W - 1, B, C))
-    xt, xb, _ = x.stride()
     desc = _CONV_DESC(DTYPES[dtype], T, B, C, W, act, xt, xb)
-    io = _CONV_IO(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(lengths), _ptr(state), y.data_ptr(),
-                         state_n.data_ptr())
+    io = _CONV_IO(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(lengths), _ptr(state), y.data_ptr(), state_n.data_ptr())
     stream = _call("rnn_causal_conv", device, desc, io)
     if not train:
         return y, state_n
-    return (y, state_n), BlockContext(device, stream, desc=desc, shape=(T, B, C, W), x=x, weight=weight, bias=bias, lengths=lengths, state=state)
+    return (y, state_n), BlockContext(device, stream, desc=desc, shape=(T, B, C, W), x=x, weight=weight, bias=bias,
+                                      lengths=lengths, state=state)
 
 
 def causal_conv(x, weight, bias=None, *, state=None, lengths=None, activation=None):
@@ -188,14 +201,18 @@ def _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, train)
     _tensor(x, "x", 3)
     _tensor(B, "B", 4)
     _tensor(A, "A", 2)
-    T, rows, H = x.shape
-    G, N = B.shape[2:]
-    device, dtype, shape = x.device, x.dtype, x.shape
-    x = _strided(x, "x", shape, x)
-    dt = _strided(dt, "dt", shape, x)
-    z = None if z is None else _strided(z, "z", shape, x)
-    B = _strided(B, "B", (T, rows, G, N), x)
-    C = _strided(C, "C", (T, rows, G, N), x)
+    T, rows, H = shape = x.shape
+    _, _, G, N = groups = B.shape
+    if groups[:2] != shape[:2]:
+        raise ValueError(f"B: shape {tuple(groups)} does not begin with {tuple(shape[:2])}")
+    device = x.device
+    x, (xt, xb, _) = _view(x, "x", shape, x)
+    dt, (dtt, dtb, _) = _view(dt, "dt", shape, x)
+    B, (Bt, Bb, Bg, _) = _view(B, "B", groups, x)
+    C, (Ct, Cb, Cg, _) = _view(C, "C", groups, x)
+    zt = zb = 0
+    if z is not None:
+        z, (zt, zb, _) = _view(z, "z", shape, x)
     A = _plain(A, "A", (H, N), torch.float32, device)
     D = _plain(D, "D", (H,), torch.float32, device)
     dt_bias = _plain(dt_bias, "dt_bias", (H,), torch.float32, device)
@@ -203,11 +220,10 @@ def _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, train)
     lengths = _lengths(lengths, rows, T, device)
     y = _dense_like(x)
     h_n = torch.empty((rows, H, N), dtype=torch.float32, device=device)
-    desc = _SCAN_DESC(DTYPES[dtype], T, rows, H, N, G, 1 if softplus else 0, 0 if z is None else 1, *x.stride()[:2],
-                                *dt.stride()[:2], *((0, 0) if z is None else z.stride()[:2]), *B.stride()[:3],
-                                *C.stride()[:3])
-    io = _SCAN_IO(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D),
-                            _ptr(dt_bias), _ptr(lengths), _ptr(h0), y.data_ptr(), h_n.data_ptr())
+    desc = _SCAN_DESC(DTYPES[x.dtype], T, rows, H, N, G, 1 if softplus else 0, 0 if z is None else 1, xt, xb, dtt, dtb, zt, zb,
+                      Bt, Bb, Bg, Ct, Cb, Cg)
+    io = _SCAN_IO(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D), _ptr(dt_bias),
+                  _ptr(lengths), _ptr(h0), y.data_ptr(), h_n.data_ptr())
     size = _bytes("rnn_selective_scan_workspace_bytes", desc)
     ws = _buffer(size, device)
     if not train:
@@ -215,8 +231,7 @@ def _selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, h0, lengths, train)
         return y, h_n
     rsize = _bytes("rnn_selective_scan_reserve_bytes", desc)
     reserve = _buffer(rsize, device)
-    stream = _call("rnn_selective_scan_train", device, desc, io, _ptr(reserve), rsize, _ptr(ws),
-                   size)
+    stream = _call("rnn_selective_scan_train", device, desc, io, _ptr(reserve), rsize, _ptr(ws), size)
     return (y, h_n), BlockContext(device, stream, desc=desc, shape=(T, rows, H, N), x=x, dt=dt, z=z, B=B, C=C, A=A, D=D, dt_bias=dt_bias,
                                   lengths=lengths, reserve=reserve)
 
@@ -264,10 +279,9 @@ def selective_scan_backward(ctx, dy, dh_n=None):
          "B": dy.new_empty(ctx.B.shape), "C": dy.new_empty(ctx.B.shape), "A": f32(H, N),
          "D": None if ctx.D is None else f32(H), "dt_bias": None if ctx.dt_bias is None else f32(H),
          "h0": f32(rows, H, N)}
-    io = _SCAN_IO(ctx.x.data_ptr(), ctx.dt.data_ptr(), _ptr(ctx.z), ctx.B.data_ptr(), ctx.C.data_ptr(),
-                            ctx.A.data_ptr(), _ptr(ctx.D), _ptr(ctx.dt_bias), _ptr(ctx.lengths), 0, 0, 0)
-    grads = _SCAN_GRADS(dy.data_ptr(), _ptr(dh_n), *(_ptr(g[k]) for k in ("x", "dt", "z", "B", "C", "A", "D",
-                                                                                    "dt_bias", "h0")))
+    io = _SCAN_IO(ctx.x.data_ptr(), ctx.dt.data_ptr(), _ptr(ctx.z), ctx.B.data_ptr(), ctx.C.data_ptr(), ctx.A.data_ptr(),
+                  _ptr(ctx.D), _ptr(ctx.dt_bias), _ptr(ctx.lengths), 0, 0, 0)
+    grads = _SCAN_GRADS(dy.data_ptr(), _ptr(dh_n), *(_ptr(g[k]) for k in ("x", "dt", "z", "B", "C", "A", "D", "dt_bias", "h0")))
     size = _bytes("rnn_selective_scan_backward_workspace_bytes", d)
     ws = _buffer(size, device)
     ctx._use(ctx.x, ctx.dt, ctx.z, ctx.B, ctx.C, ctx.A, ctx.D, ctx.dt_bias, ctx.lengths, ctx.reserve)
@@ -283,11 +297,11 @@ def selective_scan_backward(ctx, dy, dh_n=None):
 def _weight(w, name, like):
     """(w, elements between its rows) of a matrix whose rows are contiguous."""
     _tensor(w, name, 2)
-    w = _strided(w, name, w.shape, like)
-    n = w.shape[1]
-    if w.shape[0] > 1 and w.stride(0) < n:
-        w = w.contiguous()
-    return w, n if w.shape[0] == 1 else w.stride(0)
+    rows, n = w.shape
+    w, (ld, _) = _view(w, name, w.shape, like)
+    if rows == 1:
+        return w, n
+    return (w, ld) if ld >= n else (w.contiguous(), n)
 
 
 def _feed_forward(x, w_in, w_out, residual, activation, train):

@@ -106,8 +106,9 @@ def test_lengths_are_clamped_and_host_values_checked():
     assert torch.equal(y, y2) and torch.equal(last, last2)
     with pytest.raises(ValueError, match="lengths"):
         gss.causal_conv(x, w, b, lengths=[0, 13, 7])
-    with pytest.raises(ValueError, match="weight"):
-        gss.causal_conv(x, w[:8], b)
+    for bad in (w[:8], None, w[:, :0], w.bfloat16()):
+        with pytest.raises(ValueError, match="weight"):
+            gss.causal_conv(x, bad, b)
     with pytest.raises(ValueError, match="state"):
         gss.causal_conv(x, w, b, state=state[:2])
     with pytest.raises(gss.RnnError):

@@ -92,7 +92,8 @@ def test_steps_of_two_requests_at_once():
     other's eager runs: nothing is shared between the calls but the weights."""
     block = _example().StateSpaceBlock(32, 64, 16, 4, 96, dtype=torch.bfloat16, seed=1)
     xs = [torch.randn(1, 3, 32, device="cuda", dtype=torch.float32).bfloat16() for _ in range(2)]
-    states = [(torch.zeros(3, 3, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(3, 64, 16, device="cuda", dtype=torch.float32)) for _ in range(2)]
+    states = [(torch.zeros(3, 3, 64, device="cuda", dtype=torch.bfloat16),
+               torch.zeros(3, 64, 16, device="cuda", dtype=torch.float32)) for _ in range(2)]
     for x, s in zip(xs, states):
         block.step(x, s)
     torch.cuda.synchronize()
