@@ -28,13 +28,15 @@ namespace rnnk {
 namespace {
 
 constexpr int kSteps = 32;
+constexpr int kPart = kSelKeep;  // steps that the code is written out for
 
 template <typename DT, int J, bool VEC, bool COMPOSE>
-__global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanArgs a) {
+__global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(sel_waves(J), sel_waves(J)))) void sel_forward_kernel(SelectiveScanArgs a) {
   constexpr int NP = 4 * J;
   using Tile = SelTile<DT, kSteps, VEC>;
   __shared__ __attribute__((aligned(16))) DT lds_x[kSteps * Tile::kLd], lds_d[kSteps * Tile::kLd];
-  __shared__ __attribute__((aligned(16))) DT lds_z[COMPOSE ? 1 : kSteps * Tile::kLd], lds_y[COMPOSE ? 1 : kSteps * Tile::kLd];
+  // y takes x's place: a thread reads the slots of a tile of y that it then fills with the next x
+  __shared__ __attribute__((aligned(16))) DT lds_z[COMPOSE ? 1 : kSteps * Tile::kLd];
   __shared__ __attribute__((aligned(16))) float lds_b[kSteps * NP], lds_c[COMPOSE ? 1 : kSteps * NP];
   const SelPlace p(a);
   if (p.seg >= a.segs) return;
@@ -88,40 +90,69 @@ __global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanA
     lds_barrier();
     if (t + kSteps < end) load(t + kSteps);
 #pragma unroll 1
-    for (int g = 0; g < kSteps / 4; ++g) {
-      if (!COMPOSE && a.keep && g % (kSelKeep / 4) == 0 && live && t + 4 * g < end)
-        write_states<J>(a.keep + ((t / kSelKeep + g / (kSelKeep / 4)) * cells + cell) * NP + q * J, h);
-      const int at = (4 * g + q) * Tile::kLd + ch;
-      const bool on = t + 4 * g + q < p.L;  // a step past the row's end has no length
-      const float xv = on ? to_f32<DT>(lds_x[at]) : 0.f;
-      const float d = on ? step_length(to_f32<DT>(lds_d[at]) + bias, a.softplus) : 0.f;
-      const float dx = d * xv;
-      if (COMPOSE) sum_d += d;
-      float acc[4];
+    for (int half = 0; half < kSteps / kPart; ++half) {
+      const int from = half * kPart;
+      if (!COMPOSE && a.keep && live && t + from < end)
+        write_states<J>(a.keep + ((t + from) / kSelKeep * cells + cell) * NP + q * J, h);
+      // B and C of the steps ahead
+      float bv[kAhead + 1][J], cv[kAhead + 1][J];
+      auto rows = [&](int s) {
+        read_states<J>(lds_b + (from + s) * NP + q * J, bv[s % (kAhead + 1)]);
+        if (!COMPOSE) read_states<J>(lds_c + (from + s) * NP + q * J, cv[s % (kAhead + 1)]);
+      };
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float ds = quad_from(d, s), dxs = quad_from(dx, s);
-        float bv[J], cv[J];
-        read_states<J>(lds_b + (4 * g + s) * NP + q * J, bv);
-        if (!COMPOSE) read_states<J>(lds_c + (4 * g + s) * NP + q * J, cv);
-        acc[s] = 0.f;
+      for (int s = 0; s < kAhead; ++s) rows(s);
+      // what a lane forms for its own steps, 4 g + q
+      float d[kPart / 4], dx[kPart / 4], own[kPart / 4], gate[kPart / 4];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * A2[j]), h[j], dxs * bv[j]);
-          if (!COMPOSE) acc[s] = __builtin_fmaf(h[j], cv[j], acc[s]);
-        }
+      for (int g = 0; g < kPart / 4; ++g) {
+        const int at = (from + 4 * g + q) * Tile::kLd + ch;
+        const bool on = t + from + 4 * g + q < p.L;  // a step past the row's end has no length
+        d[g] = to_f32<DT>(lds_d[at]) + bias;
+        dx[g] = on ? to_f32<DT>(lds_x[at]) : 0.f;
       }
-      if (!COMPOSE) {
-        float v = __builtin_fmaf(D, xv, quad_scatter(acc, q));
-        if (z) {
-          const float zv = to_f32<DT>(lds_z[at]);
-          v *= zv * fsigmoid(zv);
+      if (a.softplus) {
+#pragma unroll
+        for (int g = 0; g < kPart / 4; ++g) d[g] = step_length(d[g], 1);
+      }
+      if (!COMPOSE && z) {
+#pragma unroll
+        for (int g = 0; g < kPart / 4; ++g) {
+          const float zv = to_f32<DT>(lds_z[(from + 4 * g + q) * Tile::kLd + ch]);
+          gate[g] = zv * fsigmoid(zv);
         }
-        lds_y[at] = from_f32<DT>(v);
+      } else {
+#pragma unroll
+        for (int g = 0; g < kPart / 4; ++g) gate[g] = 1.f;
+      }
+#pragma unroll
+      for (int g = 0; g < kPart / 4; ++g) {
+        if (!(t + from + 4 * g + q < p.L)) d[g] = 0.f;
+        own[g] = D * dx[g];
+        dx[g] *= d[g];
+        if (COMPOSE) sum_d += d[g];
+      }
+#pragma unroll
+      for (int g = 0; g < kPart / 4; ++g) {
+        float acc[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float ds = quad_from(d[g], s), dxs = quad_from(dx[g], s);
+          const int at = 4 * g + s, i = at % (kAhead + 1);
+          if (at + kAhead < kPart) rows(at + kAhead);
+          __builtin_amdgcn_sched_barrier(kSelKeepReads);
+          acc[s] = 0.f;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * A2[j]), h[j], dxs * bv[i][j]);
+            if (!COMPOSE) acc[s] = __builtin_fmaf(h[j], cv[i][j], acc[s]);
+          }
+        }
+        if (!COMPOSE) lds_x[(from + 4 * g + q) * Tile::kLd + ch] = from_f32<DT>((quad_scatter(acc, q) + own[g]) * gate[g]);
       }
     }
     lds_barrier();
-    if (!COMPOSE) Tile::store(lds_y, y, y_t, t, p.t1, p.L, p.c0, p.live);
+    if (!COMPOSE) Tile::store(lds_x, y, y_t, t, p.t1, p.L, p.c0, p.live);
   }
   if (COMPOSE) {
     if (live) write_states<J>(a.map_s + (p.seg * cells + cell) * NP + q * J, h);
@@ -130,7 +161,7 @@ __global__ __launch_bounds__(kSelThreads) void sel_forward_kernel(SelectiveScanA
     return;
   }
   // steps past the row's end
-  for (; t < p.t1; t += kSteps) Tile::store(lds_y, y, y_t, t, p.t1, p.L, p.c0, p.live);
+  for (; t < p.t1; t += kSteps) Tile::store(lds_x, y, y_t, t, p.t1, p.L, p.c0, p.live);
   if (a.h_n && live && p.seg == a.segs - 1) store_row<J>(a.h_n + cell * a.N, q * J, a.N, a.svec, h);
 }
 
@@ -278,11 +309,11 @@ int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps) {
   const int chunks = (T + 63) / 64;
   int best = 1;
   double least = T * 0.13 * scale;
-  for (int want = 2; want <= chunks && want * tiles <= 2.0 * cus; ++want) {
+  for (int want = 2; want <= chunks && want * tiles <= 4.0 * cus; ++want) {
     const int each = (chunks + want - 1) / want;
     if ((chunks + each - 1) / each != want) continue;
     const double load = want * tiles / cus;
-    const double step = load <= 1.0 ? 0.215 : 0.215 + 0.1 * (load - 1.0);
+    const double step = load <= 1.0 ? 0.215 : 0.215 + 0.05 * (load - 1.0);
     const double us = each * 64 * step * scale + 14.0;
     if (us < least) {
       least = us;

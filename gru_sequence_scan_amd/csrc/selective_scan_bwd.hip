@@ -35,7 +35,7 @@ constexpr int kSteps = kSelKeep;  // 16
 // What segment adds to c on the way to its beginning, and the sum of its
 // steps.
 template <typename DT, int J, bool VEC>
-__global__ __launch_bounds__(kSelThreads) void sel_compose_back_kernel(SelectiveScanArgs a) {
+__global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(sel_waves(J), sel_waves(J)))) void sel_compose_back_kernel(SelectiveScanArgs a) {
   constexpr int NP = 4 * J, kTile = 32;
   using Tile = SelTile<DT, kTile, VEC>;
   __shared__ __attribute__((aligned(16))) DT lds_d[kTile * Tile::kLd], lds_v[kTile * Tile::kLd], lds_z[kTile * Tile::kLd];
@@ -75,23 +75,44 @@ __global__ __launch_bounds__(kSelThreads) void sel_compose_back_kernel(Selective
     lds_barrier();
     if (t > p.t0) load(t - kTile);
 #pragma unroll 1
-    for (int g = kTile / 4 - 1; g >= 0; --g) {
-      const int at = (4 * g + q) * Tile::kLd + ch;
-      const bool on = t + 4 * g + q < p.L;
-      const float d = on ? step_length(to_f32<DT>(lds_d[at]) + bias, a.softplus) : 0.f;
-      float v = on ? to_f32<DT>(lds_v[at]) : 0.f;
-      if (z) {
-        const float zv = to_f32<DT>(lds_z[at]);
-        v = on ? v * (zv * fsigmoid(zv)) : 0.f;
+    for (int from = kTile - kSteps; from >= 0; from -= kSteps) {
+      float cv[kAhead + 1][J];  // C of the steps ahead
+      auto rows = [&](int s) { read_states<J>(lds_c + (from + s) * NP + q * J, cv[s % (kAhead + 1)]); };
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) rows(kSteps - 1 - s);
+      // a lane's own steps, 4 g + q
+      float d[kSteps / 4], v[kSteps / 4];
+#pragma unroll
+      for (int g = 0; g < kSteps / 4; ++g) {
+        const int at = (from + 4 * g + q) * Tile::kLd + ch;
+        d[g] = to_f32<DT>(lds_d[at]) + bias;
+        v[g] = to_f32<DT>(lds_v[at]);
       }
-      sum_d += d;
+      if (a.softplus) {
 #pragma unroll
-      for (int s = 3; s >= 0; --s) {
-        const float ds = quad_from(d, s), vs = quad_from(v, s);
-        float cv[J];
-        read_states<J>(lds_c + (4 * g + s) * NP + q * J, cv);
+        for (int g = 0; g < kSteps / 4; ++g) d[g] = step_length(d[g], 1);
+      }
+      if (z) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) c[j] = __builtin_amdgcn_exp2f(ds * A2[j]) * __builtin_fmaf(vs, cv[j], c[j]);
+        for (int g = 0; g < kSteps / 4; ++g) {
+          const float zv = to_f32<DT>(lds_z[(from + 4 * g + q) * Tile::kLd + ch]);
+          v[g] *= zv * fsigmoid(zv);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < kSteps / 4; ++g) {
+        const bool on = t + from + 4 * g + q < p.L;
+        d[g] = on ? d[g] : 0.f;
+        v[g] = on ? v[g] : 0.f;
+        sum_d += d[g];
+      }
+#pragma unroll
+      for (int s = kSteps - 1; s >= 0; --s) {
+        if (s >= kAhead) rows(s - kAhead);
+        __builtin_amdgcn_sched_barrier(kSelKeepReads);
+        const float ds = quad_from(d[s / 4], s % 4), vs = quad_from(v[s / 4], s % 4);
+#pragma unroll
+        for (int j = 0; j < J; ++j) c[j] = __builtin_amdgcn_exp2f(ds * A2[j]) * __builtin_fmaf(vs, cv[s % (kAhead + 1)][j], c[j]);
       }
     }
     lds_barrier();
@@ -176,9 +197,18 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int at = (4 * g + q) * Tile::kLd + ch;
+      d[g] = to_f32<DT>(lds_d[at]) + bias;
+      xd[g] = to_f32<DT>(lds_x[at]);
+    }
+    if (a.softplus) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) d[g] = step_length(d[g], 1);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
       const bool on = live && t + 4 * g + q < p.L;
-      d[g] = on ? step_length(to_f32<DT>(lds_d[at]) + bias, a.softplus) : 0.f;
-      xd[g] = on ? d[g] * to_f32<DT>(lds_x[at]) : 0.f;
+      d[g] = on ? d[g] : 0.f;
+      xd[g] = on ? d[g] * xd[g] : 0.f;
     }
     // states at the parts' beginnings
 #pragma unroll
@@ -217,8 +247,9 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
         const int gg = part * (kPart / 4) + g;
         const int at = (4 * gg + q) * Tile::kLd + ch;
         const bool on = live && t + 4 * gg + q < p.L;
-        float v = on ? to_f32<DT>(lds_v[at]) : 0.f;
-        const float xv = on ? to_f32<DT>(lds_x[at]) : 0.f;
+        float v = to_f32<DT>(lds_v[at]), xv = to_f32<DT>(lds_x[at]);
+        v = on ? v : 0.f;
+        xv = on ? xv : 0.f;
         if (z) {
           // y once more, for the gate's gradient
           float acc[4];
