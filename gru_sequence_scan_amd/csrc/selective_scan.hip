@@ -7,13 +7,15 @@
 //
 // per channel of [T, B, H]; B and C are shared by a group's channels.
 //
-// Bound by the vector units: a state's step is an exponential (a quarter of
-// the rate) and four products or sums, 32 clocks of a SIMD for 64 states,
-// while a channel's step moves 8 bytes in bf16. So the states stay in
-// registers for the whole time, four lanes a channel; the time is walked in
-// tiles of 32 steps, staged through LDS with the next tile's loads in flight,
-// and what is formed once a channel and step (step length, gate) is formed by
-// one lane in four.
+// Bound by the issue of vector instructions: a state's step is an exponential
+// (8.3 clocks of a SIMD for 64 lanes) and four products or sums (2.4 to 3.8
+// each), about 20 clocks, while a channel's step moves 8 bytes in bf16. What
+// is formed once a channel and step (step length, gate) and handed round
+// takes as many instructions again. So the states stay in registers for the
+// whole time, four lanes a channel; the time is walked in tiles of 32 steps,
+// staged through LDS with the next tile's loads in flight, and the scalars of
+// a step are formed by one lane in four, 16 steps at once. T 1000, 32 x 1024
+// x 16, bf16, with gate: 165 us; the exponentials and products alone need 68.
 //
 // Where that gives few workgroups the time is cut into segments: a first
 // launch finds what each adds to the state and the sum of its steps (its
@@ -300,20 +302,22 @@ hipError_t launch_sel_carry(const SelectiveScanArgs& a, const float* first, int 
 }
 
 // The time is cut where that is expected to be faster: into segments of whole
-// 64 steps, up to two workgroups a compute unit. A step of the walk takes 130
-// ns (N = 16) with one workgroup a compute unit, whose waves then wait for
-// their own results, and 185 with two; in the launch that composes a segment
-// 85 and 130; the two launches more cost about 14 us.
+// 64 steps, up to as many workgroups a compute unit as fit. A step of the walk
+// takes 119 ns (N = 16) with one workgroup a compute unit, 190 with two and
+// 350 with four (a SIMD issues an instruction of one wave every 7.5 clocks, of
+// two every 3.8); in the launch that composes a segment 88, 137 and 255; the
+// two launches more cost about 14 us. T = 2048, 4 x 1024 channels: 226 us in
+// one piece, 46 + 34 + 5 in 16 segments.
 int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps) {
-  const double tiles = (double)B * sel_group_tiles(H, G) * G, states = sel_padded(N) / 16.0, scale = states < 0.7 ? 0.7 : states;
+  const double tiles = (double)B * sel_group_tiles(H, G) * G, scale = 0.5 + sel_padded(N) / 32.0;
   const int chunks = (T + 63) / 64;
   int best = 1;
-  double least = T * 0.13 * scale;
-  for (int want = 2; want <= chunks && want * tiles <= 4.0 * cus; ++want) {
+  double least = T * (tiles <= cus ? 0.12 : 0.12 + 0.075 * (tiles / cus - 1.0)) * scale;
+  for (int want = 2; want <= chunks && want * tiles <= (double)sel_waves(sel_padded(N) / 4) * cus; ++want) {
     const int each = (chunks + want - 1) / want;
     if ((chunks + each - 1) / each != want) continue;
     const double load = want * tiles / cus;
-    const double step = load <= 1.0 ? 0.215 : 0.215 + 0.05 * (load - 1.0);
+    const double step = load <= 1.0 ? 0.21 : 0.21 + 0.13 * (load - 1.0);
     const double us = each * 64 * step * scale + 14.0;
     if (us < least) {
       least = us;

@@ -11,10 +11,15 @@
 //
 // The time is walked backwards in tiles of 16 steps. The training forward
 // kept the state at every tile's beginning; a tile's states and decays are
-// computed again from there and stay in registers (of J states a lane and
-// more than 64 / J steps, in parts: the states at the parts' beginnings come
-// first). So nothing is divided by a decay, which may be zero, and y is not
-// read.
+// computed again from there and stay in registers. With more than four states
+// a lane they would not fit: those walk a tile four steps at a time, and the
+// states at the four steps' beginnings, found first, wait in LDS (1024 x 16 x
+// 2048 channels, N = 32, bf16: 1207 us with eight steps at a time and all of
+// it written out, 1028 so; 1024 x 8 x 2048, N = 64: 1372 and 1171). With four
+// states a lane that costs more than the second workgroup a SIMD it allows
+// gives (T 16384, 2 x 1000 x 16: 508 us with 16 steps, 556 with eight, 598
+// with four). So nothing is divided by a decay, which may be zero, and y is
+// not read.
 //
 // dB and dC are sums over the channels: a wave adds its 16 by lane
 // permutations (16 sums at a time, one operation a value in place of four),
@@ -23,8 +28,10 @@
 // stay in registers over a workgroup's time and are added over rows and
 // segments by a third.
 //
-// Bound by the vector units, like the forward: about 30 operations a state
-// and step beside its exponential.
+// Bound by the issue of instructions, like the forward: about 120 a step for
+// the 256 states of a wave, 4.5 of them exponentials.
+// T 16384, 2 x 1000 x 16, bf16, with gate: 480 us (forward 173); 500 ragged
+// steps of 64 x 512 x 16, fp32, without: 183 us (forward 75).
 #include "selective_scan_common.hpp"
 
 namespace rnnk {
@@ -122,10 +129,19 @@ __global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(sel
   if (live && q == 0) a.map_d[p.seg * cells + cell] = sum_d;
 }
 
+// Group g of a part's steps.
+template <int PARTS>
+__device__ __forceinline__ float of_part(const float (&v)[4], int part, int g) {
+  float r = v[g];
+#pragma unroll
+  for (int i = 1; i < PARTS; ++i) r = part == i ? v[i * (4 / PARTS) + g] : r;
+  return r;
+}
+
 template <typename DT, int J, bool VEC>
 __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kernel(SelectiveScanArgs a) {
   constexpr int NP = 4 * J;
-  constexpr int kPart = J <= 4 ? kSteps : 64 / J;  // steps whose states are in registers at once
+  constexpr int kPart = J <= 4 ? kSteps : 4;  // steps whose states are in registers at once
   constexpr int kParts = kSteps / kPart;
   using Tile = SelTile<DT, kSteps, VEC>;
   constexpr int kArea = kSteps * Tile::kLd;
@@ -133,6 +149,8 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
   __shared__ __attribute__((aligned(16))) DT lds_x[kArea], lds_d[kArea], lds_z[kArea], lds_v[kArea];
   __shared__ __attribute__((aligned(16))) float lds_b[kSteps * NP], lds_c[kSteps * NP];
   __shared__ __attribute__((aligned(16))) float lds_sum[4][kSteps * 2 * NP];  // each wave's dB and dC
+  // a lane's states at the beginnings of its parts after the first
+  __shared__ __attribute__((aligned(16))) float lds_h[kParts > 1 ? (kParts - 1) * kSelThreads * J : 1];
   const SelPlace p(a);
   if (p.seg >= a.segs) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 3, ch = wave * 16 + (lane >> 2);
@@ -186,9 +204,9 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
     tv.put(lds_v);
     tb.put(lds_b, t, p.L, a.N);
     tc.put(lds_c, t, p.L, a.N);
-    float first[kParts][J];
+    float start[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) first[0][j] = kept[j];
+    for (int j = 0; j < J; ++j) start[j] = kept[j];
     lds_barrier();
     if (t > p.t0) load(t - kSteps);
 
@@ -210,32 +228,39 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
       d[g] = on ? d[g] : 0.f;
       xd[g] = on ? d[g] * xd[g] : 0.f;
     }
-    // states at the parts' beginnings
+    float first[J];
 #pragma unroll
-    for (int part = 1; part < kParts; ++part) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) first[part][j] = first[part - 1][j];
-#pragma unroll
-      for (int s = (part - 1) * kPart; s < part * kPart; ++s) {
-        const float ds = quad_from(d[s / 4], s % 4), xs = quad_from(xd[s / 4], s % 4);
-        float bv[J];
-        read_states<J>(lds_b + s * NP + q * J, bv);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          first[part][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * A2[j]), first[part][j], xs * bv[j]);
-      }
-    }
-#pragma unroll
-    for (int part = kParts - 1; part >= 0; --part) {
-      float da[kPart][J], hs[kPart + 1][J];
-#pragma unroll
-      for (int j = 0; j < J; ++j) hs[0][j] = first[part][j];
+    for (int j = 0; j < J; ++j) first[j] = start[j];
+#pragma unroll 1
+    for (int part = 0; part < kParts - 1; ++part) {
 #pragma unroll
       for (int s = 0; s < kPart; ++s) {
-        const int st = part * kPart + s;
-        const float ds = quad_from(d[st / 4], st % 4), xs = quad_from(xd[st / 4], st % 4);
+        const float ds = quad_from(of_part<kParts>(d, part, s / 4), s % 4), xs = quad_from(of_part<kParts>(xd, part, s / 4), s % 4);
         float bv[J];
-        read_states<J>(lds_b + st * NP + q * J, bv);
+        read_states<J>(lds_b + (part * kPart + s) * NP + q * J, bv);
+#pragma unroll
+        for (int j = 0; j < J; ++j) first[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * A2[j]), first[j], xs * bv[j]);
+      }
+      write_states<J>(lds_h + (part * kSelThreads + threadIdx.x) * J, first);
+    }
+#pragma unroll 1
+    for (int part = kParts - 1; part >= 0; --part) {
+      float da[kPart][J], hs[kPart + 1][J], dp[kPart / 4], xp[kPart / 4];
+#pragma unroll
+      for (int g = 0; g < kPart / 4; ++g) dp[g] = of_part<kParts>(d, part, g), xp[g] = of_part<kParts>(xd, part, g);
+#pragma unroll
+      for (int j = 0; j < J; ++j) hs[0][j] = first[j];
+      if (part > 1) {
+        read_states<J>(lds_h + ((part - 2) * kSelThreads + threadIdx.x) * J, first);
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) first[j] = start[j];
+      }
+#pragma unroll
+      for (int s = 0; s < kPart; ++s) {
+        const float ds = quad_from(dp[s / 4], s % 4), xs = quad_from(xp[s / 4], s % 4);
+        float bv[J];
+        read_states<J>(lds_b + (part * kPart + s) * NP + q * J, bv);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           da[s][j] = __builtin_amdgcn_exp2f(ds * A2[j]);
@@ -263,9 +288,9 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
           }
           const float yv = __builtin_fmaf(D, xv, quad_scatter(acc, q));
           const float zv = to_f32<DT>(lds_z[at]);
-          const SigmoidPair g = fsigmoid_pair(zv);
-          lds_z[at] = from_f32<DT>(on ? v * yv * __builtin_fmaf(zv * g.s, g.no, g.s) : 0.f);
-          v = on ? v * (zv * g.s) : 0.f;
+          const SigmoidPair sg = fsigmoid_pair(zv);
+          lds_z[at] = from_f32<DT>(on ? v * yv * __builtin_fmaf(zv * sg.s, sg.no, sg.s) : 0.f);
+          v = on ? v * (zv * sg.s) : 0.f;
         }
         sum_D = __builtin_fmaf(v, xv, sum_D);
         float sum_w[4], sum_g[4];
@@ -273,7 +298,7 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
         float val[J <= 8 ? 16 : 32];
 #pragma unroll
         for (int s = 3; s >= 0; --s) {
-          const float ds = quad_from(d[gg], s), xs = quad_from(xd[gg], s), vs = quad_from(v, s);
+          const float ds = quad_from(dp[g], s), xs = quad_from(xp[g], s), vs = quad_from(v, s);
           float bv[J], cv[J];
           read_states<J>(lds_b + (4 * gg + s) * NP + q * J, bv);
           read_states<J>(lds_c + (4 * gg + s) * NP + q * J, cv);
@@ -319,7 +344,7 @@ __global__ __launch_bounds__(kSelThreads, J <= 4 ? 2 : 1) void sel_backward_kern
         const float up = on ? (a.softplus ? dd * fsigmoid(raw) : dd) : 0.f;
         sum_bias += up;
         lds_d[at] = from_f32<DT>(up);
-        lds_x[at] = from_f32<DT>(__builtin_fmaf(d[gg], gb, D * v));
+        lds_x[at] = from_f32<DT>(__builtin_fmaf(dp[g], gb, D * v));
       }
     }
     lds_barrier();

@@ -23,7 +23,7 @@ constexpr int kSelThreads = 256;
 // 16 in bf16 185 -> 169 us.
 constexpr int kAhead = 2;
 constexpr int kSelKeepReads = 0x47F;
-constexpr int sel_waves(int J) { return J <= 4 ? 4 : J == 8 ? 2 : 1; }
+constexpr int sel_waves(int J) { return J <= 4 ? 4 : J == 8 ? 3 : 2; }
 
 template <typename DT, int E>
 struct alignas(sizeof(DT) * E) SelVec {
