@@ -14,12 +14,18 @@
 // run are read again (out of the L2, where the neighbouring run's thread put
 // them). Every load of a run is issued before the first is used: a step past
 // the row's end reads the last one again, and what is not part of the row is
-// replaced by zero.
+// replaced by zero. 1000 steps of 32 x 2048 channels, bf16, 4 taps, SiLU: 54
+// us forward, 4.9 TB/s of the 5.1 that a large copy reaches (88 with loads
+// under conditions).
 //
-// Backward computes p again from x, so the forward keeps nothing. The sums
+// Backward computes p again from x, so the forward keeps nothing. It takes
+// four channels a thread: with eight the run's x, dy and dp leave no registers
+// for a second workgroup's loads (215 us; 124 with four, of which the
+// exponential and the filter both ways take three quarters of the issue slots;
+// 430 MB at 3.5 TB/s). The sums
 // over time and batch stay in a thread's registers over all runs that it
 // takes, are joined by workgroup in LDS, and a second launch adds the
-// workgroups' sums in a fixed order.
+// workgroups' sums in a fixed order (7 us there).
 //
 // Products and sums are fp32; x, w, b, y, the state and their gradients have
 // the storage type, dw and db are fp32.
