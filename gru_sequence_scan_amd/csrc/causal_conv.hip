@@ -19,10 +19,10 @@
 // under conditions).
 //
 // Backward computes p again from x, so the forward keeps nothing. It takes
-// four channels a thread: with eight the run's x, dy and dp leave no registers
-// for a second workgroup's loads (215 us; 124 with four, of which the
-// exponential and the filter both ways take three quarters of the issue slots;
-// 430 MB at 3.5 TB/s). The sums
+// four channels a thread (with eight, a run's x, dy and dp leave no registers
+// for a second workgroup's loads) and one exponential for SiLU and its slope:
+// 124 us there, 215 without the two. 430 MB at 3.5 TB/s; vector instructions
+// take three quarters of the issue slots. The sums
 // over time and batch stay in a thread's registers over all runs that it
 // takes, are joined by workgroup in LDS, and a second launch adds the
 // workgroups' sums in a fixed order (7 us there).

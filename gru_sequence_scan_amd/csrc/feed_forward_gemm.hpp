@@ -31,16 +31,16 @@
 // rows, 1024 x 2816, bf16: 38 us of kernels in tiles of four waves, 33 so.
 //
 // Measured at 32000 rows, 1024 x 2816, bf16 (us, TFLOP/s, share of the compute
-// units' matrix cycles): g | u 439, 841, 43% (it writes 0.9 GB of g, u and h);
-// y 210, 879, 43%; dh with dg and du 450, 410, 17% (1.2 GB read, 0.5 written:
-// bound by memory); dx 410, 900, 42%; dW_in 445, 829, 44%; dW_out 233, 792,
-// 43%. What bounds the others is the card's power: at 8192^3 the same kernel
+// units' matrix cycles): g | u 445, 829, 43% (it writes 0.9 GB of g, u and h);
+// y 213, 868, 43%; dh with dg and du 445 to 496, 390, 17% (1.2 GB read, 0.5
+// written: bound by memory); dx 412, 896, 42%; dW_in 453, 815, 44%; dW_out
+// 235, 786, 43%. What bounds the others is the card's power: at 8192^3 the same kernel
 // takes 976 us on random numbers and 768 on zeros (a library product 793 and
 // 485), alone the loads of dx take 250 us and its products 257. Not faster:
 // steps of 64 bytes with two workgroups (2408 us for all six against 2200) or
 // with a longer ring (2459), 16 waves, operands through registers, k begun at
-// another place in each workgroup. fp32 at 19334 rows, 512 x 1368: 111 to 129
-// TFLOP/s of 153, dh 77 (bound by memory).
+// another place in each workgroup. fp32 at 19334 rows, 512 x 1368: 105 to 121
+// TFLOP/s of 153, dh 74 (bound by memory).
 #pragma once
 
 #include <type_traits>

@@ -9,9 +9,9 @@
 //
 // Bound by the issue of vector instructions: a state's step is an exponential
 // (8.3 clocks of a SIMD for 64 lanes) and four products or sums (2.4 to 3.8
-// each), about 20 clocks, while a channel's step moves 8 bytes in bf16. What
-// is formed once a channel and step (step length, gate) and handed round
-// takes as many instructions again. So the states stay in registers for the
+// each), about 20 clocks, while a channel's step moves 8 bytes in bf16. With
+// what is formed once a channel and step (step length, gate), handed round and
+// summed, a wave issues 33 instructions a step for its 256 states. So the states stay in registers for the
 // whole time, four lanes a channel; the time is walked in tiles of 32 steps,
 // staged through LDS with the next tile's loads in flight, and the scalars of
 // a step are formed by one lane in four, 16 steps at once. T 1000, 32 x 1024
