@@ -40,7 +40,7 @@
 // steps of 64 bytes with two workgroups (2408 us for all six against 2200) or
 // with a longer ring (2459), 16 waves, operands through registers, k begun at
 // another place in each workgroup. fp32 at 19334 rows, 512 x 1368: 105 to 121
-// TFLOP/s of 153, dh 74 (bound by memory).
+// TFLOP/s of 153, dh 80 (bound by memory).
 #pragma once
 
 #include <type_traits>
@@ -389,6 +389,23 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
       const int i = k / kAcross, j = k % kAcross;
       const int n = n_base + j * 32;
       if (n >= (OP == kFeedIn ? a.Fp : a.N)) continue;
+      // what the block needs from memory, all on its way at once (the last row again for those behind it):
+      // dh of 1759 rows, 1112 x 264, bf16, whose tiles all lie at an edge, 42 -> 31 us
+      float more[16], more_u[OP == kFeedDh ? 16 : 1];
+      if (OP == kFeedDh ? a.splits == 1 : OP == kFeedOut && a.residual && a.splits == 1) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          int64_t m = m_base + i * 32 + 8 * (v >> 2) + (v & 3);
+          m = m < a.M ? m : a.M - 1;
+          if constexpr (OP == kFeedDh) {
+            const float* gu = a.gu + m * 2 * a.Fp + n;
+            more[v] = gu[0];
+            more_u[v] = gu[a.Fp];
+          } else if constexpr (OP == kFeedOut) {
+            more[v] = to_f32<DT>(((const DT*)a.residual)[m * a.ldr + n]);
+          }
+        }
+      }
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const int64_t m = m_base + i * 32 + 8 * (v >> 2) + (v & 3);
@@ -411,11 +428,10 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
             a.gu[m * 2 * a.Fp + a.Fp + n] = u;
           }
         } else if constexpr (OP == kFeedDh) {
-          const float* gu = a.gu + m * 2 * a.Fp + n;
-          const Activated r = activate(gu[0], a.act);
+          const Activated r = activate(more[v], a.act);
           const bool on = n < a.F;
           DT* out = (DT*)a.out + m * a.ldo + n;
-          out[0] = from_f32<DT>(on ? val * gu[a.Fp] * r.slope : 0.f);
+          out[0] = from_f32<DT>(on ? val * more_u[v] * r.slope : 0.f);
           out[a.Fp] = from_f32<DT>(on ? val * r.act : 0.f);
         } else {
           int64_t row = m;
@@ -424,8 +440,7 @@ __device__ __forceinline__ void feed_results(const FeedArgs& a, const FeedItem& 
             row = second ? m - a.Fp + a.F : m;
             if (row >= (second ? 2 * (int64_t)a.F : a.F)) continue;
           }
-          const float more = OP == kFeedOut && a.residual ? to_f32<DT>(((const DT*)a.residual)[row * a.ldr + n]) : 0.f;
-          ((DT*)a.out)[row * a.ldo + n] = from_f32<DT>(val + more);
+          ((DT*)a.out)[row * a.ldo + n] = from_f32<DT>(OP == kFeedOut && a.residual ? val + more[v] : val);
         }
       }
     }
