@@ -178,21 +178,22 @@ __global__ __launch_bounds__(256) void sel_carry_kernel(SelectiveScanArgs a, con
   const bool on = n < a.N;
   const float A2 = on ? a.A[cell % a.H * a.N + n] * kLog2e : 0.f;
   float h = on && first ? first[cell * a.N + n] : 0.f;
-  constexpr int kBatch = 8;
+  float* map_s = a.map_s + i;
+  const float* map_d = a.map_d + cell;
+  constexpr int kBatch = 16;
   for (int k0 = 0; k0 < a.segs; k0 += kBatch) {
     float s[kBatch], d[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int c = k0 + k < a.segs ? k0 + k : a.segs - 1;
-      const int64_t o = (back ? a.segs - 1 - c : c) * cells + cell;
-      s[k] = a.map_s[o * NP + n];
-      d[k] = a.map_d[o];
+      const int64_t o = (back ? a.segs - 1 - c : c) * cells;
+      s[k] = map_s[o * NP];
+      d[k] = map_d[o];
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (k0 + k < a.segs) {
-        const int64_t o = (back ? a.segs - 1 - (k0 + k) : k0 + k) * cells + cell;
-        a.map_s[o * NP + n] = h;
+        map_s[(back ? a.segs - 1 - (k0 + k) : k0 + k) * cells * NP] = h;
         h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * d[k]), h, s[k]);
       }
   }
@@ -306,8 +307,9 @@ hipError_t launch_sel_carry(const SelectiveScanArgs& a, const float* first, int 
 // takes 119 ns (N = 16) with one workgroup a compute unit, 190 with two and
 // 350 with four (a SIMD issues an instruction of one wave every 7.5 clocks, of
 // two every 3.8); in the launch that composes a segment 88, 137 and 255; the
-// two launches more cost about 14 us. T = 2048, 4 x 1024 channels: 226 us in
-// one piece, 46 + 34 + 5 in 16 segments.
+// two launches more cost about 12 us and 0.1 a segment. T = 2048, 4 x 1024
+// channels: 226 us in one piece, 46 + 34 + 5 in 16 segments; T = 16384, 1 x 64
+// channels: 12 + 10 + 28 us in 256 segments, 18 + 14 + 15 in 128.
 int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps) {
   const double tiles = (double)B * sel_group_tiles(H, G) * G, scale = 0.5 + sel_padded(N) / 32.0;
   const int chunks = (T + 63) / 64;
@@ -318,7 +320,7 @@ int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps) {
     if ((chunks + each - 1) / each != want) continue;
     const double load = want * tiles / cus;
     const double step = load <= 1.0 ? 0.21 : 0.21 + 0.13 * (load - 1.0);
-    const double us = each * 64 * step * scale + 14.0;
+    const double us = each * 64 * step * scale + 12.0 + 0.1 * want;
     if (us < least) {
       least = us;
       best = want;
