@@ -125,6 +125,16 @@ def test_cut_time(T, B, H, N, lengths, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T,B,H,N,lengths", [(2100, 1, 8, 16, None), (1500, 2, 20, 8, [1500, 1025]), (1100, 1, 70, 32, None),
+                                             (1153, 3, 5, 64, [1153, 1088, 1089])])
+def test_many_segments(T, B, H, N, lengths, dtype):
+    """More segments than the launch between them takes at once, rows that end
+    at and beside a segment's edge."""
+    log(f"selective_scan segments T {T} B {B} H {H} N {N} {dtype}")
+    _check(_case(T, B, H, N, 1, dtype, 23), lengths, what="segments")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("N,G", [(16, 1), (9, 2)])
 def test_token_by_token(N, G, dtype):
     """A prompt of 40 steps at once, and step by step with the state carried."""
