@@ -167,6 +167,17 @@ __global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(sel
   if (a.h_n && live && p.seg == a.segs - 1) store_row<J>(a.h_n + cell * a.N, q * J, a.N, a.svec, h);
 }
 
+// 2^e h + s: a state after a segment. A growing channel's factor (A > 0, or
+// negative steps) can be larger than any fp32 number over a segment's steps,
+// where the walk step by step stays finite: at zero, for one. It goes in three
+// parts then. 381 is the largest exponent that is used: 2^381 takes the
+// smallest number past the largest.
+__device__ __forceinline__ float sel_past(float e, float h, float s) {
+  const bool far = e > 126.0f;
+  const float f = __builtin_amdgcn_exp2f(far ? __builtin_fminf(e, 381.0f) * (1.0f / 3.0f) : e);
+  return __builtin_fmaf(f, far ? f * (f * h) : h, s);
+}
+
 // The states that enter the segments, one thread per state: in the place of
 // what the segments add. Forward from h_0, backward from dh_n and the last
 // segment.
@@ -194,7 +205,7 @@ __global__ __launch_bounds__(256) void sel_carry_kernel(SelectiveScanArgs a, con
     for (int k = 0; k < kBatch; ++k)
       if (k0 + k < a.segs) {
         map_s[(back ? a.segs - 1 - (k0 + k) : k0 + k) * cells * NP] = h;
-        h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * d[k]), h, s[k]);
+        h = sel_past(A2 * d[k], h, s[k]);
       }
   }
 }

@@ -178,6 +178,60 @@ def test_growing_states_and_positive_A():
     _check(c, None, what="positive A")
 
 
+def _growing(T, H, N, grow):
+    """A channel that grows by exp(128) over each 64 steps of `grow`, hardly
+    elsewhere, from a state of zero."""
+    c = _case(T, 1, H, N, 1, torch.float32, 29)
+    c["A"] = 0.9 + 0.1 * torch.rand((H, N), generator=torch.Generator().manual_seed(3))
+    c["dt"] = torch.full((T, 1, H), 1e-3)
+    c["dt"][grow] = 2.2
+    c["x"][grow] = 0.0
+    c["dt_bias"] = c["h0"] = c["dh_n"] = None
+    d = gss.RnnSelectiveScanDesc(0, T, 1, H, N, 1, 0, 1, *([0] * 12))
+    assert gss.block_ops._bytes("rnn_selective_scan_workspace_bytes", d) > 0    # cut
+    return c
+
+
+@pytest.mark.parametrize("H,N", [(8, 16), (20, 5)])
+def test_cut_time_keeps_a_state_of_zero_over_any_growth(H, N):
+    """A segment's factor that no fp32 number holds leaves a state of zero at
+    zero, as the walk step by step does, forward and backward."""
+    T = 1000
+    c = _growing(T, H, N, slice(0, 700))
+    args = [c[k].cuda() for k in ("x", "dt", "A", "B", "C", "D")]
+    y, hn = gss.selective_scan(*args, z=c["z"].cuda(), softplus=False)
+    v = {k: f64(t) for k, t in c.items()}
+    yr, hr, _ = oracle.selective_scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], z=v["z"], soft=False)
+    assert_near(y, yr, torch.float32, "y")
+    assert_near(hn, hr, torch.float32, "h_n")
+    # backward the same from the other end: no state, and gradients before the growth alone
+    c = _growing(T, H, N, slice(300, T))
+    c["x"][:] = 0.0
+    c["dy"][300:] = 0.0
+    y, hn, g = _run(c, PLACE["dense"], PLACE["dense"], None, softplus=False)
+    yr, hr, gr = _reference(c, None, softplus=False)
+    assert not hn.any() and not hr.any()
+    for k in NAMES:
+        if k != "dt_bias":
+            assert_near(g[k], gr[k], torch.float32, f"d{k}")
+    assert float(g["x"].abs().max()) > 1.0
+
+
+def test_cut_time_grows_a_small_state_past_one_factor():
+    """From 2^-100 by exp(104), about 2^150, in one segment: that factor is no fp32 number, the state is."""
+    T, H, N = 640, 8, 16
+    c = _growing(T, H, N, slice(64, 128))
+    c["A"][:] = 1.0
+    c["dt"][64:128] = 104.0 / 64
+    c["dt"][:64] = c["dt"][128:] = 0.0
+    c["x"][:] = 0.0
+    c["h0"] = torch.full((1, H, N), 2.0 ** -100)
+    _, hn = gss.selective_scan(*[c[k].cuda() for k in ("x", "dt", "A", "B", "C")], h0=c["h0"].cuda(), softplus=False)
+    # the steps and their sum are exact; log2(e), its product with the sum, a third and the product with that are
+    # rounded: 104 (2^-25 + 2^-24 + 2^-25 + 2^-24), and three times an exponential (2^-23) and a product: 1.9e-5 in all
+    assert np.abs(f64(hn) / (2.0 ** -100 * np.exp(104.0)) - 1).max() < 2e-5
+
+
 def test_gradient_of_shared_inputs():
     """B and C of one group gather the gradients of all its channels, however
     many tiles of 64 they make."""
