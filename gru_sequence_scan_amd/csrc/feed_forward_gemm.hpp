@@ -62,11 +62,13 @@ struct Activated {
 __device__ __forceinline__ Activated activate(float g, int kind) {
   Activated r;
   if (kind == RNN_ACT_GELU_TANH) {
+    // beyond +-40 sigma is 0 or 1 and its slope 0 in fp32 (2 u is past 4600 there),
+    // while g^2 would overflow for large gates and make the slope 0 times infinity
     constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float g2 = g * g, u = c * g * __builtin_fmaf(0.044715f, g2, 1.0f);
-    const SigmoidPair p = fsigmoid_pair(u);
+    const float b = g > 40.0f ? 40.0f : g < -40.0f ? -40.0f : g, b2 = b * b;  // (what is no number stays so)
+    const SigmoidPair p = fsigmoid_pair(c * b * __builtin_fmaf(0.044715f, b2, 1.0f));
     r.act = g * p.s;
-    r.slope = __builtin_fmaf(g * p.s * p.no, c * __builtin_fmaf(3.0f * 0.044715f, g2, 1.0f), p.s);
+    r.slope = __builtin_fmaf(b * p.s * p.no, c * __builtin_fmaf(3.0f * 0.044715f, b2, 1.0f), p.s);
   } else {
     const SigmoidPair p = fsigmoid_pair(g);
     r.act = kind == RNN_ACT_SIGMOID ? p.s : g * p.s;

@@ -160,6 +160,24 @@ def test_large_gates():
         _check(c, kind, what=kind)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_gates_whose_square_no_fp32_number_holds(kind):
+    """Gates of 1e20 either way: the slope is 0 or 1 (the sigmoid's 0), and
+    what is not a number stays that in its gradient."""
+    rows, n, F = 70, 16, 32
+    c = _case(rows, n, F, 16, torch.float32, 8)
+    c["x"][:, 0] = 1.0
+    c["w_in"][:16] = 0.0
+    c["w_in"][:8, 0], c["w_in"][8:16, 0] = 1e20, -1e20
+    c["dy"] *= 1e-20                                      # so that dw_in's parts are of one size
+    c["r"] *= 1e20
+    _check(c, kind, what=kind)
+    x = c["x"].cuda()
+    x[3, 1] = float("nan")
+    ctx = gss.feed_forward_train(x, c["w_in"].cuda(), c["w_out"].cuda(), activation=kind)[1]
+    assert torch.isnan(gss.feed_forward_backward(ctx, c["dy"].cuda())[0][3]).all()
+
+
 def test_leading_dimensions():
     c = _case(6 * 5, 24, 40, 16, torch.float32, 2)
     x, w_in, w_out, r = (c[k].cuda() for k in ("x", "w_in", "w_out", "r"))
