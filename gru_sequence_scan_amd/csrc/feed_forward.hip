@@ -1,6 +1,6 @@
-// Gated feed-forward: how its products are tiled and split, the kernels for
-// few rows, and the copies and sums around the products
-// (feed_forward_gemm.hpp).
+// Gated feed-forward: the kernels for few rows, and the copies and sums around
+// the products (feed_forward_gemm.hpp; how those are tiled and split is in
+// feed_forward_plan.hpp).
 //
 //   g | u = x W_in^T,  h = act(g) u,  y = h W_out^T (+ residual)
 //
@@ -15,8 +15,6 @@
 // their own, sqrt(2) times the latter alone. Training keeps g and u in fp32
 // (8 bytes a hidden unit and row): rounded, they would put two more roundings
 // into every gradient.
-#include <cmath>
-
 #include "attention_common.hpp"
 #include "feed_forward_gemm.hpp"
 
@@ -269,47 +267,6 @@ hipError_t join(int op, const FeedArgs& a, hipStream_t st) {
 }
 
 }  // namespace
-
-double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
-  const double rows = p.tile == kTileBig ? 256 : 128, cols = op == kFeedIn ? rows / 2 : rows;
-  return std::ceil((double)M / rows) * std::ceil((double)N / cols);
-}
-
-// The tile and the split with the shortest expected time: rounds of the
-// workgroups that the device holds, times steps, plus the results' way out and
-// the partial products' way through memory. dh reads and writes 16 bytes
-// a result there (fp32; 12 in bf16), which two workgroups a compute unit hide
-// better than one: 32000 x 2816 bf16 422 us in small tiles and 450 in large
-// ones, 19334 x 1368 fp32 356 and 501; without that traffic large ones win
-// (dx of the same in bf16: 411 and 480 us). The constants are fitted to such
-// pairs: a step and a tile's results for each tile, 8 us for the launch that
-// adds up and 4 MB/us for the partial products (2 rows, 1424 x 2456 fp32
-// training: 286 us with the first products undivided, 141 divided; 799 rows,
-// 1032 x 624: 304 and 199).
-FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus) {
-  FeedPlan best{kTileSmall, 1};
-  double least = 0.0;
-  for (int tile : {kTileSmall, kTileBig, kTileDeep}) {
-    FeedPlan p{tile, 1};
-    const bool big = tile == kTileBig;
-    const double tiles = feed_tiles(p, M, N, op), resident = tile == kTileSmall ? 2.0 * cus : cus;
-    // us of a step, with all workgroups that the device holds at work, and of a tile's results
-    const double step = bf16_storage ? (big ? 2.0 : tile == kTileDeep ? 0.8 : 1.3) : (big ? 7.6 : tile == kTileDeep ? 2.6 : 3.9);
-    const double results = big ? (op == kFeedDh ? 90.0 : 12.0) : 6.0;
-    for (int want = 1; want <= 32 && want <= steps; ++want) {
-      const int each = (steps + want - 1) / want;
-      p.splits = (steps + each - 1) / each;
-      if (p.splits != want) continue;
-      double us = std::ceil(tiles * want / resident) * (each * step + results);
-      if (want > 1) us += 8.0 + (double)want * M * N * (op == kFeedIn ? 16.0 : 8.0) / 4e6;
-      if (least == 0.0 || us < least) {
-        least = us;
-        best = p;
-      }
-    }
-  }
-  return best;
-}
 
 // A workgroup of the second product reads all hidden values (F of each row)
 // beside its 16 rows of weights: with more than 16 rows that is what bounds it,

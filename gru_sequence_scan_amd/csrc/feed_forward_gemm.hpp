@@ -547,7 +547,8 @@ __global__ __launch_bounds__(FeedTile<TILE>::kThreads, 2) void feed_kernel(FeedA
     if (i < T::kAhead - 1 && sb.ready(a, tiles_m, tiles_n, items)) sb.fetch(a, lds);
   }
   step_barrier<0>();
-  constexpr int kLater = T::kTimes * (2 * T::kAhead - 3);
+  constexpr int kLater = T::kTimes * feed_later(T::kAhead, true, true, true, 0);
+  static_assert(T::kAhead == 2 || T::kAhead == 4, "the waits of the last steps are written for these");
   int slot = 0;
   for (int id = mine; id < items; id += grid) {
     const FeedItem w = feed_item<TILE, OP>(a, tiles_m, tiles_n, id);
@@ -617,18 +618,16 @@ __global__ __launch_bounds__(FeedTile<TILE>::kThreads, 2) void feed_kernel(FeedA
         slot = slot + 2 < T::kSlots ? slot + 2 : slot + 2 - T::kSlots;
       }
       if (kt < w.k1) {
-        // Loads that are newer than the next step's: those of the steps behind
-        // it, where all of them are counted.
-        const bool end = sa.id >= items && sb.id >= items;
-        const bool counted = sa.id < items && sb.id < items && sa.whole(a) && sb.whole(a);
-        if (sb.id < items) sb.fetch(a, lds);
-        if (sa.id < items) sa.fetch(a, lds);
+        // a step that goes through registers, or one of the workgroup's last
+        const bool more_a = sa.id < items, more_b = sb.id < items;
+        const bool direct = (!more_a || sa.whole(a)) && (!more_b || sb.whole(a));
+        if (more_b) sb.fetch(a, lds);
+        if (more_a) sa.fetch(a, lds);
         multiply(std::false_type{});
-        if (counted)
-          step_barrier<kLater>();
-        else if (T::kAhead > 2 && end && w.k1 - 2 - kt >= 2)
+        const int later = feed_later(T::kAhead, more_a, more_b, direct, w.k1 - 1 - kt);
+        if (T::kAhead > 2 && later == 4)
           step_barrier<(T::kAhead > 2 ? 4 * T::kTimes : 0)>();
-        else if (T::kAhead > 2 && end && w.k1 - 2 - kt == 1)
+        else if (T::kAhead > 2 && later == 2)
           step_barrier<(T::kAhead > 2 ? 2 * T::kTimes : 0)>();
         else
           step_barrier<0>();

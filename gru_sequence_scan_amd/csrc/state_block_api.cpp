@@ -179,23 +179,17 @@ int validate(const RnnFeedForwardDesc* d) {
   return RNN_OK;
 }
 
-struct FeedSizes {
-  int64_t m;                       // elements of 16 bytes
-  int Np, Fm, Op, Fp;              // N, F and N_out in whole 16 bytes; F in whole steps of 128 bytes
-  bool pack_x, pack_in, pack_out, pack_dy;
-  explicit FeedSizes(const RnnFeedForwardDesc* d) {
-    m = 16 / (int64_t)esize_of(d->dtype);
-    auto up = [](int64_t v, int64_t to) { return (int)((v + to - 1) / to * to); };
-    Np = up(d->N, m);
-    Fm = up(d->F, m);
-    Op = up(d->N_out, m);
-    Fp = up(d->F, 8 * m);
-    pack_x = !d->aligned || d->N % m || d->x_ld % m || d->x_ld > kFeedMostWidth;
-    pack_in = !d->aligned || d->N % m || d->in_ld % m || d->in_ld > kFeedMostWidth;
-    pack_out = !d->aligned || d->F % m || d->out_ld % m || d->out_ld > kFeedMostWidth;
-    pack_dy = !d->aligned || d->N_out % m;
+FeedSizes feed_sizes(const RnnFeedForwardDesc* d) { return FeedSizes(d->dtype == RNN_DTYPE_BF16, d->rows, d->N, d->F, d->N_out); }
+
+// Operands that the tiled kernels cannot take as they are.
+struct FeedCopies {
+  bool x, in, out, dy;
+  FeedCopies(const RnnFeedForwardDesc* d, const FeedSizes& s) {
+    x = !d->aligned || d->N % s.m || d->x_ld % s.m || d->x_ld > kFeedMostWidth;
+    in = !d->aligned || d->N % s.m || d->in_ld % s.m || d->in_ld > kFeedMostWidth;
+    out = !d->aligned || d->F % s.m || d->out_ld % s.m || d->out_ld > kFeedMostWidth;
+    dy = !d->aligned || d->N_out % s.m;
   }
-  int steps(int64_t k) const { return (int)((k + 8 * m - 1) / (8 * m)); }
 };
 
 bool feed_few(const RnnFeedForwardDesc* d) { return d->rows <= kFeedFewRows; }
@@ -214,21 +208,12 @@ struct FeedSpace {
   size_t x, in, out, dy, h, dp, part, bytes;
 };
 
-FeedPlan feed_plan_of(const RnnFeedForwardDesc* d, const FeedSizes& s, int op) {
-  switch (op) {
-    case kFeedIn: return feed_plan(op, d->rows, s.Fp, s.steps(s.Np), d->dtype == RNN_DTYPE_BF16, kPlanCus);
-    case kFeedOut: return feed_plan(op, d->rows, d->N_out, s.steps(s.Fm), d->dtype == RNN_DTYPE_BF16, kPlanCus);
-    case kFeedDh: return feed_plan(op, d->rows, s.Fp, s.steps(s.Op), d->dtype == RNN_DTYPE_BF16, kPlanCus);
-    case kFeedDx: return feed_plan(op, d->rows, d->N, s.steps(2 * (int64_t)s.Fp), d->dtype == RNN_DTYPE_BF16, kPlanCus);
-    case kFeedDwIn: return feed_plan(op, 2 * (int64_t)s.Fp, d->N, s.steps(d->rows), d->dtype == RNN_DTYPE_BF16, kPlanCus);
-    default: return feed_plan(op, d->N_out, d->F, s.steps(d->rows), d->dtype == RNN_DTYPE_BF16, kPlanCus);
-  }
-}
 size_t feed_part(const FeedPlan& p, size_t M, size_t N) { return p.splits > 1 ? p.splits * M * N * sizeof(float) : 0; }
 
 // The forward (serving or training) or the backward pass.
 FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
-  const FeedSizes s(d);
+  const FeedSizes s = feed_sizes(d);
+  const FeedCopies copy(d, s);
   const size_t e = (size_t)esize_of(d->dtype), rows = (size_t)d->rows;
   Layout l;
   FeedSpace a{};
@@ -239,24 +224,24 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
     a.bytes = l.bytes;
     return a;
   }
-  if (s.pack_x) a.x = l.take(rows * s.Np * e);
-  if (s.pack_in) a.in = l.take(2 * (size_t)d->F * s.Np * e);
-  if (s.pack_out) a.out = l.take((size_t)d->N_out * s.Fm * e);
+  if (copy.x) a.x = l.take(rows * s.Np * e);
+  if (copy.in) a.in = l.take(2 * (size_t)d->F * s.Np * e);
+  if (copy.out) a.out = l.take((size_t)d->N_out * s.Fm * e);
   size_t part = 0;
   if (back) {
-    if (s.pack_dy) a.dy = l.take(rows * s.Op * e);
+    if (copy.dy) a.dy = l.take(rows * s.Op * e);
     a.dp = l.take(rows * 2 * s.Fp * e);
-    part = feed_part(feed_plan_of(d, s, kFeedDx), rows, d->N);
-    const size_t dh = feed_part(feed_plan_of(d, s, kFeedDh), rows, s.Fp);
+    part = feed_part(s.plan(kFeedDx, kPlanCus), rows, d->N);
+    const size_t dh = feed_part(s.plan(kFeedDh, kPlanCus), rows, s.Fp);
     if (part < dh) part = dh;
-    const size_t in = feed_part(feed_plan_of(d, s, kFeedDwIn), 2 * (size_t)s.Fp, d->N);
-    const size_t out = feed_part(feed_plan_of(d, s, kFeedDwOut), d->N_out, d->F);
+    const size_t in = feed_part(s.plan(kFeedDwIn, kPlanCus), 2 * (size_t)s.Fp, d->N);
+    const size_t out = feed_part(s.plan(kFeedDwOut, kPlanCus), d->N_out, d->F);
     if (part < in) part = in;
     if (part < out) part = out;
   } else {
     if (!train) a.h = l.take(rows * s.Fp * e);
-    part = feed_part(feed_plan_of(d, s, kFeedOut), rows, d->N_out);
-    const size_t in = feed_part(feed_plan_of(d, s, kFeedIn), rows, 2 * (size_t)s.Fp);
+    part = feed_part(s.plan(kFeedOut, kPlanCus), rows, d->N_out);
+    const size_t in = feed_part(s.plan(kFeedIn, kPlanCus), rows, 2 * (size_t)s.Fp);
     if (part < in) part = in;
   }
   a.part = l.take(part);
@@ -265,9 +250,9 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
 }
 
 // g and u, then h.
-size_t feed_gu_bytes(const RnnFeedForwardDesc* d) { return (size_t)d->rows * 2 * FeedSizes(d).Fp * sizeof(float); }
+size_t feed_gu_bytes(const RnnFeedForwardDesc* d) { return (size_t)d->rows * 2 * feed_sizes(d).Fp * sizeof(float); }
 size_t feed_reserve(const RnnFeedForwardDesc* d) {
-  return feed_gu_bytes(d) + round16((size_t)d->rows * FeedSizes(d).Fp * esize_of(d->dtype));
+  return feed_gu_bytes(d) + round16((size_t)d->rows * feed_sizes(d).Fp * esize_of(d->dtype));
 }
 
 // Operands as the kernels take them; those that they cannot take as they are
@@ -310,7 +295,8 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   RETURN_IF_BAD(need_memory(ws, ws_bytes, at.bytes));
   int xcds;
   RETURN_IF_BAD(on_device(&xcds));
-  const FeedSizes s(d);
+  const FeedSizes s = feed_sizes(d);
+  const FeedCopies copy(d, s);
   const bool bf = d->dtype == RNN_DTYPE_BF16;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   char* mem = static_cast<char*>(ws);
@@ -322,13 +308,13 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
     f.h = mem + at.h; f.Fp = s.Fp; f.y = io->y;
     f.part = reinterpret_cast<float*>(mem + at.part);
     f.splits = feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
-    f.vec = !s.pack_x && !s.pack_in && !s.pack_out;
+    f.vec = !copy.x && !copy.in && !copy.out;
     return hip_status(launch_feed_few(f, bf, st));
   }
   FeedPacks packs;
-  const FeedOperand x = packs.add(io->x, d->x_ld, s.pack_x, d->rows, d->N, s.Np, mem + at.x);
-  const FeedOperand in = packs.add(io->w_in, d->in_ld, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
-  const FeedOperand out = packs.add(io->w_out, d->out_ld, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out);
+  const FeedOperand x = packs.add(io->x, d->x_ld, copy.x, d->rows, d->N, s.Np, mem + at.x);
+  const FeedOperand in = packs.add(io->w_in, d->in_ld, copy.in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
+  const FeedOperand out = packs.add(io->w_out, d->out_ld, copy.out, d->N_out, d->F, s.Fm, mem + at.out);
   RETURN_IF_HIP(packs.launch(bf, st));
   void* h = reserve ? static_cast<char*>(reserve) + feed_gu_bytes(d) : mem + at.h;
   auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
@@ -339,7 +325,7 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   a.B = in.p; a.ldb = in.ld; a.KB = s.Np;
   a.steps = s.steps(s.Np);
   a.out = h; a.ldo = s.Fp; a.gu = static_cast<float*>(reserve);
-  FeedPlan p = feed_plan_of(d, s, kFeedIn);
+  FeedPlan p = s.plan(kFeedIn, kPlanCus);
   a.splits = p.splits; a.part = reinterpret_cast<float*>(mem + at.part);
   RETURN_IF_HIP(launch(kFeedIn, a, p, st));
   a.N = d->N_out;
@@ -348,21 +334,22 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   a.steps = s.steps(s.Fm);
   a.out = io->y; a.ldo = d->N_out; a.gu = nullptr;
   a.residual = io->residual; a.ldr = io->residual ? d->residual_ld : 0;
-  p = feed_plan_of(d, s, kFeedOut);
+  p = s.plan(kFeedOut, kPlanCus);
   a.splits = p.splits;
   return hip_status(launch(kFeedOut, a, p, st));
 }
 
 int feed_backward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, const RnnFeedForwardGrads* g, const void* reserve,
                   char* mem, const FeedSpace& at, hipStream_t st) {
-  const FeedSizes s(d);
+  const FeedSizes s = feed_sizes(d);
+  const FeedCopies copy(d, s);
   const bool bf = d->dtype == RNN_DTYPE_BF16;
   const int rows = (int)d->rows;
   FeedPacks packs;
-  const FeedOperand x = packs.add(io->x, d->x_ld, s.pack_x, d->rows, d->N, s.Np, mem + at.x);
-  const FeedOperand in = packs.add(io->w_in, d->in_ld, s.pack_in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
-  const FeedOperand out = packs.add(io->w_out, d->out_ld, s.pack_out, d->N_out, d->F, s.Fm, mem + at.out);
-  const FeedOperand dy = packs.add(g->dy, d->N_out, s.pack_dy, d->rows, d->N_out, s.Op, mem + at.dy);
+  const FeedOperand x = packs.add(io->x, d->x_ld, copy.x, d->rows, d->N, s.Np, mem + at.x);
+  const FeedOperand in = packs.add(io->w_in, d->in_ld, copy.in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
+  const FeedOperand out = packs.add(io->w_out, d->out_ld, copy.out, d->N_out, d->F, s.Fm, mem + at.out);
+  const FeedOperand dy = packs.add(g->dy, d->N_out, copy.dy, d->rows, d->N_out, s.Op, mem + at.dy);
   RETURN_IF_HIP(packs.launch(bf, st));
   auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
   void* dp = mem + at.dp;
@@ -371,7 +358,7 @@ int feed_backward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, const
   base.F = d->F; base.Fp = s.Fp; base.act = d->activation;
   base.part = reinterpret_cast<float*>(mem + at.part);
   auto run = [&](int op, FeedArgs& a) {
-    const FeedPlan p = feed_plan_of(d, s, op);
+    const FeedPlan p = s.plan(op, kPlanCus);
     a.splits = p.splits;
     return launch(op, a, p, st);
   };

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "block_kernels.hpp"
+#include "feed_forward_plan.hpp"
 
 namespace rnnk {
 
@@ -75,10 +76,6 @@ hipError_t launch_selective_scan(SelectiveScanArgs a, bool bf16_storage, hipStre
 hipError_t launch_selective_scan_backward(SelectiveScanArgs a, bool bf16_storage, hipStream_t stream);
 
 // Gated feed-forward (feed_forward.hip and its instances).
-// A product's output is [M, N]; its operands are given by rows of the summed
-// dimension's neighbours ("along": [M, K]) or by rows of the outputs'
-// neighbours ("across": [K, M]).
-enum FeedOp { kFeedIn, kFeedOut, kFeedDh, kFeedDx, kFeedDwIn, kFeedDwOut, kFeedOps };
 struct FeedArgs {
   int M, N;                         // the output's rows and columns, padding of F included
   const void* A; int64_t lda; int KA;  // KA: how far the operand goes along the summed dimension
@@ -94,14 +91,6 @@ struct FeedArgs {
   int rows_split;                   // output rows from here on (padded) belong after the first F; 0: one block of rows
   float* part; int splits;          // splits > 1: partial products [splits, M, N] (kFeedIn: 2 Fp for N)
 };
-// Tile and split of one product.
-enum FeedTileKind { kTileSmall, kTileBig, kTileDeep };  // 128 x 128, 256 x 256, 128 x 128 with more loads in flight
-struct FeedPlan {
-  int tile;
-  int splits;
-};
-FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus);
-double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op);
 hipError_t launch_feed_f32(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
 hipError_t launch_feed_bf16(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
 // Few rows: both projections and the activation, then the projection back.
