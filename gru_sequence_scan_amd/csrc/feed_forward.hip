@@ -40,39 +40,105 @@ __device__ __forceinline__ void store4(DT* p, const f32x4& v, int n) {
     if (r < n) p[r] = from_f32<DT>(v[r]);
 }
 
+// Eight elements of a row of K from `col` on, zeros behind its end. Rows may
+// begin at any element: they are read 16 bytes a load all the same, which
+// global memory takes at any address, and nothing about a load is conditional:
+// what would pass the row's end is read so that it stops there, and moved down
+// where it is used. One row, 1024 x 2816: 11.4 us of both products in bf16 and
+// 18.0 in fp32; 1024 x 2815, whose rows of W_out begin anywhere: 16.7 and 18.5
+// (36 and 41 with one element a load, and every operand read so where one of
+// them was not aligned); 64 rows, 2047 x 8191, fp32: 136 (215; 127 at 2048 x 8192).
+template <typename DT>
+struct FewChunk {
+  static constexpr int E = 16 / (int)sizeof(DT), kLoads = 8 / E;
+  struct __attribute__((packed, aligned(sizeof(DT)))) Any {
+    u32x4 v;
+  };
+  u32x4 r[kLoads];
+  __device__ __forceinline__ void load(const DT* row, int col, int K) {
+    if (K < E) {  // a row of less than 16 bytes
+#pragma unroll
+      for (int h = 0; h < kLoads; ++h) {
+        DT v[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) v[j] = col + h * E + j < K ? row[col + h * E + j] : (DT)0.f;
+        __builtin_memcpy(&r[h], v, 16);
+      }
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < kLoads; ++h) {
+      const int c = col + h * E;
+      r[h] = reinterpret_cast<const Any*>(row + (c + E <= K ? c : K - E))->v;
+    }
+  }
+  __device__ __forceinline__ void end(int col, int K) {
+    if (K < E) return;
+#pragma unroll
+    for (int h = 0; h < kLoads; ++h) {
+      const int over = col + (h + 1) * E - K, by = over < 0 ? 0 : over < E ? over : E;  // elements that are not the row's
+      u32x4 v = r[h];
+      if constexpr (sizeof(DT) == 2) {
+        if (by & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+      }
+      constexpr int kOne = 4 / (int)sizeof(DT);  // elements of a word
+      if (by & kOne) v = u32x4{v[1], v[2], v[3], 0u};
+      if (by & 2 * kOne) v = u32x4{v[2], v[3], 0u, 0u};
+      if (by & 4 * kOne) v = u32x4{0u, 0u, 0u, 0u};
+      r[h] = v;
+    }
+  }
+  __device__ __forceinline__ Frag<DT> frag() const {
+    Frag<DT> f;
+    __builtin_memcpy(&f.v, r, sizeof(r));
+    return f;
+  }
+};
+
 // acc[w][t] = the weights' rows (w of 16 each) times 16 rows of x (t), over
 // this wave's share of the steps [first, steps) of 32.
 template <typename DT, int NW, int MT, int WAVES, int DEEP>
 __device__ __forceinline__ void few_product(f32x4 (&acc)[NW][MT], const DT* (&wrow)[NW], const DT* (&xrow)[MT], int K, int KX,
-                                            bool wvec, bool xvec, int first, int steps, int wave, int group) {
+                                            int first, int steps, int wave, int group) {
 #pragma unroll
   for (int w = 0; w < NW; ++w)
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[w][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int s0 = first + wave; s0 < steps; s0 += WAVES * DEEP) {
-    Frag<DT> fw[DEEP][NW], fx[DEEP][MT];
+    FewChunk<DT> fw[DEEP][NW], fx[DEEP][MT];
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
-      const int step = s0 + d * WAVES;
-      const int col = step < steps ? step * 32 + 8 * group : K > KX ? K : KX;  // past the end: zeros
+      const int step = s0 + d * WAVES, col = step * 32 + 8 * group;
+      if (step >= steps) break;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) fw[d][w] = load8<DT, false>(wrow[w], col, K, wvec);
+      for (int w = 0; w < NW; ++w) fw[d][w].load(wrow[w], col, K);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) fx[d][t] = load8<DT, false>(xrow[t], col, KX, xvec);
+      for (int t = 0; t < MT; ++t) fx[d][t].load(xrow[t], col, KX);
     }
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d)
+    for (int d = 0; d < DEEP; ++d) {
+      const int step = s0 + d * WAVES, col = step * 32 + 8 * group;
+      if (step >= steps) break;
+      if (step * 32 + 32 > K) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) fw[d][w].end(col, K);
+      }
+      if (step * 32 + 32 > KX) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) fx[d][t].end(col, KX);
+      }
 #pragma unroll
       for (int w = 0; w < NW; ++w)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[w][t] = mma(fw[d][w], fx[d][t], acc[w][t]);
+        for (int t = 0; t < MT; ++t) acc[w][t] = mma(fw[d][w].frag(), fx[d][t].frag(), acc[w][t]);
+    }
   }
 }
 
 template <typename DT, int MT>
 __global__ __launch_bounds__(kInWaves * 64) void feed_few_in_kernel(FeedFewArgs a) {
   __shared__ f32x4 sums[kInWaves][2 * MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, group = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, group = lane >> 4;
   const int f0 = blockIdx.x * 16;
   const DT *wrow[2], *xrow[MT];
   const int f = f0 + i < a.F ? f0 + i : a.F - 1;
@@ -84,7 +150,7 @@ __global__ __launch_bounds__(kInWaves * 64) void feed_few_in_kernel(FeedFewArgs 
     xrow[t] = (const DT*)a.x + m * a.ldx;
   }
   f32x4 acc[2][MT];
-  few_product<DT, 2, MT, kInWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.n, a.n, a.vec, a.vec, 0, (a.n + 31) / 32, wave, group);
+  few_product<DT, 2, MT, kInWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.n, a.n, 0, (a.n + 31) / 32, wave, group);
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     sums[wave][t][lane] = acc[0][t];
@@ -108,7 +174,7 @@ __global__ __launch_bounds__(kInWaves * 64) void feed_few_in_kernel(FeedFewArgs 
 template <typename DT, int MT>
 __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArgs a) {
   __shared__ f32x4 sums[kOutWaves][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, group = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, group = lane >> 4;
   const int n0 = blockIdx.x * 16;
   const int steps = (a.F + 31) / 32, each = (steps + a.splits - 1) / a.splits, first = blockIdx.y * each;
   const DT *wrow[1], *xrow[MT];
@@ -119,7 +185,7 @@ __global__ __launch_bounds__(kOutWaves * 64) void feed_few_out_kernel(FeedFewArg
     xrow[t] = (const DT*)a.h + (int64_t)m * a.Fp;
   }
   f32x4 acc[1][MT];
-  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, a.vec, true, first,
+  few_product<DT, 1, MT, kOutWaves, MT <= 2 ? 4 : 2>(acc, wrow, xrow, a.F, a.Fp, first,
                                                      steps - first < each ? steps : first + each, wave, group);
 #pragma unroll
   for (int t = 0; t < MT; ++t) sums[wave][t][lane] = acc[0][t];

@@ -308,7 +308,6 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
     f.h = mem + at.h; f.Fp = s.Fp; f.y = io->y;
     f.part = reinterpret_cast<float*>(mem + at.part);
     f.splits = feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
-    f.vec = !copy.x && !copy.in && !copy.out;
     return hip_status(launch_feed_few(f, bf, st));
   }
   FeedPacks packs;

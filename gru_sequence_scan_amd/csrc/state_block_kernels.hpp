@@ -105,7 +105,6 @@ struct FeedFewArgs {
   int Fp;
   void* y;
   float* part; int splits;          // splits > 1: partial second products [splits, rows, n_out] (workspace)
-  int vec;                          // rows take 16-byte accesses
 };
 int feed_few_splits(int64_t rows, int F, int n_out, int cus);
 hipError_t launch_feed_few(const FeedFewArgs& a, bool bf16_storage, hipStream_t stream);

@@ -96,6 +96,34 @@ def test_places(rows, place, kind, dtype):
     _check(_case(rows, 72, 136, 88, dtype, 3), kind, place, what=place)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("n,F", [(64, 96), (63, 97), (33, 6), (3, 2), (72, 39), (5, 260)])
+@pytest.mark.parametrize("rows", [1, 17, 64])
+def test_few_rows_at_any_address(rows, n, F, dtype):
+    """Few rows read each operand 16 bytes at a time wherever it begins: every
+    one alone off its alignment, rows of any length, with what lies around
+    them not a number, and the same bits as from aligned tensors."""
+    log(f"feed_forward any address rows {rows} n {n} F {F} {dtype}")
+    c = _case(rows, n, F, 24, dtype, rows + n * F)
+
+    def off(t, by):
+        wide = torch.full((t.shape[0] * (t.shape[1] + 5) + 16,), float("nan"), dtype=dtype, device="cuda")
+        out = wide[by:by + t.shape[0] * (t.shape[1] + 5)].view(t.shape[0], -1)[:, :t.shape[1]]
+        out.copy_(t)
+        return out
+
+    x, w_in, w_out = (c[k].cuda() for k in ("x", "w_in", "w_out"))
+    y = gss.feed_forward(x, w_in, w_out)
+    v = {k: f64(t) for k, t in c.items()}
+    from oracle.state_block import activation
+    extra = 0.0 if dtype == torch.float32 else _bounds(v["x"], v["w_in"], v["w_out"], v["dy"], "silu", activation)[0]
+    assert_near(y, oracle.feed_forward(v["x"], v["w_in"], v["w_out"]), dtype, "y", extra)
+    for by in (0, 1, 2, 3, 7):
+        for args in ((off(x, by), w_in, w_out), (x, off(w_in, by), w_out), (x, w_in, off(w_out, by)),
+                     (off(x, by), off(w_in, by + 1), off(w_out, by + 2))):
+            assert torch.equal(gss.feed_forward(*args), y), by
+
+
 def _torch_act(g, kind):
     if kind == "gelu_tanh":
         c = (2 / np.pi) ** 0.5
