@@ -181,15 +181,24 @@ int validate(const RnnFeedForwardDesc* d) {
 
 FeedSizes feed_sizes(const RnnFeedForwardDesc* d) { return FeedSizes(d->dtype == RNN_DTYPE_BF16, d->rows, d->N, d->F, d->N_out); }
 
-// Operands that the tiled kernels cannot take as they are.
+// Operands that the tiled kernels cannot take as they are, and that are copied.
 struct FeedCopies {
   bool x, in, out, dy;
+  // those that may have to be, as far as the descriptor tells: what the workspace has room for
   FeedCopies(const RnnFeedForwardDesc* d, const FeedSizes& s) {
-    x = !d->aligned || d->N % s.m || d->x_ld % s.m || d->x_ld > kFeedMostWidth;
-    in = !d->aligned || d->N % s.m || d->in_ld % s.m || d->in_ld > kFeedMostWidth;
-    out = !d->aligned || d->F % s.m || d->out_ld % s.m || d->out_ld > kFeedMostWidth;
-    dy = !d->aligned || d->N_out % s.m;
+    x = !d->aligned || rows_off(s, d->N, d->x_ld);
+    in = !d->aligned || rows_off(s, d->N, d->in_ld);
+    out = !d->aligned || rows_off(s, d->F, d->out_ld);
+    dy = !d->aligned || rows_off(s, d->N_out, d->N_out);
   }
+  // those that have to be, each by itself
+  FeedCopies(const RnnFeedForwardDesc* d, const FeedSizes& s, const RnnFeedForwardIO* io, const void* up) {
+    x = !aligned(io->x, 16) || rows_off(s, d->N, d->x_ld);
+    in = !aligned(io->w_in, 16) || rows_off(s, d->N, d->in_ld);
+    out = !aligned(io->w_out, 16) || rows_off(s, d->F, d->out_ld);
+    dy = !aligned(up, 16) || rows_off(s, d->N_out, d->N_out);
+  }
+  static bool rows_off(const FeedSizes& s, int64_t n, int64_t ld) { return n % s.m || ld % s.m || ld > kFeedMostWidth; }
 };
 
 bool feed_few(const RnnFeedForwardDesc* d) { return d->rows <= kFeedFewRows; }
@@ -296,7 +305,7 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   int xcds;
   RETURN_IF_BAD(on_device(&xcds));
   const FeedSizes s = feed_sizes(d);
-  const FeedCopies copy(d, s);
+  const FeedCopies copy(d, s, io, nullptr);
   const bool bf = d->dtype == RNN_DTYPE_BF16;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   char* mem = static_cast<char*>(ws);
@@ -341,7 +350,7 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
 int feed_backward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, const RnnFeedForwardGrads* g, const void* reserve,
                   char* mem, const FeedSpace& at, hipStream_t st) {
   const FeedSizes s = feed_sizes(d);
-  const FeedCopies copy(d, s);
+  const FeedCopies copy(d, s, io, g->dy);
   const bool bf = d->dtype == RNN_DTYPE_BF16;
   const int rows = (int)d->rows;
   FeedPacks packs;

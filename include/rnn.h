@@ -728,9 +728,11 @@ typedef struct RnnFeedForwardDesc {
   int64_t rows;          /* >= 1                                               */
   int32_t N, F, N_out;   /* widths of x, h and y, >= 1                         */
   int32_t aligned;       /* 1: x, w_in, w_out and dy are multiples of 16 bytes
-                            (else RNN_E_ALIGN). 0: they need not be; they are
-                            copied to the workspace, as are (in either case)
-                            those whose rows are not                           */
+                            (else RNN_E_ALIGN). 0: they need not be; those
+                            that are not are copied to the workspace, which
+                            has room for all, as are (in either case) those
+                            whose rows are no whole 16 bytes, at every call;
+                            up to 64 rows are served without copies          */
   int64_t x_ld;          /* elements between rows of x (>= N)                  */
   int64_t in_ld;         /* ... of w_in (>= N)                                 */
   int64_t out_ld;        /* ... of w_out (>= F)                                */

@@ -124,6 +124,34 @@ def test_few_rows_at_any_address(rows, n, F, dtype):
             assert torch.equal(gss.feed_forward(*args), y), by
 
 
+@pytest.mark.parametrize("which", ["x", "w_in", "w_out", "dy"])
+def test_one_operand_off_its_alignment_copies_no_other(which, monkeypatch):
+    """What is not an operand's copy stays as it was in the workspace: with x
+    alone off its alignment no weight is copied, and so on."""
+    rows, n, F, n_out = 200, 72, 136, 88
+    c = _case(rows, n, F, n_out, torch.bfloat16, 12)
+    put = {k: (shifted if k == which else lambda t: t.cuda())(c[k]) for k in ("x", "w_in", "w_out", "dy")}
+    sizes = {"x": rows * n * 2, "w_in": 2 * F * n * 2, "w_out": n_out * F * 2, "dy": rows * n_out * 2}
+    made = []
+
+    def buffer(size, device):
+        made.append(torch.full((size,), 0xA5, dtype=torch.uint8, device=device))
+        return made[-1]
+
+    monkeypatch.setattr(gss.state_block_ops, "_buffer", buffer)
+    y, ctx = gss.feed_forward_train(put["x"], put["w_in"], put["w_out"])
+    got = (y,) + gss.feed_forward_backward(ctx, put["dy"])
+    forward, _, backward = made
+    monkeypatch.undo()
+    aligned = {k: c[k].cuda() for k in put}
+    y, ctx = gss.feed_forward_train(aligned["x"], aligned["w_in"], aligned["w_out"])
+    assert all(torch.equal(a, b) for a, b in zip(got, (y,) + gss.feed_forward_backward(ctx, aligned["dy"])))
+    for ws, room in ((forward, ("x", "w_in", "w_out")), (backward, ("x", "w_in", "w_out", "dy"))):
+        if ws is forward and which == "dy":
+            continue                                      # nothing is off its alignment there
+        assert int((ws == 0xA5).sum()) >= sum(sizes[k] for k in room if k != which)
+
+
 def _torch_act(g, kind):
     if kind == "gelu_tanh":
         c = (2 / np.pi) ** 0.5
