@@ -167,8 +167,17 @@ __global__ __launch_bounds__(kInWaves * 64) void feed_few_in_kernel(FeedFewArgs 
   const int m = 16 * wave + i, fo = f0 + 4 * group;
   f32x4 h;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) h[r] = fo + r < a.F ? activate(g[r], a.act).act * u[r] : 0.f;
-  if (m < a.rows) store4((DT*)a.h + (int64_t)m * a.Fp + fo, h, a.Fp - fo);
+  for (int r = 0; r < 4; ++r) {
+    if (fo + r >= a.F) g[r] = u[r] = 0.f;
+    h[r] = activate(g[r], a.act).act * u[r];
+  }
+  if (m >= a.rows) return;
+  store4((DT*)a.h + (int64_t)m * a.Fp + fo, h, a.Fp - fo);
+  if (a.gu) {  // F is padded to whole fours
+    float* gu = a.gu + (int64_t)m * 2 * a.Fp + fo;
+    *reinterpret_cast<f32x4*>(gu) = g;
+    *reinterpret_cast<f32x4*>(gu + a.Fp) = u;
+  }
 }
 
 template <typename DT, int MT>

@@ -201,7 +201,15 @@ struct FeedCopies {
   static bool rows_off(const FeedSizes& s, int64_t n, int64_t ld) { return n % s.m || ld % s.m || ld > kFeedMostWidth; }
 };
 
-bool feed_few(const RnnFeedForwardDesc* d) { return d->rows <= kFeedFewRows; }
+// Serving takes the few-row kernels up to 64 rows. So does training forward,
+// but with more than 32 rows for weights up to 2^23 numbers each: 64 rows, 1024
+// x 2816, bf16, with the backward pass 79 us in tiles and 69 so, 2048 x 4096 101
+// and 98, 2048 x 5632 116 and 126; 32 rows, 2048 x 8192, 140 and 135, fp32 329
+// and 290.
+bool feed_few(const RnnFeedForwardDesc* d, bool train) {
+  if (d->rows > kFeedFewRows) return false;
+  return !train || d->rows <= 32 || (int64_t)(d->N > d->N_out ? d->N : d->N_out) * d->F <= 1 << 23;
+}
 
 // Where things lie in a workspace, one after the other.
 struct Layout {
@@ -226,8 +234,8 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
   const size_t e = (size_t)esize_of(d->dtype), rows = (size_t)d->rows;
   Layout l;
   FeedSpace a{};
-  if (!train && !back && feed_few(d)) {  // any alignment is taken there
-    a.h = l.take(rows * s.Fp * e);
+  if (!back && feed_few(d, train)) {  // any alignment is taken there
+    if (!train) a.h = l.take(rows * s.Fp * e);
     const size_t splits = (size_t)feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
     a.part = l.take(splits > 1 ? splits * rows * d->N_out * sizeof(float) : 0);
     a.bytes = l.bytes;
@@ -309,12 +317,13 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   const bool bf = d->dtype == RNN_DTYPE_BF16;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   char* mem = static_cast<char*>(ws);
-  if (!reserve && feed_few(d)) {
+  void* h = reserve ? static_cast<char*>(reserve) + feed_gu_bytes(d) : mem + at.h;
+  if (feed_few(d, reserve != nullptr)) {
     FeedFewArgs f{};
     f.rows = (int)d->rows; f.n = d->N; f.F = d->F; f.n_out = d->N_out; f.act = d->activation;
     f.x = io->x; f.ldx = d->x_ld; f.w_in = io->w_in; f.ld_in = d->in_ld; f.w_out = io->w_out; f.ld_out = d->out_ld;
     f.residual = io->residual; f.ldr = io->residual ? d->residual_ld : 0;
-    f.h = mem + at.h; f.Fp = s.Fp; f.y = io->y;
+    f.h = h; f.Fp = s.Fp; f.gu = static_cast<float*>(reserve); f.y = io->y;
     f.part = reinterpret_cast<float*>(mem + at.part);
     f.splits = feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
     return hip_status(launch_feed_few(f, bf, st));
@@ -324,7 +333,6 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   const FeedOperand in = packs.add(io->w_in, d->in_ld, copy.in, 2 * (int64_t)d->F, d->N, s.Np, mem + at.in);
   const FeedOperand out = packs.add(io->w_out, d->out_ld, copy.out, d->N_out, d->F, s.Fm, mem + at.out);
   RETURN_IF_HIP(packs.launch(bf, st));
-  void* h = reserve ? static_cast<char*>(reserve) + feed_gu_bytes(d) : mem + at.h;
   auto* launch = bf ? launch_feed_bf16 : launch_feed_f32;
   FeedArgs a{};
   a.F = d->F; a.Fp = s.Fp; a.act = d->activation;

@@ -101,8 +101,9 @@ struct FeedFewArgs {
   const void* w_in; int64_t ld_in;
   const void* w_out; int64_t ld_out;
   const void* residual; int64_t ldr;
-  void* h;                          // [rows, Fp] (workspace)
+  void* h;                          // [rows, Fp] (workspace, or kept by training)
   int Fp;
+  float* gu;                        // [rows, 2 Fp] the two projections in fp32, or null
   void* y;
   float* part; int splits;          // splits > 1: partial second products [splits, rows, n_out] (workspace)
 };

@@ -124,6 +124,20 @@ def test_few_rows_at_any_address(rows, n, F, dtype):
             assert torch.equal(gss.feed_forward(*args), y), by
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("rows,n,F,n_out", [(1, 264, 1030, 96), (17, 33, 70, 520), (32, 520, 2056, 130), (33, 200, 1000, 64),
+                                            (64, 130, 97, 7), (40, 2056, 4104, 2056)])
+def test_training_of_few_rows(rows, n, F, n_out, dtype):
+    """Up to 64 rows (up to 32 with large weights: the last case is in tiles)
+    training takes serving's kernels forward and keeps the projections."""
+    log(f"feed_forward few rows training {rows} n {n} F {F} n_out {n_out} {dtype}")
+    c = _case(rows, n, F, n_out, dtype, rows)
+    y = _check(c, "gelu_tanh", what="few")[0]
+    served = gss.feed_forward(*(c[k].cuda() for k in ("x", "w_in", "w_out")), residual=c["r"].cuda(), activation="gelu_tanh")
+    if n < 2000:
+        assert torch.equal(y, served)
+
+
 @pytest.mark.parametrize("which", ["x", "w_in", "w_out", "dy"])
 def test_one_operand_off_its_alignment_copies_no_other(which, monkeypatch):
     """What is not an operand's copy stays as it was in the workspace: with x

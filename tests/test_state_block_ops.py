@@ -406,6 +406,18 @@ def test_feed_sizes():
     assert _feed_size(_FEED_SIZES[2], aligned=0) > _feed_size(_FEED_SIZES[2])
 
 
+def test_training_of_few_rows_copies_nothing_forward():
+    """Nor does it lay out tiles of 128 rows for them: no workspace but the
+    divided sums' (none here)."""
+    for rows in (1, 32, 64):
+        assert _feed_size(_FEED_SIZES[1], rows=rows) == _feed_size(_FEED_SIZES[1], rows=rows, aligned=0, x_ld=65, in_ld=65) == 0
+    assert _feed_size(_FEED_SIZES[1], rows=65, x_ld=65) > _feed_size(_FEED_SIZES[1], rows=65)
+    big = dict(N=2048, N_out=2048, x_ld=2048, in_ld=2048, residual_ld=2048, aligned=0)
+    few, many = dict(big, F=8192, out_ld=8192, rows=32), dict(big, F=8192, out_ld=8192, rows=33)
+    assert _feed_size(_FEED_SIZES[1], **few) < 1 << 24 < _feed_size(_FEED_SIZES[1], **many)     # the weights' copies
+    assert _feed_size(_FEED_SIZES[1], **dict(big, F=4096, out_ld=4096, rows=64)) < 1 << 24
+
+
 def test_feed_pointers():
     L = ops._lib()
     d = _feed(aligned=0)
