@@ -60,6 +60,8 @@ inline FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_sto
   return best;
 }
 
+constexpr int kFeedFewRows = 64;
+
 // The widths as the products see them, and their plans.
 struct FeedSizes {
   int64_t m, rows;     // elements of 16 bytes
@@ -71,6 +73,15 @@ struct FeedSizes {
     Fm = up(F, m);
     Op = up(N_out, m);
     Fp = up(F, 8 * m);
+  }
+  // Serving takes the few-row kernels up to 64 rows. So does training forward,
+  // but with more than 32 rows for weights up to 2^23 numbers each: 64 rows, 1024
+  // x 2816, bf16, with the backward pass 79 us in tiles and 69 so, 2048 x 4096 101
+  // and 98, 2048 x 5632 116 and 126; 32 rows, 2048 x 8192, 140 and 135, fp32 329
+  // and 290.
+  bool few(bool train) const {
+    if (rows > kFeedFewRows) return false;
+    return !train || rows <= 32 || (int64_t)(N > N_out ? N : N_out) * F <= 1 << 23;
   }
   int steps(int64_t k) const { return (int)((k + 8 * m - 1) / (8 * m)); }
   FeedPlan plan(int op, int cus) const {

@@ -201,16 +201,6 @@ struct FeedCopies {
   static bool rows_off(const FeedSizes& s, int64_t n, int64_t ld) { return n % s.m || ld % s.m || ld > kFeedMostWidth; }
 };
 
-// Serving takes the few-row kernels up to 64 rows. So does training forward,
-// but with more than 32 rows for weights up to 2^23 numbers each: 64 rows, 1024
-// x 2816, bf16, with the backward pass 79 us in tiles and 69 so, 2048 x 4096 101
-// and 98, 2048 x 5632 116 and 126; 32 rows, 2048 x 8192, 140 and 135, fp32 329
-// and 290.
-bool feed_few(const RnnFeedForwardDesc* d, bool train) {
-  if (d->rows > kFeedFewRows) return false;
-  return !train || d->rows <= 32 || (int64_t)(d->N > d->N_out ? d->N : d->N_out) * d->F <= 1 << 23;
-}
-
 // Where things lie in a workspace, one after the other.
 struct Layout {
   size_t bytes = 0;
@@ -234,7 +224,7 @@ FeedSpace feed_space(const RnnFeedForwardDesc* d, bool train, bool back) {
   const size_t e = (size_t)esize_of(d->dtype), rows = (size_t)d->rows;
   Layout l;
   FeedSpace a{};
-  if (!back && feed_few(d, train)) {  // any alignment is taken there
+  if (!back && s.few(train)) {  // any alignment is taken there
     if (!train) a.h = l.take(rows * s.Fp * e);
     const size_t splits = (size_t)feed_few_splits(d->rows, d->F, d->N_out, kPlanCus);
     a.part = l.take(splits > 1 ? splits * rows * d->N_out * sizeof(float) : 0);
@@ -318,7 +308,7 @@ int feed_forward(const RnnFeedForwardDesc* d, const RnnFeedForwardIO* io, void* 
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   char* mem = static_cast<char*>(ws);
   void* h = reserve ? static_cast<char*>(reserve) + feed_gu_bytes(d) : mem + at.h;
-  if (feed_few(d, reserve != nullptr)) {
+  if (s.few(reserve != nullptr)) {
     FeedFewArgs f{};
     f.rows = (int)d->rows; f.n = d->N; f.F = d->F; f.n_out = d->N_out; f.act = d->activation;
     f.x = io->x; f.ldx = d->x_ld; f.w_in = io->w_in; f.ld_in = d->in_ld; f.w_out = io->w_out; f.ld_out = d->out_ld;

@@ -94,7 +94,6 @@ struct FeedArgs {
 hipError_t launch_feed_f32(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
 hipError_t launch_feed_bf16(int op, const FeedArgs& a, const FeedPlan& p, hipStream_t stream);
 // Few rows: both projections and the activation, then the projection back.
-constexpr int kFeedFewRows = 64;
 struct FeedFewArgs {
   int rows, n, F, n_out, act;
   const void* x; int64_t ldx;

@@ -81,3 +81,58 @@ int main(int, char** v) {
 def test_no_wait_is_too_short_and_the_last_tile_has_none_too_long(tmp_path, ahead):
     # with two steps ahead the last steps have nothing newer than what comes next
     assert _run(tmp_path, _PACE, ahead).strip() == f"ok 1 1 {1 if ahead == 4 else 0}"
+
+
+# The instance (type, product, tile, divided or not) and the ways out (a tile
+# that is whole, one at an edge) of the products that sizes take; of many random
+# sizes, those that the given ones leave out.
+_COVER = r"""
+#include <random>
+#include <set>
+#include <string>
+std::set<std::string> taken(bool bf, int64_t rows, int N, int F, int N_out) {
+  const char* ops[] = {"in", "out", "dh", "dx", "dw_in", "dw_out"};
+  const char* tiles[] = {"small", "big", "deep"};
+  const FeedSizes s(bf, rows, N, F, N_out);
+  std::set<std::string> all;
+  for (int op = 0; op < kFeedOps; ++op) {
+    if (op <= kFeedOut && s.few(true) && s.few(false)) continue;
+    const FeedPlan p = s.plan(op, 256);
+    const int64_t h = p.tile == kTileBig ? 256 : 128, w = op == kFeedIn ? h / 2 : h;
+    const int64_t M = op == kFeedDwIn ? 2 * (int64_t)s.Fp : op == kFeedDwOut ? N_out : rows;
+    const int64_t last = op == kFeedIn || op == kFeedDh || op == kFeedDwOut ? F : op == kFeedOut ? N_out : N;
+    const std::string name = std::string(bf ? "bf16 " : "f32 ") + ops[op] + " " + tiles[p.tile] + (p.splits > 1 ? " divided" : " undivided");
+    if (M >= h && last >= w) all.insert(name + " whole");
+    if (M % h || last % w) all.insert(name + " edge");
+  }
+  return all;
+}
+int main(int, char** v) {
+  std::set<std::string> have, missing;
+  FILE* f = fopen(v[1], "r");
+  long bf, rows, N, F, N_out;
+  while (fscanf(f, "%ld %ld %ld %ld %ld", &bf, &rows, &N, &F, &N_out) == 5)
+    for (auto& name : taken(bf, rows, N, F, N_out)) have.insert(name);
+  std::mt19937_64 rng(1);
+  auto size = [&](double most) { return (int)exp(std::uniform_real_distribution<>(0, log(most))(rng)); };
+  for (int i = 0; i < 200000; ++i) {
+    const bool b = rng() & 1;
+    const int r = size(70000), n = size(20000), h = size(40000), o = rng() & 1 ? n : size(20000);
+    if ((double)r * n * h > 3e11) continue;
+    for (auto& name : taken(b, r, n, h, o))
+      if (!have.count(name)) missing.insert(name);
+  }
+  for (auto& name : missing) puts(name.c_str());
+  printf("%zu\n", have.size());
+}
+"""
+
+
+def test_the_gpu_tests_take_every_tile_and_split(tmp_path):
+    pytest.importorskip("gru_sequence_scan_amd")
+    from feed_plan_shapes import SHAPES
+    from test_gpu_feed_forward import SIZES
+    sizes = [(t == "bf16",) + tuple(s) for t, *s in SHAPES] + [(bf,) + s for s in SIZES for bf in (False, True)]
+    (tmp_path / "sizes").write_text("".join(" ".join(str(int(v)) for v in s) + "\n" for s in sizes))
+    out = _run(tmp_path, _COVER, tmp_path / "sizes").split("\n")[:-1]
+    assert out[:-1] == [] and int(out[-1]) >= 140
