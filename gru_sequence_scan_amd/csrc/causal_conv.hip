@@ -385,7 +385,7 @@ hipError_t run_width(const CausalConvArgs& a, bool back, hipStream_t st) {
 
 // About four workgroups a compute unit over all channel tiles, fewer where
 // the runs do not fill them.
-int conv_parts(int T, int B, int C, bool bf, int cus) {
+int conv_parts(int T, int B, int C, int cus) {
   const int E = kBackWide, groups = (C + E - 1) / E, lanes = channel_lanes(groups);
   const int64_t tiles = (groups + lanes - 1) / lanes, slots = kConvThreads / lanes;
   const int64_t units = (int64_t)((T + kRun - 1) / kRun) * B;
@@ -394,7 +394,7 @@ int conv_parts(int T, int B, int C, bool bf, int cus) {
   return (int)(parts < 1 ? 1 : parts);
 }
 
-double conv_threads(int T, int B, int C, bool) {
+double conv_threads(int T, int B, int C) {
   const double runs = T <= 8 ? T : (T + kRun - 1) / kRun;
   return runs * B * (double)C + kConvThreads;
 }

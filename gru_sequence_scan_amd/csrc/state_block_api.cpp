@@ -26,13 +26,13 @@ int validate(const RnnCausalConvDesc* d) {
   if (d->activation != RNN_ACT_NONE && d->activation != RNN_ACT_SILU) return RNN_E_UNSUPPORTED;
   if (d->x_t < 0 || d->x_b < 0 || d->T > kMaxGrid - 64) return RNN_E_SHAPE;
   // the forward launch, and the one that adds up the gradients of the filter
-  if (conv_threads(d->T, d->B, d->C, d->dtype == RNN_DTYPE_BF16) > kMaxThreads) return RNN_E_SHAPE;
+  if (conv_threads(d->T, d->B, d->C) > kMaxThreads) return RNN_E_SHAPE;
   if (8.0 * ((double)d->C + 32.0) * (d->W + 1) > kMaxThreads) return RNN_E_SHAPE;
   return RNN_OK;
 }
 
 size_t conv_workspace(const RnnCausalConvDesc* d) {
-  return (size_t)conv_parts(d->T, d->B, d->C, d->dtype == RNN_DTYPE_BF16, kPlanCus) * (d->W + 1) * d->C * sizeof(float);
+  return (size_t)conv_parts(d->T, d->B, d->C, kPlanCus) * (d->W + 1) * d->C * sizeof(float);
 }
 
 int conv_args(const RnnCausalConvDesc* d, const RnnCausalConvIO* io, CausalConvArgs* a) {
@@ -446,7 +446,7 @@ int rnn_causal_conv_backward(const RnnCausalConvDesc* desc, const RnnCausalConvI
   a.dy = grads->dy; a.dstate_n = grads->dstate_n;
   a.dx = grads->dx; a.dw = grads->dweight; a.db = grads->dbias; a.dstate = grads->dstate;
   a.part = static_cast<float*>(workspace);
-  a.parts = conv_parts(desc->T, desc->B, desc->C, desc->dtype == RNN_DTYPE_BF16, kPlanCus);
+  a.parts = conv_parts(desc->T, desc->B, desc->C, kPlanCus);
   for (const void* p : {a.dy, a.dstate_n, (const void*)a.dx, (const void*)a.dstate})
     if (!aligned(p, 16)) a.vec = 0;
   return hip_status(launch_causal_conv_backward(a, desc->dtype == RNN_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)));

@@ -29,9 +29,9 @@ struct CausalConvArgs {
   int wvec;                         // the filters and the bias take 8-byte accesses
 };
 // Workgroups along time and batch of the backward pass, each with one partial sum.
-int conv_parts(int T, int B, int C, bool bf16_storage, int cus);
-// Threads of the longest launch (0: backward is no longer than that).
-double conv_threads(int T, int B, int C, bool bf16_storage);
+int conv_parts(int T, int B, int C, int cus);
+// Threads of the longest launch (backward is no longer than that).
+double conv_threads(int T, int B, int C);
 hipError_t launch_causal_conv(const CausalConvArgs& a, bool bf16_storage, hipStream_t stream);
 hipError_t launch_causal_conv_backward(const CausalConvArgs& a, bool bf16_storage, hipStream_t stream);
 
