@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <initializer_list>
 
 namespace rnnk {
 
