@@ -167,15 +167,14 @@ __global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(sel
   if (a.h_n && live && p.seg == a.segs - 1) store_row<J>(a.h_n + cell * a.N, q * J, a.N, a.svec, h);
 }
 
-// 2^e h + s: a state after a segment. A growing channel's factor (A > 0, or
-// negative steps) can be larger than any fp32 number over a segment's steps,
-// where the walk step by step stays finite: at zero, for one. It goes in three
-// parts then. 381 is the largest exponent that is used: 2^381 takes the
+// 2^e h + s for e > 126: a state after a segment. A growing channel's factor
+// (A > 0, or negative steps) can be larger than any fp32 number over a segment's
+// steps, where the walk step by step stays finite: at zero, for one. It goes in
+// three parts then. 381 is the largest exponent that is used: 2^381 takes the
 // smallest number past the largest.
 __device__ __forceinline__ float sel_past(float e, float h, float s) {
-  const bool far = e > 126.0f;
-  const float f = __builtin_amdgcn_exp2f(far ? __builtin_fminf(e, 381.0f) * (1.0f / 3.0f) : e);
-  return __builtin_fmaf(f, far ? f * (f * h) : h, s);
+  const float f = __builtin_amdgcn_exp2f(__builtin_fminf(e, 381.0f) * (1.0f / 3.0f));
+  return __builtin_fmaf(f, f * (f * h), s);
 }
 
 // The states that enter the segments, one thread per state: in the place of
@@ -201,12 +200,21 @@ __global__ __launch_bounds__(256) void sel_carry_kernel(SelectiveScanArgs a, con
       s[k] = map_s[o * NP];
       d[k] = map_d[o];
     }
+    bool far = false;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (k0 + k < a.segs) {
-        map_s[(back ? a.segs - 1 - (k0 + k) : k0 + k) * cells * NP] = h;
-        h = sel_past(A2 * d[k], h, s[k]);
-      }
+    for (int k = 0; k < kBatch; ++k) far |= A2 * d[k] > 126.0f;
+    auto walk = [&](auto past) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < a.segs) {
+          map_s[(back ? a.segs - 1 - (k0 + k) : k0 + k) * cells * NP] = h;
+          h = past(A2 * d[k], s[k]);
+        }
+    };
+    if (!far)
+      walk([&](float e, float add) { return __builtin_fmaf(__builtin_amdgcn_exp2f(e), h, add); });
+    else
+      walk([&](float e, float add) { return e > 126.0f ? sel_past(e, h, add) : __builtin_fmaf(__builtin_amdgcn_exp2f(e), h, add); });
   }
 }
 
