@@ -16,7 +16,8 @@
 // the row's end reads the last one again, and what is not part of the row is
 // replaced by zero. 1000 steps of 32 x 2048 channels, bf16, 4 taps, SiLU: 54
 // us forward, 4.9 TB/s of the 5.1 that a large copy reaches (88 with loads
-// under conditions).
+// under conditions). With x off its alignment, a channel at a time: 62 us for 47
+// of aligned calls timed the same way, one after the other (backward 131 for 122).
 //
 // Backward computes p again from x, so the forward keeps nothing. It takes
 // four channels a thread (with eight, a run's x, dy and dp leave no registers

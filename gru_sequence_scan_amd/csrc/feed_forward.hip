@@ -27,9 +27,11 @@ namespace {
 // divide the summed dimension, and their sums meet in LDS. The weights are the
 // first operand of the 16x16 instructions and go straight from memory into
 // registers; a result lane holds four neighbouring hidden units of one row.
-// One row, 1024 x 2816, bf16: 5.2 us for g | u (2.2 TB/s of weights) and 6.1
-// for y, most of it the way of one load and of the sums through LDS. 64 rows,
-// 1024 x 4096: 10.2, 7.9 and 3.9 us for adding up the divided sums.
+// One row, 1024 x 2816, bf16: 5.5 us for g | u (2.1 TB/s of weights) and 5.8
+// for y, most of it the way of one load and of the sums through LDS; fp32 9.5
+// and 9.6. 64 rows, 1024 x 4096, bf16: 10.6, 8.6 and 3.9 us for adding up the
+// divided sums, fp32 23.0, 14.7 and 4.0: with four blocks of rows the registers
+// hold two of a wave's steps, so that its four are two trips to memory.
 // ---------------------------------------------------------------------------
 constexpr int kInWaves = 8, kOutWaves = 16;
 

@@ -34,13 +34,19 @@
 // units' matrix cycles): g | u 445, 829, 43% (it writes 0.9 GB of g, u and h);
 // y 213, 868, 43%; dh with dg and du 445 to 496, 390, 17% (1.2 GB read, 0.5
 // written: bound by memory); dx 412, 896, 42%; dW_in 453, 815, 44%; dW_out
-// 235, 786, 43%. What bounds the others is the card's power: at 8192^3 the same kernel
-// takes 976 us on random numbers and 768 on zeros (a library product 793 and
-// 485), alone the loads of dx take 250 us and its products 257. Not faster:
+// 235, 786, 43%. What bounds the others: a step of 256 x 256 in bf16 takes 2060
+// clocks of a compute unit's matrix units and 2050 of its LDS port (196 kB read,
+// 64 kB written, 128 bytes a clock), and a step of y 2.5 us, both and more: the
+// two run largely one after the other, since every step begins behind its barrier
+// with all waves reading. (Alone the loads of dx take 250 us and its products
+// 257.) The card's power is the smaller part: at 8192^3 the same kernel takes
+// 976 us on random numbers and 768 on zeros, a library product 793 and 485; of
+// y's size the library takes 141 us. Not faster:
 // steps of 64 bytes with two workgroups (2408 us for all six against 2200) or
 // with a longer ring (2459), 16 waves, operands through registers, k begun at
 // another place in each workgroup. fp32 at 19334 rows, 512 x 1368: 105 to 121
-// TFLOP/s of 153, dh 80 (bound by memory).
+// TFLOP/s of 153, dh 80 (bound by memory); products of few tiles reach 50 to 80,
+// since whole tiles leave places empty (400 rows, 1024 x 2816: g | u 74 us).
 #pragma once
 
 #include <type_traits>

@@ -30,12 +30,15 @@ inline double feed_tiles(const FeedPlan& p, int64_t M, int64_t N, int op) {
 // the partial products' way through memory. dh reads and writes 16 bytes
 // a result there (fp32; 12 in bf16), which two workgroups a compute unit hide
 // better than one: 32000 x 2816 bf16 422 us in small tiles and 450 in large
-// ones, 19334 x 1368 fp32 356 and 501; without that traffic large ones win
-// (dx of the same in bf16: 411 and 480 us). The constants are fitted to such
+// ones, 19334 x 1368 fp32 356 (now 339) and 501; without that traffic large ones
+// win (dx of the same in bf16: 411 us, 480 in small ones). The constants are fitted to such
 // pairs: a step and a tile's results for each tile, 8 us for the launch that
 // adds up and 4 MB/us for the partial products (2 rows, 1424 x 2456 fp32
 // training: 286 us with the first products undivided, 141 divided; 799 rows,
-// 1032 x 624: 304 and 199).
+// 1032 x 624: 304 and 199). Of all tiles and divisions by up to 16, tried one
+// product at a time in fp32 training, the best were 0 to 12% of the whole pass
+// faster than the plan's (1361 rows, 1376 x 268: 2%; 400 rows, 1024 x 2816: 3%;
+// 700 rows, 534 x 6864: 9%; 3306 rows, 1168 x 160: 12%).
 inline FeedPlan feed_plan(int op, int64_t M, int64_t N, int steps, bool bf16_storage, int cus) {
   FeedPlan best{kTileSmall, 1};
   double least = 0.0;

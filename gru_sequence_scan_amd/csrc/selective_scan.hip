@@ -8,14 +8,16 @@
 // per channel of [T, B, H]; B and C are shared by a group's channels.
 //
 // Bound by the issue of vector instructions: a state's step is an exponential
-// (8.3 clocks of a SIMD for 64 lanes) and four products or sums (2.4 to 3.8
-// each), about 20 clocks, while a channel's step moves 8 bytes in bf16. With
-// what is formed once a channel and step (step length, gate), handed round and
-// summed, a wave issues 33 instructions a step for its 256 states. So the states stay in registers for the
-// whole time, four lanes a channel; the time is walked in tiles of 32 steps,
-// staged through LDS with the next tile's loads in flight, and the scalars of
-// a step are formed by one lane in four, 16 steps at once. T 1000, 32 x 1024
-// x 16, bf16, with gate: 165 us; the exponentials and products alone need 68.
+// (3.5 ns of a SIMD for 64 lanes) and four products or sums (1.75 ns each,
+// however many waves there are): 10.1 ns together in a loop of nothing else,
+// while a channel's step moves 8 bytes in bf16. With what is formed once a
+// channel and step (step length, gate), handed round and summed, a wave issues
+// 33 instructions a step for its 256 states. So the states stay in registers
+// for the whole time, four lanes a channel; the time is walked in tiles of 32
+// steps, staged through LDS with the next tile's loads in flight, and the
+// scalars of a step are formed by one lane in four, 16 steps at once. T 1000,
+// 32 x 1024 x 16, bf16, with gate: 167 us, of which its instructions take 130;
+// the states' own exponentials and products alone need 81.
 //
 // Where that gives few workgroups the time is cut into segments: a first
 // launch finds what each adds to the state and the sum of its steps (its
@@ -324,11 +326,18 @@ hipError_t launch_sel_carry(const SelectiveScanArgs& a, const float* first, int 
 // The time is cut where that is expected to be faster: into segments of whole
 // 64 steps, up to as many workgroups a compute unit as fit. A step of the walk
 // takes 119 ns (N = 16) with one workgroup a compute unit, 190 with two and
-// 350 with four (a SIMD issues an instruction of one wave every 7.5 clocks, of
-// two every 3.8); in the launch that composes a segment 88, 137 and 255; the
-// two launches more cost about 12 us and 0.1 a segment. T = 2048, 4 x 1024
-// channels: 226 us in one piece, 46 + 34 + 5 in 16 segments; T = 16384, 1 x 64
-// channels: 12 + 10 + 28 us in 256 segments, 18 + 14 + 15 in 128.
+// 350 with four (more waves fill each other's waits); in the launch that
+// composes a segment 88, 137 and 255; the two launches more cost about 12 us
+// and 0.1 a segment. T = 2048, 4 x 1024 channels: 226 us in one piece, 46 + 34 +
+// 5 in 16 segments; T = 16384, 1 x 64 channels: 12 + 10 + 28 us in 256 segments,
+// 18 + 14 + 15 in 128. The backward pass takes the same cut, which gains it as
+// much (all of a pass in bf16 with gate, forward + backward, us):
+//   T, rows x channels x N    one piece     4         8         16        64        as cut
+//   2048, 4 x 1024 x 16       217 + 597   107 + 209  84 + 164  77 + 160  76 + 159  83 + 171
+//   16384, 2 x 1000 x 16     1706 + 4689  746 + 1531 382 + 786 291 + 602 251 + 567 278 + 577
+//   4096, 8 x 512 x 16        426 + 1179  197 + 398 153 + 311 140 + 301 134 + 302 140 + 300
+//   4096, 2 x 1024 x 64      1076 + 4297  494 + 1320 259 + 687 208 + 675 215 + 708 208 + 676
+//   500 ragged, 64 x 512 x 16  75 + 205   105 + 223 104 + 220 (8 pieces are all)    74 + 203
 int sel_segments(int T, int B, int H, int N, int G, int cus, int* seg_steps) {
   const double tiles = (double)B * sel_group_tiles(H, G) * G, scale = 0.5 + sel_padded(N) / 32.0;
   const int chunks = (T + 63) / 64;

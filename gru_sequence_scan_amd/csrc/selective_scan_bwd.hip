@@ -17,8 +17,8 @@
 // 2048 channels, N = 32, bf16: 1207 us with eight steps at a time and all of
 // it written out, 1028 so; 1024 x 8 x 2048, N = 64: 1372 and 1171). With four
 // states a lane that costs more than the second workgroup a SIMD it allows
-// gives (T 16384, 2 x 1000 x 16: 508 us with 16 steps, 556 with eight, 598
-// with four). So nothing is divided by a decay, which may be zero, and y is
+// gives (T 16384, 2 x 1000 x 16: 508 us with 16 steps, where it takes 468 now,
+// 556 with eight, 598 with four). So nothing is divided by a decay, which may be zero, and y is
 // not read.
 //
 // dB and dC are sums over the channels: a wave adds its 16 by lane
@@ -29,9 +29,9 @@
 // segments by a third.
 //
 // Bound by the issue of vector instructions, like the forward: 100 a step for
-// the 256 states of a wave, 4.5 of them exponentials; 92% of the slots busy.
-// T 16384, 2 x 1000 x 16, bf16, with gate: 480 us (forward 173); 500 ragged
-// steps of 64 x 512 x 16, fp32, without: 183 us (forward 75).
+// the 256 states of a wave, 4.5 of them exponentials. T 16384, 2 x 1000 x 16,
+// bf16, with gate: 468 us, of which its instructions take 375 (forward 165 and
+// 133); 500 ragged steps of 64 x 512 x 16, fp32, without: 180 us (forward 74).
 #include "selective_scan_common.hpp"
 
 namespace rnnk {
