@@ -350,7 +350,8 @@ def feed_forward(x, w_in, w_out, *, residual=None, activation="silu"):
     weights and the residual may be strided (contiguous last dimension).
     Returns y [..., N_out]. In bf16 the hidden values are rounded once on the
     way into the second product. A serving step is a few rows (64 at most take
-    a path of their own)."""
+    a path of their own, which reads operands at any address; with more, one
+    that is off 16 bytes, or whose rows are no whole 16 bytes, is copied)."""
     return _feed_forward(x, w_in, w_out, residual, activation, False)
 
 
