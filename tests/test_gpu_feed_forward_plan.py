@@ -22,7 +22,7 @@ def test_every_tile_and_split(dtype, rows, n, F, n_out):
     g = torch.Generator(device="cuda").manual_seed(rows + n + F)
 
     def normal(a, b, scale=1.0):
-        return (torch.randn((a, b), generator=g, device="cuda") * scale).to(torch.bfloat16 if bf else torch.float32)
+        return (torch.randn((a, b), generator=g, device="cuda", dtype=torch.float32) * scale).to(torch.bfloat16 if bf else torch.float32)
 
     x, r, dy = normal(rows, n), normal(rows, n_out, 2.0), normal(rows, n_out)
     w_in, w_out = normal(2 * F, n, n ** -0.5), normal(n_out, F, F ** -0.5)

@@ -182,8 +182,8 @@ def _growing(T, H, N, grow):
     """A channel that grows by exp(128) over each 64 steps of `grow`, hardly
     elsewhere, from a state of zero."""
     c = _case(T, 1, H, N, 1, torch.float32, 29)
-    c["A"] = 0.9 + 0.1 * torch.rand((H, N), generator=torch.Generator().manual_seed(3))
-    c["dt"] = torch.full((T, 1, H), 1e-3)
+    c["A"] = 0.9 + 0.1 * torch.rand((H, N), generator=torch.Generator().manual_seed(3), dtype=torch.float32)
+    c["dt"] = torch.full((T, 1, H), 1e-3, dtype=torch.float32)
     c["dt"][grow] = 2.2
     c["x"][grow] = 0.0
     c["dt_bias"] = c["h0"] = c["dh_n"] = None
@@ -225,7 +225,7 @@ def test_cut_time_grows_a_small_state_past_one_factor():
     c["dt"][64:128] = 104.0 / 64
     c["dt"][:64] = c["dt"][128:] = 0.0
     c["x"][:] = 0.0
-    c["h0"] = torch.full((1, H, N), 2.0 ** -100)
+    c["h0"] = torch.full((1, H, N), 2.0 ** -100, dtype=torch.float32)
     _, hn = gss.selective_scan(*[c[k].cuda() for k in ("x", "dt", "A", "B", "C")], h0=c["h0"].cuda(), softplus=False)
     # the steps and their sum are exact; log2(e), its product with the sum, a third and the product with that are
     # rounded: 104 (2^-25 + 2^-24 + 2^-25 + 2^-24), and three times an exponential (2^-23) and a product: 1.9e-5 in all
