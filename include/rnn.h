@@ -657,7 +657,9 @@ int rnn_causal_conv_backward(const RnnCausalConvDesc* desc, const RnnCausalConvI
  *   d_t = softplus(dt_t + dt_bias)                    (or dt_t + dt_bias)
  *   h_t[n] = exp(d_t A[n]) h_{t-1}[n] + d_t x_t B_t[n]
  *   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)     (without z: no factor)
- * Channel h reads B and C of group h / (H / G). A must be finite. */
+ * Channel h reads B and C of group h / (H / G). A must be finite, and so must
+ * every step's factor exp(d_t A) in fp32 (a channel may grow without bound over
+ * many steps: a state of zero stays zero). */
 typedef struct RnnSelectiveScanDesc {
   int32_t dtype;         /* RnnDtype of x, dt, z, B, C, y and their gradients  */
   int32_t T, B, H;       /* >= 1                                               */
